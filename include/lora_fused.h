@@ -273,6 +273,128 @@ lora_status lora_dora_norm(const void *W, const void *A, const void *B, int64_t 
                            int32_t r, float alpha, float *norm, void *workspace,
                            size_t workspace_bytes, hipStream_t stream);
 
+/* ---- frozen weights in 4 bits (MXFP4) ------------------------------------
+ * The frozen W may be held in microscaled 4-bit floating point: e2m1 codes
+ * (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives) in blocks of 32 along k
+ * with one scale byte s per block, W'[i][j] = code * 2^(s - 127).  Every W'
+ * is exactly a bf16.  The layers compute with W' in place of W, forward and
+ * backward, and X, dY and the adapters stay bf16: the gradients are those of
+ * the layer that the forward computed.
+ *
+ * Storage, N16 = ceil(n / 16) and KB = 4 ceil(k / 128):
+ *   codes   [N16][KB][16][16] bytes: byte i of (c, b, j) holds W'[32b + 2i][16c + j]
+ *           in its low nibble and W'[32b + 2i + 1][16c + j] in its high one
+ *   scales  [N16][KB][16] bytes
+ * both 16-byte aligned, lora_mxfp4_codes_size() and lora_mxfp4_scales_size()
+ * bytes.  Padding columns and rows hold zero codes; quantising writes them.
+ *
+ * lora_mxfp4_quantize: with a the block's largest magnitude, the scale is
+ * 2^e, e = floor(log2 a) - 2, one more where a / 2^e >= 7, clamped to
+ * [-125, 125]; each code is the nearest to w / 2^e (ties to the even code,
+ * at most 6).  A block of zeros gets s = 127, and a block with an infinity or
+ * a NaN s = 255: all its values then read as NaN.  Bytes 0, 1, 253 and 254
+ * are not written by it but read as the powers of two they stand for (past
+ * bf16's range as infinities). */
+size_t lora_mxfp4_codes_size(int64_t k, int64_t n);
+size_t lora_mxfp4_scales_size(int64_t k, int64_t n);
+lora_status lora_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *codes, void *scales,
+                                hipStream_t stream);
+/* W' as row-major k x n bf16 (exact). */
+lora_status lora_mxfp4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, void *W,
+                                  hipStream_t stream);
+
+/* The frozen layer over W': Y = X W' and dX = dY W'^T.  m == 0 returns at
+ * once. */
+size_t lora_mxfp4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n);
+lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t m, int64_t k,
+                                  int64_t n, void *Y, void *workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+size_t lora_mxfp4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n);
+lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, const void *scales, int64_t m, int64_t k,
+                                  int64_t n, void *dX, void *workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
+/* lora_linear_fwd / lora_linear_bwd and multi_lora_linear_fwd / _bwd with W'
+ * in place of W: the same arguments, outputs, checks and errors. */
+size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r);
+lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales, const void *A,
+                                  const void *B, int64_t m, int64_t k, int64_t n, int32_t r, float alpha,
+                                  float p, uint64_t seed, uint64_t offset, void *Y, float *S,
+                                  uint32_t *keep_bits, void *workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r);
+lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales,
+                                  const void *A, const void *B, const float *S, const uint32_t *keep_bits,
+                                  int64_t m, int64_t k, int64_t n, int32_t r, float alpha, float p, void *dX,
+                                  void *dA, void *dB, void *workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                           int32_t num_adapters, int32_t num_segments);
+lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales,
+                                        const lora_adapter *adapters, int32_t num_adapters,
+                                        const int64_t *seg_off, const int32_t *seg_adapter,
+                                        int32_t num_segments, int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                        uint64_t seed, uint64_t offset, void *Y, float *S,
+                                        uint32_t *keep_bits, void *workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
+size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                           int32_t num_adapters, int32_t num_segments);
+lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales,
+                                        const lora_adapter *adapters, int32_t num_adapters,
+                                        const int64_t *seg_off, const int32_t *seg_adapter,
+                                        int32_t num_segments, const float *S, const uint32_t *keep_bits,
+                                        int64_t m, int64_t k, int64_t n, int32_t r_max, void *dX,
+                                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- optimizer ------------------------------------------------------------
+ * One AdamW step over many tensors (the adapters' A and B of a model):
+ *   m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32 (each constant, 1 - beta among them, rounded from its double), everything
+ * updated in place.
+ *
+ * Types: param is fp32, or bf16 (param_bf16 = 1) with or without an fp32
+ * master copy; with one the master is updated and param becomes its nearest
+ * bf16, without one w is read from param and rounded to it.  grad is fp32 or
+ * bf16 (grad_bf16 = 1).  state_bits = 32: m and v are n floats.
+ * state_bits = 8: m and v are n e4m3 bytes (OCP FP8), codes of m and of
+ * sqrt(v), and m_scale and v_scale ceil(n / 256) floats: value = code * scale
+ * of its block of 256.  A new moment x of a block with largest magnitude a
+ * becomes scale = a / 448 and a code drawn between the two neighbours of
+ * x / scale so that its mean is x / scale (a positive v keeps at least the
+ * smallest code, so the division stays bounded; a below 2^-100 gives zeros).
+ * The draw of value i is word (offset + i) % 4 of Philox4x32-10 at counter
+ * (offset + i) / 4 under key seed + t * 0x9E3779B97F4A7C15 (mod 2^64), its low
+ * half for m and its high half for v.  offset is a multiple of 8; tensors
+ * with disjoint ranges [offset, offset + n) draw independently.
+ *
+ * An infinite or NaN gradient makes its own w and moments NaN (or infinite)
+ * and nothing else.
+ *
+ * t = step (>= 1) or, where step_dev is not NULL, the int64 it points to on
+ * the device, read when the kernels run (a captured call then follows the
+ * caller's counter; with `step` a replay repeats the captured t).
+ *
+ * `tensors` is a host array, read during the call only.  Records with n = 0
+ * are skipped.  Either every record has a master copy or none.  No two
+ * records may share memory that the call writes. */
+typedef struct {
+    void *param;
+    const void *grad;
+    float *master;
+    void *m;
+    void *v;
+    float *m_scale;
+    float *v_scale;
+    int64_t n;
+    uint64_t offset;
+} lora_adamw_tensor;
+
+lora_status lora_adamw_step(const lora_adamw_tensor *tensors, int32_t count, int32_t param_bf16,
+                            int32_t grad_bf16, int32_t state_bits, double lr, double beta1,
+                            double beta2, double eps, double weight_decay, int64_t step,
+                            const int64_t *step_dev, uint64_t seed, hipStream_t stream);
+
 /* ---- pieces exposed for testing and as the frozen-layer baseline -------- */
 
 /* The dropout mask alone (same bits the forward stores). */

@@ -15,6 +15,14 @@ from ._lib import (  # noqa: F401
     multi_lora_check_segments, multi_lora_fwd_workspace_size, multi_lora_linear_bwd,
     multi_lora_linear_fwd,
 )
+from .adamw import AdamwTable, LoraAdamW, adamw_table, lora_adamw_step  # noqa: F401,E402
+from .mxfp4 import (  # noqa: F401,E402
+    Mxfp4Weight, lora_mxfp4_dequantize, lora_mxfp4_frozen_bwd, lora_mxfp4_frozen_bwd_workspace_size,
+    lora_mxfp4_frozen_fwd, lora_mxfp4_frozen_fwd_workspace_size, lora_mxfp4_linear_bwd,
+    lora_mxfp4_linear_bwd_workspace_size, lora_mxfp4_linear_fwd, lora_mxfp4_linear_fwd_workspace_size,
+    lora_mxfp4_quantize, multi_lora_mxfp4_bwd_workspace_size, multi_lora_mxfp4_fwd_workspace_size,
+    multi_lora_mxfp4_linear_bwd, multi_lora_mxfp4_linear_fwd,
+)
 from .autograd import (  # noqa: F401,E402
     LoraLinear, LoraLinearFunction, MultiLoraLinearFunction, lora_linear, multi_lora_linear,
 )

@@ -33,6 +33,12 @@ EXPORTS = [
     "lora_last_error_message", "lora_pack_greedy", "lora_microbatch_segments",
     "lora_check_bubble_lemma", "lora_dora_norm_workspace_size", "lora_dora_norm",
     "lora_linear_bwd_noalloc_max_scratch", "lora_linear_bwd_noalloc", "lora_linear_fwd_concat",
+    "lora_mxfp4_codes_size", "lora_mxfp4_scales_size", "lora_mxfp4_quantize", "lora_mxfp4_dequantize",
+    "lora_mxfp4_frozen_fwd_workspace_size", "lora_mxfp4_frozen_fwd", "lora_mxfp4_frozen_bwd_workspace_size",
+    "lora_mxfp4_frozen_bwd", "lora_mxfp4_linear_fwd_workspace_size", "lora_mxfp4_linear_fwd",
+    "lora_mxfp4_linear_bwd_workspace_size", "lora_mxfp4_linear_bwd", "multi_lora_mxfp4_fwd_workspace_size",
+    "multi_lora_mxfp4_linear_fwd", "multi_lora_mxfp4_bwd_workspace_size", "multi_lora_mxfp4_linear_bwd",
+    "lora_adamw_step",
 ]
 
 
@@ -62,6 +68,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, I32, I64, U64, F32, SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64,
                                  ctypes.c_float, ctypes.c_size_t)
+    F64 = ctypes.c_double
     sigs = {
         "lora_linear_fwd_workspace_size": (SZ, [I64, I64, I64, I32]),
         "lora_linear_bwd_workspace_size": (SZ, [I64, I64, I64, I32]),
@@ -91,6 +98,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_profiling_reset": (I32, []),
         "lora_profiling_query": (I32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int64),
                                        ctypes.POINTER(ctypes.c_double)]),
+        "lora_mxfp4_codes_size": (SZ, [I64, I64]),
+        "lora_mxfp4_scales_size": (SZ, [I64, I64]),
+        "lora_mxfp4_quantize": (I32, [P, I64, I64, P, P, P]),
+        "lora_mxfp4_dequantize": (I32, [P, P, I64, I64, P, P]),
+        "lora_mxfp4_frozen_fwd_workspace_size": (SZ, [I64, I64, I64]),
+        "lora_mxfp4_frozen_bwd_workspace_size": (SZ, [I64, I64, I64]),
+        "lora_mxfp4_frozen_fwd": (I32, [P, P, P, I64, I64, I64, P, P, SZ, P]),
+        "lora_mxfp4_frozen_bwd": (I32, [P, P, P, I64, I64, I64, P, P, SZ, P]),
+        "lora_mxfp4_linear_fwd_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "lora_mxfp4_linear_bwd_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "lora_mxfp4_linear_fwd": (I32, [P, P, P, P, P, I64, I64, I64, I32, F32, F32, U64, U64, P, P, P,
+                                        P, SZ, P]),
+        "lora_mxfp4_linear_bwd": (I32, [P, P, P, P, P, P, P, P, I64, I64, I64, I32, F32, F32, P, P, P,
+                                        P, SZ, P]),
+        "multi_lora_mxfp4_fwd_workspace_size": (SZ, [I64, I64, I64, I32, I32, I32]),
+        "multi_lora_mxfp4_bwd_workspace_size": (SZ, [I64, I64, I64, I32, I32, I32]),
+        "multi_lora_mxfp4_linear_fwd": (I32, [P, P, P, P, I32, P, P, I32, I64, I64, I64, I32, U64, U64,
+                                              P, P, P, P, SZ, P]),
+        "multi_lora_mxfp4_linear_bwd": (I32, [P, P, P, P, P, I32, P, P, I32, P, P, I64, I64, I64, I32,
+                                              P, P, SZ, P]),
+        "lora_adamw_step": (I32, [P, I32, I32, I32, I32, F64, F64, F64, F64, F64, I64, P, U64, P]),
         "lora_status_string": (ctypes.c_char_p, [I32]),
         "lora_last_error_message": (ctypes.c_char_p, []),
     }
@@ -131,6 +159,42 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.
     if workspace is not None:
         return workspace
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+class _on_device:
+    """The device of a call's tensors as the current one, with `stream` (given
+    explicitly) or that device's current stream as the one that outputs and
+    scratch are allocated for; yields the stream's handle."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guard = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+            self.guard = torch.cuda.stream(self.stream)
+            self.guard.__enter__()
+            return ctypes.c_void_p(self.stream.cuda_stream)
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor]):
+    """(pointer, bytes) of the caller's workspace, or of one allocated here."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,257 @@
+"""AdamW over many tensors in one call, with moments in 8 or 32 bits.
+
+`lora_adamw_step` has the name of its C-ABI entry point in include/lora_fused.h
+and works on an `adamw_table`; `LoraAdamW` is a torch optimizer over it."""
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+import numpy as np
+import torch
+
+from ._lib import _check, _on_device, load
+
+BLOCK = 256  # values that share a scale of the 8-bit moments
+_PARAM, _GRAD, _MASTER, _M, _V, _M_SCALE, _V_SCALE, _N, _OFFSET = range(9)
+
+
+class AdamwTable:
+    """The records of one call (mirrors of lora_adamw_tensor, 72 bytes each) and
+    the tensors they point into, which stay alive with it."""
+
+    def __init__(self, records, tensors, device, param_bf16: bool, grad_bf16: bool, state_bits: int):
+        self.records, self.tensors, self.device = records, tensors, device
+        self.param_bf16, self.grad_bf16, self.state_bits = param_bf16, grad_bf16, state_bits
+
+
+def _column(ts: Sequence[torch.Tensor], name: str, count: int, dtypes, numels=None):
+    """Their addresses, after the checks that every tensor of the column shares."""
+    if len(ts) != count:
+        raise ValueError(f"{name} must have one tensor per parameter ({count}), got {len(ts)}")
+    dtype = ts[0].dtype if count else dtypes[0]
+    if dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
+    for i, t in enumerate(ts):
+        if t.dtype != dtype:
+            raise TypeError(f"{name}[{i}] is {t.dtype}, {name}[0] {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        if numels is not None and t.numel() != numels[i]:
+            raise ValueError(f"{name}[{i}] must have {numels[i]} values, got {t.numel()}")
+    return [t.data_ptr() for t in ts], dtype
+
+
+def _apart(records, widths) -> None:
+    """Refuse records that share memory which a step writes."""
+    spans = []
+    n = records[:, _N].astype(np.int64)
+    for col, width in widths:
+        size = -(-n // BLOCK) * 4 if col in (_M_SCALE, _V_SCALE) else n * width
+        at = records[:, col].astype(np.int64)
+        spans.append(np.stack([at, at + size], 1)[size > 0])
+    s = np.concatenate(spans)
+    s = s[np.argsort(s[:, 0], kind="stable")]
+    if (s[1:, 0] < s[:-1, 1]).any():
+        raise ValueError("two of the tensors that a step writes share memory")
+
+
+def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=None,
+                offsets: Optional[Sequence[int]] = None) -> AdamwTable:
+    """The records of lora_adamw_step for these tensors: params fp32 or bf16,
+    grads fp32 or bf16, and moments as float32, or as float8_e4m3fn with m_scales
+    and v_scales of one float32 for each 256 values.  masters: fp32 copies of
+    bf16 params.  offsets: each tensor's first counter of the random roundings
+    (a multiple of 8; by default the tensors follow one another)."""
+    params, grads, ms, vs = list(params), list(grads), list(ms), list(vs)
+    count = len(params)
+    if count == 0:
+        raise ValueError("params must not be empty")
+    device = params[0].device
+    numels = [p.numel() for p in params]
+    held8 = ms[0].dtype == torch.float8_e4m3fn if ms else False
+    moment = (torch.float8_e4m3fn,) if held8 else (torch.float32,)
+    f32, either = (torch.float32,), (torch.float32, torch.bfloat16)
+    rec = np.zeros((count, 9), dtype=np.uint64)
+    rec[:, _PARAM], pt = _column(params, "params", count, either)
+    rec[:, _GRAD], gt = _column(grads, "grads", count, either, numels)
+    rec[:, _M], _ = _column(ms, "ms", count, moment, numels)
+    rec[:, _V], _ = _column(vs, "vs", count, moment, numels)
+    tensors = [params, grads, ms, vs]
+    widths = [(_PARAM, 2 if pt == torch.bfloat16 else 4), (_M, 1 if held8 else 4), (_V, 1 if held8 else 4)]
+    if held8:
+        blocks = [-(-e // BLOCK) for e in numels]
+        for col, ts, name in ((_M_SCALE, m_scales, "m_scales"), (_V_SCALE, v_scales, "v_scales")):
+            if ts is None:
+                raise ValueError("8-bit moments need m_scales and v_scales")
+            rec[:, col], _ = _column(list(ts), name, count, f32, blocks)
+            tensors.append(list(ts))
+            widths.append((col, 4))
+    elif m_scales is not None or v_scales is not None:
+        raise ValueError("m_scales and v_scales go with float8_e4m3fn moments")
+    if masters is not None:
+        if pt != torch.bfloat16:
+            raise ValueError("master copies go with bf16 params")
+        rec[:, _MASTER], _ = _column(list(masters), "masters", count, f32, numels)
+        tensors.append(list(masters))
+        widths.append((_MASTER, 4))
+    if offsets is None:
+        padded = [(e + 7) // 8 * 8 for e in numels]
+        offsets = np.concatenate([[0], np.cumsum(padded)[:-1]])
+    elif len(offsets) != count or any(int(o) % 8 or int(o) < 0 for o in offsets):
+        raise ValueError("offsets must be one multiple of 8 (>= 0) per parameter")
+    rec[:, _N], rec[:, _OFFSET] = numels, np.asarray(offsets, dtype=np.uint64)
+    # the device last, so that host tests can reach every other check with CPU tensors
+    for ts in tensors:
+        for t in ts:
+            if t.device.type != "cuda" or t.device != device:
+                raise ValueError(f"a tensor is on {t.device}: all must be on one GPU ({device})")
+    _apart(rec, widths)
+    return AdamwTable(rec, tensors, device, pt == torch.bfloat16, gt == torch.bfloat16, 8 if held8 else 32)
+
+
+def lora_adamw_step(table: AdamwTable, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                    weight_decay: float = 0.0, step: int = 0, step_dev: Optional[torch.Tensor] = None, seed: int = 0,
+                    stream=None) -> None:
+    """One step (the step-th, from 1; or the one whose number the int64 device
+    tensor step_dev holds) over the table's tensors, in place."""
+    if step_dev is not None:
+        if step_dev.dtype != torch.int64 or step_dev.numel() != 1 or step_dev.device != table.device:
+            raise ValueError(f"step_dev must be one int64 on {table.device}")
+        step_dev = step_dev.data_ptr()
+    rec = table.records
+    with _on_device(table.device, stream) as st:
+        _check(load().lora_adamw_step(rec.ctypes.data, len(rec), int(table.param_bf16), int(table.grad_bf16),
+                                      table.state_bits, lr, beta1, beta2, eps, weight_decay, step, step_dev,
+                                      seed % (1 << 64), st))
+
+
+class LoraAdamW(torch.optim.Optimizer):
+    """AdamW (decoupled weight decay) for adapter tensors, all of a group in one
+    call of the library.
+
+    state_bits: 8 or 32, the bits of a moment.  master: bf16 parameters get an
+    fp32 copy that is updated in their place (a bf16 loses updates below half of
+    its last place).  seed: of the 8-bit moments' random rounding.  capturable:
+    the step number lives on the device, so that a captured step() counts on in
+    every replay; the group's learning rate and decay are those of the capture.
+
+    Parameters are contiguous GPU tensors, fp32 or bf16.  A parameter without a
+    gradient is left out of a step (the shared counter of a capturable group goes
+    on).  A parameter whose values are replaced from outside keeps its master copy
+    until its state is cleared."""
+
+    def __init__(self, params, lr: float = 1e-4, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
+                 state_bits: int = 8, master: bool = True, seed: int = 0, capturable: bool = False):
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits = {state_bits} must be 8 or 32")
+        if not lr >= 0.0 or not weight_decay >= 0.0 or not eps >= 0.0:
+            raise ValueError(f"lr = {lr}, weight_decay = {weight_decay} and eps = {eps} must be >= 0")
+        if not all(0.0 <= b < 1.0 for b in betas):
+            raise ValueError(f"betas = {betas} must be in [0, 1)")
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
+                                      state_bits=state_bits, master=master, seed=seed, capturable=capturable))
+
+    def _counter(self, group, device) -> torch.Tensor:
+        """The step counter that a captured group's parameters on a device share."""
+        for p in group["params"]:
+            at = self.state[p].get("step") if p in self.state else None
+            if isinstance(at, torch.Tensor) and at.device == device:
+                return at
+        return torch.zeros(1, dtype=torch.int64, device=device)
+
+    def _new_state(self, p: torch.Tensor, group) -> dict:
+        n, dev = p.numel(), p.device
+        # counters of the random rounding: past every other parameter's
+        ends = [st["offset"] + st["m"].numel() for st in self.state.values() if st]
+        st = {"step": self._counter(group, dev) if group["capturable"] else 0,
+              "offset": -(-max(ends, default=0) // BLOCK) * BLOCK}
+        if group["state_bits"] == 8:
+            st["m"], st["v"] = (torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+                                for _ in range(2))
+            st["m_scale"], st["v_scale"] = (torch.zeros((n + BLOCK - 1) // BLOCK, device=dev) for _ in range(2))
+        else:
+            st["m"], st["v"] = (torch.zeros(n, dtype=torch.float32, device=dev) for _ in range(2))
+        if group["master"] and p.dtype == torch.bfloat16:
+            st["master"] = p.detach().reshape(-1).float()
+        return st
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            calls = {}  # the tensors of one call share a device, types and a step
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.is_sparse:
+                    raise ValueError("gradients must be dense")
+                st = self.state[p]
+                if not st:
+                    st.update(self._new_state(p, group))
+                key = (p.device, p.dtype, p.grad.dtype, "master" in st)
+                if not group["capturable"]:
+                    st["step"] += 1
+                    key += (st["step"],)
+                calls.setdefault(key, []).append(p)
+            if group["capturable"]:
+                for device in {key[0] for key in calls}:
+                    self._counter(group, device).add_(1)
+            for ps in calls.values():
+                self._step(ps, group)
+        return loss
+
+    def _table(self, ps) -> AdamwTable:
+        """The table of these parameters, built at their first step together; later steps
+        read every address anew (gradients are new tensors, parameters may have moved)."""
+        states = [self.state[p] for p in ps]
+        grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in ps]
+        tables = self.__dict__.setdefault("_tables", {})
+        key = tuple(map(id, ps)) + (ps[0].dtype, grads[0].dtype)
+        table = tables.get(key)
+        if table is None:
+            each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
+            table = adamw_table([p.detach() for p in ps], grads, each("m"), each("v"), m_scales=each("m_scale"),
+                                v_scales=each("v_scale"), masters=each("master"), offsets=each("offset"))
+            table.params = ps  # alive, so that their ids stay theirs
+            if len(tables) >= 64:
+                tables.clear()
+            tables[key] = table
+            return table
+        rec = table.records
+        for p in ps:
+            if not p.is_contiguous():
+                raise ValueError("parameters must be contiguous")
+        rec[:, _PARAM] = [p.data_ptr() for p in ps]
+        rec[:, _GRAD] = [g.data_ptr() for g in grads]
+        for name, col in (("m", _M), ("v", _V), ("m_scale", _M_SCALE), ("v_scale", _V_SCALE), ("master", _MASTER)):
+            if name in states[0]:
+                rec[:, col] = [st[name].data_ptr() for st in states]
+        table.tensors = [grads]
+        return table
+
+    def _step(self, ps, group) -> None:
+        st = self.state[ps[0]]
+        at = dict(step_dev=st["step"]) if group["capturable"] else dict(step=st["step"])
+        lora_adamw_step(self._table(ps), lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
+                        eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"], **at)
+
+    def load_state_dict(self, state_dict) -> None:
+        """The moments keep their own types (torch's loader would cast them to
+        the parameters')."""
+        saved = state_dict["state"]
+        super().load_state_dict(dict(state_dict, state={}))
+        self.__dict__.pop("_tables", None)
+        for group, old in zip(self.param_groups, state_dict["param_groups"]):
+            for p, i in zip(group["params"], old["params"]):
+                if i not in saved:
+                    continue
+                st = {name: x.to(device=p.device, copy=True) if isinstance(x, torch.Tensor) else x
+                      for name, x in saved[i].items()}
+                if group["capturable"]:  # one counter again
+                    st["step"] = self._counter(group, p.device).copy_(torch.as_tensor(st["step"]))
+                elif isinstance(st["step"], torch.Tensor):
+                    st["step"] = int(st["step"])
+                self.state[p] = st

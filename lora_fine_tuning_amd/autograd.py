@@ -13,29 +13,43 @@ from collections import OrderedDict
 
 import torch
 
-from . import _lib
+from . import _lib, mxfp4
+from .mxfp4 import Mxfp4Weight
+
+
+def _weight_tensors(W):
+    """The tensors of a frozen weight (one bf16 tensor, or an Mxfp4Weight's two)."""
+    return (W.codes, W.scales) if isinstance(W, Mxfp4Weight) else (W,)
+
+
+def _weight_again(tensors, k: int, n: int):
+    return Mxfp4Weight(*tensors, k, n) if len(tensors) == 2 else tensors[0]
 
 
 class LoraLinearFunction(torch.autograd.Function):
-    """Y = X W + alpha * (dropout(X) A) B for X (..., k) bf16; W k x n is frozen
-    (no gradient); A k x r and B r x n receive gradients."""
+    """Y = X W + alpha * (dropout(X) A) B for X (..., k) bf16; W k x n, a bf16
+    tensor or an Mxfp4Weight, is frozen (no gradient); A k x r and B r x n
+    receive gradients."""
 
     @staticmethod
     def forward(ctx, X, W, A, B, alpha: float, p: float, seed: int, offset: int):
         lead = X.shape[:-1]
         X2 = X.reshape(-1, X.shape[-1]).contiguous()
-        Y, S, keep = _lib.lora_linear_fwd(X2, W, A, B, alpha, p, seed, offset)
-        ctx.save_for_backward(X2, W, A, B, S, keep if keep is not None else torch.empty(0, device=X.device))
+        fwd = mxfp4.lora_mxfp4_linear_fwd if isinstance(W, Mxfp4Weight) else _lib.lora_linear_fwd
+        Y, S, keep = fwd(X2, W, A, B, alpha, p, seed, offset)
+        ctx.save_for_backward(X2, A, B, S, keep if keep is not None else torch.empty(0, device=X.device),
+                              *_weight_tensors(W))
         ctx.alpha, ctx.p, ctx.lead, ctx.has_keep = alpha, p, lead, keep is not None
         return Y.reshape(*lead, W.shape[1])
 
     @staticmethod
     def backward(ctx, dY):
-        X2, W, A, B, S, keep = ctx.saved_tensors
+        X2, A, B, S, keep, *held = ctx.saved_tensors
+        W = _weight_again(held, X2.shape[1], B.shape[1])
+        bwd = mxfp4.lora_mxfp4_linear_bwd if isinstance(W, Mxfp4Weight) else _lib.lora_linear_bwd
         dY2 = dY.reshape(-1, dY.shape[-1]).contiguous()
         want_dX = ctx.needs_input_grad[0]
-        dX, dA, dB = _lib.lora_linear_bwd(dY2, X2, W, A, B, S, keep if ctx.has_keep else None,
-                                          ctx.alpha, ctx.p, want_dX=want_dX)
+        dX, dA, dB = bwd(dY2, X2, W, A, B, S, keep if ctx.has_keep else None, ctx.alpha, ctx.p, want_dX=want_dX)
         dX = dX.reshape(*ctx.lead, W.shape[0]) if want_dX else None
         return dX, None, dA, dB, None, None, None, None
 
@@ -111,19 +125,21 @@ class MultiLoraLinearFunction(torch.autograd.Function):
     def forward(ctx, X, W, seg_off, seg_adapter, alphas, ps, seed: int, offset: int, *AB):
         As, Bs = AB[0::2], AB[1::2]
         st = _adapter_set(As, Bs, alphas, ps)
-        Y, S, keep = _lib.multi_lora_linear_fwd(X, W, st.table, st.num, seg_off, seg_adapter, st.r_max, seed,
-                                                offset)
-        ctx.save_for_backward(X, W, seg_off, seg_adapter, S, keep)
+        fwd = mxfp4.multi_lora_mxfp4_linear_fwd if isinstance(W, Mxfp4Weight) else _lib.multi_lora_linear_fwd
+        Y, S, keep = fwd(X, W, st.table, st.num, seg_off, seg_adapter, st.r_max, seed, offset)
+        ctx.save_for_backward(X, seg_off, seg_adapter, S, keep, *_weight_tensors(W))
         ctx.adapter_set = st
         return Y
 
     @staticmethod
     def backward(ctx, dY):
-        X, W, seg_off, seg_adapter, S, keep = ctx.saved_tensors
+        X, seg_off, seg_adapter, S, keep, *held = ctx.saved_tensors
         st = ctx.adapter_set
+        W = _weight_again(held, st.k, st.n)
+        bwd = mxfp4.multi_lora_mxfp4_linear_bwd if isinstance(W, Mxfp4Weight) else _lib.multi_lora_linear_bwd
         dAs, dBs = st.gradient_buffers()
-        dX = _lib.multi_lora_linear_bwd(dY.contiguous(), X, W, st.table, st.num, seg_off, seg_adapter, S, keep,
-                                        st.r_max, want_dX=ctx.needs_input_grad[0])
+        dX = bwd(dY.contiguous(), X, W, st.table, st.num, seg_off, seg_adapter, S, keep, st.r_max,
+                 want_dX=ctx.needs_input_grad[0])
         grads = []
         for da, db in zip(dAs, dBs):
             grads += [da, db]
@@ -136,16 +152,20 @@ def multi_lora_linear(X, W, seg_off, seg_adapter, As, Bs, alphas, ps, seed: int 
 
 
 class LoraLinear(torch.nn.Module):
-    """A frozen k x n weight with one LoRA adapter (A k x r, B r x n; B starts
-    at zero).  Dropout draws from the library's counter-based generator under
+    """A frozen k x n weight, a tensor (kept in bf16) or an Mxfp4Weight, with
+    one LoRA adapter (A k x r, B r x n; B starts at zero).  Dropout draws from the library's counter-based generator under
     this module's own seed; each training call advances the counter past the
     elements it used, so successive calls get fresh masks and a rerun from the
     same state reproduces them.  In eval mode dropout is off."""
 
-    def __init__(self, weight: torch.Tensor, r: int, alpha: float, p: float = 0.0, seed: int = 0):
+    def __init__(self, weight, r: int, alpha: float, p: float = 0.0, seed: int = 0):
         super().__init__()
-        k, n = weight.shape
-        self.register_buffer("weight", weight.detach().to(torch.bfloat16).contiguous())
+        self.k, self.n = k, n = weight.shape
+        if isinstance(weight, Mxfp4Weight):
+            self.register_buffer("weight_codes", weight.codes)
+            self.register_buffer("weight_scales", weight.scales)
+        else:
+            self.register_buffer("weight", weight.detach().to(torch.bfloat16).contiguous())
         gen = torch.Generator(device="cpu").manual_seed(seed)
         a = torch.randn(k, r, generator=gen) / k ** 0.5
         self.A = torch.nn.Parameter(a.to(device=weight.device, dtype=torch.bfloat16))
@@ -159,4 +179,6 @@ class LoraLinear(torch.nn.Module):
         if p > 0.0:
             used = X.numel() // X.shape[-1] * X.shape[-1]
             self.offset += (used + 7) // 8 * 8
-        return LoraLinearFunction.apply(X, self.weight, self.A, self.B, self.alpha, p, self.seed, offset)
+        held = (self.weight_codes, self.weight_scales) if hasattr(self, "weight_codes") else (self.weight,)
+        W = _weight_again(held, self.k, self.n)
+        return LoraLinearFunction.apply(X, W, self.A, self.B, self.alpha, p, self.seed, offset)

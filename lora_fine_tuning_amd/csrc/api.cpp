@@ -11,6 +11,7 @@
 #include <string>
 #include <vector>
 
+#include "api_checks.hpp"
 #include "device_common.hpp"
 #include "host_status.hpp"
 #include "launch.hpp"
@@ -28,16 +29,6 @@ using namespace lora;
 // ---------------------------------------------------------------------------
 static thread_local std::string g_last_error;
 
-static lora_status fail(lora_status st, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return st;
-}
-
 namespace lora {
 lora_status host_fail(lora_status st, const char *fmt, ...) {
     char buf[512];
@@ -49,10 +40,6 @@ lora_status host_fail(lora_status st, const char *fmt, ...) {
     return st;
 }
 }  // namespace lora
-
-static lora_status hip_fail(hipError_t e, const char *what) {
-    return fail(LORA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
 
 extern "C" const char *lora_status_string(lora_status s) {
     // A C caller may pass any int; read it as one (a C++ load of an enum value
@@ -111,7 +98,7 @@ extern "C" lora_status lora_profiling_enable(int32_t enable, int32_t capacity) {
     g_prof_used = 0;
     g_prof_on = false;
     if (!enable) return LORA_OK;
-    if (capacity <= 0 || capacity > (1 << 20)) return fail(LORA_ERR_INVALID_ARG, "profiling capacity %d", capacity);
+    if (capacity <= 0 || capacity > (1 << 20)) return host_fail(LORA_ERR_INVALID_ARG, "profiling capacity %d", capacity);
     g_prof_pool.resize((size_t)capacity);
     for (auto &s : g_prof_pool) {
         s.name = "";
@@ -133,7 +120,7 @@ extern "C" lora_status lora_profiling_reset(void) {
 }
 
 extern "C" lora_status lora_profiling_query(const char *name_substring, int64_t *launches, double *total_ms) {
-    if (!name_substring || !launches || !total_ms) return fail(LORA_ERR_INVALID_ARG, "NULL argument");
+    if (!name_substring || !launches || !total_ms) return host_fail(LORA_ERR_INVALID_ARG, "NULL argument");
     std::lock_guard<std::mutex> lk(g_prof_mu);
     int64_t n = 0;
     double tot = 0.0;
@@ -154,71 +141,9 @@ extern "C" lora_status lora_profiling_query(const char *name_substring, int64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Argument checks
-// ---------------------------------------------------------------------------
-static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-#define REQUIRE(cond, ...)                                        \
-    do {                                                          \
-        if (!(cond)) return fail(LORA_ERR_INVALID_ARG, __VA_ARGS__); \
-    } while (0)
-
-static lora_status check_shape(int64_t m, int64_t k, int64_t n) {
-    REQUIRE(m >= 0 && m < (1LL << 31), "m = %lld out of range [0, 2^31)", (long long)m);
-    REQUIRE(k > 0 && k < (1LL << 31), "k = %lld out of range (0, 2^31)", (long long)k);
-    REQUIRE(n > 0 && n < (1LL << 31), "n = %lld out of range (0, 2^31)", (long long)n);
-    REQUIRE(k % 8 == 0, "k = %lld must be a multiple of 8", (long long)k);
-    REQUIRE(n % 8 == 0, "n = %lld must be a multiple of 8", (long long)n);
-    REQUIRE(m * k < (1LL << 46) && m * n < (1LL << 46), "tensor too large");
-    return LORA_OK;
-}
-
-static lora_status check_rank(int32_t r) {
-    REQUIRE(r >= 1 && r <= 256, "rank r = %d must be in [1, 256]", r);
-    return LORA_OK;
-}
-
-// The GEMM epilogues and the dS/dB kernel address B (r x n bf16) and A
-// (k x r bf16) with 32-bit byte offsets.
-static lora_status check_b_size(int32_t r, int64_t k, int64_t n) {
-    if ((int64_t)r * n * 2 >= (1LL << 31))
-        return fail(LORA_ERR_UNSUPPORTED, "B of %d x %lld bf16 exceeds 2 GiB", r, (long long)n);
-    if ((int64_t)r * k * 2 >= (1LL << 31))
-        return fail(LORA_ERR_UNSUPPORTED, "A of %lld x %d bf16 exceeds 2 GiB", (long long)k, r);
-    return LORA_OK;
-}
-
-static lora_status check_p(float p) {
-    REQUIRE(p >= 0.0f && p < 1.0f, "dropout p = %g must be in [0, 1)", (double)p);
-    return LORA_OK;
-}
-
-#define CHECK(x)                          \
-    do {                                  \
-        lora_status _st = (x);            \
-        if (_st != LORA_OK) return _st;   \
-    } while (0)
-
-#define REQ_PTR(p, align) \
-    REQUIRE((p) != nullptr && aligned((p), (align)), #p " must be non-NULL and %d-byte aligned", (int)(align))
-
-// ---------------------------------------------------------------------------
 // Workspace plans
 // ---------------------------------------------------------------------------
 namespace {
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-struct Carve {
-    size_t off = 0;
-    size_t take(size_t bytes) {
-        size_t o = off;
-        off = align_up(off + bytes);
-        return o;
-    }
-};
-
 struct FwdPlan {
     int RS;
     int chunk_cap_f1;  // grid size of F1 (upper bound on chunks)
@@ -321,8 +246,6 @@ BwdPlan plan_bwd(int64_t m, int64_t k, int64_t n, int32_t RS, bool multi, int32_
     return p;
 }
 
-char *ws_at(void *ws, size_t off) { return (char *)ws + off; }
-
 AdapterSource single_source(const void *A, const void *B, void *dA, void *dB, int32_t r, float alpha, float p) {
     AdapterSource s{};
     s.A = A;
@@ -337,12 +260,6 @@ AdapterSource single_source(const void *A, const void *B, void *dA, void *dB, in
     return s;
 }
 }  // namespace
-
-#define HIPCHK(call, what)                         \
-    do {                                           \
-        hipError_t _e = (call);                    \
-        if (_e != hipSuccess) return hip_fail(_e, what); \
-    } while (0)
 
 // ---------------------------------------------------------------------------
 // Single adapter
@@ -379,7 +296,7 @@ extern "C" lora_status lora_linear_fwd(const void *X, const void *W, const void 
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     const FwdPlan pl = plan_fwd(m, k, r, false, 0);
     if (workspace_bytes < pl.bytes)
-        return fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
+        return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     if (pl.bytes) REQ_PTR(workspace, 16);
 
     AdapterSource src = single_source(A, B, nullptr, nullptr, r, alpha, p);
@@ -414,14 +331,14 @@ extern "C" lora_status lora_linear_fwd_concat(const void *X, const void *W, cons
     REQ_PTR(A, 2);
     REQ_PTR(B, 2);
     if (r != 8 && r != 16)
-        return fail(LORA_ERR_UNSUPPORTED, "the concatenated forward takes r = 8 or 16 (r = %d)", r);
+        return host_fail(LORA_ERR_UNSUPPORTED, "the concatenated forward takes r = 8 or 16 (r = %d)", r);
     if (!aligned(A, 16) || !aligned(B, 16))
-        return fail(LORA_ERR_UNSUPPORTED, "the concatenated forward needs A and B 16-byte aligned");
+        return host_fail(LORA_ERR_UNSUPPORTED, "the concatenated forward needs A and B 16-byte aligned");
     if (m == 0) return LORA_OK;
     REQ_PTR(X, 16);
     REQ_PTR(Y, 16);
     REQ_PTR(S, 4);
-    if (!aligned(S, 16)) return fail(LORA_ERR_UNSUPPORTED, "the concatenated forward needs S 16-byte aligned");
+    if (!aligned(S, 16)) return host_fail(LORA_ERR_UNSUPPORTED, "the concatenated forward needs S 16-byte aligned");
     HIPCHK(launch_gemm_cat(X, W, A, B, Y, S, (int)m, (int)n, (int)k, r, alpha, stream), "concatenated F2 launch");
     return LORA_OK;
 }
@@ -450,7 +367,7 @@ extern "C" lora_status lora_linear_bwd(const void *dY, const void *X, const void
     }
     const BwdPlan pl = plan_bwd(m, k, n, r, false, 0, 1);
     if (workspace_bytes < pl.bytes)
-        return fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
+        return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     if (pl.bytes) REQ_PTR(workspace, 16);
 
     AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
@@ -539,7 +456,7 @@ extern "C" lora_status multi_lora_linear_fwd(const void *X, const void *W, const
     REQ_PTR(keep_bits, 4);
     const FwdPlan pl = plan_fwd(m, k, r_max, true, num_segments);
     if (workspace_bytes < pl.bytes)
-        return fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
+        return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     REQ_PTR(workspace, 16);
 
     AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
@@ -587,7 +504,7 @@ extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, cons
     }
     const BwdPlan pl = plan_bwd(m, k, n, r_max, true, num_segments, num_adapters);
     if (workspace_bytes < pl.bytes)
-        return fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
+        return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     REQ_PTR(workspace, 16);
 
     AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
@@ -671,11 +588,11 @@ extern "C" lora_status lora_dora_norm(const void *W, const void *A, const void *
     REQ_PTR(B, 16);
     REQ_PTR(norm, 4);
     if ((int64_t)(r + 32) * n * 2 >= (1LL << 31) || k * (int64_t)r * 2 >= (1LL << 31))
-        return fail(LORA_ERR_UNSUPPORTED, "A or B exceeds 2 GiB");
+        return host_fail(LORA_ERR_UNSUPPORTED, "A or B exceeds 2 GiB");
     const DoraPlan pl = dora_plan(k, n, r);
     const size_t need = (size_t)pl.splits * (size_t)n * sizeof(float);
     if (workspace_bytes < need)
-        return fail(LORA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+        return host_fail(LORA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, need);
     REQ_PTR(workspace, 16);
     HIPCHK(launch_dora_norm(W, A, B, (int)k, (int)n, r, alpha, pl, (float *)workspace, norm, stream),
            "DoRA norm launch");
@@ -744,13 +661,13 @@ static lora_status scratch_of_current_device(void **out) {
     int dev = -1;
     HIPCHK(hipGetDevice(&dev), "hipGetDevice");
     if (dev < 0 || dev >= kScratchDevices)
-        return fail(LORA_ERR_UNSUPPORTED, "device %d: the static scratch serves devices 0..%d", dev,
+        return host_fail(LORA_ERR_UNSUPPORTED, "device %d: the static scratch serves devices 0..%d", dev,
                     kScratchDevices - 1);
     std::lock_guard<std::mutex> lk(g_scratch_mu);
     if (g_scratch_ptr[dev] == nullptr) {
         void *p = nullptr;
         HIPCHK(hipGetSymbolAddress(&p, HIP_SYMBOL(scratch)), "hipGetSymbolAddress(scratch)");
-        if (p == nullptr) return fail(LORA_ERR_HIP, "hipGetSymbolAddress(scratch) returned NULL");
+        if (p == nullptr) return host_fail(LORA_ERR_HIP, "hipGetSymbolAddress(scratch) returned NULL");
         g_scratch_ptr[dev] = p;
     }
     *out = g_scratch_ptr[dev];
@@ -767,7 +684,7 @@ extern "C" lora_status lora_linear_bwd_noalloc(const void *dY, const void *X, co
     CHECK(check_rank(r));
     const size_t need = plan_bwd(m, k, n, r, false, 0, 1).bytes;
     if (need > kScratchBytes)
-        return fail(LORA_ERR_UNSUPPORTED,
+        return host_fail(LORA_ERR_UNSUPPORTED,
                     "shape m=%lld k=%lld n=%lld r=%d needs %zu bytes of scratch; the static scratch holds %zu "
                     "(use lora_linear_bwd with a workspace)",
                     (long long)m, (long long)k, (long long)n, r, need, kScratchBytes);

@@ -242,4 +242,12 @@ inline DoraPlan dora_plan(int64_t k, int64_t n, int r) {
 hipError_t launch_dora_norm(const void *W, const void *A, const void *B, int k, int n, int r, float alpha,
                             const DoraPlan &pl, float *part, float *norm, hipStream_t stream);
 
+// MXFP4 weights: blocks of 32 rows of the padded k, groups of 16 columns of
+// the padded n (the storage is described in mxfp4_kernels.hip).
+inline int64_t mx_blocks(int64_t k) { return (k + 127) / 128 * 4; }
+inline int64_t mx_groups(int64_t n) { return (n + 15) / 16; }
+hipError_t launch_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *codes, void *scales, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, void *W,
+                                   hipStream_t stream);
+
 }  // namespace lora

@@ -1,0 +1,219 @@
+// C-ABI entry points over a frozen weight held in MXFP4: packing, the frozen
+// layer and the LoRA layer in both adapter forms.
+#include <hip/hip_runtime.h>
+
+#include "api_checks.hpp"
+#include "launch.hpp"
+#include "lora_fused.h"
+
+using namespace lora;
+
+static lora_status check_weight(int64_t k, int64_t n, const void *codes, const void *scales) {
+    CHECK(check_shape(0, k, n));
+    REQUIRE(k * n < (1LL << 46), "weight too large");
+    REQ_PTR(codes, 16);
+    REQ_PTR(scales, 16);
+    return LORA_OK;
+}
+
+extern "C" size_t lora_mxfp4_codes_size(int64_t k, int64_t n) {
+    if (k <= 0 || n <= 0 || k >= (1LL << 31) || n >= (1LL << 31)) return 0;
+    return (size_t)mx_blocks(k) * (size_t)mx_groups(n) * 256;
+}
+
+extern "C" size_t lora_mxfp4_scales_size(int64_t k, int64_t n) { return lora_mxfp4_codes_size(k, n) / 16; }
+
+extern "C" lora_status lora_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *codes, void *scales,
+                                           hipStream_t stream) {
+    CHECK(check_weight(k, n, codes, scales));
+    REQ_PTR(W, 16);
+    HIPCHK(launch_mxfp4_quantize(W, k, n, codes, scales, stream), "MXFP4 quantise launch");
+    return LORA_OK;
+}
+
+extern "C" lora_status lora_mxfp4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, void *W,
+                                             hipStream_t stream) {
+    CHECK(check_weight(k, n, codes, scales));
+    REQ_PTR(W, 16);
+    HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, W, stream), "MXFP4 dequantise launch");
+    return LORA_OK;
+}
+
+// The expanded weight sits at the start of the workspace, the bf16 layer's own
+// workspace after it.
+static size_t expanded_bytes(int64_t k, int64_t n) { return align_up((size_t)k * (size_t)n * 2); }
+
+static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
+    return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && k * n < (1LL << 46);
+}
+
+#define REQ_WORKSPACE(need)                                                                            \
+    do {                                                                                               \
+        if (workspace_bytes < (need))                                                                  \
+            return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, (size_t)(need)); \
+        REQ_PTR(workspace, 16);                                                                        \
+    } while (0)
+
+extern "C" size_t lora_mxfp4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n) {
+    return sizes_ok(m, k, n) && m > 0 ? expanded_bytes(k, n) : 0;
+}
+
+extern "C" size_t lora_mxfp4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n) {
+    return sizes_ok(m, k, n) && m > 0 ? expanded_bytes(k, n) : 0;
+}
+
+extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t m,
+                                             int64_t k, int64_t n, void *Y, void *workspace,
+                                             size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(k, n, codes, scales));
+    if (m == 0) return LORA_OK;
+    REQ_PTR(X, 16);
+    REQ_PTR(Y, 16);
+    REQ_WORKSPACE(lora_mxfp4_frozen_fwd_workspace_size(m, k, n));
+    HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return lora_frozen_fwd(X, workspace, m, k, n, Y, stream);
+}
+
+extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, const void *scales, int64_t m,
+                                             int64_t k, int64_t n, void *dX, void *workspace,
+                                             size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(k, n, codes, scales));
+    if (m == 0) return LORA_OK;
+    REQ_PTR(dY, 16);
+    REQ_PTR(dX, 16);
+    REQ_WORKSPACE(lora_mxfp4_frozen_bwd_workspace_size(m, k, n));
+    HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return lora_frozen_bwd(dY, workspace, m, k, n, dX, stream);
+}
+
+extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
+    if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
+    return expanded_bytes(k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
+}
+
+extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
+    if (!sizes_ok(m, k, n) || r < 1) return 0;
+    return expanded_bytes(k, n) + lora_linear_bwd_workspace_size(m, k, n, r);
+}
+
+extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales, const void *A,
+                                             const void *B, int64_t m, int64_t k, int64_t n, int32_t r,
+                                             float alpha, float p, uint64_t seed, uint64_t offset, void *Y,
+                                             float *S, uint32_t *keep_bits, void *workspace,
+                                             size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(k, n, codes, scales));
+    CHECK(check_rank(r));
+    CHECK(check_p(p));
+    CHECK(check_b_size(r, k, n));
+    REQUIRE(offset % 8 == 0, "offset = %llu must be a multiple of 8", (unsigned long long)offset);
+    REQ_PTR(A, 2);
+    REQ_PTR(B, 2);
+    if (m == 0) return LORA_OK;
+    REQ_PTR(X, 16);
+    REQ_PTR(Y, 16);
+    REQ_PTR(S, 4);
+    REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
+    REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
+    REQ_WORKSPACE(lora_mxfp4_linear_fwd_workspace_size(m, k, n, r));
+    const size_t w = expanded_bytes(k, n);
+    HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return lora_linear_fwd(X, workspace, A, B, m, k, n, r, alpha, p, seed, offset, Y, S, keep_bits,
+                           ws_at(workspace, w), workspace_bytes - w, stream);
+}
+
+extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales,
+                                             const void *A, const void *B, const float *S,
+                                             const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r,
+                                             float alpha, float p, void *dX, void *dA, void *dB, void *workspace,
+                                             size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(k, n, codes, scales));
+    CHECK(check_rank(r));
+    CHECK(check_p(p));
+    CHECK(check_b_size(r, k, n));
+    REQ_PTR(A, 2);
+    REQ_PTR(B, 2);
+    REQ_PTR(dA, 2);
+    REQ_PTR(dB, 2);
+    if (m > 0) {
+        REQ_PTR(dY, 16);
+        REQ_PTR(X, 16);
+        REQ_PTR(S, 4);
+        REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
+        REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
+        REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
+    }
+    REQ_WORKSPACE(lora_mxfp4_linear_bwd_workspace_size(m, k, n, r));
+    const size_t w = expanded_bytes(k, n);
+    if (m > 0 && dX != nullptr)
+        HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return lora_linear_bwd(dY, X, workspace, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
+                           ws_at(workspace, w), workspace_bytes - w, stream);
+}
+
+extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                                      int32_t num_adapters, int32_t num_segments) {
+    if (!sizes_ok(m, k, n) || m == 0 || r_max < 1) return 0;
+    return expanded_bytes(k, n) + multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+}
+
+extern "C" size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                                      int32_t num_adapters, int32_t num_segments) {
+    if (!sizes_ok(m, k, n) || r_max < 1) return 0;
+    return expanded_bytes(k, n) + multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+}
+
+extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales,
+                                                   const lora_adapter *adapters, int32_t num_adapters,
+                                                   const int64_t *seg_off, const int32_t *seg_adapter,
+                                                   int32_t num_segments, int64_t m, int64_t k, int64_t n,
+                                                   int32_t r_max, uint64_t seed, uint64_t offset, void *Y,
+                                                   float *S, uint32_t *keep_bits, void *workspace,
+                                                   size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(k, n, codes, scales));
+    const size_t w = expanded_bytes(k, n);
+    // everything else is checked before the weight is expanded, by the call on no rows
+    CHECK(multi_lora_linear_fwd(X, codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max,
+                                seed, offset, Y, S, keep_bits, workspace, workspace_bytes, stream));
+    if (m == 0) return LORA_OK;
+    REQ_PTR(X, 16);
+    REQ_PTR(Y, 16);
+    REQ_PTR(S, 4);
+    REQ_PTR(keep_bits, 4);
+    REQ_WORKSPACE(multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments));
+    HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return multi_lora_linear_fwd(X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, m, k, n,
+                                 r_max, seed, offset, Y, S, keep_bits, ws_at(workspace, w), workspace_bytes - w,
+                                 stream);
+}
+
+extern "C" lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const void *codes,
+                                                   const void *scales, const lora_adapter *adapters,
+                                                   int32_t num_adapters, const int64_t *seg_off,
+                                                   const int32_t *seg_adapter, int32_t num_segments,
+                                                   const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
+                                                   int64_t n, int32_t r_max, void *dX, void *workspace,
+                                                   size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(k, n, codes, scales));
+    // (the forward on no rows makes the same checks of the adapter and segment tables, and enqueues nothing)
+    CHECK(multi_lora_linear_fwd(X, codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max,
+                                0, 0, nullptr, nullptr, nullptr, workspace, workspace_bytes, stream));
+    if (m > 0) {
+        REQ_PTR(dY, 16);
+        REQ_PTR(X, 16);
+        REQ_PTR(S, 4);
+        REQ_PTR(keep_bits, 4);
+        REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
+    }
+    REQ_WORKSPACE(multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments));
+    const size_t w = expanded_bytes(k, n);
+    if (m > 0 && dX != nullptr)
+        HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return multi_lora_linear_bwd(dY, X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
+                                 keep_bits, m, k, n, r_max, dX, ws_at(workspace, w), workspace_bytes - w, stream);
+}

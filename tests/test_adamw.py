@@ -1,0 +1,639 @@
+"""The AdamW step over many tensors, moments in 32 and in 8 bits.
+
+The reference below is written from the formulas in 64 bits with numpy, its
+Philox4x32-10 with plain integers from the published round function.
+
+Tolerances, derived.  e = 2^-24 is half an fp32 step, and the constants (beta,
+1 - beta, the corrections) are each rounded once, so
+* m and v, each two products and a sum, are within 4 e of the sum of their
+  terms' magnitudes;
+* the update lr m' / (sqrt(v') + eps) takes a product, a root, a sum, a
+  quotient and a product more on both: within 16 e of itself plus what the
+  error of m moves it by (v's terms are all positive, so its relative error is
+  4 e and the root's 2 e, inside the 16);
+* w adds a product and a difference: 3 e of its terms;
+* a bf16 parameter is rounded once more, 2^-8 of itself.
+8-bit moments are drawn between neighbours, so a code is one of the two
+neighbours of the exact value (or a third at most where rounding crossed one),
+and their mean over many draws is the exact value.
+"""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import lora_fine_tuning_amd as lf
+from lora_fine_tuning_amd import _lib
+from lora_fine_tuning_amd.adamw import AdamwTable
+from parity import log
+
+E = 2.0 ** -24
+BLOCK = 256
+FAKE = 0x10000
+F8 = torch.float8_e4m3fn
+
+
+def f64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def philox_words(counters, key):
+    """The 32-bit word of each counter: word c % 4 of the block c // 4."""
+    out = []
+    mask = 0xFFFFFFFF
+    for c in counters:
+        x = [(c // 4) & mask, (c // 4) >> 32, 0, 0]
+        k = [key & mask, key >> 32]
+        for _ in range(10):
+            a, b = x[0] * 0xD2511F53, x[2] * 0xCD9E8D57
+            x = [(b >> 32) ^ x[1] ^ k[0], b & mask, (a >> 32) ^ x[3] ^ k[1], a & mask]
+            k = [(k[0] + 0x9E3779B9) & mask, (k[1] + 0xBB67AE85) & mask]
+        out.append(x[c % 4])
+    return np.array(out, dtype=np.int64)
+
+
+def ref_step(w, g, m, v, h, t):
+    """(w, m, v) after step t, in 64 bits, and the bounds of fp32's error in each."""
+    b1, b2, lr, eps, wd = h["beta1"], h["beta2"], h["lr"], h["eps"], h["weight_decay"]
+    m2, v2 = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g * g
+    em = 4 * E * (np.abs(b1 * m) + np.abs((1 - b1) * g))
+    ev = 4 * E * v2 + 2.0 ** -148  # (v may be subnormal)
+    den = np.sqrt(v2 / (1 - b2 ** t)) + eps
+    up = lr * m2 / (1 - b1 ** t) / den
+    w2 = w * (1 - lr * wd) - up
+    ew = 3 * E * (np.abs(w) + np.abs(up)) + 16 * E * np.abs(up) + lr * em / (1 - b1 ** t) / den
+    return (w2, m2, v2), (ew, em, ev)
+
+
+def nearest_codes(x):
+    """x over blocks of 256 as (e4m3 codes, scales), rounded to the nearest."""
+    n = x.numel()
+    pad = torch.nn.functional.pad(x, (0, -n % BLOCK)).view(-1, BLOCK)
+    scale = pad.abs().amax(1) / 448
+    codes = (pad / scale.clamp_min(1e-30)[:, None]).reshape(-1)[:n].to(F8)
+    return codes, scale
+
+
+def spread(scale, n):
+    return np.repeat(f64(scale), BLOCK)[:n]
+
+
+HYPER = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.02)
+
+
+class Tensors:
+    """One call's tensors (on the GPU) with random contents; `shift`: elements past a 16-byte boundary."""
+
+    def __init__(self, sizes, bits, ptype, gtype, master, seed=0, shift=0, fresh=False):
+        g = torch.Generator().manual_seed(seed)
+        self.sizes, self.bits = sizes, bits
+
+        def put(x):
+            b = torch.zeros(x.numel() + 16, dtype=torch.uint8, device="cuda").view(F8) if x.dtype == F8 else \
+                torch.zeros(x.numel() + 16, dtype=x.dtype, device="cuda")
+            v = b[shift:shift + x.numel()]
+            v.copy_(x)
+            return v
+
+        self.w, self.g, self.m, self.v, self.ms, self.vs, self.master = [], [], [], [], [], [], []
+        for n in sizes:
+            size = float(10.0 ** torch.empty(1).uniform_(-5, 1, generator=g))
+            w = torch.randn(n, generator=g)
+            self.g.append(put((torch.randn(n, generator=g) * size).to(gtype)))
+            m = torch.zeros(n) if fresh else 0.3 * size * torch.randn(n, generator=g)
+            u = torch.zeros(n) if fresh else size * (0.2 + torch.rand(n, generator=g))
+            self.master.append(put(w))
+            self.w.append(put(w.to(ptype)))
+            if bits == 32:
+                self.m.append(put(m))
+                self.v.append(put(u * u))
+            else:
+                for x, codes, scales in ((m, self.m, self.ms), (u, self.v, self.vs)):
+                    c, s = nearest_codes(x)
+                    codes.append(put(c))
+                    scales.append(s.cuda())
+        if not master:
+            self.master = None
+        self.table = lf.adamw_table(self.w, self.g, self.m, self.v, m_scales=self.ms or None,
+                                    v_scales=self.vs or None, masters=self.master)
+
+    def before(self, i):
+        """(w, g, m, v) of tensor i in 64 bits."""
+        n = self.sizes[i]
+        m, v = f64(self.m[i]), f64(self.v[i])
+        if self.bits == 8:
+            m, v = m * spread(self.ms[i], n), (v * spread(self.vs[i], n)) ** 2
+        return f64(self.w[i] if self.master is None else self.master[i]), f64(self.g[i]), m, v
+
+    def everything(self):
+        ts = self.w + self.m + self.v + self.ms + self.vs + (self.master or [])
+        return [t.view(torch.uint8).clone() if t.dtype == F8 else t.clone() for t in ts]
+
+
+def check(T, i, before, h, t, offset, seed):
+    w, g, m, v = before
+    n = T.sizes[i]
+    (w2, m2, v2), (ew, em, ev) = ref_step(w, g, m, v, h, t)
+    if T.bits == 8:  # the old moments are products of two fp32 numbers, rounded (and squared)
+        em, ev = em + E * np.abs(m), ev + 4 * E * v2
+        ew = ew + h["lr"] * E * np.abs(m) / (1 - h["beta1"] ** t) / (np.sqrt(v2 / (1 - h["beta2"] ** t)) + h["eps"])
+    got = f64(T.w[i] if T.master is None else T.master[i])
+    half = 0 if T.master is not None or T.w[i].dtype == torch.float32 else 2.0 ** -8
+    assert (np.abs(got - w2) <= half * np.abs(w2) + (1 + half) * ew).all(), (i, np.abs(got - w2).max())
+    if T.master is not None:
+        assert torch.equal(T.w[i], T.master[i].bfloat16())
+    if T.bits == 32:
+        assert (np.abs(f64(T.m[i]) - m2) <= em).all() and (np.abs(f64(T.v[i]) - v2) <= ev).all()
+        return
+    words = philox_words(range(offset, offset + n), (seed + t * 0x9E3779B97F4A7C15) % (1 << 64)) if n <= 1100 else None
+    for name, x, ex, codes, scales, bits in (
+            ("m", m2, em, T.m[i], T.ms[i], None if words is None else words & 0xFFFF),
+            ("v", np.sqrt(v2), ev / (2 * np.sqrt(np.maximum(v2, 1e-300))) + 2 * E * np.sqrt(v2), T.v[i], T.vs[i],
+             None if words is None else words >> 16)):
+        nb = -(-n // BLOCK)
+        a = np.zeros(nb * BLOCK)
+        a[:n] = np.abs(x)
+        top = a.reshape(nb, BLOCK).max(1)
+        err = np.zeros(nb * BLOCK)
+        err[:n] = ex
+        etop = err.reshape(nb, BLOCK).max(1)
+        assert (np.abs(f64(scales) - top / 448) <= (etop + 2 * E * top) / 448).all(), name
+        y = np.abs(x) / np.maximum(np.repeat(top / 448, BLOCK)[:n], 1e-300)
+        rel = (ex + 8 * E * np.abs(x)) / np.maximum(np.repeat(top / 448, BLOCK)[:n], 1e-300) + 448 * 4 * E
+        step = np.maximum(2.0 ** (np.floor(np.log2(np.maximum(y, 1e-300))) - 3), 2.0 ** -9)
+        c = f64(codes)
+        if name == "m":
+            assert (np.sign(c) * np.sign(x) >= 0).all()
+        c = np.abs(c)
+        assert (c <= 448).all() and (np.abs(c - y) <= step * (1 + 1e-5) + rel).all(), name
+        if name == "v":
+            assert (c[x > 0] > 0).all()
+        if bits is not None:  # the very draw: only a value next to a border may fall on its other side
+            want = np.floor(np.minimum(y, 448) / step + bits / 65536) * step
+            want = np.where((want == 0) & (y > 0) & (name == "v"), 2.0 ** -9, want)
+            frac = np.minimum(y, 448) / step + bits / 65536
+            border = np.abs(frac - np.round(frac)) <= rel / step + 2.0 ** -19
+            assert ((c == want) | border).all(), name
+            assert border.mean() < 0.02 or n < 100, name
+
+
+# ---- refusals (host) ------------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def lib():
+    if torch.cuda.is_available():
+        pytest.skip("host-only checks; a GPU is visible")
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("library not built")
+    return _lib.load()
+
+
+def record(**kw):
+    names = ["param", "grad", "master", "m", "v", "m_scale", "v_scale", "n", "offset"]
+    r = dict(param=FAKE, grad=FAKE, master=0, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, n=8, offset=0)
+    r.update(kw)
+    return np.array([[r[k] for k in names]], dtype=np.uint64)
+
+
+def test_step_rejects(lib):
+    def call(rec=None, count=1, pbf=1, gbf=1, bits=8, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0, step=1, dev=None,
+             null=False):
+        rec = record() if rec is None else rec
+        return lib.lora_adamw_step(None if null else rec.ctypes.data, count, pbf, gbf, bits, lr, b1, b2, eps, wd, step,
+                                   dev, 0, None)
+
+    nan, inf = float("nan"), float("inf")
+    for kw in (dict(count=-1), dict(null=True), dict(pbf=2), dict(gbf=-1), dict(bits=16), dict(lr=nan), dict(lr=inf),
+               dict(wd=nan), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=nan), dict(eps=-1.0), dict(eps=nan),
+               dict(step=0), dict(step=-3), dict(dev=FAKE + 4)):
+        assert call(**kw) == -1, kw
+        assert lib.lora_last_error_message()
+    for kw in (dict(param=0), dict(grad=0), dict(m=0), dict(v=0), dict(m_scale=0), dict(v_scale=0), dict(param=FAKE + 1),
+               dict(grad=FAKE + 1), dict(m_scale=FAKE + 2), dict(offset=4), dict(n=1 << 40), dict(master=FAKE + 2)):
+        assert call(record(**kw)) == -1, kw
+    assert call(record(m=FAKE + 2), bits=32) == -1
+    assert call(record(master=FAKE), pbf=0) == -1
+    assert call(np.concatenate([record(master=FAKE), record()]), count=2) == -1
+    # nothing to do
+    assert call(count=0) == 0 and call(record(n=0, param=0)) == 0 and call(count=0, null=True) == 0
+
+
+def test_table_rejects():
+    # every check but the device's is reached by CPU tensors
+    z = lambda n, t=torch.float32: torch.zeros(n, dtype=t)  # noqa: E731
+    bf = torch.bfloat16
+    f = lf.adamw_table
+    with pytest.raises(ValueError, match="empty"):
+        f([], [], [], [])
+    with pytest.raises(TypeError, match="params must be"):
+        f([z(4, torch.float16)], [z(4)], [z(4)], [z(4)])
+    with pytest.raises(ValueError, match="one tensor per parameter"):
+        f([z(4)], [z(4), z(4)], [z(4)], [z(4)])
+    with pytest.raises(ValueError, match="contiguous"):
+        f([z(8).view(2, 4).t()], [z(8)], [z(8)], [z(8)])
+    with pytest.raises(ValueError, match="GPU"):
+        f([z(4)], [z(4)], [z(4)], [z(4)])
+
+
+def test_philox_words_pin():
+    # the block function's published zero test vector
+    assert [hex(int(w)) for w in philox_words(range(4), 0)] == ["0x6627e8d5", "0xe169c58d", "0xbc57ac4c", "0x9b00dbd8"]
+
+
+# ---- the step (GPU) -----------------------------------------------------------------------------------
+
+SIZES = [[1], [7], [8], [255], [256], [257], [511, 512, 513], [2047], [2048, 1], [4095], [4096], [4097, 3, 8200],
+         [1000, 1, 260, 33]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("ptype,gtype,master", [("bf16", "bf16", True), ("bf16", "bf16", False), ("bf16", "f32", True),
+                                                ("bf16", "f32", False), ("f32", "f32", False), ("f32", "bf16", False)])
+def test_step_matches_formulas(bits, ptype, gtype, master):
+    types = {"bf16": torch.bfloat16, "f32": torch.float32}
+    for k, sizes in enumerate(SIZES):
+        for shift in (0, 1):
+            log(f"adamw bits={bits} {ptype} {gtype} master={master} sizes={sizes} shift={shift}")
+            T = Tensors(sizes, bits, types[ptype], types[gtype], master, seed=k, shift=shift, fresh=k % 3 == 2)
+            before = [T.before(i) for i in range(len(sizes))]
+            t = 1 if k % 3 == 2 else 3 + 50 * k
+            lf.lora_adamw_step(T.table, step=t, seed=k * 77, **HYPER)
+            torch.cuda.synchronize()
+            offset = 0
+            for i, n in enumerate(sizes):
+                check(T, i, before[i], HYPER, t, offset, k * 77)
+                offset += (n + 7) // 8 * 8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_hyperparameters(bits):
+    for k, h in enumerate([dict(HYPER, beta1=0.0), dict(HYPER, beta2=0.0), dict(HYPER, lr=0.0),
+                           dict(HYPER, weight_decay=0.0), dict(HYPER, eps=1.0), dict(HYPER, beta1=0.5, beta2=0.9)]):
+        T = Tensors([600], bits, torch.float32, torch.float32, False, seed=k)
+        before = T.before(0)
+        lf.lora_adamw_step(T.table, step=2, seed=5, **h)
+        torch.cuda.synchronize()
+        check(T, 0, before, h, 2, 0, 5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_many_tensors_equal_single_calls(bits):
+    # more tensors than one launch holds, sizes from nothing to several chunks
+    sizes = [(37 * i * i) % 9000 for i in range(101)]
+    a = Tensors(sizes, bits, torch.bfloat16, torch.bfloat16, True, seed=3)
+    b = Tensors(sizes, bits, torch.bfloat16, torch.bfloat16, True, seed=3)
+    lf.lora_adamw_step(a.table, step=4, seed=9, **HYPER)
+    rec = b.table.records
+    for i in range(len(sizes)):
+        one = AdamwTable(rec[i:i + 1], b.table.tensors, b.table.device, True, True, bits)
+        lf.lora_adamw_step(one, step=4, seed=9, **HYPER)
+    torch.cuda.synchronize()
+    for x, y in zip(a.everything(), b.everything()):
+        assert torch.equal(x, y)
+    c = Tensors(sizes, bits, torch.bfloat16, torch.bfloat16, True, seed=3)
+    lf.lora_adamw_step(c.table, step=4, seed=9, **HYPER)
+    for x, y in zip(a.everything(), c.everything()):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_neighbours_stay_as_they_were():
+    # values around each tensor, in the same allocation
+    n = 1003
+    bufs = {name: torch.full((n + 64,), 3.0, dtype=t, device="cuda")
+            for name, t in (("w", torch.bfloat16), ("k", torch.float32), ("ms", torch.float32), ("vs", torch.float32))}
+    codes = {name: torch.full((n + 64,), 0x38, dtype=torch.uint8, device="cuda") for name in ("m", "v")}
+    g = torch.randn(n, device="cuda")
+    lf.lora_adamw_step(lf.adamw_table([bufs["w"][24:24 + n]], [g], [codes["m"][24:24 + n].view(F8)],
+                                      [codes["v"][24:24 + n].view(F8)], m_scales=[bufs["ms"][3:7]],
+                                      v_scales=[bufs["vs"][3:7]], masters=[bufs["k"][24:24 + n]]), step=1, **HYPER)
+    torch.cuda.synchronize()
+    for b in (bufs["w"], bufs["k"]):
+        assert (b[:24] == 3).all() and (b[24 + n:] == 3).all()
+    # (a step of about lr = 1e-3 moves the master, while its nearest bf16 stays 3: half a step there is 2^-7)
+    assert (bufs["k"][24:24 + n] != 3).all() and (bufs["w"][24:24 + n] == 3).all()
+    for b in (bufs["ms"], bufs["vs"]):
+        assert (b[:3] == 3).all() and (b[7:] == 3).all()
+    for b in codes.values():
+        assert (b[:24] == 0x38).all() and (b[24 + n:] == 0x38).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_infinite_and_nan_gradients_stay_with_their_value(bits):
+    n = 700
+    a = Tensors([n], bits, torch.float32, torch.float32, False, seed=1)
+    b = Tensors([n], bits, torch.float32, torch.float32, False, seed=1)
+    for t in (a, b):
+        t.g[0][[5, 300, 301]] = 0.0
+    a.g[0][5], a.g[0][300], a.g[0][301] = float("nan"), float("inf"), -float("inf")
+    for t in (a, b):
+        lf.lora_adamw_step(t.table, step=3, **HYPER)
+    torch.cuda.synchronize()
+    rest = torch.ones(n, dtype=torch.bool)
+    rest[[5, 300, 301]] = False
+    for x, y in ((a.w, b.w), (a.m, b.m), (a.v, b.v)):
+        x, y = x[0].float().cpu(), y[0].float().cpu()
+        assert torch.equal(x[rest], y[rest]) and torch.isfinite(x[rest]).all()
+        assert not torch.isfinite(x[~rest]).any()
+    for x, y in zip(a.ms + a.vs, b.ms + b.vs):
+        assert torch.isfinite(x).all()
+
+
+@pytest.mark.gpu
+def test_zero_and_tiny_gradients():
+    n = 512
+    w = torch.ones(n, device="cuda")
+    z = lambda: torch.zeros(n, dtype=torch.uint8, device="cuda").view(F8)  # noqa: E731
+    m, v, ms, vs = z(), z(), torch.zeros(2, device="cuda"), torch.zeros(2, device="cuda")
+    g = torch.zeros(n, device="cuda")
+    g[256:] = 1e-35  # its square is below fp32's smallest number
+    lf.lora_adamw_step(lf.adamw_table([w], [g], [m], [v], m_scales=[ms], v_scales=[vs]), step=1, lr=1e-3, eps=1e-8)
+    torch.cuda.synchronize()
+    assert (w == 1).all() and not m.float().any() and not v.float().any() and not ms.any() and not vs.any()
+
+
+@pytest.mark.gpu
+def test_rounding_is_unbiased():
+    # the mean code over many steps from the same state is the exact value: with N draws of a step s the
+    # mean's standard deviation is at most s / (2 sqrt N); 5 of them, over all values together
+    n, N = 256, 400
+    T = Tensors([n], 8, torch.float32, torch.float32, False, seed=2)
+    w, g, m, v = T.before(0)
+    (_, m2, v2), _ = ref_step(w, g, m, v, HYPER, 9)
+    start = T.everything()
+    sums = np.zeros((2, n))
+    for seed in range(N):
+        for t, x in zip(T.w + T.m + T.v + T.ms + T.vs, start):
+            (t.view(torch.uint8) if t.dtype == F8 else t).copy_(x)
+        lf.lora_adamw_step(T.table, step=9, seed=seed, **HYPER)
+        sums[0] += f64(T.m[0]) * spread(T.ms[0], n)
+        sums[1] += f64(T.v[0]) * spread(T.vs[0], n)
+    for mean, x in ((sums[0] / N, m2), (sums[1] / N, np.sqrt(v2))):
+        top = np.abs(x).max()
+        step = np.maximum(2.0 ** (np.floor(np.log2(np.abs(x) * 448 / top)) - 3), 2.0 ** -9) * top / 448
+        z = (mean - x) / (step / (2 * np.sqrt(N)))
+        assert np.abs(z).max() < 5, np.abs(z).max()
+        assert abs(z.sum()) / np.sqrt(n) < 5
+
+
+@pytest.mark.gpu
+def test_small_changes_accumulate():
+    # a constant gradient: v approaches g^2 in steps of a thousandth, each far below an e4m3 step.  The
+    # expected v after t steps is (1 - b2^t) g^2; its random walk adds at most half a step of u each time a
+    # code changes.  4096 equal values average it out: their mean u^2 is within 5% of the formula.
+    n, steps = 4096, 300
+    w, g = torch.zeros(n, device="cuda"), torch.full((n,), 0.5, device="cuda")
+    g[::256] = 0.8  # a block's largest value is always exact, so let it be another one
+    z = lambda: torch.zeros(n, dtype=torch.uint8, device="cuda").view(F8)  # noqa: E731
+    m, v, ms, vs = z(), z(), torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")
+    table = lf.adamw_table([w], [g], [m], [v], m_scales=[ms], v_scales=[vs])
+    for t in range(1, steps + 1):
+        lf.lora_adamw_step(table, lr=0.0, step=t, seed=1)
+    torch.cuda.synchronize()
+    keep = np.arange(n) % 256 != 0
+    mean_m = (f64(m) * spread(ms, n))[keep].mean()
+    mean_v = ((f64(v) * spread(vs, n)) ** 2)[keep].mean()
+    assert abs(mean_m / 0.5 - 1) < 0.05
+    assert abs(mean_v / ((1 - 0.999 ** steps) * 0.25) - 1) < 0.05, mean_v
+
+
+@pytest.mark.gpu
+def test_shared_memory_is_refused():
+    x = torch.zeros(64, device="cuda")
+    z = lambda: torch.zeros(32, device="cuda")  # noqa: E731
+    with pytest.raises(ValueError, match="share memory"):
+        lf.adamw_table([x[:32], x[16:48]], [z(), z()], [z(), z()], [z(), z()])
+    with pytest.raises(ValueError, match="share memory"):
+        lf.adamw_table([x[:32]], [z()], [x[:32]], [z()])
+    with pytest.raises(ValueError, match="m_scales"):
+        lf.adamw_table([z()], [z()], [z().to(F8)], [z().to(F8)])
+    with pytest.raises(ValueError, match="go with bf16"):
+        lf.adamw_table([z()], [z()], [z()], [z()], masters=[z()])
+    with pytest.raises(ValueError, match="multiple of 8"):
+        lf.adamw_table([z()], [z()], [z()], [z()], offsets=[4])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_step_follows_the_device_counter(bits):
+    a = Tensors([700, 5000], bits, torch.bfloat16, torch.bfloat16, True, seed=6)
+    b = Tensors([700, 5000], bits, torch.bfloat16, torch.bfloat16, True, seed=6)
+    counter = torch.zeros(1, dtype=torch.int64, device="cuda")
+    start = a.everything()
+
+    def run():
+        counter.add_(1)
+        lf.lora_adamw_step(a.table, step_dev=counter, seed=4, **HYPER)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    torch.cuda.synchronize()
+    counter.zero_()
+    for t, x in zip(a.w + a.m + a.v + a.ms + a.vs + a.master, start):
+        (t.view(torch.uint8) if t.dtype == F8 else t).copy_(x)
+    for rep in range(3):
+        for t in (a, b):
+            for i, g in enumerate(t.g):
+                g.copy_(torch.randn(g.numel(), generator=torch.Generator().manual_seed(rep * 10 + i)))
+        graph.replay()
+        torch.cuda.synchronize()
+        before = [b.before(i) for i in range(2)]
+        lf.lora_adamw_step(b.table, step=rep + 1, seed=4, **HYPER)
+        torch.cuda.synchronize()
+        for x, y in zip(a.w + (a.master or []), b.w + (b.master or [])):
+            # the corrections are computed in fp32 on the device, in 64 bits on the host: a few e apart
+            assert torch.allclose(x.double(), y.double(), rtol=2.0 ** -7 if x.dtype == torch.bfloat16 else 8 * E,
+                                  atol=64 * E * HYPER["lr"] * 20)
+        for x, y in zip(a.m + a.v, b.m + b.v):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))  # (they do not depend on the corrections)
+        assert before is not None
+
+
+# ---- the optimizer --------------------------------------------------------------------------------------
+
+def model(seed=0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.nn.Parameter(torch.randn(s, generator=g).to("cuda", dtype)) for s in ((64, 8), (8, 40), (3,), (700,))]
+
+
+def gradients(ps, t):
+    g = torch.Generator().manual_seed(1000 + t)
+    for p in ps:
+        p.grad = torch.randn(p.shape, generator=g).to(p.device, p.dtype)
+
+
+@pytest.mark.gpu
+def test_optimizer_32_follows_the_formulas_over_steps():
+    ps = model()
+    opt = lf.LoraAdamW([{"params": ps[:2]}, {"params": ps[2:], "lr": 1e-2, "weight_decay": 0.1}], lr=1e-3,
+                       state_bits=32)
+    ref = [(f64(p).reshape(-1), np.zeros(p.numel()), np.zeros(p.numel())) for p in ps]
+    slack = [np.zeros(p.numel()) for p in ps]
+    for t in range(1, 21):
+        gradients(ps, t)
+        opt.step()
+        for i, p in enumerate(ps):
+            h = dict(beta1=0.9, beta2=0.999, eps=1e-8, lr=1e-3 if i < 2 else 1e-2, weight_decay=0.0 if i < 2 else 0.1)
+            (w, m, v), (ew, em, _) = ref_step(ref[i][0], f64(p.grad).reshape(-1), ref[i][1], ref[i][2], h, t)
+            # an error of the moments lives on for about ten steps of m, and moves the update by its share
+            slack[i] += ew + 10 * h["lr"] * em / (1 - 0.9 ** t) / (np.sqrt(v / (1 - 0.999 ** t)) + 1e-8) + \
+                20 * E * np.abs(h["lr"] * 10)
+            ref[i] = (w, m, v)
+    torch.cuda.synchronize()
+    for p, (w, _, _), s in zip(ps, ref, slack):
+        assert (np.abs(f64(p).reshape(-1) - w) <= s).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_state_round_trip(bits):
+    a = model(dtype=torch.bfloat16)
+    opt = lf.LoraAdamW(a, lr=1e-2, state_bits=bits, seed=3)
+    for t in range(3):
+        gradients(a, t)
+        opt.step()
+    b = [torch.nn.Parameter(p.detach().clone()) for p in a]
+    opt2 = lf.LoraAdamW(b, lr=1e-2, state_bits=bits, seed=3)
+    opt2.load_state_dict(opt.state_dict())
+    for p in b:
+        st = opt2.state[p]
+        assert st["m"].dtype == (F8 if bits == 8 else torch.float32) and st["master"].dtype == torch.float32
+    for t in range(3, 6):
+        for ps, o in ((a, opt), (b, opt2)):
+            gradients(ps, t)
+            o.step()
+    torch.cuda.synchronize()
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+        for name, x in opt.state[p].items():
+            y = opt2.state[q][name]
+            if isinstance(x, torch.Tensor):
+                assert x.data_ptr() != y.data_ptr()
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+            else:
+                assert x == y
+    # independent ranges of random counters
+    spans = sorted((opt.state[p]["offset"], opt.state[p]["m"].numel()) for p in a)
+    assert all(x + n <= y for (x, n), (y, _) in zip(spans, spans[1:]))
+
+
+@pytest.mark.gpu
+def test_optimizer_skips_parameters_without_gradients():
+    ps = model()
+    opt = lf.LoraAdamW(ps, lr=1e-2)
+    gradients(ps, 0)
+    ps[1].grad = None
+    kept = ps[1].detach().clone()
+    opt.step()
+    assert torch.equal(ps[1], kept) and ps[1] not in opt.state
+    gradients(ps, 1)
+    opt.step()
+    assert not torch.equal(ps[1], kept)
+    assert opt.state[ps[1]]["step"] == 1 and opt.state[ps[0]]["step"] == 2
+
+
+@pytest.mark.gpu
+def test_optimizer_refuses():
+    p = torch.nn.Parameter(torch.zeros(8, 4, device="cuda").t())
+    p.grad = torch.zeros_like(p)
+    with pytest.raises(ValueError, match="contiguous"):
+        lf.LoraAdamW([p]).step()
+    q = torch.nn.Parameter(torch.zeros(4))
+    q.grad = torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU"):
+        lf.LoraAdamW([q]).step()
+    for kw in (dict(state_bits=4), dict(lr=-1.0), dict(betas=(0.9, 1.0)), dict(eps=-1e-8)):
+        with pytest.raises(ValueError):
+            lf.LoraAdamW(model(), **kw)
+
+
+@pytest.mark.gpu
+def test_optimizer_captured_with_the_layer():
+    # forward, backward and step in one graph, over a packed weight: every replay is an eager step
+    k, n, m = 136, 72, 40
+    g = torch.Generator().manual_seed(0)
+    W4 = lf.lora_mxfp4_quantize((torch.randn(k, n, generator=g) * k ** -0.5).bfloat16().cuda())
+    X = torch.randn(m, k, generator=g).bfloat16().cuda()
+    target = torch.randn(m, n, generator=g).bfloat16().cuda()
+
+    def make():
+        layer = lf.LoraLinear(W4, 8, 2.0, seed=1)
+        with torch.no_grad():
+            layer.B.copy_(torch.randn(8, n, generator=torch.Generator().manual_seed(4)) * 0.1)
+        return layer, lf.LoraAdamW(layer.parameters(), lr=1e-2, seed=2, capturable=True)
+
+    def step(layer, opt):
+        opt.zero_grad(set_to_none=True)
+        y = layer(X)
+        y.backward((y.detach() - target))
+        opt.step()
+
+    layer, opt = make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(layer, opt)
+        step(layer, opt)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(layer, opt)
+    twin, opt2 = make()
+    for _ in range(2):
+        step(twin, opt2)
+    for rep in range(3):
+        X.copy_(torch.randn(m, k, generator=torch.Generator().manual_seed(50 + rep)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        step(twin, opt2)
+        torch.cuda.synchronize()
+        assert torch.equal(layer.A, twin.A) and torch.equal(layer.B, twin.B), rep
+    assert int(opt.state[layer.A]["step"]) == int(opt2.state[twin.A]["step"]) == 5
+
+
+@pytest.mark.gpu
+def test_fine_tuning_step_over_mixed_adapters():
+    # the operators together: packed base weight, a mixed batch's forward and backward, 8-bit AdamW on
+    # every adapter's tensors; the updates against the formulas on the gradients that came out
+    k, n, ranks = 264, 136, [16, 8, 5]
+    g = torch.Generator().manual_seed(9)
+    W4 = lf.lora_mxfp4_quantize((torch.randn(k, n, generator=g) * k ** -0.5).bfloat16().cuda())
+    As = [torch.nn.Parameter((torch.randn(k, r, generator=g) * k ** -0.5).bfloat16().cuda()) for r in ranks]
+    Bs = [torch.nn.Parameter((torch.randn(r, n, generator=g) * 0.1).bfloat16().cuda()) for r in ranks]
+    so = torch.tensor([0, 50, 51, 200], dtype=torch.int64, device="cuda")
+    sa = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    opt = lf.LoraAdamW(As + Bs, lr=1e-3, weight_decay=0.01, seed=1)
+    for t in range(1, 4):
+        X = torch.randn(200, k, generator=g).bfloat16().cuda()
+        dY = torch.randn(200, n, generator=g).bfloat16().cuda()
+        opt.zero_grad()
+        lf.multi_lora_linear(X, W4, so, sa, As, Bs, [2.0, 1.0, 0.5], [0.1, 0.0, 0.2], t, 0).backward(dY)
+        before = []
+        for p in As + Bs:
+            st = opt.state.get(p)
+            size = p.numel()
+            if st:
+                before.append((f64(st["master"]), f64(st["m"]) * spread(st["m_scale"], size),
+                               (f64(st["v"]) * spread(st["v_scale"], size)) ** 2))
+            else:
+                before.append((f64(p).reshape(-1), np.zeros(size), np.zeros(size)))
+        opt.step()
+        torch.cuda.synchronize()
+        h = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01)
+        for p, (w, m, v) in zip(As + Bs, before):
+            (w2, m2, v2), (ew, _, _) = ref_step(w, f64(p.grad).reshape(-1), m, v, h, t)
+            ew = ew + 2 * E * h["lr"] * np.abs(m) / (1 - 0.9 ** t) / (np.sqrt(v2 / (1 - 0.999 ** t)) + 1e-8)
+            assert (np.abs(f64(opt.state[p]["master"]) - w2) <= ew).all()
+            assert torch.equal(p.detach().reshape(-1), opt.state[p]["master"].bfloat16())
