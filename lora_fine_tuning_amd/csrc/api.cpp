@@ -275,6 +275,33 @@ extern "C" size_t lora_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n
     return plan_bwd(m, k, n, r, false, 0, 1).bytes;
 }
 
+// F1: keep_bits and S; with s2 also the split of alpha S for F2's extra K columns.
+static lora_status forward_s(const FwdPlan &pl, const void *X, const AdapterSource &src, int64_t m, int64_t k,
+                             int32_t r, uint64_t seed, uint64_t offset, float *S, uint32_t *keep_bits,
+                             void *workspace, uint16_t *s2, hipStream_t stream) {
+    float *spart = (float *)ws_at(workspace, pl.off_spart);
+    if (pl.f1w) {
+        HIPCHK(launch_f1w(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, S, r, spart, pl.KS,
+                          pl.ksl, stream, s2, pl.s2_rp), "F1 launch");
+    } else {
+        float *sout = pl.KS > 1 ? spart : S;
+        HIPCHK(launch_f1(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, sout, r, pl.KS,
+                         pl.ksl, stream), "F1 launch");
+        if (pl.KS > 1)
+            HIPCHK(launch_sum_partials(sout, pl.KS, (size_t)m * r, (size_t)m * r, S, "sum_s_partials", stream),
+                   "S reduction launch");
+    }
+    return LORA_OK;
+}
+
+namespace lora {
+lora_status forward_s_only(const void *X, const void *A, int64_t m, int64_t k, int32_t r, float p, uint64_t seed,
+                           uint64_t offset, float *S, uint32_t *keep_bits, void *workspace, hipStream_t stream) {
+    return forward_s(plan_fwd(m, k, r, false, 0), X, single_source(A, nullptr, nullptr, nullptr, r, 1.0f, p), m, k, r, seed,
+                     offset, S, keep_bits, workspace, nullptr, stream);
+}
+}  // namespace lora
+
 extern "C" lora_status lora_linear_fwd(const void *X, const void *W, const void *A, const void *B,
                                        int64_t m, int64_t k, int64_t n, int32_t r, float alpha,
                                        float p, uint64_t seed, uint64_t offset, void *Y, float *S,
@@ -299,21 +326,10 @@ extern "C" lora_status lora_linear_fwd(const void *X, const void *W, const void 
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     if (pl.bytes) REQ_PTR(workspace, 16);
 
-    AdapterSource src = single_source(A, B, nullptr, nullptr, r, alpha, p);
-    float *spart = (float *)ws_at(workspace, pl.off_spart);
+    const AdapterSource src = single_source(A, B, nullptr, nullptr, r, alpha, p);
     // the extra-K form needs B's rows 16-byte aligned (n % 8 == 0 is checked above)
     uint16_t *s2 = (pl.s2_rp > 0 && aligned(B, 16)) ? (uint16_t *)ws_at(workspace, pl.off_s2) : nullptr;
-    if (pl.f1w) {
-        HIPCHK(launch_f1w(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, S, r, spart, pl.KS,
-                          pl.ksl, stream, s2, pl.s2_rp), "F1 launch");
-    } else {
-        float *sout = pl.KS > 1 ? spart : S;
-        HIPCHK(launch_f1(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, sout, r, pl.KS,
-                         pl.ksl, stream), "F1 launch");
-        if (pl.KS > 1)
-            HIPCHK(launch_sum_partials(sout, pl.KS, (size_t)m * r, (size_t)m * r, S, "sum_s_partials", stream),
-                   "S reduction launch");
-    }
+    CHECK(forward_s(pl, X, src, m, k, r, seed, offset, S, keep_bits, workspace, s2, stream));
     if (s2)
         HIPCHK(launch_gemm_kext(X, W, Y, (int)m, (int)n, (int)k, s2, 2 * pl.s2_rp, B, r, stream), "F2 launch");
     else

@@ -242,6 +242,11 @@ inline DoraPlan dora_plan(int64_t k, int64_t n, int r) {
 hipError_t launch_dora_norm(const void *W, const void *A, const void *B, int k, int n, int r, float alpha,
                             const DoraPlan &pl, float *part, float *norm, hipStream_t stream);
 
+// F1 alone (api.cpp): keep_bits and S = s (keep . X) A, with a workspace of
+// lora_linear_fwd_workspace_size bytes.
+lora_status forward_s_only(const void *X, const void *A, int64_t m, int64_t k, int32_t r, float p, uint64_t seed,
+                           uint64_t offset, float *S, uint32_t *keep_bits, void *workspace, hipStream_t stream);
+
 // MXFP4 weights: blocks of 32 rows of the padded k, groups of 16 columns of
 // the padded n (the storage is described in mxfp4_kernels.hip).
 inline int64_t mx_blocks(int64_t k) { return (k + 127) / 128 * 4; }
@@ -249,5 +254,16 @@ inline int64_t mx_groups(int64_t n) { return (n + 15) / 16; }
 hipError_t launch_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *codes, void *scales, hipStream_t stream);
 hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, void *W,
                                    hipStream_t stream);
+
+// Y = X W' (+ alpha S B) straight from the packed weight (mxfp4_gemm.hip).
+struct MxGemmPlan {
+    int kind;  // tile shape; 0: not for this shape
+    int tiles_m, tiles_n, KS, per;
+    size_t part_bytes;  // fp32 partial sums of the k slices
+};
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int want = 0);
+hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
+                             int n, const float *S, const void *B, int r, float alpha, void *Y, float *part,
+                             hipStream_t stream);
 
 }  // namespace lora

@@ -51,11 +51,13 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
     do {                                                                                               \
         if (workspace_bytes < (need))                                                                  \
             return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, (size_t)(need)); \
-        REQ_PTR(workspace, 16);                                                                        \
+        if ((need) > 0) REQ_PTR(workspace, 16);                                                        \
     } while (0)
 
 extern "C" size_t lora_mxfp4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n) {
-    return sizes_ok(m, k, n) && m > 0 ? expanded_bytes(k, n) : 0;
+    if (!sizes_ok(m, k, n) || m == 0) return 0;
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
+    return pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n);
 }
 
 extern "C" size_t lora_mxfp4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n) {
@@ -71,6 +73,12 @@ extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, c
     REQ_PTR(X, 16);
     REQ_PTR(Y, 16);
     REQ_WORKSPACE(lora_mxfp4_frozen_fwd_workspace_size(m, k, n));
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
+    if (pl.kind) {
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, Y,
+                                 (float *)workspace, stream), "MXFP4 product launch");
+        return LORA_OK;
+    }
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_frozen_fwd(X, workspace, m, k, n, Y, stream);
 }
@@ -90,7 +98,8 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
 
 extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
-    return expanded_bytes(k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) + lora_linear_fwd_workspace_size(m, k, n, r);
 }
 
 extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
@@ -118,6 +127,14 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
     REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     REQ_WORKSPACE(lora_mxfp4_linear_fwd_workspace_size(m, k, n, r));
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
+    if (pl.kind) {
+        CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, ws_at(workspace, align_up(pl.part_bytes)),
+                             stream));
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, S, B, r, alpha, Y, (float *)workspace,
+                                 stream), "MXFP4 product launch");
+        return LORA_OK;
+    }
     const size_t w = expanded_bytes(k, n);
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_linear_fwd(X, workspace, A, B, m, k, n, r, alpha, p, seed, offset, Y, S, keep_bits,

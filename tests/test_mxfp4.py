@@ -158,7 +158,9 @@ def test_layer_rejects(lib):
     assert fz(F, F, F + 4, 4, 64, 64, F, F, big, None) == INVALID
     assert fz(None, F, F, 0, 64, 64, None, None, 0, None) == 0
     assert lib.lora_mxfp4_frozen_bwd(F, F, F, 4, 64, 64, None, F, big, None) == INVALID
-    assert lib.lora_mxfp4_frozen_bwd(F, F, F, 4096, 4096, 4096, F, F, 0, None) == WORKSPACE
+    need = lib.lora_mxfp4_frozen_bwd_workspace_size(4096, 4096, 4096)
+    if need:
+        assert lib.lora_mxfp4_frozen_bwd(F, F, F, 4096, 4096, 4096, F, F, need - 1, None) == WORKSPACE
 
     def fwd(**kw):
         a = dict(X=F, c=F, s=F, A=F, B=F, m=64, k=64, n=64, r=8, p=0.1, off=0, Y=F, S=F, keep=F, ws=F, wsb=big)
@@ -170,7 +172,8 @@ def test_layer_rejects(lib):
                dict(S=None), dict(r=0), dict(r=257), dict(p=1.0), dict(p=-0.1), dict(off=4), dict(keep=None),
                dict(k=12), dict(n=12), dict(S=F + 2), dict(keep=F + 2), dict(p=float("nan"))):
         assert fwd(**kw) == INVALID, kw
-    assert fwd(m=4096, k=4096, n=4096, wsb=16) == WORKSPACE
+    need = lib.lora_mxfp4_linear_fwd_workspace_size(512, 4096, 4096, 256)  # partial sums of S at least
+    assert need > 0 and fwd(m=512, k=4096, n=4096, r=256, wsb=need - 1) == WORKSPACE
     assert fwd(r=256, n=1 << 22) == UNSUPPORTED
     assert fwd(m=0, X=None, Y=None, S=None, keep=None, ws=None, wsb=0) == 0
 
