@@ -161,40 +161,49 @@ def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
-class _on_device:
-    """The device of a call's tensors as the current one, with `stream` (given
-    explicitly) or that device's current stream as the one that outputs and
-    scratch are allocated for; yields the stream's handle."""
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to be entered through _on_device: `stream` is given
+    explicitly, or the tensors' device is not the current one."""
+    return stream is not None or device.index != torch._C._cuda_getDevice()
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guard = device, stream, None
 
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-            self.guard = torch.cuda.stream(self.stream)
-            self.guard.__enter__()
-            return ctypes.c_void_p(self.stream.cuda_stream)
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+def _on_device(device, stream):
+    """The context in which outputs and scratch of a call are allocated and its
+    kernels enqueued: `stream`, or the current stream of `device`."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _handle(device) -> int:
+    """The handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _need_on(t, shape, dtype, name: str, dev) -> None:
+    """A contiguous tensor of this shape and type on `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, the weight on {dev}")
 
 
 def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor]):
-    """(pointer, bytes) of the caller's workspace, or of one allocated here."""
+    """(pointer, bytes, tensor) of the caller's workspace, or of one allocated here."""
     if workspace is None:
         if nbytes == 0:
-            return None, 0
+            return None, 0, None
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 # ----------------------------------------------------------------------------

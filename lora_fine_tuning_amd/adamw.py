@@ -9,7 +9,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from ._lib import _check, _on_device, load
+from ._lib import _check, _elsewhere, _handle, _on_device, load
 
 BLOCK = 256  # values that share a scale of the 8-bit moments
 _PARAM, _GRAD, _MASTER, _M, _V, _M_SCALE, _V_SCALE, _N, _OFFSET = range(9)
@@ -21,6 +21,7 @@ class AdamwTable:
 
     def __init__(self, records, tensors, device, param_bf16: bool, grad_bf16: bool, state_bits: int):
         self.records, self.tensors, self.device = records, tensors, device
+        self.address = records.ctypes.data
         self.param_bf16, self.grad_bf16, self.state_bits = param_bf16, grad_bf16, state_bits
 
 
@@ -114,15 +115,17 @@ def lora_adamw_step(table: AdamwTable, *, lr: float, beta1: float = 0.9, beta2: 
                     stream=None) -> None:
     """One step (the step-th, from 1; or the one whose number the int64 device
     tensor step_dev holds) over the table's tensors, in place."""
+    if _elsewhere(table.device, stream):
+        with _on_device(table.device, stream):
+            return lora_adamw_step(table, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
+                                   step=step, step_dev=step_dev, seed=seed)
     if step_dev is not None:
         if step_dev.dtype != torch.int64 or step_dev.numel() != 1 or step_dev.device != table.device:
             raise ValueError(f"step_dev must be one int64 on {table.device}")
         step_dev = step_dev.data_ptr()
-    rec = table.records
-    with _on_device(table.device, stream) as st:
-        _check(load().lora_adamw_step(rec.ctypes.data, len(rec), int(table.param_bf16), int(table.grad_bf16),
-                                      table.state_bits, lr, beta1, beta2, eps, weight_decay, step, step_dev,
-                                      seed % (1 << 64), st))
+    _check(load().lora_adamw_step(table.address, len(table.records), table.param_bf16, table.grad_bf16,
+                                  table.state_bits, lr, beta1, beta2, eps, weight_decay, step, step_dev,
+                                  seed % (1 << 64), _handle(table.device)))
 
 
 class LoraAdamW(torch.optim.Optimizer):

@@ -259,11 +259,16 @@ hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_
 struct MxGemmPlan {
     int kind;  // tile shape; 0: not for this shape
     int tiles_m, tiles_n, KS, per;
-    size_t part_bytes;  // fp32 partial sums of the k slices
+    bool finish;           // a second launch adds partial sums and the LoRA term
+    size_t part_bytes;     // fp32 partial sums of the k slices
+    int SK, jobs;          // > 0: the product's launch also forms S = X A, in SK partial sums, by `jobs` work-groups
+    size_t spart_bytes;
 };
-MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int want = 0);
+// r == 0: no adapter; dropout: S comes from F1.
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout);
+// S: written where the plan forms it (SK > 0), else read (r > 0).
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
-                             int n, const float *S, const void *B, int r, float alpha, void *Y, float *part,
-                             hipStream_t stream);
+                             int n, const void *A, const void *B, int r, float alpha, float *S, void *Y, float *part,
+                             float *spart, hipStream_t stream);
 
 }  // namespace lora

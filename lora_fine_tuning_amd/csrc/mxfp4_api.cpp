@@ -2,6 +2,8 @@
 // layer and the LoRA layer in both adapter forms.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "api_checks.hpp"
 #include "launch.hpp"
 #include "lora_fused.h"
@@ -56,8 +58,8 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
 
 extern "C" size_t lora_mxfp4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n) {
     if (!sizes_ok(m, k, n) || m == 0) return 0;
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
-    return pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, false);
+    return pl.kind ? pl.part_bytes : expanded_bytes(k, n);
 }
 
 extern "C" size_t lora_mxfp4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n) {
@@ -73,10 +75,10 @@ extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, c
     REQ_PTR(X, 16);
     REQ_PTR(Y, 16);
     REQ_WORKSPACE(lora_mxfp4_frozen_fwd_workspace_size(m, k, n));
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, false);
     if (pl.kind) {
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, Y,
-                                 (float *)workspace, stream), "MXFP4 product launch");
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, nullptr, Y,
+                                 (float *)workspace, nullptr, stream), "MXFP4 product launch");
         return LORA_OK;
     }
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
@@ -98,8 +100,10 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
 
 extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
-    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) + lora_linear_fwd_workspace_size(m, k, n, r);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, false);
+    if (!pl.kind) return expanded_bytes(k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
+    // (the plans with and without dropout differ in where S is formed only)
+    return align_up(pl.part_bytes) + std::max(pl.spart_bytes, lora_linear_fwd_workspace_size(m, k, n, r));
 }
 
 extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
@@ -127,12 +131,12 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
     REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     REQ_WORKSPACE(lora_mxfp4_linear_fwd_workspace_size(m, k, n, r));
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, p != 0.0f);
     if (pl.kind) {
-        CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, ws_at(workspace, align_up(pl.part_bytes)),
-                             stream));
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, S, B, r, alpha, Y, (float *)workspace,
-                                 stream), "MXFP4 product launch");
+        char *rest = ws_at(workspace, align_up(pl.part_bytes));
+        if (pl.SK == 0) CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, rest, stream));
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, A, B, r, alpha, S, Y, (float *)workspace,
+                                 (float *)rest, stream), "MXFP4 product launch");
         return LORA_OK;
     }
     const size_t w = expanded_bytes(k, n);

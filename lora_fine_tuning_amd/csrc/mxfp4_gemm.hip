@@ -1,5 +1,5 @@
-// Y = X W' for few and middling numbers of rows, W' in MXFP4 (mxfp4_kernels.hip
-// describes the storage), with the LoRA term alpha S B added before the store.
+// Y = X W' + alpha S B for few and middling numbers of rows, W' in MXFP4
+// (mxfp4_kernels.hip describes the storage).
 //
 // With few rows the weight's bytes bound the product, so it is read packed, a
 // quarter of its bf16 bytes, and expanded in registers: one 16-byte LDS read
@@ -12,12 +12,22 @@
 // A work-group covers 16 WM MB rows and 16 WN NB columns; its waves split the
 // rows (WM), the columns (WN) and each stage's k (WK chunks of 128).  Stages of
 // X, codes and scales come through an NS-deep LDS ring by direct-to-LDS loads,
-// NS - 1 stages ahead.  X rows take 256 bytes a chunk with their 16-byte pieces
-// XORed by the row, so 16 rows read at one piece fall on 16 different bank
-// ranges.  Waves along k are added in LDS in wave order.  Where the tiles would
+// NS - 1 stages ahead.  X rows take 256 bytes a chunk; piece 4 g + j (16 bytes)
+// of row i sits at place (4 j + g) ^ (i mod 16).  A 16-byte read serves lanes
+// 0-3, 12-15 and 20-27 (and so on) together: with g in the low bits of the place
+// those 16 lanes fall on 16 different bank ranges (with j there, on 8).  Waves along k are added in LDS in wave order.  Where the tiles would
 // leave CUs idle, work-groups split k further: each slice writes fp32 partial
-// sums and a second launch adds them in slice order.
+// sums and a finishing launch adds them in slice order.
+//
+// Up to 128 rows the adapter rides along: without dropout S = X A is formed by
+// further work-groups of the same launch (partial sums over 1024 of k each),
+// and the finishing launch adds those, writes S and adds alpha S B.  Else F1
+// forms S first, and the shapes for many rows add alpha S B in the product's own
+// epilogue, as rank-deep MFMA steps, where k is not split.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "launch.hpp"
@@ -32,6 +42,20 @@ __device__ __forceinline__ void wait_vmcnt_lds() {
     __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
 }
 
+// dma16 with a scalar byte offset added to the address; a lane whose own
+// offset is kOOB reads zeros whatever it is.
+__device__ __forceinline__ void dma16_at(sgpr4_t desc, uint32_t voff, uint32_t soff, uint32_t lds_base) {
+    uint32_t saved_m0;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %4\n\t"
+        "buffer_load_dwordx4 %1, %2, %3 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved_m0)
+        : "v"(voff), "s"(desc), "s"(soff), "s"(lds_base)
+        : "memory");
+}
+
 struct MxGemmParams {
     const uint16_t *X;
     const uint8_t *codes, *scales;
@@ -41,22 +65,30 @@ struct MxGemmParams {
     int groups, blocks;  // N16, KB
     int tiles_m, tiles_n;
     int KS, per;         // slices of k, stages of a slice
-    const float *S;      // LoRA: M x r fp32 (nullptr: none)
+    const float *S;      // the epilogue's LoRA term: M x r fp32 (nullptr: none)
     const uint16_t *B;   // r x N
     int r;
     float alpha;
+    const uint16_t *A;   // partial sums of S = X A by further work-groups (nullptr: none)
+    float *spart;        // [SK][M][rs], rs = r rounded up to 4
+    int rs, SK, jobs;        // partial sums; work-groups that form them (a multiple of 8)
 };
 
+constexpr int kSK = 1024;  // k of one partial sum of S
+
 __device__ __forceinline__ float mx_scale(uint32_t s) {
-    return __uint_as_float((s << 23) | ((s == 0u || s == 255u) ? 0x00400000u : 0u));
+    return __uint_as_float(max(s << 23, 0x00400000u));
 }
 
-// Eight codes (one dword) -> an MFMA operand.
+// Byte e of a dword of codes -> two bf16; all four -> an MFMA operand.
+__device__ __forceinline__ uint32_t mx_pair(uint32_t w, float scale, int e) {
+    return __builtin_bit_cast(uint32_t, e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)
+                                        : e == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)
+                                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)
+                                                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+}
 __device__ __forceinline__ uint4 mx_frag(uint32_t w, float scale) {
-    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3)));
+    return make_uint4(mx_pair(w, scale, 0), mx_pair(w, scale, 1), mx_pair(w, scale, 2), mx_pair(w, scale, 3));
 }
 
 template <int WM_, int WN_, int WK_, int MB_, int NB_, int XR_, int NS_>
@@ -65,13 +97,74 @@ struct MxTile {
     static constexpr int NW = WM * WN * WK, TM = 16 * WM * MB, TN = 16 * WN * NB, KW = 128 * WK;
     static constexpr int G = WN * NB;                  // column groups
     static constexpr int XU = XR * WK / 4, WU = G * WK, SU = (G * WK + 15) / 16;  // 1 KiB loads of a stage
-    static constexpr int UPW = (XU + WU + SU + NW - 1) / NW;                      // per wave
+    static constexpr int XPW = (XU + NW - 1) / NW, WPW = (WU + NW - 1) / NW, UPW = XPW + WPW + 1;  // per wave
     static constexpr int XB = XU * 1024, WB = WU * 1024, STAGE = XB + WB + SU * 1024;
     static constexpr int SPARE = NS * STAGE;  // 1 KiB that surplus loads fill with zeros
     static constexpr int RED = (WK - 1) * WM * WN * MB * NB * 1024;
     static constexpr int LDS = SPARE + 1024 > RED ? SPARE + 1024 : RED;
-    static_assert(XR * WK % 4 == 0 && LDS <= 160 * 1024, "tile does not fit");
+    static constexpr bool RIDE = WM == 1;  // the adapter's S rides along, a second launch adds alpha S B
+    static_assert(SU <= NW && LDS <= 160 * 1024, "tile does not fit");
 };
+
+// One work-group's share of S = X A: k from kSK * (job % SK), 128 a wave, the row
+// tile job / SK % tiles_m, and 16 RT ranks.  X's rows and A's columns come straight from memory
+// (8 two-byte loads make a 16-rank operand: A's rows are r values long), every
+// load of a wave before its first use; the waves are added in LDS in wave order.
+template <class T>
+__device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *smem) {
+    constexpr int MB = T::MB, RT = MB == 4 ? 2 : 4;
+    static_assert(T::NW == 8 && T::WM == 1 && 8 * MB * RT * 1024 <= T::LDS, "no room for the partial sums");
+    const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int ks = job % P.SK, m0 = job / P.SK % P.tiles_m * T::TM, r0 = job / (P.SK * P.tiles_m) * 16 * RT;
+    if (r0 >= P.r) return;  // (the count is rounded up)
+    const int k0 = ks * kSK + wave * (kSK / 8);
+    // rows past M read as zeros; the host keeps A under 2 GiB
+    const __amdgpu_buffer_rsrc_t rX = make_rsrc(P.X + (size_t)m0 * P.K, (uint64_t)min(P.M - m0, T::TM) * P.K * 2u);
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(P.A, (uint64_t)P.K * P.r * 2u);
+    f32x4_t acc[MB][RT];
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kSK / 8 / 32; ++j) {
+        const int k = k0 + 32 * j + 8 * lg;
+        uint4 x[MB], w[RT];
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+            x[a] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                       rX, k < P.K ? ((uint32_t)(16 * a + l16) * (uint32_t)P.K + (uint32_t)k) * 2u : kOOB, 0, 0));
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const int rank = r0 + 16 * t + l16;
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
+                    rA, rank < P.r && k < P.K ? ((uint32_t)(k + e) * (uint32_t)P.r + (uint32_t)rank) * 2u : kOOB, 0, 0);
+            w[t] = make_uint4(pack2(h[0], h[1]), pack2(h[2], h[3]), pack2(h[4], h[5]), pack2(h[6], h[7]));
+        }
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[a][t] = mfma16x16x32(w[t], x[a], acc[a][t]);
+    }
+    f32x4_t *red = (f32x4_t *)smem;
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) red[(wave * MB * RT + a * RT + t) * 64 + lane] = acc[a][t];
+    __syncthreads();
+    if (wave >= MB * RT) return;
+    // wave w adds tile w of every wave: lane (g, l) has ranks 4g .. 4g+3 of row l
+    f32x4_t sum = red[wave * 64 + lane];
+#pragma unroll
+    for (int c = 1; c < 8; ++c) sum += red[(c * MB * RT + wave) * 64 + lane];
+    const int row = m0 + 16 * (wave / RT) + l16, rank = r0 + 16 * (wave % RT) + 4 * lg;
+    if (row >= P.M) return;
+    if (rank < P.rs) *(f32x4_t *)(P.spart + ((size_t)ks * P.M + row) * P.rs + rank) = sum;  // (zeros past r)
+}
 
 template <class T>
 __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) {
@@ -89,11 +182,17 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
     // into one L2 once.
     const int total = P.tiles_m * P.tiles_n * P.KS;
     int id = blockIdx.x;
+    if constexpr (T::RIDE) {
+        if (id < P.jobs) return s_job<T>(P, id, mx_smem);
+        id -= P.jobs;
+    }
     {
         const int xcd = id & 7, local = id >> 3, each = total >> 3, rem = total & 7;
         id = xcd * each + min(xcd, rem) + local;
     }
-    const int tm = id % P.tiles_m, tn = id / P.tiles_m % P.tiles_n, ks = id / (P.tiles_m * P.tiles_n);
+    int tm = 0, tn = id, ks = 0;  // (the divisions are skipped where there is nothing to divide)
+    if (P.tiles_m > 1) tn = id / P.tiles_m, tm = id - tn * P.tiles_m;
+    if (P.KS > 1) ks = tn / P.tiles_n, tn -= ks * P.tiles_n;
     const int m0 = tm * T::TM, n0 = tn * T::TN, g0 = tn * G;
     const int k0 = ks * P.per * T::KW;
     const int nit = min(P.per, (P.K - k0 + T::KW - 1) / T::KW);  // >= 1: the host sizes the slices
@@ -105,48 +204,56 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
     const sgpr4_t dW = make_desc(P.codes + (size_t)g0 * group_bytes, ng * group_bytes);
     const sgpr4_t dS = make_desc(P.scales + (size_t)g0 * (group_bytes / 16), ng * (group_bytes / 16));
 
-    // This wave's loads of a stage: byte offset in the source at stage 0, and
-    // the k it stands for (a load past `lim` fills zeros).
-    uint32_t off[T::UPW];
-    int pos[T::UPW], lim[T::UPW];
-#pragma unroll
-    for (int i = 0; i < T::UPW; ++i) {
-        const int u = wave + T::NW * i;
-        off[i] = 0;
-        pos[i] = 0;
-        lim[i] = -1;
-        if (u < T::XU) {
-            const int c = u / (XR / 4), row = (u % (XR / 4)) * 4 + (lane >> 4);
-            const int piece = (lane & 15) ^ (row & 15);
-            pos[i] = k0 + 128 * c + 8 * piece;
-            off[i] = (uint32_t)row * row_bytes + (uint32_t)pos[i] * 2u;
-            lim[i] = m0 + row < P.M ? P.K : -1;
-        } else if (u < T::XU + T::WU) {
-            const int q = u - T::XU, c = q / G, g = q % G;
-            pos[i] = k0 + 128 * c + 32 * lg;
-            off[i] = (uint32_t)g * group_bytes + (uint32_t)(pos[i] / 32) * 256u + (uint32_t)l16 * 16u;
-            lim[i] = g0 + g < P.groups ? P.blocks * 32 : -1;
-        } else if (u < T::XU + T::WU + T::SU) {
-            const int q = (u - T::XU - T::WU) * 16 + (lane >> 2), c = q / G, g = q % G;
-            pos[i] = k0 + 128 * c + 32 * (lane & 3);
-            off[i] = (uint32_t)g * (group_bytes / 16) + (uint32_t)(pos[i] / 32) * 16u;
-            lim[i] = q < G * WK && g0 + g < P.groups ? P.blocks * 32 : -1;
-        }
+    // This wave's loads of a stage: XPW of X, WPW of codes, one of scales; where a
+    // kind has no load left for a wave, zeros into the spare space, so that every
+    // wave counts the same loads.  xo, wo, so: byte offsets at stage 0 (kOOB: zeros);
+    // xk, wk32, sk32: the k a lane reads in a wave's first chunk.
+    const int xrow4 = lane >> 4;
+    int xk;
+    uint32_t xo[T::XPW], wo[T::WPW], so = kOOB;
+    {
+        const int place = (lane & 15) ^ ((4 * (wave % (XR < 16 ? XR / 4 : 4)) + xrow4) & 15);
+        xk = k0 + 8 * ((place & 3) * 4 + (place >> 2));
     }
-    auto issue = [&](int it, int buf) {
-        const uint32_t base = lds0 + (uint32_t)buf * T::STAGE;
-        const int dk = it * T::KW;
+    const uint32_t xlane = (uint32_t)xrow4 * row_bytes + (uint32_t)xk * 2u;
+    auto xchunk = [&](int i) { return (wave + T::NW * i) / (XR / 4); };
 #pragma unroll
-        for (int i = 0; i < T::UPW; ++i) {
-            const int u = wave + T::NW * i;
-            const bool live = it < nit && pos[i] + dk < lim[i];
-            const uint32_t step = u < T::XU ? 2u * T::KW : u < T::XU + T::WU ? 8u * T::KW : T::KW / 2u;
-            const uint32_t o = live ? off[i] + (uint32_t)it * step : kOOB;
-            const uint32_t dst = u < T::XU + T::WU + T::SU ? base + (uint32_t)u * 1024u : lds0 + T::SPARE;
-            if (u < T::XU) dma16(dX, o, dst);
-            else if (u < T::XU + T::WU) dma16(dW, o, dst);
-            else dma16(dS, o, dst);
+    for (int i = 0; i < T::XPW; ++i) {
+        const int u = wave + T::NW * i, row = u % (XR / 4) * 4;
+        xo[i] = u < T::XU && row + xrow4 < P.M - m0 ? xlane + (uint32_t)row * row_bytes + (uint32_t)xchunk(i) * 256u : kOOB;
+    }
+    const uint32_t wlane = (uint32_t)(k0 / 32) * 256u + (uint32_t)lane * 16u;
+    auto wchunk = [&](int i) { return (wave + T::NW * i) / G; };
+#pragma unroll
+    for (int i = 0; i < T::WPW; ++i) {
+        const int u = wave + T::NW * i, g = u % G;
+        wo[i] = u < T::WU && g0 + g < P.groups ? wlane + (uint32_t)g * group_bytes + (uint32_t)wchunk(i) * 1024u : kOOB;
+    }
+    const int sq = wave * 16 + (lane >> 2), schunk = sq / G, sg = sq % G;
+    if (sq < G * WK && g0 + sg < P.groups)
+        so = (uint32_t)sg * (group_bytes / 16) + (uint32_t)(k0 / 32 + 4 * schunk + (lane & 3)) * 16u;
+    // One load of stage `it` into buffer `buf`.  A stage that lies inside K whole
+    // advances by the scalar offset alone; the last ones test each lane's k.
+    const int nfull = min(nit, (P.K - k0) / T::KW), kpad = P.blocks * 32;
+    auto issue_one = [&](int it, int buf, int i) {
+        const uint32_t base = lds0 + (uint32_t)buf * T::STAGE + (uint32_t)wave * 1024u, spare = lds0 + T::SPARE;
+        const int dk = it < nit ? it * T::KW : 0x20000000;  // past every limit
+        const bool whole = it < nfull;
+        if (i < T::XPW) {
+            dma16_at(dX, whole || xk + 128 * xchunk(i) + dk < P.K ? xo[i] : kOOB, (uint32_t)dk * 2u,
+                     T::XU % T::NW == 0 || wave + T::NW * i < T::XU ? base + T::NW * i * 1024u : spare);
+        } else if (i < T::XPW + T::WPW) {
+            const int j = i - T::XPW;
+            dma16_at(dW, whole || k0 + 32 * lg + 128 * wchunk(j) + dk < kpad ? wo[j] : kOOB, (uint32_t)dk * 8u,
+                     T::WU % T::NW == 0 || wave + T::NW * j < T::WU ? base + T::XB + T::NW * j * 1024u : spare);
+        } else {
+            dma16_at(dS, whole || k0 + 32 * (lane & 3) + 128 * schunk + dk < kpad ? so : kOOB, (uint32_t)dk / 2u,
+                     wave < T::SU ? base + T::XB + T::WB : spare);
         }
+    };
+    auto issue = [&](int it, int buf) {
+#pragma unroll
+        for (int i = 0; i < T::UPW; ++i) issue_one(it, buf, i);
     };
 
     f32x4_t acc[MB][NB];
@@ -159,40 +266,92 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
 #pragma unroll
     for (int a = 0; a < MB; ++a) xrow[a] = ((wm * MB + a) * 16 + l16) & (XR < 16 ? XR - 1 : -1);
 
+    // x[j % 2] holds X's rows of step j, q and sc the wave's codes and scales of
+    // the stage, w the operand of the next column group.
+    uint4 x[2][MB], q[NB];
+    float sc[NB];
+    uint32_t xplace[4];
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s) issue(s, s);
-    int buf = 0;
-    for (int it = 0; it < nit; ++it) {
-        // this stage has landed, and this wave's reads of the last one are done
-        wait_vmcnt_lds<T::UPW *(NS - 2)>();
-        asm volatile("" ::: "memory");  // keep the LDS reads below the barrier
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        // the buffer of stage it - 1, which every wave has read
-        issue(it + NS - 1, buf == 0 ? NS - 1 : buf - 1);
-        const lds_char *sx = smem + buf * T::STAGE + wk * XR * 256;
+    for (int j = 0; j < 4; ++j)
+        xplace[j] = (uint32_t)(wk * XR * 256 + xrow[0] * 256 + (((4 * j + lg) ^ (xrow[0] & 15)) << 4));
+    auto read_x = [&](int buf, int j, int a) {  // (rows 16 apart share a place)
+        x[j & 1][a] = *(const uint4 *)(smem + buf * T::STAGE + xplace[j] + a * 4096);
+    };
+    auto read_w = [&](int buf) {
         const lds_char *sw = smem + buf * T::STAGE + T::XB + (wk * G + wn * NB) * 1024 + lane * 16;
         const lds_char *ss = smem + buf * T::STAGE + T::XB + T::WB + (wk * G + wn * NB) * 64 + lane;
-        uint4 q[NB];
-        float sc[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             q[b] = *(const uint4 *)(sw + b * 1024);
             sc[b] = mx_scale(*(const uint8_t *)(ss + b * 64));
         }
+    };
+    auto dword = [](const uint4 &v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
+    // Step j's MFMAs, each followed by a share of the work that is due meanwhile:
+    // the next group's conversions (codes `qc`, scale `c` of this step, or of step
+    // j + 1's first group), the next step's X rows, and what `side` does.
+    uint4 w;
+    auto step = [&](int j, const uint32_t (&qc)[NB], const float (&c)[NB], uint32_t qnext, float cnext, int xbuf, auto side) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 x[MB];
+        for (int b = 0; b < NB; ++b) {
+            const uint4 now = w;
+            const uint32_t src = b + 1 < NB ? qc[b + 1 < NB ? b + 1 : 0] : qnext;
+            const float scale = b + 1 < NB ? c[b + 1 < NB ? b + 1 : 0] : cnext;
+            uint32_t n[4];
 #pragma unroll
-            for (int a = 0; a < MB; ++a) x[a] = *(const uint4 *)(sx + xrow[a] * 256 + (((4 * lg + j) ^ (xrow[a] & 15)) << 4));
+            for (int a = 0; a < MB; ++a) {
+                acc[a][b] = mfma16x16x32(now, x[j & 1][a], acc[a][b]);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint4 w = mx_frag(j == 0 ? q[b].x : j == 1 ? q[b].y : j == 2 ? q[b].z : q[b].w, sc[b]);
-#pragma unroll
-                for (int a = 0; a < MB; ++a) acc[a][b] = mfma16x16x32(w, x[a], acc[a][b]);
+                for (int e = a * 4 / MB; e < (a + 1) * 4 / MB; ++e) n[e] = mx_pair(src, scale, e);
+                if (b == 0 && j < 3) read_x(xbuf, j + 1, a);
+                side(b * MB + a);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            w = make_uint4(n[0], n[1], n[2], n[3]);
         }
-        buf = buf == NS - 1 ? 0 : buf + 1;
+    };
+    // A stage has landed (`later` ones may be in flight), and this wave's LDS reads
+    // are done; after the barrier both hold for every wave.
+    auto stage_ready = [&](auto later) {
+        wait_vmcnt_lds<T::UPW * decltype(later)::value>();
+        asm volatile("" ::: "memory");  // keep LDS reads and loads into LDS on their side of the barrier
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+#pragma unroll 1
+    for (int s = 0; s < NS; ++s) issue(s, s);
+    stage_ready(std::integral_constant<int, NS - 1>{});
+    read_w(0);
+#pragma unroll
+    for (int a = 0; a < MB; ++a) read_x(0, 0, a);
+    int buf = 0;
+    for (int it = 0; it < nit; ++it) {
+        w = mx_frag(q[0].x, sc[0]);
+        uint32_t qc[NB];
+        float c[NB];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qc[b] = dword(q[b], j);
+            step(j, qc, sc, dword(q[0], j + 1), sc[0], buf, [](int) {});
+        }
+        // step 3's operands are in registers: this stage's buffer takes stage it + NS, and
+        // the next stage's first operands are read while step 3 multiplies
+#pragma unroll
+        for (int b = 0; b < NB; ++b) qc[b] = q[b].w, c[b] = sc[b];
+        const int next = buf == NS - 1 ? 0 : buf + 1, here = buf;
+        stage_ready(std::integral_constant<int, NS - 2>{});
+        read_w(next);
+#pragma unroll
+        for (int a = 0; a < MB; ++a) read_x(next, 0, a);
+        constexpr int EACH = (T::UPW + MB * NB - 1) / (MB * NB);
+        step(3, qc, c, 0u, 1.f, 0, [&](int i) {
+#pragma unroll
+            for (int e = 0; e < EACH; ++e)
+                if (i * EACH + e < T::UPW) issue_one(it + NS, here, i * EACH + e);
+        });
+        buf = next;
     }
     wait_vmcnt<0>();  // (the last loads fill zeros: nothing may land in the space used below)
 
@@ -210,7 +369,7 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
         }
         __syncthreads();
         if (wk > 0) return;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < WK - 1; ++c)
 #pragma unroll
             for (int a = 0; a < MB; ++a)
@@ -220,7 +379,7 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
     }
 
     // alpha S B: ranks 32 a step, alpha S split into bf16 hi + lo
-    if (P.S != nullptr && ks == 0) {
+    if (!T::RIDE && P.S != nullptr) {
         const __amdgpu_buffer_rsrc_t rS = make_rsrc(P.S + (size_t)m0 * P.r, (uint64_t)min(P.M - m0, T::TM) * P.r * 4u);
         const __amdgpu_buffer_rsrc_t rB = make_rsrc(P.B, (uint64_t)P.r * P.N * 2u);
         for (int r0 = 0; r0 < P.r; r0 += 32) {
@@ -254,85 +413,254 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
         }
     }
 
-    // lane (g, l): columns 4g .. 4g+3 of a group, row l
+    // lane (g, l): columns 4g .. 4g+3 of a group, row l.  Rows past M and columns
+    // past N are dropped by the buffer's bounds (the host keeps a tile's rows
+    // under 2^31 bytes).
+    const bool direct = P.part == nullptr;
+    const int rows = min(P.M - m0, T::TM);
+    const __amdgpu_buffer_rsrc_t rY =
+        direct ? make_rsrc(P.Y + (size_t)m0 * P.N, (uint64_t)rows * P.N * 2u)
+               : make_rsrc(P.part + ((size_t)ks * P.M + m0) * P.N, (uint64_t)rows * P.N * 4u);
 #pragma unroll
     for (int a = 0; a < MB; ++a) {
-        const int row = m0 + (wm * MB + a) * 16 + l16;
-        if (row >= P.M) continue;
+        const uint32_t row = (uint32_t)((wm * MB + a) * 16 + l16);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int col = n0 + (wn * NB + b) * 16 + 4 * lg;
-            if (col >= P.N) continue;
-            if (P.KS == 1)
-                *(uint2 *)(P.Y + (size_t)row * P.N + col) =
-                    make_uint2(pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3]));
+            const uint32_t at = row < (uint32_t)rows && col < P.N ? row * (uint32_t)P.N + (uint32_t)col : kOOB / 4;
+            typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+            typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+            if (direct)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2_t{pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3])}, rY, at * 2u, 0, 0);
             else
-                *(f32x4_t *)(P.part + ((size_t)ks * P.M + row) * P.N + col) = acc[a][b];
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[a][b]), rY, at * 4u, 0, 0);
         }
     }
 }
 
-// Y = the slices' sums in slice order, rounded; 8 columns a thread.
-__global__ __launch_bounds__(256) void mxfp4_sum_kernel(const float *part, int KS, int64_t count, uint16_t *Y) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (at >= count) return;
-    float4 a = *(const float4 *)(part + at), b = *(const float4 *)(part + at + 4);
-    for (int s = 1; s < KS; ++s) {
-        const float4 c = *(const float4 *)(part + s * count + at), d = *(const float4 *)(part + s * count + at + 4);
-        a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-        b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+// Y = the k slices' partial sums in slice order, and alpha S B, rounded.  A
+// work-group takes 16 rows of 128 columns, a wave 32 columns: the sums start the
+// accumulators, then 32 ranks an MFMA step, alpha S split into bf16 hi + lo.  S
+// (the sum of SK partials in order, or given) goes to LDS first, and the first
+// column tile writes a summed S out.  (Adding the ranks with plain FMAs took twice
+// the kernel's time at rank 64: one wave a SIMD, 20 instructions a rank.)
+struct MxFinishParams {
+    const float *part;
+    int KS, M, N;
+    const float *spart;  // [SK][M][rs] or, with SK == 0, S itself; r == 0: no adapter
+    int SK, r, rs;
+    const uint16_t *B;
+    float alpha;
+    float *S;
+    uint16_t *Y;
+};
+
+constexpr int kFinishRanks = 64;  // ranks of B in LDS at a time
+
+__global__ __launch_bounds__(256) void mxfp4_finish_kernel(MxFinishParams P) {
+    __shared__ float sS[16][260];  // alpha S, zero past r (rows 16 bytes past a bank period)
+    __shared__ uint4 sB[kFinishRanks * 16];
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row0 = (int)blockIdx.y * 16, n0 = (int)blockIdx.x * 128;
+    // B's first ranks are on their way while S and the product are summed: 16-byte
+    // pieces, 16 a rank (B may be unaligned)
+    uint4 b[kFinishRanks / 16];
+    const int br = tid >> 4, bc = tid & 15;
+    auto load_b = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kFinishRanks / 16; ++i) {
+            b[i] = make_uint4(0u, 0u, 0u, 0u);
+            const int r = r0 + 16 * i + br;
+            if (r < P.r && n0 + 8 * bc < P.N) __builtin_memcpy(&b[i], P.B + (size_t)r * P.N + n0 + 8 * bc, 16);
+        }
+    };
+    const int rpad = (P.r + 31) & ~31;
+    if (P.r > 0) {
+        load_b(0);
+        const int row = row0 + br;  // 16 threads a row of S, 4 ranks at a time
+#pragma unroll 1
+        for (int r = 4 * bc; r < rpad; r += 64) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < P.M && r < P.r) {
+                if (P.SK > 0) {
+                    const float *ps = P.spart + (size_t)row * P.rs + r;
+                    const size_t part = (size_t)P.M * P.rs;
+#pragma unroll 1
+                    for (int c = 0; c < P.SK; c += 8) {
+                        float4 u[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            u[e] = c + e < P.SK ? *(const float4 *)(ps + (c + e) * part) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v.x += u[e].x, v.y += u[e].y, v.z += u[e].z, v.w += u[e].w;
+                    }
+                    if (blockIdx.x == 0) {
+                        float *d = P.S + (size_t)row * P.r + r;
+                        d[0] = v.x;
+                        if (r + 1 < P.r) d[1] = v.y;
+                        if (r + 2 < P.r) d[2] = v.z;
+                        if (r + 3 < P.r) d[3] = v.w;
+                    }
+                } else {
+                    const float *s = P.spart + (size_t)row * P.r + r;
+                    v.x = s[0];
+                    if (r + 1 < P.r) v.y = s[1];
+                    if (r + 2 < P.r) v.z = s[2];
+                    if (r + 3 < P.r) v.w = s[3];
+                }
+            }
+            *(float4 *)&sS[br][r] = make_float4(P.alpha * v.x, P.alpha * v.y, P.alpha * v.z, P.alpha * v.w);
+        }
     }
-    *(uint4 *)(Y + at) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                                    pack_bf16x2(b.z, b.w));
+    // lane (g, l): row l, columns 4g .. 4g+3 of the wave's two 16-column tiles
+    const int row = row0 + l16, col = n0 + 32 * wave + 4 * lg;
+    f32x4_t acc[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+    const bool live0 = row < P.M && col < P.N, live1 = row < P.M && col + 16 < P.N;
+    const size_t slice = (size_t)P.M * P.N;
+    const float *src = P.part + (size_t)row * P.N + col;
+#pragma unroll 1
+    for (int s = 0; s < P.KS; s += 4) {
+        f32x4_t t[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            t[e][0] = t[e][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (live0 && s + e < P.KS) t[e][0] = *(const f32x4_t *)(src + (s + e) * slice);
+            if (live1 && s + e < P.KS) t[e][1] = *(const f32x4_t *)(src + (s + e) * slice + 16);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0] += t[e][0], acc[1] += t[e][1];
+    }
+    // B's pieces in 256-byte rows, piece c of rank k at c ^ place(k): the transposing
+    // reads of ranks {0-3, 8-11} mod 16 by a half-wave then fall on different banks
+    auto place = [](int k) { return (4 * (k & 3)) ^ (2 * ((k >> 3) & 1)); };
+#pragma unroll 1
+    for (int r0 = 0; r0 < P.r; r0 += kFinishRanks) {
+        if (r0 > 0) __syncthreads();  // the last ranks have been read
+#pragma unroll
+        for (int i = 0; i < kFinishRanks / 16; ++i) sB[(16 * i + br) * 16 + (bc ^ place(16 * i + br))] = b[i];
+        __syncthreads();
+        if (r0 + kFinishRanks < P.r) load_b(r0 + kFinishRanks);
+#pragma unroll 1
+        for (int q = 0; q < kFinishRanks && r0 + q < P.r; q += 32) {
+            float v[8];
+            *(float4 *)&v[0] = *(const float4 *)&sS[l16][r0 + q + 8 * lg];
+            *(float4 *)&v[4] = *(const float4 *)&sS[l16][r0 + q + 8 * lg + 4];
+            uint4 hi, lo;
+            split_frag(v, hi, lo);
+            const int k = q + 8 * lg + (l16 >> 2);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int c = 4 * wave + 2 * t + ((l16 & 3) >> 1);
+                const lds_char *p = (const lds_char *)sB + k * 256 + ((c ^ place(k)) << 4) + (l16 & 1) * 8;
+                const uint2 w0 = lds_read_tr4(p), w1 = lds_read_tr4(p + 1024);
+                const uint4 w = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                acc[t] = mfma16x16x32(w, hi, acc[t]);
+                acc[t] = mfma16x16x32(w, lo, acc[t]);
+            }
+        }
+    }
+    uint16_t *dst = P.Y + (size_t)row * P.N + col;
+    if (live0) *(uint2 *)dst = make_uint2(pack_bf16x2(acc[0][0], acc[0][1]), pack_bf16x2(acc[0][2], acc[0][3]));
+    if (live1) *(uint2 *)(dst + 16) = make_uint2(pack_bf16x2(acc[1][0], acc[1][1]), pack_bf16x2(acc[1][2], acc[1][3]));
 }
 
 template <class T>
 hipError_t launch_t(const MxGemmParams &P, hipStream_t stream) {
     if (T::LDS > 64 * 1024)
         (void)hipFuncSetAttribute((const void *)mxfp4_gemm_kernel<T>, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
-    hipLaunchKernelGGL((mxfp4_gemm_kernel<T>), dim3((unsigned)(P.tiles_m * P.tiles_n * P.KS)), dim3(64 * T::NW), T::LDS,
-                       stream, P);
+    hipLaunchKernelGGL((mxfp4_gemm_kernel<T>), dim3((unsigned)(P.tiles_m * P.tiles_n * P.KS + P.jobs)), dim3(64 * T::NW),
+                       T::LDS, stream, P);
     return hipGetLastError();
 }
 
-using Tile4 = MxTile<1, 1, 8, 1, 1, 4, 3>;      // up to 4 rows, 16 columns
-using Tile16 = MxTile<1, 1, 8, 1, 1, 16, 3>;    // up to 16 rows, 16 columns
-using Tile32 = MxTile<1, 2, 4, 2, 2, 32, 3>;    // up to 32 rows, 64 columns
-using Tile64 = MxTile<1, 4, 2, 4, 2, 64, 3>;    // up to 64 rows, 128 columns
-using Tile128 = MxTile<2, 4, 1, 4, 2, 128, 3>;  // 128 rows, 128 columns
-using TileBig = MxTile<2, 4, 1, 4, 4, 128, 3>;  // 128 rows, 256 columns
+// Tile shapes, and what a call with one costs.  `stage`: microseconds a stage
+// takes a work-group when a full round of them runs (measured at k = 14336 and
+// 28672, 2.4 GHz); `share`: work-groups that a CU holds.
+struct MxKind {
+    hipError_t (*launch)(const MxGemmParams &, hipStream_t);
+    int tm, tn, kw, ranks;  // ranks: of one job of S, 0 where S does not ride along
+    float stage;
+    int share;
+};
+template <class T>
+constexpr MxKind kind_of(float stage) {
+    return MxKind{launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? (T::MB == 4 ? 32 : 64) : 0, stage,
+                  std::min(160 * 1024 / T::LDS, 4)};
+}
+const MxKind kKinds[] = {
+    kind_of<MxTile<1, 1, 8, 1, 1, 4, 3>>(0.36f),   // 4 rows x 16 columns
+    kind_of<MxTile<1, 2, 4, 1, 1, 4, 3>>(0.31f),   // 4 x 32
+    kind_of<MxTile<1, 1, 8, 1, 1, 16, 3>>(0.60f),  // 16 x 16
+    kind_of<MxTile<1, 2, 4, 1, 2, 16, 3>>(0.53f),  // 16 x 64
+    kind_of<MxTile<1, 2, 4, 2, 1, 32, 3>>(0.61f),  // 32 x 32
+    kind_of<MxTile<1, 4, 2, 2, 2, 32, 3>>(0.67f),  // 32 x 128
+    kind_of<MxTile<1, 4, 2, 4, 2, 64, 3>>(1.00f),  // 64 x 128
+    kind_of<MxTile<2, 4, 1, 2, 4, 64, 3>>(0.98f),  // 64 x 256
+    kind_of<MxTile<2, 4, 1, 4, 4, 128, 3>>(1.65f), // 128 x 256
+};
 
 }  // namespace
 
-MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int want) {
-    MxGemmPlan p{};
-    if (m <= 0 || k > (1 << 20) || n > (1 << 27) || m > 16384) return p;
-    const int64_t tiles64 = (m + 127) / 128 * ((n + 255) / 256);
-    p.kind = m <= 4 ? 1 : m <= 16 ? 2 : m <= 32 ? 3 : m <= 64 ? 4 : tiles64 >= 128 ? 6 : 5;
-    if (want) p.kind = want;
-    static const int tm[] = {0, Tile4::TM, Tile16::TM, Tile32::TM, Tile64::TM, Tile128::TM, TileBig::TM};
-    static const int tn[] = {0, Tile4::TN, Tile16::TN, Tile32::TN, Tile64::TN, Tile128::TN, TileBig::TN};
-    static const int kw[] = {0, Tile4::KW, Tile16::KW, Tile32::KW, Tile64::KW, Tile128::KW, TileBig::KW};
-    p.tiles_m = (int)((m + tm[p.kind] - 1) / tm[p.kind]);
-    p.tiles_n = (int)((n + tn[p.kind] - 1) / tn[p.kind]);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, stages = (k + kw[p.kind] - 1) / kw[p.kind];
-    int64_t KS = 1;
-    if (tiles < 192) KS = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, stages / 4));
-    p.per = (int)((stages + KS - 1) / KS);
-    p.KS = (int)((stages + p.per - 1) / p.per);
-    p.part_bytes = p.KS > 1 ? (size_t)p.KS * m * n * sizeof(float) : 0;
-    return p;
+// The cheapest of the tile shapes, each with k split as far as pays, and of
+// expanding the weight for the bf16 product, by a model of their times:
+//   shape:  3.5 us + rounds (stages x stage time + 1 us), at least the weight's
+//           bytes at 6 TB/s; a finishing launch 3.5 us and its partial sums at 8 TB/s
+//   expand: 2.5 us + 2.53 bytes an element at 6 TB/s + 3.5 us + rounds of 256
+//           256 x 256 tiles (k / 64 x 1.35 us)
+// Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 17.1
+// (18), 300 x 14336 x 4096 45 (46), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
+// (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (188; packed 245).
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout) {
+    MxGemmPlan best{};
+    // (a tile's offsets stay below 2^31 within these)
+    if (m <= 0 || k > (1 << 20) || n > (1 << 21) || m > (1 << 19)) return best;
+    const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const double weight = (double)k * n;
+    double least = 6.0 + weight * 2.53 / 6e6 + (double)cdiv(cdiv(m, 256) * cdiv(n, 256), 256) * (double)cdiv(k, 64) * 1.35;
+    for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
+        const MxKind &K = kKinds[kind - 1];
+        if ((kind <= 2 && m > 4) || (kind <= 4 && m > 16)) continue;  // (4 rows in LDS; columns too narrow)
+        MxGemmPlan p{};
+        p.kind = kind;
+        p.tiles_m = (int)cdiv(m, K.tm);
+        p.tiles_n = (int)cdiv(n, K.tn);
+        const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, stages = cdiv(k, K.kw);
+        if (tiles > (1 << 20)) continue;
+        if (r > 0 && K.ranks > 0 && !dropout && m <= 128) {
+            p.SK = (int)cdiv(k, kSK);
+            p.jobs = (int)cdiv(p.SK * p.tiles_m * cdiv(r, K.ranks), 8) * 8;
+            p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
+        }
+        for (int want = 1; want <= 16 && want <= stages; ++want) {
+            p.per = (int)cdiv(stages, want);
+            p.KS = (int)cdiv(stages, p.per);
+            if (p.KS != want) continue;
+            p.finish = p.KS > 1 || (r > 0 && K.ranks > 0);
+            p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
+            const int64_t groups = tiles * p.KS + p.jobs, slots = 256 * K.share;
+            double t = (double)cdiv(groups, slots) * (p.per * K.stage + 1.0);
+            t = 3.5 + std::max(t, weight * 0.53 / 6e6);
+            if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 8e6;
+            if (t < least) {
+                least = t;
+                best = p;
+            }
+        }
+    }
+    return best;
 }
 
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
-                             int n, const float *S, const void *B, int r, float alpha, void *Y, float *part,
-                             hipStream_t stream) {
+                             int n, const void *A, const void *B, int r, float alpha, float *S, void *Y, float *part,
+                             float *spart, hipStream_t stream) {
     MxGemmParams P{};
     P.X = (const uint16_t *)X;
     P.codes = (const uint8_t *)codes;
     P.scales = (const uint8_t *)scales;
     P.Y = (uint16_t *)Y;
-    P.part = part;
+    P.part = pl.finish ? part : nullptr;
     P.M = m;
     P.N = n;
     P.K = k;
@@ -342,26 +670,23 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     P.tiles_n = pl.tiles_n;
     P.KS = pl.KS;
     P.per = pl.per;
-    P.S = S;
+    P.S = r > 0 && !pl.finish ? S : nullptr;
+    P.A = (const uint16_t *)A;
+    P.spart = spart;
+    P.SK = pl.SK;
+    P.rs = (r + 3) / 4 * 4;
     P.B = (const uint16_t *)B;
     P.r = r;
     P.alpha = alpha;
+    P.jobs = pl.jobs;
     int slot = prof_begin("mxfp4_gemm", stream);
-    hipError_t e = hipErrorInvalidValue;
-    switch (pl.kind) {
-    case 1: e = launch_t<Tile4>(P, stream); break;
-    case 2: e = launch_t<Tile16>(P, stream); break;
-    case 3: e = launch_t<Tile32>(P, stream); break;
-    case 4: e = launch_t<Tile64>(P, stream); break;
-    case 5: e = launch_t<Tile128>(P, stream); break;
-    case 6: e = launch_t<TileBig>(P, stream); break;
-    }
+    const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
-    if (e != hipSuccess || pl.KS == 1) return e;
-    slot = prof_begin("mxfp4_sum", stream);
-    const int64_t count = (int64_t)m * n;
-    hipLaunchKernelGGL(mxfp4_sum_kernel, dim3((unsigned)((count / 8 + 255) / 256)), dim3(256), 0, stream, part, pl.KS, count,
-                       (uint16_t *)Y);
+    if (e != hipSuccess || !pl.finish) return e;
+    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)B, alpha, S, (uint16_t *)Y};
+    slot = prof_begin("mxfp4_finish", stream);
+    hipLaunchKernelGGL(mxfp4_finish_kernel, dim3((unsigned)((n + 127) / 128), (unsigned)((m + 15) / 16)), dim3(256), 0, stream,
+                       F);
     prof_end(slot, stream);
     return hipGetLastError();
 }

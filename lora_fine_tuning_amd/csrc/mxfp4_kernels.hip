@@ -27,9 +27,9 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
 
 // The float 2^(s - 127) of a scale byte: s = 0 is the subnormal 2^-127, and
-// s = 255 a NaN (the conversions then give NaN for every code).
+// s = 255 an infinity (the conversions then give NaN for every code).
 __device__ __forceinline__ float mx_scale(uint32_t s) {
-    return __uint_as_float((s << 23) | ((s == 0u || s == 255u) ? 0x00400000u : 0u));
+    return __uint_as_float(max(s << 23, 0x00400000u));
 }
 
 // Two codes (byte B of w) -> two bf16, exact.
