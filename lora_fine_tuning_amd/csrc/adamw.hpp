@@ -22,7 +22,7 @@ struct AdamwPlan {
 // Work-groups of one launch (2^24 x 256 threads is the limit of a grid), and
 // the values of the largest tensor.
 constexpr int64_t kAdamwMaxChunks = (1 << 24) - 1;
-constexpr int64_t kAdamwMaxValues = kAdamwMaxChunks * 4096;
+constexpr int64_t kAdamwMaxValues = kAdamwMaxChunks * 2048;
 
 hipError_t launch_adamw(const lora_adamw_tensor *tensors, int32_t count, const AdamwPlan &pl, hipStream_t stream);
 

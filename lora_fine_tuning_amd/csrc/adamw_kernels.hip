@@ -15,11 +15,15 @@
 // smallest code: with m above zero and u at zero the next update would divide
 // by eps alone.
 //
-// A work-group takes 4096 values of one tensor and finds the tensor in the
-// launch's table (kernel arguments: nothing is copied or kept).  Streaming
-// bytes bound it: 16-byte loads, a block's 256 values in 32 lanes so its
-// maximum takes five lane exchanges and no LDS.
+// A work-group takes 2048 values of one tensor and finds the tensor in the
+// launch's table (kernel arguments: nothing is copied or kept).  A full chunk
+// takes 8 values a lane: 16-byte loads, and a block's 256 values in 32 lanes, so
+// its maximum takes five lane exchanges and no LDS.  A tensor's last, partial
+// chunk takes a value a lane, a block the whole work-group: both forms are short,
+// and none has a bounds check for each value of a vector.
 #include <hip/hip_runtime.h>
+
+#include <cmath>
 
 #include "adamw.hpp"
 #include "device_common.hpp"
@@ -29,7 +33,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kChunk = 4096;  // values per work-group: 256 threads x 8 values x 2
+constexpr int kChunk = 2048;  // values per work-group: 256 threads x 8 values
 
 struct AdamwKernelTensor {
     void *param;
@@ -45,210 +49,224 @@ constexpr int kPerLaunch = 48;
 struct AdamwArgs {
     AdamwKernelTensor t[kPerLaunch];
     int32_t first[kPerLaunch];  // first chunk of each tensor
-    uint64_t vec;               // bit i: every pointer of tensor i is aligned for 16-byte pieces
     int32_t count;
     float decay, lr, b1, a1, b2, a2, eps;  // decay = 1 - lr wd, a = 1 - b
-    float rc1, rc2;             // 1 / (1 - b^t), where t is known on the host
+    float rc1, rc2;                        // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t), where t is known on the host
     float ln_b1, ln_b2;
     const int64_t *step_dev;
     uint64_t seed, step;
 };
-static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
+static_assert(sizeof(AdamwArgs) <= 4096 && kPerLaunch <= 64, "kernel arguments; a lane for each tensor");
 
 constexpr float kTop = 448.f;           // largest e4m3
 constexpr float kLeast = 0.001953125f;  // smallest e4m3, 2^-9
 constexpr float kTiny = 7.888609e-31f;  // 2^-100
 
-__device__ __forceinline__ float max32(float x) {  // over the 32 lanes of a block
-    x = fmaxf(x, __shfl_xor(x, 1));
-    x = fmaxf(x, __shfl_xor(x, 2));
-    x = fmaxf(x, __shfl_xor(x, 4));
-    x = fmaxf(x, __shfl_xor(x, 8));
-    return fmaxf(x, __shfl_xor(x, 16));
-}
-
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
 
-// y in [0, 448] to floor(y / step + r / 65536) e4m3 steps.  From 2^-6 on a
-// step is the float's mantissa past 3 bits, below it is 2^-9.
-__device__ __forceinline__ float e4m3_at_random(float y, uint32_t r) {
-    const float big = __uint_as_float((__float_as_uint(y) + (r << 4)) & 0xFFF00000u);
-    const uint32_t fixed = (uint32_t)(fminf(y, 0.015625f) * 536870912.f);  // y / 2^-9 in 2^-20 parts
-    const float small = (float)((fixed + (r << 4)) >> 20) * kLeast;
-    return y >= 0.015625f ? big : small;
+struct AdamwStep {
+    float b1, a1, b2, a2, decay, lr, eps, rc1, rc2;
+    // One value: m, v and w after the step, and the new root of v.  v_sqrt and
+    // v_rcp are within one unit in the last place; the update is the one place
+    // that uses them.
+    __device__ __forceinline__ float operator()(float g, float &w, float &m, float &v) const {
+        m = b1 * m + a1 * g;
+        v = b2 * v + a2 * (g * g);
+        const float u = __builtin_amdgcn_sqrtf(v);
+        w = w * decay - lr * ((m * rc1) * __builtin_amdgcn_rcpf(u * rc2 + eps));
+        return u;
+    }
+};
+
+// x / scale (inv = 1 / scale) to one of its two e4m3 neighbours, the upper one
+// where the fraction of a step and r / 65536 make 1 or more; `least` for a
+// positive value that came out as zero.
+__device__ __forceinline__ uint32_t e4m3_at_random(float x, float inv, uint32_t r16_high) {
+    const float y = __builtin_copysignf(fminf(fabsf(x) * inv, kTop), x);
+    return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, (int)r16_high, 0, 0) & 255u;
 }
 
 template <int BITS, bool MASTER, bool PBF, bool GBF>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs P) {
-    int lo = 0, hi = P.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (P.first[mid] <= (int)blockIdx.x) lo = mid;
-        else hi = mid - 1;
-    }
-    const AdamwKernelTensor T = P.t[lo];
-    const bool vec = (P.vec >> lo) & 1;
-    float rc1 = P.rc1, rc2 = P.rc2;
-    uint64_t step = P.step;
+    const int tid = threadIdx.x, lane = tid & 63;
+    // the tensor whose chunks include this work-group's: a lane looks at each
+    const int32_t mine = lane < P.count ? P.first[min(lane, kPerLaunch - 1)] : 0x7FFFFFFF;
+    const int at = __builtin_popcountll(__ballot(mine <= (int)blockIdx.x)) - 1;
+    const AdamwKernelTensor T = P.t[at];
+    const int64_t e0 = (int64_t)((int)blockIdx.x - P.first[at]) * kChunk;
+    AdamwStep step{P.b1, P.a1, P.b2, P.a2, P.decay, P.lr, P.eps, P.rc1, P.rc2};
+    uint64_t t = P.step;
     if (P.step_dev != nullptr) {
-        step = (uint64_t)*P.step_dev;
-        rc1 = 1.f / -expm1f((float)(int64_t)step * P.ln_b1);
-        rc2 = 1.f / -expm1f((float)(int64_t)step * P.ln_b2);
+        t = (uint64_t)*P.step_dev;
+        step.rc1 = 1.f / -expm1f((float)(int64_t)t * P.ln_b1);
+        step.rc2 = 1.f / sqrtf(-expm1f((float)(int64_t)t * P.ln_b2));
     }
-    const uint64_t key = P.seed + step * 0x9E3779B97F4A7C15ull;
-    const int64_t chunk0 = (int64_t)((int)blockIdx.x - P.first[lo]) * kChunk;
+    const uint64_t key = P.seed + t * 0x9E3779B97F4A7C15ull;
 
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int64_t e0 = chunk0 + half * (kChunk / 2) + (int)threadIdx.x * 8;
-        const int live = (int)max((int64_t)0, min((int64_t)8, T.n - e0));  // may be 0: the lane still joins its block's maximum
-        const bool wide = vec && live == 8;
+    if (e0 + kChunk <= T.n) {
+        const int64_t e = e0 + tid * 8;
         float g[8], w[8], m[8], v[8];
+        // (whole vectors at the alignment of their values)
+        auto load_f32 = [&](const void *src, float (&x)[8]) { __builtin_memcpy(x, (const float *)src + e, 32); };
+        auto store_f32 = [&](void *dst, const float (&x)[8]) { __builtin_memcpy((float *)dst + e, x, 32); };
+        auto load_bf16 = [&](const void *src, float (&x)[8]) {
+            uint32_t q[4];
+            __builtin_memcpy(q, (const uint16_t *)src + e, 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = w[i] = m[i] = v[i] = 0.f;
-        auto load_f32 = [&](const float *src, float (&x)[8]) {
-            if (wide) {
-                const float4 a = ((const float4 *)(src + e0))[0], b = ((const float4 *)(src + e0))[1];
-                x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < live) x[i] = src[e0 + i];
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(q[i] << 16);
+                x[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
             }
         };
-        auto load_bf16 = [&](const uint16_t *src, float (&x)[8]) {
-            if (wide) {
-                const uint4 a = *(const uint4 *)(src + e0);
-                const uint32_t q[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = __uint_as_float(q[i] << 16);
-                    x[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < live) x[i] = bf16_to_f32(src[e0 + i]);
-            }
-        };
-        auto load_codes = [&](const uint8_t *src, float scale, float (&x)[8]) {
-            uint32_t q[2] = {0u, 0u};
-            if (wide) {
-                const uint2 a = *(const uint2 *)(src + e0);
-                q[0] = a.x, q[1] = a.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < live) q[i >> 2] |= (uint32_t)src[e0 + i] << (8 * (i & 3));
-            }
+        uint32_t qm[2], qv[2];
+        float sm = 0.f, sv = 0.f;
+        if constexpr (BITS == 8) {
+            __builtin_memcpy(qm, (const uint8_t *)T.m + e, 8);
+            __builtin_memcpy(qv, (const uint8_t *)T.v + e, 8);
+            sm = T.m_scale[e >> 8];
+            sv = T.v_scale[e >> 8];
+        } else {
+            load_f32(T.m, m);
+            load_f32(T.v, v);
+        }
+        if constexpr (GBF) load_bf16(T.grad, g);
+        else load_f32(T.grad, g);
+        if constexpr (MASTER) load_f32(T.master, w);
+        else if constexpr (PBF) load_bf16(T.param, w);
+        else load_f32(T.param, w);
+        if constexpr (BITS == 8) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
-                const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
-                x[4 * i] = a[0] * scale, x[4 * i + 1] = a[1] * scale;
-                x[4 * i + 2] = b[0] * scale, x[4 * i + 3] = b[1] * scale;
+                const auto m0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)qm[i], false), m1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)qm[i], true);
+                const auto v0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)qv[i], false), v1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)qv[i], true);
+                m[4 * i] = m0[0] * sm, m[4 * i + 1] = m0[1] * sm, m[4 * i + 2] = m1[0] * sm, m[4 * i + 3] = m1[1] * sm;
+                v[4 * i] = v0[0] * sv, v[4 * i + 1] = v0[1] * sv, v[4 * i + 2] = v1[0] * sv, v[4 * i + 3] = v1[1] * sv;
             }
-        };
-        if constexpr (GBF) load_bf16((const uint16_t *)T.grad, g);
-        else load_f32((const float *)T.grad, g);
-        if constexpr (MASTER) load_f32(T.master, w);
-        else if constexpr (PBF) load_bf16((const uint16_t *)T.param, w);
-        else load_f32((const float *)T.param, w);
-        if constexpr (BITS == 32) {
-            load_f32((const float *)T.m, m);
-            load_f32((const float *)T.v, v);
-        } else {
-            const int64_t blk = e0 >> 8;
-            load_codes((const uint8_t *)T.m, live > 0 ? T.m_scale[blk] : 0.f, m);
-            load_codes((const uint8_t *)T.v, live > 0 ? T.v_scale[blk] : 0.f, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= v[i];
         }
+        float u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m[i] = P.b1 * m[i] + P.a1 * g[i];
-            v[i] = P.b2 * v[i] + P.a2 * (g[i] * g[i]);
-            w[i] = w[i] * P.decay - P.lr * ((m[i] * rc1) / (sqrtf(v[i] * rc2) + P.eps));
-        }
-        auto store_f32 = [&](float *dst, const float (&x)[8]) {
-            if (wide) {
-                ((float4 *)(dst + e0))[0] = make_float4(x[0], x[1], x[2], x[3]);
-                ((float4 *)(dst + e0))[1] = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < live) dst[e0 + i] = x[i];
-            }
-        };
+        for (int i = 0; i < 8; ++i) u[i] = step(g[i], w[i], m[i], v[i]);
         if constexpr (MASTER) store_f32(T.master, w);
         if constexpr (PBF) {
-            uint32_t q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(w[2 * i], w[2 * i + 1]);
-            uint16_t *dst = (uint16_t *)T.param;
-            if (wide) {
-                *(uint4 *)(dst + e0) = make_uint4(q[0], q[1], q[2], q[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < live) dst[e0 + i] = (uint16_t)(q[i >> 1] >> (16 * (i & 1)));
-            }
+            const uint32_t q[4] = {pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
+                                   pack_bf16x2(w[6], w[7])};
+            __builtin_memcpy((uint16_t *)T.param + e, q, 16);
         } else {
-            store_f32((float *)T.param, w);
+            store_f32(T.param, w);
         }
         if constexpr (BITS == 32) {
-            store_f32((float *)T.m, m);
-            store_f32((float *)T.v, v);
+            store_f32(T.m, m);
+            store_f32(T.v, v);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = sqrtf(v[i]);
-            // scales from the finite values; an infinity or a NaN is stored as NaN
-            float tm = 0.f, tv = 0.f;
+            float tm = 0.f, tv = 0.f, odd = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                tm = fmaxf(tm, finite(m[i]) ? fabsf(m[i]) : 0.f);
-                tv = fmaxf(tv, finite(v[i]) ? v[i] : 0.f);
+                tm = fmaxf(tm, fabsf(m[i]));
+                tv = fmaxf(tv, u[i]);
+                odd += (m[i] + u[i]) * 0.f;  // NaN if any of them is infinite or NaN
             }
-            tm = max32(tm);
-            tv = max32(tv);
+            const bool strange = __any(odd != 0.f || odd != odd);
+            if (strange) {  // scales from the finite values; the others are stored as NaN
+                tm = tv = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    tm = fmaxf(tm, finite(m[i]) ? fabsf(m[i]) : 0.f);
+                    tv = fmaxf(tv, finite(u[i]) ? u[i] : 0.f);
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                tm = fmaxf(tm, __shfl_xor(tm, d));
+                tv = fmaxf(tv, __shfl_xor(tv, d));
+            }
             tm = tm < kTiny ? 0.f : tm;
             tv = tv < kTiny ? 0.f : tv;
             const float im = tm > 0.f ? kTop / tm : 0.f, iv = tv > 0.f ? kTop / tv : 0.f;
-            float cm[8], cv[8];
+            uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const PhiloxOut rnd = philox10((T.offset + (uint64_t)e0) / 4 + q, key);
+                const PhiloxOut rnd = philox10((T.offset + (uint64_t)e) / 4 + q, key);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int i = 4 * q + j;
-                    const float a = e4m3_at_random(fminf(fabsf(m[i]) * im, kTop), rnd.w[j] & 0xFFFFu);
-                    float b = e4m3_at_random(fminf(v[i] * iv, kTop), rnd.w[j] >> 16);
-                    if (b == 0.f && v[i] * iv > 0.f) b = kLeast;
-                    cm[i] = finite(m[i]) ? __builtin_copysignf(a, m[i]) : __builtin_nanf("");
-                    cv[i] = finite(v[i]) ? b : __builtin_nanf("");
+                    uint32_t a = e4m3_at_random(m[i], im, rnd.w[j] << 16);
+                    uint32_t b = e4m3_at_random(u[i], iv, rnd.w[j] & 0xFFFF0000u);
+                    if (u[i] * iv > 0.f) b = max(b, 1u);
+                    if (strange) {
+                        a = finite(m[i]) ? a : 0x7Fu;
+                        b = finite(u[i]) ? b : 0x7Fu;
+                    }
+                    cm[q] |= a << (8 * j);
+                    cv[q] |= b << (8 * j);
                 }
             }
-            auto store_codes = [&](uint8_t *dst, const float (&c)[8]) {
-                uint32_t q[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    int p = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
-                    q[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], p, true);
-                }
-                if (wide) {
-                    *(uint2 *)(dst + e0) = make_uint2(q[0], q[1]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < live) dst[e0 + i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
-                }
-            };
-            store_codes((uint8_t *)T.m, cm);
-            store_codes((uint8_t *)T.v, cv);
-            if ((threadIdx.x & 31) == 0 && live > 0) {
-                T.m_scale[e0 >> 8] = tm / kTop;
-                T.v_scale[e0 >> 8] = tv / kTop;
+            __builtin_memcpy((uint8_t *)T.m + e, cm, 8);
+            __builtin_memcpy((uint8_t *)T.v + e, cv, 8);
+            if ((tid & 31) == 0) {
+                T.m_scale[e >> 8] = tm / kTop;
+                T.v_scale[e >> 8] = tv / kTop;
             }
+        }
+        return;
+    }
+
+    __shared__ float tops[2][8];
+#pragma unroll 1
+    for (int p = 0; p < kChunk / 256 && e0 + 256 * p < T.n; ++p) {
+        const int64_t e = e0 + 256 * p + tid;
+        const bool live = e < T.n;
+        const int64_t i = live ? e : T.n - 1;  // (in bounds; its result is dropped)
+        const float g = GBF ? bf16_to_f32(((const uint16_t *)T.grad)[i]) : ((const float *)T.grad)[i];
+        float w = MASTER ? T.master[i] : PBF ? bf16_to_f32(((const uint16_t *)T.param)[i]) : ((const float *)T.param)[i];
+        float m, v;
+        if constexpr (BITS == 32) {
+            m = ((const float *)T.m)[i];
+            v = ((const float *)T.v)[i];
+        } else {
+            m = __builtin_amdgcn_cvt_f32_fp8((int)((const uint8_t *)T.m)[i], 0) * T.m_scale[i >> 8];
+            v = __builtin_amdgcn_cvt_f32_fp8((int)((const uint8_t *)T.v)[i], 0) * T.v_scale[i >> 8];
+            v *= v;
+        }
+        const float u = step(g, w, m, v);
+        if constexpr (BITS == 8) {
+            float tm = live && finite(m) ? fabsf(m) : 0.f, tv = live && finite(u) ? u : 0.f;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                tm = fmaxf(tm, __shfl_xor(tm, d));
+                tv = fmaxf(tv, __shfl_xor(tv, d));
+            }
+            if (lane == 0) tops[p & 1][tid >> 6] = tm, tops[p & 1][4 + (tid >> 6)] = tv;
+            __syncthreads();  // (every lane has read its moments and scales too)
+            const float *o = tops[p & 1];
+            tm = fmaxf(fmaxf(o[0], o[1]), fmaxf(o[2], o[3]));
+            tv = fmaxf(fmaxf(o[4], o[5]), fmaxf(o[6], o[7]));
+            tm = tm < kTiny ? 0.f : tm;
+            tv = tv < kTiny ? 0.f : tv;
+            const float im = tm > 0.f ? kTop / tm : 0.f, iv = tv > 0.f ? kTop / tv : 0.f;
+            const uint64_t c = T.offset + (uint64_t)e;
+            const PhiloxOut rnd = philox10(c / 4, key);
+            const int j = (int)(c & 3);
+            const uint32_t r = j == 0 ? rnd.w[0] : j == 1 ? rnd.w[1] : j == 2 ? rnd.w[2] : rnd.w[3];
+            uint32_t a = e4m3_at_random(m, im, r << 16), b = e4m3_at_random(u, iv, r & 0xFFFF0000u);
+            if (u * iv > 0.f) b = max(b, 1u);
+            if (live) {
+                ((uint8_t *)T.m)[e] = finite(m) ? (uint8_t)a : 0x7F;
+                ((uint8_t *)T.v)[e] = finite(u) ? (uint8_t)b : 0x7F;
+                if (tid == 0) {
+                    T.m_scale[e >> 8] = tm / kTop;
+                    T.v_scale[e >> 8] = tv / kTop;
+                }
+            }
+        } else if (live) {
+            ((float *)T.m)[e] = m;
+            ((float *)T.v)[e] = v;
+        }
+        if (live) {
+            if constexpr (MASTER) T.master[e] = w;
+            if constexpr (PBF) ((uint16_t *)T.param)[e] = (uint16_t)(pack_bf16x2(w, 0.f) & 0xFFFFu);
+            else ((float *)T.param)[e] = w;
         }
     }
 }
@@ -259,12 +277,6 @@ AdamwFn pick(bool master, bool pbf, bool gbf) {
     if (master) return gbf ? adamw_kernel<BITS, true, true, true> : adamw_kernel<BITS, true, true, false>;
     if (pbf) return gbf ? adamw_kernel<BITS, false, true, true> : adamw_kernel<BITS, false, true, false>;
     return gbf ? adamw_kernel<BITS, false, false, true> : adamw_kernel<BITS, false, false, false>;
-}
-
-bool wide_ok(const lora_adamw_tensor &t, int bits) {
-    const uintptr_t all = (uintptr_t)t.param | (uintptr_t)t.grad | (uintptr_t)t.master;
-    const uintptr_t moments = (uintptr_t)t.m | (uintptr_t)t.v;
-    return all % 16 == 0 && moments % (bits == 8 ? 8 : 16) == 0;
 }
 
 }  // namespace
@@ -281,7 +293,7 @@ hipError_t launch_adamw(const lora_adamw_tensor *tensors, int32_t count, const A
     a.a2 = (float)(1.0 - pl.beta2);
     a.eps = (float)pl.eps;
     a.rc1 = (float)pl.rc1;
-    a.rc2 = (float)pl.rc2;
+    a.rc2 = (float)std::sqrt(pl.rc2);
     a.ln_b1 = (float)pl.ln_b1;
     a.ln_b2 = (float)pl.ln_b2;
     a.step_dev = pl.step_dev;
@@ -294,7 +306,6 @@ hipError_t launch_adamw(const lora_adamw_tensor *tensors, int32_t count, const A
         hipLaunchKernelGGL(fn, dim3((unsigned)chunks), dim3(256), 0, stream, a);
         prof_end(slot, stream);
         a.count = 0;
-        a.vec = 0;
         chunks = 0;
         return hipGetLastError();
     };
@@ -308,7 +319,6 @@ hipError_t launch_adamw(const lora_adamw_tensor *tensors, int32_t count, const A
         }
         a.t[a.count] = AdamwKernelTensor{t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_scale, t.n, t.offset};
         a.first[a.count] = (int32_t)chunks;
-        if (wide_ok(t, pl.bits)) a.vec |= 1ull << a.count;
         ++a.count;
         chunks += c;
     }
