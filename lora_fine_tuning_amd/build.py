@@ -19,7 +19,8 @@ LIB_NAME = "liblora_fused.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cpp", "mxfp4_api.cpp", "adamw_api.cpp", "packer.cpp", "lowrank_kernels.hip", "gemm_kernels.hip",
-           "dora_kernels.hip", "mxfp4_kernels.hip", "mxfp4_gemm.hip", "adamw_kernels.hip"]
+           "dora_kernels.hip", "mxfp4_kernels.hip", "mxfp4_gemm.hip", "mxfp4_gemm_t.hip", "mxfp4_join.hip",
+           "adamw_kernels.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-I", INCLUDE, "-I", CSRC,
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -246,19 +246,6 @@ BwdPlan plan_bwd(int64_t m, int64_t k, int64_t n, int32_t RS, bool multi, int32_
     return p;
 }
 
-AdapterSource single_source(const void *A, const void *B, void *dA, void *dB, int32_t r, float alpha, float p) {
-    AdapterSource s{};
-    s.A = A;
-    s.B = B;
-    s.dA = dA;
-    s.dB = dB;
-    s.r = r;
-    s.alpha = alpha;
-    s.p = p;
-    s.table = nullptr;
-    s.r_cap = r;
-    return s;
-}
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -359,6 +346,43 @@ extern "C" lora_status lora_linear_fwd_concat(const void *X, const void *W, cons
     return LORA_OK;
 }
 
+// B1 and B2: dA, dB, and dS (with its split for B3 where the plan has one) in the workspace.
+static lora_status backward_low_rank(const BwdPlan &pl, const void *dY, const void *X, const AdapterSource &src,
+                                     const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                                     int32_t r, float p, void *workspace, hipStream_t stream) {
+    float *dS = (float *)ws_at(workspace, pl.off_ds);
+    float *dSpart = pl.ds_parts > 1 ? (float *)ws_at(workspace, pl.off_dspart) : dS;
+    float *dBpart = (float *)ws_at(workspace, pl.off_dbpart);
+    float *dApart = (float *)ws_at(workspace, pl.off_dapart);
+    uint16_t *dss = pl.dss_ld > 0 ? (uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
+    const int chunks = pl.chunk_cap_bwd;
+    if (m > 0) HIPCHK(launch_b1(dY, S, (int)m, (int)n, r, src, pl.b1, dSpart, dBpart, stream), "B1 launch");
+    HIPCHK(launch_b1_reduce(dSpart, m > 0 ? pl.ds_parts : 1, dS, dBpart, (int)m, (int)n, r, src, pl.b1.rows,
+                            pl.b1.slots, stream, dss, pl.dss_ld),
+           "dS/dB reduction launch");
+    if (pl.b2w) {
+        HIPCHK(launch_b2w(X, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, pl.items2,
+                          dApart, nullptr, stream, dss, pl.dss_ld), "B2 launch");
+    } else {
+        if (m > 0)
+            HIPCHK(launch_b2(X, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, chunks,
+                             pl.C2, dApart, stream), "B2 launch");
+        HIPCHK(launch_grad_reduce(1, dApart, (int)m, (int)k, (int)n, r, src, pl.rows2, chunks, stream),
+               "dA reduction launch");
+    }
+    return LORA_OK;
+}
+
+namespace lora {
+lora_status backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+                                   const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r,
+                                   void *workspace, const float **dS_out, hipStream_t stream) {
+    const BwdPlan pl = plan_bwd(m, k, n, r, false, 0, 1);
+    *dS_out = (const float *)ws_at(workspace, pl.off_ds);
+    return backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, r, src.p, workspace, stream);
+}
+}  // namespace lora
+
 extern "C" lora_status lora_linear_bwd(const void *dY, const void *X, const void *W, const void *A,
                                        const void *B, const float *S, const uint32_t *keep_bits,
                                        int64_t m, int64_t k, int64_t n, int32_t r, float alpha,
@@ -386,27 +410,10 @@ extern "C" lora_status lora_linear_bwd(const void *dY, const void *X, const void
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     if (pl.bytes) REQ_PTR(workspace, 16);
 
-    AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
-    float *dS = (float *)ws_at(workspace, pl.off_ds);
-    float *dSpart = pl.ds_parts > 1 ? (float *)ws_at(workspace, pl.off_dspart) : dS;
-    float *dBpart = (float *)ws_at(workspace, pl.off_dbpart);
-    float *dApart = (float *)ws_at(workspace, pl.off_dapart);
-    uint16_t *dss = pl.dss_ld > 0 ? (uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
-    const int chunks = pl.chunk_cap_bwd;
-    if (m > 0) HIPCHK(launch_b1(dY, S, (int)m, (int)n, r, src, pl.b1, dSpart, dBpart, stream), "B1 launch");
-    HIPCHK(launch_b1_reduce(dSpart, m > 0 ? pl.ds_parts : 1, dS, dBpart, (int)m, (int)n, r, src, pl.b1.rows,
-                            pl.b1.slots, stream, dss, pl.dss_ld),
-           "dS/dB reduction launch");
-    if (pl.b2w) {
-        HIPCHK(launch_b2w(X, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, pl.items2,
-                          dApart, nullptr, stream, dss, pl.dss_ld), "B2 launch");
-    } else {
-        if (m > 0)
-            HIPCHK(launch_b2(X, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, chunks,
-                             pl.C2, dApart, stream), "B2 launch");
-        HIPCHK(launch_grad_reduce(1, dApart, (int)m, (int)k, (int)n, r, src, pl.rows2, chunks, stream),
-               "dA reduction launch");
-    }
+    const AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
+    CHECK(backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, r, p, workspace, stream));
+    const float *dS = (const float *)ws_at(workspace, pl.off_ds);
+    const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, r, p == 0.0f ? nullptr : keep_bits,
                            (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
@@ -441,17 +448,33 @@ extern "C" size_t multi_lora_bwd_workspace_size(int64_t m, int64_t k, int64_t n,
     return plan_bwd(m, k, n, r_max, true, num_segments, num_adapters).bytes;
 }
 
-static AdapterSource multi_source(const lora_adapter *adapters, int32_t nad, const int64_t *seg_off,
-                                  const int32_t *seg_adapter, int32_t nseg, int32_t r_max) {
-    AdapterSource s{};
-    s.table = adapters;
-    s.num_adapters = nad;
-    s.r_cap = r_max;
-    s.seg_off = seg_off;
-    s.seg_adapter = seg_adapter;
-    s.num_segments = nseg;
-    s.r = r_max;
-    return s;
+// The router and F1: keep_bits and S.
+static lora_status multi_forward_s(const FwdPlan &pl, const void *X, AdapterSource src, int64_t m, int64_t k,
+                                   uint64_t seed, uint64_t offset, float *S, uint32_t *keep_bits, void *workspace,
+                                   hipStream_t stream) {
+    const int32_t r_max = src.r_cap;
+    src.chunks_f1 = (const ChunkEntry *)ws_at(workspace, pl.off_t_f1);
+    src.count_f1 = (const int32_t *)ws_at(workspace, pl.off_c_f1);
+    src.chunks_bwd = (const ChunkEntry *)ws_at(workspace, pl.off_t_bwd);
+    src.count_bwd = (const int32_t *)ws_at(workspace, pl.off_c_bwd);
+    HIPCHK(launch_router(src.seg_off, src.seg_adapter, src.num_segments, (int)m, src.table, src.num_adapters, r_max,
+                         (ChunkEntry *)src.chunks_f1, (int32_t *)src.count_f1, pl.chunk_cap_f1,
+                         (ChunkEntry *)src.chunks_bwd, (int32_t *)src.count_bwd, kBwdRows, pl.chunk_cap_bwd,
+                         nullptr, nullptr, 0, 0, stream),
+           "router launch");
+    float *spart = (float *)ws_at(workspace, pl.off_spart);
+    if (pl.f1w) {
+        HIPCHK(launch_f1w(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, S, r_max, spart,
+                          pl.KS, pl.ksl, stream), "F1 launch");
+    } else {
+        float *sout = pl.KS > 1 ? spart : S;
+        HIPCHK(launch_f1(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, sout, r_max, pl.KS,
+                         pl.ksl, stream), "F1 launch");
+        if (pl.KS > 1)
+            HIPCHK(launch_sum_partials(sout, pl.KS, (size_t)m * r_max, (size_t)m * r_max, S, "sum_s_partials",
+                                       stream), "S reduction launch");
+    }
+    return LORA_OK;
 }
 
 extern "C" lora_status multi_lora_linear_fwd(const void *X, const void *W, const lora_adapter *adapters,
@@ -475,55 +498,17 @@ extern "C" lora_status multi_lora_linear_fwd(const void *X, const void *W, const
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     REQ_PTR(workspace, 16);
 
-    AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
-    src.chunks_f1 = (const ChunkEntry *)ws_at(workspace, pl.off_t_f1);
-    src.count_f1 = (const int32_t *)ws_at(workspace, pl.off_c_f1);
-    src.chunks_bwd = (const ChunkEntry *)ws_at(workspace, pl.off_t_bwd);
-    src.count_bwd = (const int32_t *)ws_at(workspace, pl.off_c_bwd);
-    HIPCHK(launch_router(seg_off, seg_adapter, num_segments, (int)m, adapters, num_adapters, r_max,
-                         (ChunkEntry *)src.chunks_f1, (int32_t *)src.count_f1, pl.chunk_cap_f1,
-                         (ChunkEntry *)src.chunks_bwd, (int32_t *)src.count_bwd, kBwdRows, pl.chunk_cap_bwd,
-                         nullptr, nullptr, 0, 0, stream),
-           "router launch");
-    float *spart = (float *)ws_at(workspace, pl.off_spart);
-    if (pl.f1w) {
-        HIPCHK(launch_f1w(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, S, r_max, spart,
-                          pl.KS, pl.ksl, stream), "F1 launch");
-    } else {
-        float *sout = pl.KS > 1 ? spart : S;
-        HIPCHK(launch_f1(X, (int)m, (int)k, src, pl.chunk_cap_f1, seed, offset, keep_bits, sout, r_max, pl.KS,
-                         pl.ksl, stream), "F1 launch");
-        if (pl.KS > 1)
-            HIPCHK(launch_sum_partials(sout, pl.KS, (size_t)m * r_max, (size_t)m * r_max, S, "sum_s_partials",
-                                       stream), "S reduction launch");
-    }
+    const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+    CHECK(multi_forward_s(pl, X, src, m, k, seed, offset, S, keep_bits, workspace, stream));
     HIPCHK(launch_gemm(true, 1, X, W, Y, (int)m, (int)n, (int)k, S, r_max, nullptr, 0, src, stream), "F2 launch");
     return LORA_OK;
 }
 
-extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, const void *W,
-                                             const lora_adapter *adapters, int32_t num_adapters,
-                                             const int64_t *seg_off, const int32_t *seg_adapter,
-                                             int32_t num_segments, const float *S, const uint32_t *keep_bits,
-                                             int64_t m, int64_t k, int64_t n, int32_t r_max, void *dX,
-                                             void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    CHECK(check_shape(m, k, n));
-    CHECK(check_multi(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max));
-    CHECK(check_b_size(r_max, k, n));
-    REQ_PTR(W, 16);
-    if (m > 0) {
-        REQ_PTR(dY, 16);
-        REQ_PTR(X, 16);
-        REQ_PTR(S, 4);
-        REQ_PTR(keep_bits, 4);
-        REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
-    }
-    const BwdPlan pl = plan_bwd(m, k, n, r_max, true, num_segments, num_adapters);
-    if (workspace_bytes < pl.bytes)
-        return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
-    REQ_PTR(workspace, 16);
-
-    AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+// The router, B1 and B2: dA, dB, and dS (with its split for B3 where the plan has one) in the workspace.
+static lora_status multi_backward_low_rank(const BwdPlan &pl, const void *dY, const void *X, AdapterSource src,
+                                           const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                                           void *workspace, hipStream_t stream) {
+    const int32_t r_max = src.r_cap;
     src.chunks_f1 = (const ChunkEntry *)ws_at(workspace, pl.off_t_f1);
     src.count_f1 = (const int32_t *)ws_at(workspace, pl.off_c_f1);
     src.chunks_bwd = (const ChunkEntry *)ws_at(workspace, pl.off_t_bwd);
@@ -531,7 +516,7 @@ extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, cons
     src.chunks_b1 = (const ChunkEntry *)ws_at(workspace, pl.off_t_b1);
     src.count_b1 = (const int32_t *)ws_at(workspace, pl.off_c_b1);
     int32_t *aditems = (int32_t *)ws_at(workspace, pl.off_aditems);
-    HIPCHK(launch_router(seg_off, seg_adapter, num_segments, (int)m, adapters, num_adapters, r_max,
+    HIPCHK(launch_router(src.seg_off, src.seg_adapter, src.num_segments, (int)m, src.table, src.num_adapters, r_max,
                          (ChunkEntry *)src.chunks_f1, (int32_t *)src.count_f1, pl.chunk_cap_f1,
                          (ChunkEntry *)src.chunks_bwd, (int32_t *)src.count_bwd, pl.rows2, pl.chunk_cap_bwd,
                          (ChunkEntry *)src.chunks_b1, (int32_t *)src.count_b1, pl.b1.rows, pl.b1.slots, stream,
@@ -557,6 +542,51 @@ extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, cons
         HIPCHK(launch_grad_reduce(1, dApart, (int)m, (int)k, (int)n, r_max, src, pl.rows2, chunks, stream),
                "dA reduction launch");
     }
+    return LORA_OK;
+}
+
+namespace lora {
+lora_status multi_forward_s_only(const void *X, const AdapterSource &src, int64_t m, int64_t k, uint64_t seed,
+                                 uint64_t offset, float *S, uint32_t *keep_bits, void *workspace, hipStream_t stream) {
+    return multi_forward_s(plan_fwd(m, k, src.r_cap, true, src.num_segments), X, src, m, k, seed, offset, S, keep_bits,
+                           workspace, stream);
+}
+
+lora_status multi_backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+                                         const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *workspace,
+                                         const float **dS_out, hipStream_t stream) {
+    const BwdPlan pl = plan_bwd(m, k, n, src.r_cap, true, src.num_segments, src.num_adapters);
+    *dS_out = (const float *)ws_at(workspace, pl.off_ds);
+    return multi_backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, workspace, stream);
+}
+}  // namespace lora
+
+extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, const void *W,
+                                             const lora_adapter *adapters, int32_t num_adapters,
+                                             const int64_t *seg_off, const int32_t *seg_adapter,
+                                             int32_t num_segments, const float *S, const uint32_t *keep_bits,
+                                             int64_t m, int64_t k, int64_t n, int32_t r_max, void *dX,
+                                             void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_multi(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max));
+    CHECK(check_b_size(r_max, k, n));
+    REQ_PTR(W, 16);
+    if (m > 0) {
+        REQ_PTR(dY, 16);
+        REQ_PTR(X, 16);
+        REQ_PTR(S, 4);
+        REQ_PTR(keep_bits, 4);
+        REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
+    }
+    const BwdPlan pl = plan_bwd(m, k, n, r_max, true, num_segments, num_adapters);
+    if (workspace_bytes < pl.bytes)
+        return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
+    REQ_PTR(workspace, 16);
+
+    const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+    CHECK(multi_backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, workspace, stream));
+    const float *dS = (const float *)ws_at(workspace, pl.off_ds);
+    const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, r_max, keep_bits, (int)((k + 31) / 32),
                            src, stream, dss, pl.dss_ld), "B3 launch");

@@ -88,6 +88,33 @@ struct AdapterSource {
     const int32_t *count_b1;
 };
 
+inline AdapterSource single_source(const void *A, const void *B, void *dA, void *dB, int32_t r, float alpha, float p) {
+    AdapterSource s{};
+    s.A = A;
+    s.B = B;
+    s.dA = dA;
+    s.dB = dB;
+    s.r = r;
+    s.alpha = alpha;
+    s.p = p;
+    s.table = nullptr;
+    s.r_cap = r;
+    return s;
+}
+
+inline AdapterSource multi_source(const lora_adapter *adapters, int32_t nad, const int64_t *seg_off,
+                                  const int32_t *seg_adapter, int32_t nseg, int32_t r_max) {
+    AdapterSource s{};
+    s.table = adapters;
+    s.num_adapters = nad;
+    s.r_cap = r_max;
+    s.seg_off = seg_off;
+    s.seg_adapter = seg_adapter;
+    s.num_segments = nseg;
+    s.r = r_max;
+    return s;
+}
+
 // Which router table a kernel's work items come from.
 enum WorkTable { kTabF1 = 0, kTabBwd = 1, kTabB1 = 2 };
 
@@ -264,11 +291,43 @@ struct MxGemmPlan {
     int SK, jobs;          // > 0: the product's launch also forms S = X A, in SK partial sums, by `jobs` work-groups
     size_t spart_bytes;
 };
-// r == 0: no adapter; dropout: S comes from F1.
-MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout);
-// S: written where the plan forms it (SK > 0), else read (r > 0).
+// r == 0: no adapter.  kMxDropout: S comes from F1; kMxMixed: so it does, and the
+// partial sums go to launch_mxfp4_join.
+enum MxForm { kMxPlain = 0, kMxDropout = 1, kMxMixed = 2 };
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form);
+// S: written where the plan forms it (SK > 0), else read (r > 0).  Y NULL: the
+// product's partial sums alone (kMxMixed, with r = 0 here).
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
                              int n, const void *A, const void *B, int r, float alpha, float *S, void *Y, float *part,
                              float *spart, hipStream_t stream);
+
+// dX = dY W'^T (+ scale keep.(dS A^T)) straight from the packed weight
+// (mxfp4_gemm_t.hip).
+struct MxGemmTPlan {
+    int kind;  // tile shape; 0: not for this shape
+    int tiles_m, tiles_k, KS, per;
+    bool finish;
+    size_t part_bytes;
+};
+MxGemmTPlan mx_gemm_t_plan(int64_t m, int64_t k, int64_t n, int r);
+hipError_t launch_mxfp4_gemm_t(const MxGemmTPlan &pl, const void *dY, const void *codes, const void *scales, int m, int k,
+                               int n, void *dX, float *part, hipStream_t stream);
+
+// The partial sums of either product ([KS][m][n]) and the adapters' term
+// (mxfp4_join.hip): up for Y, with segments only; otherwise for dX.
+hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, const float *S, int RS,
+                             const uint32_t *keep, const AdapterSource &src, void *Y, hipStream_t stream);
+
+// The layers' low-rank steps alone (api.cpp), in a workspace of the bf16 layer's
+// size.  B1 and B2 write dA, dB and dS (m x r fp32, in the workspace, where
+// *dS_out points afterwards).
+lora_status backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+                                   const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r,
+                                   void *workspace, const float **dS_out, hipStream_t stream);
+lora_status multi_forward_s_only(const void *X, const AdapterSource &src, int64_t m, int64_t k, uint64_t seed,
+                                 uint64_t offset, float *S, uint32_t *keep_bits, void *workspace, hipStream_t stream);
+lora_status multi_backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+                                         const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *workspace,
+                                         const float **dS_out, hipStream_t stream);
 
 }  // namespace lora

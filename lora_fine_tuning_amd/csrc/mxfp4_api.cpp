@@ -58,12 +58,14 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
 
 extern "C" size_t lora_mxfp4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n) {
     if (!sizes_ok(m, k, n) || m == 0) return 0;
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, false);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, kMxPlain);
     return pl.kind ? pl.part_bytes : expanded_bytes(k, n);
 }
 
 extern "C" size_t lora_mxfp4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n) {
-    return sizes_ok(m, k, n) && m > 0 ? expanded_bytes(k, n) : 0;
+    if (!sizes_ok(m, k, n) || m == 0) return 0;
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, 0);
+    return pl.kind ? pl.part_bytes : expanded_bytes(k, n);
 }
 
 extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t m,
@@ -75,7 +77,7 @@ extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, c
     REQ_PTR(X, 16);
     REQ_PTR(Y, 16);
     REQ_WORKSPACE(lora_mxfp4_frozen_fwd_workspace_size(m, k, n));
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, false);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, kMxPlain);
     if (pl.kind) {
         HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, nullptr, Y,
                                  (float *)workspace, nullptr, stream), "MXFP4 product launch");
@@ -94,13 +96,22 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
     REQ_PTR(dY, 16);
     REQ_PTR(dX, 16);
     REQ_WORKSPACE(lora_mxfp4_frozen_bwd_workspace_size(m, k, n));
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, 0);
+    if (pl.kind) {
+        HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, dX, (float *)workspace, stream),
+               "MXFP4 transposed product launch");
+        if (pl.finish)
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, nullptr, 0, nullptr,
+                                     AdapterSource{}, dX, stream), "MXFP4 sum launch");
+        return LORA_OK;
+    }
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_frozen_bwd(dY, workspace, m, k, n, dX, stream);
 }
 
 extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, false);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, kMxPlain);
     if (!pl.kind) return expanded_bytes(k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
     // (the plans with and without dropout differ in where S is formed only)
     return align_up(pl.part_bytes) + std::max(pl.spart_bytes, lora_linear_fwd_workspace_size(m, k, n, r));
@@ -108,7 +119,8 @@ extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int
 
 extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || r < 1) return 0;
-    return expanded_bytes(k, n) + lora_linear_bwd_workspace_size(m, k, n, r);
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) + lora_linear_bwd_workspace_size(m, k, n, r);
 }
 
 extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales, const void *A,
@@ -131,7 +143,7 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
     REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     REQ_WORKSPACE(lora_mxfp4_linear_fwd_workspace_size(m, k, n, r));
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, p != 0.0f);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, p != 0.0f ? kMxDropout : kMxPlain);
     if (pl.kind) {
         char *rest = ws_at(workspace, align_up(pl.part_bytes));
         if (pl.SK == 0) CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, rest, stream));
@@ -168,6 +180,20 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
         REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     }
     REQ_WORKSPACE(lora_mxfp4_linear_bwd_workspace_size(m, k, n, r));
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
+    if (pl.kind) {
+        const float *dS = nullptr;
+        const AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
+        CHECK(backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, r, ws_at(workspace, align_up(pl.part_bytes)), &dS,
+                                     stream));
+        if (dX != nullptr) {
+            HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
+                   "MXFP4 transposed product launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, dS, r,
+                                     p == 0.0f ? nullptr : keep_bits, src, dX, stream), "MXFP4 sum launch");
+        }
+        return LORA_OK;
+    }
     const size_t w = expanded_bytes(k, n);
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
@@ -178,13 +204,17 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
 extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                       int32_t num_adapters, int32_t num_segments) {
     if (!sizes_ok(m, k, n) || m == 0 || r_max < 1) return 0;
-    return expanded_bytes(k, n) + multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed);
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) +
+           multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
 }
 
 extern "C" size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                       int32_t num_adapters, int32_t num_segments) {
     if (!sizes_ok(m, k, n) || r_max < 1) return 0;
-    return expanded_bytes(k, n) + multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r_max);
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) +
+           multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
 }
 
 extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales,
@@ -196,7 +226,6 @@ extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *co
                                                    size_t workspace_bytes, hipStream_t stream) {
     CHECK(check_shape(m, k, n));
     CHECK(check_weight(k, n, codes, scales));
-    const size_t w = expanded_bytes(k, n);
     // everything else is checked before the weight is expanded, by the call on no rows
     CHECK(multi_lora_linear_fwd(X, codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max,
                                 seed, offset, Y, S, keep_bits, workspace, workspace_bytes, stream));
@@ -206,6 +235,18 @@ extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *co
     REQ_PTR(S, 4);
     REQ_PTR(keep_bits, 4);
     REQ_WORKSPACE(multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments));
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed);
+    if (pl.kind) {
+        const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+        CHECK(multi_forward_s_only(X, src, m, k, seed, offset, S, keep_bits, ws_at(workspace, align_up(pl.part_bytes)),
+                                   stream));
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, nullptr, nullptr,
+                                 (float *)workspace, nullptr, stream), "MXFP4 product launch");
+        HIPCHK(launch_mxfp4_join(true, (const float *)workspace, pl.KS, (int)m, (int)n, S, r_max, nullptr, src, Y, stream),
+               "MXFP4 sum launch");
+        return LORA_OK;
+    }
+    const size_t w = expanded_bytes(k, n);
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return multi_lora_linear_fwd(X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, m, k, n,
                                  r_max, seed, offset, Y, S, keep_bits, ws_at(workspace, w), workspace_bytes - w,
@@ -232,6 +273,20 @@ extern "C" lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X
         REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
     }
     REQ_WORKSPACE(multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments));
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r_max);
+    if (pl.kind) {
+        const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+        const float *dS = nullptr;
+        CHECK(multi_backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, ws_at(workspace, align_up(pl.part_bytes)),
+                                           &dS, stream));
+        if (dX != nullptr) {
+            HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
+                   "MXFP4 transposed product launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, dS, r_max, keep_bits, src, dX,
+                                     stream), "MXFP4 sum launch");
+        }
+        return LORA_OK;
+    }
     const size_t w = expanded_bytes(k, n);
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");

@@ -27,34 +27,15 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
-#include "device_common.hpp"
 #include "launch.hpp"
+#include "mxfp4.hpp"
 
 namespace lora {
 
 namespace {
-
-// Vector memory down to N loads in flight, and no LDS read in flight.
-template <int N>
-__device__ __forceinline__ void wait_vmcnt_lds() {
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
-}
-
-// dma16 with a scalar byte offset added to the address; a lane whose own
-// offset is kOOB reads zeros whatever it is.
-__device__ __forceinline__ void dma16_at(sgpr4_t desc, uint32_t voff, uint32_t soff, uint32_t lds_base) {
-    uint32_t saved_m0;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %4\n\t"
-        "buffer_load_dwordx4 %1, %2, %3 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved_m0)
-        : "v"(voff), "s"(desc), "s"(soff), "s"(lds_base)
-        : "memory");
-}
 
 struct MxGemmParams {
     const uint16_t *X;
@@ -75,21 +56,6 @@ struct MxGemmParams {
 };
 
 constexpr int kSK = 1024;  // k of one partial sum of S
-
-__device__ __forceinline__ float mx_scale(uint32_t s) {
-    return __uint_as_float(max(s << 23, 0x00400000u));
-}
-
-// Byte e of a dword of codes -> two bf16; all four -> an MFMA operand.
-__device__ __forceinline__ uint32_t mx_pair(uint32_t w, float scale, int e) {
-    return __builtin_bit_cast(uint32_t, e == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)
-                                        : e == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)
-                                        : e == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)
-                                                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
-}
-__device__ __forceinline__ uint4 mx_frag(uint32_t w, float scale) {
-    return make_uint4(mx_pair(w, scale, 0), mx_pair(w, scale, 1), mx_pair(w, scale, 2), mx_pair(w, scale, 3));
-}
 
 template <int WM_, int WN_, int WK_, int MB_, int NB_, int XR_, int NS_>
 struct MxTile {
@@ -186,10 +152,7 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
         if (id < P.jobs) return s_job<T>(P, id, mx_smem);
         id -= P.jobs;
     }
-    {
-        const int xcd = id & 7, local = id >> 3, each = total >> 3, rem = total & 7;
-        id = xcd * each + min(xcd, rem) + local;
-    }
+    id = xcd_order(id, total);
     int tm = 0, tn = id, ks = 0;  // (the divisions are skipped where there is nothing to divide)
     if (P.tiles_m > 1) tn = id / P.tiles_m, tm = id - tn * P.tiles_m;
     if (P.KS > 1) ks = tn / P.tiles_n, tn -= ks * P.tiles_n;
@@ -428,8 +391,6 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
         for (int b = 0; b < NB; ++b) {
             const int col = n0 + (wn * NB + b) * 16 + 4 * lg;
             const uint32_t at = row < (uint32_t)rows && col < P.N ? row * (uint32_t)P.N + (uint32_t)col : kOOB / 4;
-            typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
-            typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
             if (direct)
                 __builtin_amdgcn_raw_buffer_store_b64(
                     u32x2_t{pack_bf16x2(acc[a][b][0], acc[a][b][1]), pack_bf16x2(acc[a][b][2], acc[a][b][3])}, rY, at * 2u, 0, 0);
@@ -568,8 +529,9 @@ __global__ __launch_bounds__(256) void mxfp4_finish_kernel(MxFinishParams P) {
 
 template <class T>
 hipError_t launch_t(const MxGemmParams &P, hipStream_t stream) {
-    if (T::LDS > 64 * 1024)
-        (void)hipFuncSetAttribute((const void *)mxfp4_gemm_kernel<T>, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds((const void *)mxfp4_gemm_kernel<T>, T::LDS, done);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((mxfp4_gemm_kernel<T>), dim3((unsigned)(P.tiles_m * P.tiles_n * P.KS + P.jobs)), dim3(64 * T::NW),
                        T::LDS, stream, P);
     return hipGetLastError();
@@ -612,7 +574,7 @@ const MxKind kKinds[] = {
 // Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 17.1
 // (18), 300 x 14336 x 4096 45 (46), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
 // (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (188; packed 245).
-MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout) {
+static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form) {
     MxGemmPlan best{};
     // (a tile's offsets stay below 2^31 within these)
     if (m <= 0 || k > (1 << 20) || n > (1 << 21) || m > (1 << 19)) return best;
@@ -628,7 +590,7 @@ MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout) {
         p.tiles_n = (int)cdiv(n, K.tn);
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, stages = cdiv(k, K.kw);
         if (tiles > (1 << 20)) continue;
-        if (r > 0 && K.ranks > 0 && !dropout && m <= 128) {
+        if (r > 0 && K.ranks > 0 && form == kMxPlain && m <= 128) {
             p.SK = (int)cdiv(k, kSK);
             p.jobs = (int)cdiv(p.SK * p.tiles_m * cdiv(r, K.ranks), 8) * 8;
             p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
@@ -637,7 +599,7 @@ MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout) {
             p.per = (int)cdiv(stages, want);
             p.KS = (int)cdiv(stages, p.per);
             if (p.KS != want) continue;
-            p.finish = p.KS > 1 || (r > 0 && K.ranks > 0);
+            p.finish = p.KS > 1 || (r > 0 && (K.ranks > 0 || form == kMxMixed));
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
             const int64_t groups = tiles * p.KS + p.jobs, slots = 256 * K.share;
             double t = (double)cdiv(groups, slots) * (p.per * K.stage + 1.0);
@@ -650,6 +612,10 @@ MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, bool dropout) {
         }
     }
     return best;
+}
+
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form) {
+    return remembered<MxGemmPlan>(m, k, n, 4 * r + (int)form, [&] { return find_plan(m, k, n, r, form); });
 }
 
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
@@ -682,7 +648,7 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     int slot = prof_begin("mxfp4_gemm", stream);
     const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
-    if (e != hipSuccess || !pl.finish) return e;
+    if (e != hipSuccess || !pl.finish || Y == nullptr) return e;
     const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)B, alpha, S, (uint16_t *)Y};
     slot = prof_begin("mxfp4_finish", stream);
     hipLaunchKernelGGL(mxfp4_finish_kernel, dim3((unsigned)((n + 127) / 128), (unsigned)((m + 15) / 16)), dim3(256), 0, stream,

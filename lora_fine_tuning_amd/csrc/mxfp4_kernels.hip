@@ -16,8 +16,8 @@
 // Padding columns and rows hold zero codes, padding blocks the scale byte 127.
 #include <hip/hip_runtime.h>
 
-#include "device_common.hpp"
 #include "launch.hpp"
+#include "mxfp4.hpp"
 
 namespace lora {
 
@@ -25,18 +25,6 @@ namespace {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
-
-// The float 2^(s - 127) of a scale byte: s = 0 is the subnormal 2^-127, and
-// s = 255 an infinity (the conversions then give NaN for every code).
-__device__ __forceinline__ float mx_scale(uint32_t s) {
-    return __uint_as_float(max(s << 23, 0x00400000u));
-}
-
-// Two codes (byte B of w) -> two bf16, exact.
-template <int B>
-__device__ __forceinline__ uint32_t mx_pair(uint32_t w, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, B));
-}
 
 // Two bf16 over the scale, rounded to the nearest code (ties to the even one,
 // magnitudes past 6 to 6), into byte B of `old`.
@@ -136,10 +124,10 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint8_t *co
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const uint32_t w = d == 0 ? q[c].x : d == 1 ? q[c].y : d == 2 ? q[c].z : q[c].w;
-                p[c][0] = mx_pair<0>(w, sc[c]);
-                p[c][1] = mx_pair<1>(w, sc[c]);
-                p[c][2] = mx_pair<2>(w, sc[c]);
-                p[c][3] = mx_pair<3>(w, sc[c]);
+                p[c][0] = mx_pair(w, sc[c], 0);
+                p[c][1] = mx_pair(w, sc[c], 1);
+                p[c][2] = mx_pair(w, sc[c], 2);
+                p[c][3] = mx_pair(w, sc[c], 3);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {

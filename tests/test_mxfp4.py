@@ -23,7 +23,7 @@ import torch
 import lora_fine_tuning_amd as lf
 import oracle
 from lora_fine_tuning_amd import _lib
-from parity import bf16_randn, log
+from parity import bf16_randn, log, offset_view
 
 GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
 BF, HALF = 2.0 ** -8, 2.0 ** -24
@@ -367,12 +367,26 @@ def test_frozen_forward_and_backward(m, k, n):
     near("dX", dXb[:m], dy @ W.T, n * HALF * (np.abs(dy) @ np.abs(W).T))
 
 
+# sums split over many work-groups, and every number of row tiles, in both directions
+DEEP = [(1, 4096, 4104), (9, 1288, 8200), (24, 4096, 2048), (70, 2568, 4096), (128, 1024, 6152), (400, 776, 2056), (1100, 1288, 1032)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n", DEEP)
+def test_frozen_deep(m, k, n):
+    test_frozen_forward_and_backward(m, k, n)
+
+
 LAYER = [
     # m, k, n, r, alpha, p
     (1, 4096, 520, 16, 2.0, 0.0), (1, 264, 136, 5, -0.7, 0.0), (1, 72, 40, 1, 2.0, 0.3), (2, 1032, 264, 64, 0.5, 0.0),
     (5, 2056, 136, 200, 1.0, 0.0), (16, 520, 1032, 8, 2.0, 0.1), (17, 136, 72, 33, 1.0, 0.0), (40, 1288, 264, 128, 0.5, 0.0),
     (48, 392, 520, 256, 1.0, 0.05), (63, 264, 264, 13, 2.0, 0.0), (100, 904, 392, 32, 2.0, 0.2), (130, 648, 520, 100, 1.0, 0.0),
     (333, 1032, 776, 5, 2.0, 0.2), (520, 400, 264, 130, 0.5, 0.1), (700, 264, 1032, 16, 2.0, 0.1),
+    # S formed beside the product over several row tiles, at odd ranks
+    (65, 1032, 264, 7, 1.0, 0.0), (100, 4104, 136, 31, -2.0, 0.0), (128, 2056, 520, 66, 0.5, 0.0), (128, 264, 72, 255, 1.0, 0.0),
+    # more rows, and a contraction split over work-groups in both directions
+    (1030, 520, 136, 16, 2.0, 0.0), (2, 8200, 4104, 16, 2.0, 0.1), (30, 4104, 8200, 12, 2.0, 0.0),
 ]
 
 
@@ -423,6 +437,25 @@ def test_layer_forward_and_backward(case):
     # without an input gradient the others stay the same
     none, dA2, dB2 = lf.lora_mxfp4_linear_bwd(dY.cuda(), Xd, W4, Ad, Bd, S, keep, alpha, p, want_dX=False)
     assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,r,p", [(1, 16, 0.0), (33, 9, 0.0), (33, 64, 0.1), (300, 40, 0.1), (700, 16, 0.0)])
+def test_unaligned_adapter_gives_the_same(m, r, p):
+    # A and B one element past a 16-byte boundary: the same sums in the same order
+    k, n = 1032, 520
+    X, W4, W, A, B, dY = layer_case(m, k, n, r, seed=31)
+    X, dY = X.cuda(), dY.cuda()
+
+    def run(A, B):
+        Y, S, keep = lf.lora_mxfp4_linear_fwd(X, W4, A, B, 2.0, p, 3, 0)
+        return (Y, S, *lf.lora_mxfp4_linear_bwd(dY, X, W4, A, B, S, keep, 2.0, p))
+
+    Y, S, dX, dA, dB = run(offset_view(A), offset_view(B))
+    want, slack = layer_reference(X.cpu(), W, A, B, dY.cpu(), 2.0, p, 3, 0)
+    for name, t in (("Y", Y), ("dX", dX), ("dA", dA), ("dB", dB)):
+        near(name, t, want[name], slack[name])
+    assert (np.abs(f64(S) - want["S"]) <= slack["S"] + 1e-30).all()
 
 
 @pytest.mark.gpu
@@ -495,6 +528,56 @@ def test_mixed_matches_definition(m):
     assert used == set(range(4))  # (an adapter with no rows gets zeros: its reference is an empty sum)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [5, 77, 300])
+def test_mixed_short_segments(m):
+    # many segments within one tile of rows, empty ones among them, ranks 1 to 256, unaligned matrices;
+    # an infinity in one adapter's B and A shows in its own rows only
+    k, n, ranks = 392, 136, [1, 256, 33, 7, 64]
+    alphas, ps = [2.0, 0.25, 0.5, -1.0, 1.0], [0.0, 0.1, 0.2, 0.0, 0.05]
+    g = torch.Generator().manual_seed(m + 1)
+    X, W4, W, _, _, dY = layer_case(m, k, n, 8, seed=160 + m)
+    As = [bf16_randn((k, r), k ** -0.5, g) for r in ranks]
+    Bs = [bf16_randn((r, n), 0.02 ** 0.5, g) for r in ranks]
+    cuts = torch.randint(0, m + 1, (24,), generator=g).sort().values.tolist()
+    seg_off = [0, *cuts, m]
+    seg_ad = torch.randint(0, 5, (len(seg_off) - 1,), generator=g).tolist()
+    so = torch.tensor(seg_off, dtype=torch.int64, device="cuda")
+    sa = torch.tensor(seg_ad, dtype=torch.int32, device="cuda")
+    Ad, Bd = [offset_view(a) for a in As], [offset_view(b) for b in Bs]
+    dAs, dBs = [torch.zeros_like(a) for a in Ad], [torch.zeros_like(b) for b in Bd]
+    table = lf.adapter_table(Ad, Bd, alphas, ps, dAs, dBs)
+    Xd, dYd = X.cuda(), dY.cuda()
+
+    def run():
+        Yb = torch.full((m + 2, n), 5.0, dtype=torch.bfloat16, device="cuda")
+        dXb = torch.full((m + 2, k), 5.0, dtype=torch.bfloat16, device="cuda")
+        _, S, keep = lf.multi_lora_mxfp4_linear_fwd(Xd, W4, table, 5, so, sa, 256, 3, 8, Y=Yb[:m])
+        lf.multi_lora_mxfp4_linear_bwd(dYd, Xd, W4, table, 5, so, sa, S, keep, 256, dX=dXb[:m])
+        torch.cuda.synchronize()
+        assert (Yb[m:] == 5).all() and (dXb[m:] == 5).all()
+        return Yb[:m], dXb[:m]
+
+    Y, dX = run()
+    for s, a in enumerate(seg_ad):
+        lo, hi = seg_off[s], seg_off[s + 1]
+        if hi > lo:
+            want, slack = layer_reference(X[lo:hi], W, As[a], Bs[a], dY[lo:hi], alphas[a], ps[a], 3, 8 + lo * k)
+            near(f"Y[{s}]", Y[lo:hi], want["Y"], slack["Y"])
+            near(f"dX[{s}]", dX[lo:hi], want["dX"], slack["dX"])
+    Y, dX = Y.clone(), dX.clone()
+    hit = seg_ad[max(range(len(seg_ad)), key=lambda s: seg_off[s + 1] - seg_off[s])]
+    Ad[hit][3, 0] = float("inf")
+    Bd[hit][0, 5] = float("inf")
+    Y2, dX2 = run()
+    other = torch.ones(m, dtype=torch.bool)
+    for s, a in enumerate(seg_ad):
+        if a == hit:
+            other[seg_off[s]:seg_off[s + 1]] = False
+    assert torch.equal(Y2[other], Y[other]) and torch.equal(dX2[other], dX[other])
+    assert not torch.isfinite(Y2[~other].float()).all()
+
+
 # ---- use: streams, graphs, autograd ---------------------------------------------------------------
 
 @pytest.mark.gpu
@@ -544,6 +627,53 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in got:
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 50, 600])
+def test_captured_mixed_layers_side_by_side(m):
+    # two graphs of the same shapes, replayed at once on two streams, with eager calls between
+    k, n, ranks = 520, 264, [16, 40]
+    g = torch.Generator().manual_seed(m)
+    _, W4, _, _, _, _ = layer_case(m, k, n, 8, seed=12)
+    so = torch.tensor([0, m // 2, m], dtype=torch.int64, device="cuda")
+    sa = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    sides = []
+    for i in range(2):
+        As = [bf16_randn((k, r), k ** -0.5, g).cuda() for r in ranks]
+        Bs = [bf16_randn((r, n), 0.02 ** 0.5, g).cuda() for r in ranks]
+        dAs, dBs = [torch.zeros_like(a) for a in As], [torch.zeros_like(b) for b in Bs]
+        table = lf.adapter_table(As, Bs, [2.0, 0.5], [0.1, 0.0], dAs, dBs)
+        X, dY = bf16_randn((m, k), 1.0, g).cuda(), bf16_randn((m, n), 1.0, g).cuda()
+
+        def run(X=X, dY=dY, table=table, dAs=dAs, dBs=dBs, As=As, Bs=Bs):
+            Y, S, keep = lf.multi_lora_mxfp4_linear_fwd(X, W4, table, 2, so, sa, 40, 3, 8)
+            dX = lf.multi_lora_mxfp4_linear_bwd(dY, X, W4, table, 2, so, sa, S, keep, 40)
+            return Y, S, dX, *dAs, *dBs
+
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        sides.append((run, stream, graph, out, X, dY))
+    for rep in range(3):
+        for _, _, _, _, X, dY in sides:
+            X.copy_(bf16_randn(X.shape, 1.0, g))
+            dY.copy_(bf16_randn(dY.shape, 1.0, g))
+        torch.cuda.synchronize()
+        for _, stream, graph, _, _, _ in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for run, _, _, out, _, _ in sides:
+            got = [t.clone() for t in out]
+            for i, (a, b) in enumerate(zip(got, run())):
+                assert torch.equal(a, b), f"replay {rep}: output {i}"
+            torch.cuda.synchronize()
 
 
 @pytest.mark.gpu
