@@ -224,9 +224,11 @@ class LoraAdamW(torch.optim.Optimizer):
             tables[key] = table
             return table
         rec = table.records
-        for p in ps:
+        for p, g, st, n in zip(ps, grads, states, rec[:, _N].tolist()):
             if not p.is_contiguous():
                 raise ValueError("parameters must be contiguous")
+            if not n == p.numel() == g.numel() == st["m"].numel():
+                raise ValueError(f"a parameter had {n} values when its moments were made, now {p.numel()}")
         rec[:, _PARAM] = [p.data_ptr() for p in ps]
         rec[:, _GRAD] = [g.data_ptr() for g in grads]
         for name, col in (("m", _M), ("v", _V), ("m_scale", _M_SCALE), ("v_scale", _V_SCALE), ("master", _MASTER)):

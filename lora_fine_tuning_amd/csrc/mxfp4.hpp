@@ -66,6 +66,17 @@ inline hipError_t allow_lds(const void *fn, size_t bytes, std::atomic<uint64_t> 
     return hipSuccess;
 }
 
+// Microseconds of expanding a weight of `values` and of the bf16 product over it,
+// of m x out with a contraction of `depth`: two launches of 3 us, 2.53 bytes a
+// value at 6 TB/s, and rounds of 256 256 x 256 tiles that take 1.4 us for 64 of
+// the depth (1.1 where half of the CUs or fewer have one).  Measured, model in
+// brackets: 1 x 4096 x 4096 85 (84), 2000 x 4096 x 4096 86 (84), 8192 x 4096 x 4096
+// 201 (192), 16 x 4096 x 14336 (dX) 265 (277), 2000 x 8192 x 28672 (dX) 738 (732).
+inline double expanded_us(int64_t m, int64_t out, int64_t depth, double values) {
+    const int64_t tiles = ((m + 255) / 256) * ((out + 255) / 256);
+    return 6.0 + values * 2.53 / 6e6 + (double)((tiles + 255) / 256 * ((depth + 63) / 64)) * (tiles <= 128 ? 1.1 : 1.4);
+}
+
 // `find`'s answers for the shapes a thread asked for last (a plan takes a few
 // microseconds to find, a call asks twice, and a program's shapes come back).
 template <class Plan, class Find>

@@ -569,8 +569,7 @@ const MxKind kKinds[] = {
 // expanding the weight for the bf16 product, by a model of their times:
 //   shape:  3.5 us + rounds (stages x stage time + 1 us), at least the weight's
 //           bytes at 6 TB/s; a finishing launch 3.5 us and its partial sums at 8 TB/s
-//   expand: 2.5 us + 2.53 bytes an element at 6 TB/s + 3.5 us + rounds of 256
-//           256 x 256 tiles (k / 64 x 1.35 us)
+//   expand: expanded_us
 // Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 17.1
 // (18), 300 x 14336 x 4096 45 (46), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
 // (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (188; packed 245).
@@ -580,7 +579,7 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form)
     if (m <= 0 || k > (1 << 20) || n > (1 << 21) || m > (1 << 19)) return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const double weight = (double)k * n;
-    double least = 6.0 + weight * 2.53 / 6e6 + (double)cdiv(cdiv(m, 256) * cdiv(n, 256), 256) * (double)cdiv(k, 64) * 1.35;
+    double least = expanded_us(m, n, k, weight);
     for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
         const MxKind &K = kKinds[kind - 1];
         if ((kind <= 2 && m > 4) || (kind <= 4 && m > 16)) continue;  // (4 rows in LDS; columns too narrow)

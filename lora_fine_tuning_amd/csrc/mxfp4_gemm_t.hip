@@ -297,7 +297,7 @@ static MxGemmTPlan find_plan(int64_t m, int64_t k, int64_t n, int r) {
         return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const double weight = (double)k * n;
-    double least = 6.0 + weight * 2.53 / 6e6 + (double)cdiv(cdiv(m, 256) * cdiv(k, 256), 256) * (double)cdiv(n, 64) * 1.35;
+    double least = expanded_us(m, k, n, weight);
     for (int kind = 1; kind <= (int)(sizeof(kKindsT) / sizeof(kKindsT[0])); ++kind) {
         const MxKindT &K = kKindsT[kind - 1];
         MxGemmTPlan p{};
