@@ -78,8 +78,8 @@ struct MxTile {
 // load of a wave before its first use; the waves are added in LDS in wave order.
 template <class T>
 __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *smem) {
-    constexpr int MB = T::MB, RT = MB == 4 ? 2 : 4;
-    static_assert(T::NW == 8 && T::WM == 1 && 8 * MB * RT * 1024 <= T::LDS, "no room for the partial sums");
+    constexpr int MB = T::MB, RT = MB > 2 ? 2 : 4;
+    static_assert(T::NW == 8 && T::WM == 1 && MB * RT <= 8 && 8 * MB * RT * 1024 <= T::LDS, "no room for the partial sums");
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int ks = job % P.SK, m0 = job / P.SK % P.tiles_m * T::TM, r0 = job / (P.SK * P.tiles_m) * 16 * RT;
@@ -548,7 +548,7 @@ struct MxKind {
 };
 template <class T>
 constexpr MxKind kind_of(float stage) {
-    return MxKind{launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? (T::MB == 4 ? 32 : 64) : 0, stage,
+    return MxKind{launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? (T::MB > 2 ? 32 : 64) : 0, stage,
                   std::min(160 * 1024 / T::LDS, 4)};
 }
 const MxKind kKinds[] = {
@@ -558,6 +558,7 @@ const MxKind kKinds[] = {
     kind_of<MxTile<1, 2, 4, 1, 2, 16, 3>>(0.53f),  // 16 x 64
     kind_of<MxTile<1, 2, 4, 2, 1, 32, 3>>(0.61f),  // 32 x 32
     kind_of<MxTile<1, 4, 2, 2, 2, 32, 3>>(0.67f),  // 32 x 128
+    kind_of<MxTile<1, 4, 2, 3, 2, 48, 3>>(0.78f),  // 48 x 128
     kind_of<MxTile<1, 4, 2, 4, 2, 64, 3>>(1.00f),  // 64 x 128
     kind_of<MxTile<2, 4, 1, 2, 4, 64, 3>>(0.98f),  // 64 x 256
     kind_of<MxTile<2, 4, 1, 4, 4, 128, 3>>(1.65f), // 128 x 256
@@ -570,9 +571,9 @@ const MxKind kKinds[] = {
 //   shape:  3.5 us + rounds (stages x stage time + 1 us), at least the weight's
 //           bytes at 6 TB/s; a finishing launch 3.5 us and its partial sums at 8 TB/s
 //   expand: expanded_us
-// Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 17.1
-// (18), 300 x 14336 x 4096 45 (46), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
-// (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (188; packed 245).
+// Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 16.5
+// (16), 300 x 14336 x 4096 45 (48), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
+// (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (192; packed 245).
 static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form) {
     MxGemmPlan best{};
     // (a tile's offsets stay below 2^31 within these)

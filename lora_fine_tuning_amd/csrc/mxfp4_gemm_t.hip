@@ -282,6 +282,7 @@ constexpr MxKindT kind_t(float stage) {
 const MxKindT kKindsT[] = {
     kind_t<MxTileT<1, 2, 1, 16, 3>>(1.13f),   // 16 rows
     kind_t<MxTileT<1, 2, 2, 32, 3>>(1.27f),   // 32
+    kind_t<MxTileT<1, 2, 3, 48, 3>>(1.45f),   // 48
     kind_t<MxTileT<1, 2, 4, 64, 2>>(1.70f),   // 64
     kind_t<MxTileT<2, 1, 4, 128, 2>>(1.60f),  // 128
 };
