@@ -60,6 +60,12 @@ def parse():
     ap.add_argument("--hbm", action="store_true",
                     help="instead of the headline step: the practical HBM ceiling of this part (a 2 GiB "
                          "device copy and a 4 GiB read-only reduction, median of flushed trials)")
+    ap.add_argument("--mxfp4", action="store_true",
+                    help="instead of the headline step: the layer over a frozen weight in MXFP4 against the "
+                         "same layer over the bf16 weight, from one token to a training batch")
+    ap.add_argument("--adamw", action="store_true",
+                    help="instead of the headline step: the AdamW step over a model's adapter tensors, with "
+                         "moments in 32 and in 8 bits")
     ap.add_argument("--concat", action="store_true",
                     help="instead of the headline step: the forward at p = 0, concatenated [W | A] "
                          "(one GEMM launch) against the split path and the frozen GEMM")
@@ -224,6 +230,107 @@ def dora_report(args):
                                     "sample": f"{len(cols)} of {n} columns"}
         print(json.dumps(line), flush=True)
         del W, A, B, ws
+
+
+def mxfp4_report(args):
+    """The frozen weight in MXFP4: packing 28672 x 8192, then the layer (r 16, no
+    dropout for the forward alone, p 0.1 for forward and backward) over the packed
+    and over the bf16 weight, k = 4096 -> n = 14336, from 1 to 8192 tokens.  Times
+    are medians of event-timed trials after a cache flush, so the weight comes from
+    HBM, as it does between the other layers of a model; two event records and the
+    launches of a cold call are part of them."""
+    import torch
+
+    import lora_fine_tuning_amd as lf
+
+    lf.load()
+    timer = Timer(torch, torch.cuda.current_stream())
+
+    def timed(fn):
+        return timer.median(fn, args.steps, args.warmup)
+
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def rand(*shape, scale):
+        return (torch.randn(*shape, device="cuda", generator=g) * scale).bfloat16()
+
+    k, n = 28672, 8192
+    W = rand(k, n, scale=k ** -0.5)
+    W4 = lf.lora_mxfp4_quantize(W)
+    nbytes = 2 * k * n + W4.codes.numel() + W4.scales.numel()
+    for name, fn in (("quantise", lambda: lf.lora_mxfp4_quantize(W, codes=W4.codes, scales=W4.scales)),
+                     ("dequantise", lambda: lf.lora_mxfp4_dequantize(W4, out=W))):
+        ms = timed(fn)
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        print(json.dumps({"metric": f"MXFP4 {name}, GB/s of compulsory traffic", "value": gbs, "unit": "GB/s", "ms": ms,
+                          "steps": args.steps, "warmup": args.warmup, "higher_is_better": True, "dtype": "bf16, e2m1",
+                          "data": "synthetic", "config": {"workload": f"W {k} x {n}"},
+                          "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                                       "frac": gbs / PEAK_HBM_GBS, "traffic": None}}), flush=True)
+    del W, W4
+    k, n, r = 4096, 14336, 16
+    W = rand(k, n, scale=k ** -0.5)
+    W4 = lf.lora_mxfp4_quantize(W)
+    A, B = rand(k, r, scale=k ** -0.5), rand(r, n, scale=0.02 ** 0.5)
+    held = (W4.codes.numel() + W4.scales.numel(), 2 * k * n)
+    for m in (1, 16, 128, 1024, 8192):
+        X, dY = rand(m, k, scale=1.0), rand(m, n, scale=1.0)
+
+        def step(w, fwd, bwd):
+            Y, S, keep = fwd(X, w, A, B, 2.0, 0.1, 1, 0)
+            bwd(dY, X, w, A, B, S, keep, 2.0, 0.1)
+
+        fwd4 = timed(lambda: lf.lora_mxfp4_linear_fwd(X, W4, A, B, 2.0, 0.0))
+        fwd16 = timed(lambda: lf.lora_linear_fwd(X, W, A, B, 2.0, 0.0))
+        both4 = timed(lambda: step(W4, lf.lora_mxfp4_linear_fwd, lf.lora_mxfp4_linear_bwd))
+        both16 = timed(lambda: step(W, lf.lora_linear_fwd, lf.lora_linear_bwd))
+        print(json.dumps({"metric": "LoRA linear over an MXFP4 weight, tokens/s forward and backward",
+                          "value": m / (both4 * 1e-3), "unit": "tokens/s", "ms": both4, "ms_forward": fwd4,
+                          "steps": args.steps, "warmup": args.warmup, "higher_is_better": True, "dtype": "bf16",
+                          "data": "synthetic", "config": {"workload": f"m {m}, k {k}, n {n}, r {r}"},
+                          "weight_bytes": {"mxfp4": held[0], "bf16": held[1]},
+                          "bf16_weight": {"ms": both16, "ms_forward": fwd16, "speedup": both16 / both4,
+                                          "speedup_forward": fwd16 / fwd4}}), flush=True)
+
+
+def adamw_report(args):
+    """One AdamW step over the adapters (r 16) of the seven projections of a
+    32-layer LLaMA-8B-shaped model, 448 bf16 tensors with fp32 master copies: bytes
+    moved are the compulsory ones (gradient read, master and moments read and
+    written, parameter written), medians of event-timed trials after a cache flush."""
+    import torch
+
+    import lora_fine_tuning_amd as lf
+    from synth import DECODER_PROJECTIONS
+
+    lf.load()
+    timer = Timer(torch, torch.cuda.current_stream())
+    sizes = [s * 16 for _ in range(32) for _, k, n in DECODER_PROJECTIONS for s in (k, n)]
+    for bits in (32, 8):
+        mk = lambda dtype: [torch.zeros(z, dtype=dtype, device="cuda") for z in sizes]  # noqa: E731
+        params, masters = mk(torch.bfloat16), mk(torch.float32)
+        grads = [torch.randn(z, device="cuda").bfloat16() for z in sizes]
+        if bits == 8:
+            ms, vs = ([t.view(torch.float8_e4m3fn) for t in mk(torch.uint8)] for _ in range(2))
+            scales = {name: [torch.zeros(-(-z // 256), device="cuda") for z in sizes] for name in ("m_scales", "v_scales")}
+        else:
+            ms, vs, scales = mk(torch.float32), mk(torch.float32), {}
+        table = lf.adamw_table(params, grads, ms, vs, masters=masters, **scales)
+        count = [0]
+
+        def step():
+            count[0] += 1
+            lf.lora_adamw_step(table, lr=1e-4, weight_decay=0.01, step=count[0], seed=3)
+
+        step_ms = timer.median(step, args.steps, args.warmup)
+        per = 2 + 2 + 8 + (16 if bits == 32 else 4 + 16 / 256)
+        gbs = per * sum(sizes) / (step_ms * 1e-3) / 1e9
+        print(json.dumps({"metric": "AdamW step over adapter tensors, GB/s of compulsory traffic", "value": gbs,
+                          "unit": "GB/s", "ms": step_ms, "steps": args.steps, "warmup": args.warmup,
+                          "higher_is_better": True, "dtype": f"bf16 with fp32 master, moments in {bits} bits",
+                          "data": "synthetic", "config": {"workload": f"{len(sizes)} tensors, {sum(sizes)} values"},
+                          "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                                       "frac": gbs / PEAK_HBM_GBS, "traffic": None}}), flush=True)
 
 
 def pack_report(args):
@@ -639,6 +746,12 @@ def main():
         return
     if args.hbm:
         hbm_report(args)
+        return
+    if args.mxfp4:
+        mxfp4_report(args)
+        return
+    if args.adamw:
+        adamw_report(args)
         return
     if args.concat:
         concat_report(args)

@@ -286,7 +286,8 @@ lora_status lora_dora_norm(const void *W, const void *A, const void *B, int64_t 
  *           in its low nibble and W'[32b + 2i + 1][16c + j] in its high one
  *   scales  [N16][KB][16] bytes
  * both 16-byte aligned, lora_mxfp4_codes_size() and lora_mxfp4_scales_size()
- * bytes.  Padding columns and rows hold zero codes; quantising writes them.
+ * bytes.  Padding columns and rows hold zero codes and scale bytes of 127, as
+ * quantising writes them.
  *
  * lora_mxfp4_quantize: with a the block's largest magnitude, the scale is
  * 2^e, e = floor(log2 a) - 2, one more where a / 2^e >= 7, clamped to
@@ -361,8 +362,9 @@ lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const voi
  * sqrt(v), and m_scale and v_scale ceil(n / 256) floats: value = code * scale
  * of its block of 256.  A new moment x of a block with largest magnitude a
  * becomes scale = a / 448 and a code drawn between the two neighbours of
- * x / scale so that its mean is x / scale (a positive v keeps at least the
- * smallest code, so the division stays bounded; a below 2^-100 gives zeros).
+ * x / scale so that its mean is x / scale (a positive root keeps at least the
+ * smallest code, so the division stays bounded; a below 2^-100 gives zeros, and
+ * v below the smallest normal float, 2^-126, has the root zero).
  * The draw of value i is word (offset + i) % 4 of Philox4x32-10 at counter
  * (offset + i) / 4 under key seed + t * 0x9E3779B97F4A7C15 (mod 2^64), its low
  * half for m and its high half for v.  offset is a multiple of 8; tensors

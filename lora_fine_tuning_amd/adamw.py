@@ -32,13 +32,14 @@ def _column(ts: Sequence[torch.Tensor], name: str, count: int, dtypes, numels=No
     dtype = ts[0].dtype if count else dtypes[0]
     if dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
-    for i, t in enumerate(ts):
-        if t.dtype != dtype:
-            raise TypeError(f"{name}[{i}] is {t.dtype}, {name}[0] {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        if numels is not None and t.numel() != numels[i]:
-            raise ValueError(f"{name}[{i}] must have {numels[i]} values, got {t.numel()}")
+    if any(t.dtype is not dtype for t in ts):
+        i = next(i for i, t in enumerate(ts) if t.dtype != dtype)
+        raise TypeError(f"{name}[{i}] is {ts[i].dtype}, {name}[0] {dtype}")
+    if not all(t.is_contiguous() for t in ts):
+        raise ValueError(f"{name}[{next(i for i, t in enumerate(ts) if not t.is_contiguous())}] must be contiguous")
+    if numels is not None and [t.numel() for t in ts] != numels:
+        i = next(i for i, t in enumerate(ts) if t.numel() != numels[i])
+        raise ValueError(f"{name}[{i}] must have {numels[i]} values, got {ts[i].numel()}")
     return [t.data_ptr() for t in ts], dtype
 
 
@@ -104,7 +105,7 @@ def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=
     # the device last, so that host tests can reach every other check with CPU tensors
     for ts in tensors:
         for t in ts:
-            if t.device.type != "cuda" or t.device != device:
+            if t.device != device or not t.is_cuda:
                 raise ValueError(f"a tensor is on {t.device}: all must be on one GPU ({device})")
     _apart(rec, widths)
     return AdamwTable(rec, tensors, device, pt == torch.bfloat16, gt == torch.bfloat16, 8 if held8 else 32)

@@ -41,9 +41,9 @@ extern "C" lora_status lora_mxfp4_dequantize(const void *codes, const void *scal
     return LORA_OK;
 }
 
-// The expanded weight sits at the start of the workspace, the bf16 layer's own
-// workspace after it.
-static size_t expanded_bytes(int64_t k, int64_t n) { return align_up((size_t)k * (size_t)n * 2); }
+// The expanded weight (none without rows) sits at the start of the workspace, the
+// bf16 layer's own workspace after it.
+static size_t expanded_bytes(int64_t m, int64_t k, int64_t n) { return m > 0 ? align_up((size_t)k * (size_t)n * 2) : 0; }
 
 static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
     return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && k * n < (1LL << 46);
@@ -59,13 +59,13 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
 extern "C" size_t lora_mxfp4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n) {
     if (!sizes_ok(m, k, n) || m == 0) return 0;
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, kMxPlain);
-    return pl.kind ? pl.part_bytes : expanded_bytes(k, n);
+    return pl.kind ? pl.part_bytes : expanded_bytes(m, k, n);
 }
 
 extern "C" size_t lora_mxfp4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n) {
     if (!sizes_ok(m, k, n) || m == 0) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, 0);
-    return pl.kind ? pl.part_bytes : expanded_bytes(k, n);
+    return pl.kind ? pl.part_bytes : expanded_bytes(m, k, n);
 }
 
 extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t m,
@@ -112,7 +112,7 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
 extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, kMxPlain);
-    if (!pl.kind) return expanded_bytes(k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
+    if (!pl.kind) return expanded_bytes(m, k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
     // (the plans with and without dropout differ in where S is formed only)
     return align_up(pl.part_bytes) + std::max(pl.spart_bytes, lora_linear_fwd_workspace_size(m, k, n, r));
 }
@@ -120,7 +120,7 @@ extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int
 extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || r < 1) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
-    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) + lora_linear_bwd_workspace_size(m, k, n, r);
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) + lora_linear_bwd_workspace_size(m, k, n, r);
 }
 
 extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, const void *scales, const void *A,
@@ -151,7 +151,7 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
                                  (float *)rest, stream), "MXFP4 product launch");
         return LORA_OK;
     }
-    const size_t w = expanded_bytes(k, n);
+    const size_t w = expanded_bytes(m, k, n);
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_linear_fwd(X, workspace, A, B, m, k, n, r, alpha, p, seed, offset, Y, S, keep_bits,
                            ws_at(workspace, w), workspace_bytes - w, stream);
@@ -194,10 +194,10 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
         }
         return LORA_OK;
     }
-    const size_t w = expanded_bytes(k, n);
+    const size_t w = expanded_bytes(m, k, n);
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
-    return lora_linear_bwd(dY, X, workspace, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
+    return lora_linear_bwd(dY, X, m > 0 ? workspace : codes, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
                            ws_at(workspace, w), workspace_bytes - w, stream);
 }
 
@@ -205,7 +205,7 @@ extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int6
                                                       int32_t num_adapters, int32_t num_segments) {
     if (!sizes_ok(m, k, n) || m == 0 || r_max < 1) return 0;
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed);
-    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) +
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) +
            multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
 }
 
@@ -213,7 +213,7 @@ extern "C" size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int6
                                                       int32_t num_adapters, int32_t num_segments) {
     if (!sizes_ok(m, k, n) || r_max < 1) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r_max);
-    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(k, n)) +
+    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) +
            multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
 }
 
@@ -246,7 +246,7 @@ extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *co
                "MXFP4 sum launch");
         return LORA_OK;
     }
-    const size_t w = expanded_bytes(k, n);
+    const size_t w = expanded_bytes(m, k, n);
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return multi_lora_linear_fwd(X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, m, k, n,
                                  r_max, seed, offset, Y, S, keep_bits, ws_at(workspace, w), workspace_bytes - w,
@@ -287,9 +287,9 @@ extern "C" lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X
         }
         return LORA_OK;
     }
-    const size_t w = expanded_bytes(k, n);
+    const size_t w = expanded_bytes(m, k, n);
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
-    return multi_lora_linear_bwd(dY, X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
+    return multi_lora_linear_bwd(dY, X, m > 0 ? workspace : codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
                                  keep_bits, m, k, n, r_max, dX, ws_at(workspace, w), workspace_bytes - w, stream);
 }

@@ -559,6 +559,52 @@ def test_optimizer_refuses():
 
 
 @pytest.mark.gpu
+def test_optimizer_refuses_parameters_of_another_size():
+    # a parameter whose values were swapped for fewer: the step is refused before anything runs
+    ps = model()
+    opt = lf.LoraAdamW(ps)
+    gradients(ps, 0)
+    opt.step()
+    keep = ps[1].detach().clone()
+    ps[0].grad = None
+    ps[0].data = ps[0].data.flatten()[:-1].clone()
+    ps[0].grad = torch.zeros_like(ps[0])
+    with pytest.raises(ValueError, match="moments"):
+        opt.step()
+    assert torch.equal(ps[1], keep)
+
+
+@pytest.mark.gpu
+def test_one_tensor_past_32_bits():
+    # 2^32 values and a bit: its last values step like a small tensor's at the same counters
+    n, tail = (1 << 32) + 515, 4099
+
+    def state(count, fill):
+        w = torch.zeros(count, dtype=torch.bfloat16, device="cuda")
+        g = torch.zeros(count, dtype=torch.bfloat16, device="cuda")
+        m, v = (torch.zeros(count, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+        ms, vs = (torch.zeros(-(-count // 256), device="cuda") for _ in range(2))
+        w[-tail:], g[-tail:] = fill
+        return w, g, m, v, ms, vs
+
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    fill = [torch.randn(tail, device="cuda", generator=gen).bfloat16() for _ in range(2)]
+    first = (n - tail) // 256 * 256  # where the small tensor starts
+    big, small = state(n, fill), state(n - first, fill)
+    for (w, g, m, v, ms, vs), offset in ((big, 0), (small, first)):
+        table = lf.adamw_table([w], [g], [m], [v], m_scales=[ms], v_scales=[vs], offsets=[offset])
+        for t in (1, 2):
+            lf.lora_adamw_step(table, step=t, seed=5, **HYPER)
+    torch.cuda.synchronize()
+    count = n - first
+    for a, b in zip(big[:1] + big[2:4], small[:1] + small[2:4]):
+        assert torch.equal(a[-count:].view(torch.uint8), b.view(torch.uint8))
+    for a, b in zip(big[4:], small[4:]):
+        assert torch.equal(a[-b.numel():], b)
+    assert not big[2][:first].view(torch.uint8).any() and big[2][-tail:].view(torch.uint8).any()
+
+
+@pytest.mark.gpu
 def test_optimizer_captured_with_the_layer():
     # forward, backward and step in one graph, over a packed weight: every replay is an eager step
     k, n, m = 136, 72, 40

@@ -688,6 +688,48 @@ def test_no_rows():
 
 
 @pytest.mark.gpu
+def test_weight_past_32_bits():
+    # 2^32 values, codes past 2^31 bytes: the same 1024 columns over and over
+    k, n, m, wide = 4096, 1 << 20, 3, 1024
+    X, small, W, _, _, dY = layer_case(m, k, wide, 8, seed=91)
+    rep = n // wide
+    W4 = lf.Mxfp4Weight(small.codes.repeat(rep, 1, 1, 1), small.scales.repeat(rep, 1, 1), k, n)
+    back = lf.lora_mxfp4_dequantize(W4)
+    one = lf.lora_mxfp4_dequantize(small)
+    assert torch.equal(back[:, -wide:], one) and torch.equal(back[-1].view(rep, wide), one[-1].expand(rep, wide))
+    again = lf.lora_mxfp4_quantize(back)
+    assert torch.equal(again.codes, W4.codes) and torch.equal(again.scales, W4.scales)
+    del back, again
+    Y = lf.lora_mxfp4_frozen_fwd(X.cuda(), W4).view(m, rep, wide)
+    assert torch.equal(Y, Y[:, :1].expand(m, rep, wide))
+    near("Y", Y[:, -1], f64(X) @ W, k * HALF * (np.abs(f64(X)) @ np.abs(W)))
+    wider = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")
+    wider[:, -wide:] = dY.cuda()
+    dX = lf.lora_mxfp4_frozen_bwd(wider, W4)
+    near("dX", dX, f64(dY) @ W.T, wide * HALF * (np.abs(f64(dY)) @ np.abs(W).T))  # (sums of zeros round nothing)
+
+
+@pytest.mark.gpu
+def test_no_rows_mixed():
+    # no rows: the tables' gradients become zeros, and no scratch is needed for a weight that is not read
+    k, n = 136, 72
+    X, W4, W, _, _, dY = layer_case(4, k, n, 8, seed=1)
+    As = [bf16_randn((k, r), 1.0, torch.Generator().manual_seed(r)).cuda() for r in (8, 40)]
+    Bs = [bf16_randn((r, n), 1.0, torch.Generator().manual_seed(r)).cuda() for r in (8, 40)]
+    dAs, dBs = [torch.full_like(a, 7.0) for a in As], [torch.full_like(b, 7.0) for b in Bs]
+    table = lf.adapter_table(As, Bs, [1.0, 1.0], [0.0, 0.1], dAs, dBs)
+    so = torch.zeros(3, dtype=torch.int64, device="cuda")
+    sa = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    X0, dY0 = X[:0].cuda(), dY[:0].cuda()
+    Y, S, keep = lf.multi_lora_mxfp4_linear_fwd(X0, W4, table, 2, so, sa, 40)
+    dX = lf.multi_lora_mxfp4_linear_bwd(dY0, X0, W4, table, 2, so, sa, S, keep, 40)
+    torch.cuda.synchronize()
+    assert Y.shape == (0, n) and dX.shape == (0, k)
+    assert not any(t.any() for t in (*dAs, *dBs))
+    assert lf.lora_mxfp4_linear_bwd_workspace_size(0, 8192, 8192, 8) == _lib.lora_linear_bwd_workspace_size(0, 8192, 8192, 8)
+
+
+@pytest.mark.gpu
 def test_binding_rejects_on_the_gpu():
     X, W4, W, A, B, dY = layer_case(4, 136, 72, 8, seed=1)
     X, A, B = X.cuda(), A.cuda(), B.cuda()
