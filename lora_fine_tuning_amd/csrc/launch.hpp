@@ -291,15 +291,20 @@ struct MxGemmPlan {
     int SK, jobs;          // > 0: the product's launch also forms S = X A, in SK partial sums, by `jobs` work-groups
     size_t spart_bytes;
 };
-// r == 0: no adapter.  kMxDropout: S comes from F1; kMxMixed: so it does, and the
-// partial sums go to launch_mxfp4_join.
-enum MxForm { kMxPlain = 0, kMxDropout = 1, kMxMixed = 2 };
+// r == 0: no adapter.  kMxMixed: S comes from F1, and the partial sums go to
+// launch_mxfp4_join.
+enum MxForm { kMxPlain = 0, kMxMixed = 1 };
+struct MxDropout {
+    float p;
+    uint64_t seed, offset;
+    uint32_t *keep;  // NULL: no mask is applied or written
+};
 MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form);
-// S: written where the plan forms it (SK > 0), else read (r > 0).  Y NULL: the
+// S and drop.keep: written where the plan forms S (SK > 0), else S is read (r > 0).  Y NULL: the
 // product's partial sums alone (kMxMixed, with r = 0 here).
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
-                             int n, const void *A, const void *B, int r, float alpha, float *S, void *Y, float *part,
-                             float *spart, hipStream_t stream);
+                             int n, const void *A, const void *B, int r, float alpha, const MxDropout &drop, float *S,
+                             void *Y, float *part, float *spart, hipStream_t stream);
 
 // dX = dY W'^T (+ scale keep.(dS A^T)) straight from the packed weight
 // (mxfp4_gemm_t.hip).

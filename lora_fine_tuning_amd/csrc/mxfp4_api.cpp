@@ -79,7 +79,7 @@ extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, c
     REQ_WORKSPACE(lora_mxfp4_frozen_fwd_workspace_size(m, k, n));
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, kMxPlain);
     if (pl.kind) {
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, nullptr, Y,
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, MxDropout{}, nullptr, Y,
                                  (float *)workspace, nullptr, stream), "MXFP4 product launch");
         return LORA_OK;
     }
@@ -113,7 +113,6 @@ extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int
     if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, kMxPlain);
     if (!pl.kind) return expanded_bytes(m, k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
-    // (the plans with and without dropout differ in where S is formed only)
     return align_up(pl.part_bytes) + std::max(pl.spart_bytes, lora_linear_fwd_workspace_size(m, k, n, r));
 }
 
@@ -143,12 +142,12 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
     REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     REQ_WORKSPACE(lora_mxfp4_linear_fwd_workspace_size(m, k, n, r));
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, p != 0.0f ? kMxDropout : kMxPlain);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, kMxPlain);
     if (pl.kind) {
         char *rest = ws_at(workspace, align_up(pl.part_bytes));
         if (pl.SK == 0) CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, rest, stream));
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, A, B, r, alpha, S, Y, (float *)workspace,
-                                 (float *)rest, stream), "MXFP4 product launch");
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, A, B, r, alpha,
+                                 MxDropout{p, seed, offset, keep_bits}, S, Y, (float *)workspace, (float *)rest, stream), "MXFP4 product launch");
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
@@ -240,7 +239,7 @@ extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *co
         const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
         CHECK(multi_forward_s_only(X, src, m, k, seed, offset, S, keep_bits, ws_at(workspace, align_up(pl.part_bytes)),
                                    stream));
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, nullptr, nullptr,
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, MxDropout{}, nullptr, nullptr,
                                  (float *)workspace, nullptr, stream), "MXFP4 product launch");
         HIPCHK(launch_mxfp4_join(true, (const float *)workspace, pl.KS, (int)m, (int)n, S, r_max, nullptr, src, Y, stream),
                "MXFP4 sum launch");

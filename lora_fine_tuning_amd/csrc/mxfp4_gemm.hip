@@ -19,11 +19,12 @@
 // leave CUs idle, work-groups split k further: each slice writes fp32 partial
 // sums and a finishing launch adds them in slice order.
 //
-// Up to 128 rows the adapter rides along: without dropout S = X A is formed by
-// further work-groups of the same launch (partial sums over 1024 of k each),
-// and the finishing launch adds those, writes S and adds alpha S B.  Else F1
-// forms S first, and the shapes for many rows add alpha S B in the product's own
-// epilogue, as rank-deep MFMA steps, where k is not split.
+// With the shapes for up to 64 rows the adapter rides along: keep and keep.X A
+// are formed by further work-groups of the same launch (partial sums over 1024 of
+// k each), and the finishing launch adds those, writes S and adds alpha S B.  F1
+// took 9 to 14 us before the product.  With the shapes for more rows F1 forms S
+// first, and they add alpha S B in their own epilogue, as rank-deep MFMA steps,
+// where k is not split.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -53,6 +54,9 @@ struct MxGemmParams {
     const uint16_t *A;   // partial sums of S = X A by further work-groups (nullptr: none)
     float *spart;        // [SK][M][rs], rs = r rounded up to 4
     int rs, SK, jobs;        // partial sums; work-groups that form them (a multiple of 8)
+    uint32_t *keep;          // their dropout mask, M x ceil(K / 32) words, written here (nullptr: none)
+    uint64_t seed, offset;
+    uint32_t drop;           // threshold of the mask's 16-bit numbers
 };
 
 constexpr int kSK = 1024;  // k of one partial sum of S
@@ -68,17 +72,22 @@ struct MxTile {
     static constexpr int SPARE = NS * STAGE;  // 1 KiB that surplus loads fill with zeros
     static constexpr int RED = (WK - 1) * WM * WN * MB * NB * 1024;
     static constexpr int LDS = SPARE + 1024 > RED ? SPARE + 1024 : RED;
+    static constexpr int SHARE = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;  // work-groups that a CU holds
+    // 16-rank tiles of a job of S (few enough registers for SHARE work-groups a CU)
+    static constexpr int RT = MB > 2 || XR == 4 ? 2 : 4;
     static constexpr bool RIDE = WM == 1;  // the adapter's S rides along, a second launch adds alpha S B
     static_assert(SU <= NW && LDS <= 160 * 1024, "tile does not fit");
 };
 
-// One work-group's share of S = X A: k from kSK * (job % SK), 128 a wave, the row
+// One work-group's share of keep.X A: k from kSK * (job % SK), 128 a wave, the row
 // tile job / SK % tiles_m, and 16 RT ranks.  X's rows and A's columns come straight from memory
 // (8 two-byte loads make a 16-rank operand: A's rows are r values long), every
 // load of a wave before its first use; the waves are added in LDS in wave order.
+// A lane's 8 elements of X are one counter of the dropout mask and one byte of
+// keep, which the first rank tile's work-groups write.
 template <class T>
 __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *smem) {
-    constexpr int MB = T::MB, RT = MB > 2 ? 2 : 4;
+    constexpr int MB = T::MB, RT = T::RT;
     static_assert(T::NW == 8 && T::WM == 1 && MB * RT <= 8 && 8 * MB * RT * 1024 <= T::LDS, "no room for the partial sums");
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -110,6 +119,18 @@ __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *sme
                 h[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
                     rA, rank < P.r && k < P.K ? ((uint32_t)(k + e) * (uint32_t)P.r + (uint32_t)rank) * 2u : kOOB, 0, 0);
             w[t] = make_uint4(pack2(h[0], h[1]), pack2(h[2], h[3]), pack2(h[4], h[5]), pack2(h[6], h[7]));
+        }
+        if (P.keep != nullptr) {
+            const uint32_t row_bytes = (uint32_t)((P.K + 31) / 32) * 4u;
+#pragma unroll
+            for (int a = 0; a < MB; ++a) {
+                const int row = m0 + 16 * a + l16;
+                const uint32_t byte =
+                    k < P.K ? keep_byte(P.offset + (uint64_t)row * (uint64_t)P.K + (uint64_t)k, P.seed, P.drop) : 0u;
+                x[a] = apply_keep(x[a], byte);
+                if (r0 == 0 && row < P.M && (uint32_t)k / 8u < row_bytes)
+                    ((uint8_t *)P.keep)[(size_t)row * row_bytes + k / 8] = (uint8_t)byte;
+            }
         }
 #pragma unroll
         for (int a = 0; a < MB; ++a)
@@ -412,7 +433,7 @@ struct MxFinishParams {
     const float *spart;  // [SK][M][rs] or, with SK == 0, S itself; r == 0: no adapter
     int SK, r, rs;
     const uint16_t *B;
-    float alpha;
+    float alpha, undrop;  // undrop: 1 / (1 - p), the scale of a summed S
     float *S;
     uint16_t *Y;
 };
@@ -457,6 +478,7 @@ __global__ __launch_bounds__(256) void mxfp4_finish_kernel(MxFinishParams P) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v.x += u[e].x, v.y += u[e].y, v.z += u[e].z, v.w += u[e].w;
                     }
+                    v.x *= P.undrop, v.y *= P.undrop, v.z *= P.undrop, v.w *= P.undrop;
                     if (blockIdx.x == 0) {
                         float *d = P.S + (size_t)row * P.r + r;
                         d[0] = v.x;
@@ -548,8 +570,7 @@ struct MxKind {
 };
 template <class T>
 constexpr MxKind kind_of(float stage) {
-    return MxKind{launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? (T::MB > 2 ? 32 : 64) : 0, stage,
-                  std::min(160 * 1024 / T::LDS, 4)};
+    return MxKind{launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? 16 * T::RT : 0, stage, T::SHARE};
 }
 const MxKind kKinds[] = {
     kind_of<MxTile<1, 1, 8, 1, 1, 4, 3>>(0.36f),   // 4 rows x 16 columns
@@ -571,6 +592,7 @@ const MxKind kKinds[] = {
 //   shape:  3.5 us + rounds (stages x stage time + 1 us), at least the weight's
 //           bytes at 6 TB/s; a finishing launch 3.5 us and its partial sums at 8 TB/s
 //   expand: expanded_us
+//   S apart: 9 us and X's bytes at 4 TB/s (its work-groups beside a shape's add to the rounds)
 // Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 16.5
 // (16), 300 x 14336 x 4096 45 (48), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
 // (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (192; packed 245).
@@ -580,7 +602,8 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form)
     if (m <= 0 || k > (1 << 20) || n > (1 << 21) || m > (1 << 19)) return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const double weight = (double)k * n;
-    double least = expanded_us(m, n, k, weight);
+    const double f1 = r > 0 && form == kMxPlain ? 9.0 + (double)m * k * 2 / 4e6 : 0.0;
+    double least = expanded_us(m, n, k, weight) + f1;
     for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
         const MxKind &K = kKinds[kind - 1];
         if ((kind <= 2 && m > 4) || (kind <= 4 && m > 16)) continue;  // (4 rows in LDS; columns too narrow)
@@ -590,7 +613,7 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form)
         p.tiles_n = (int)cdiv(n, K.tn);
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, stages = cdiv(k, K.kw);
         if (tiles > (1 << 20)) continue;
-        if (r > 0 && K.ranks > 0 && form == kMxPlain && m <= 128) {
+        if (r > 0 && K.ranks > 0 && form == kMxPlain) {
             p.SK = (int)cdiv(k, kSK);
             p.jobs = (int)cdiv(p.SK * p.tiles_m * cdiv(r, K.ranks), 8) * 8;
             p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
@@ -603,7 +626,7 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form)
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
             const int64_t groups = tiles * p.KS + p.jobs, slots = 256 * K.share;
             double t = (double)cdiv(groups, slots) * (p.per * K.stage + 1.0);
-            t = 3.5 + std::max(t, weight * 0.53 / 6e6);
+            t = 3.5 + std::max(t, weight * 0.53 / 6e6) + (p.jobs == 0 ? f1 : 0.0);
             if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 8e6;
             if (t < least) {
                 least = t;
@@ -619,8 +642,8 @@ MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form) {
 }
 
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
-                             int n, const void *A, const void *B, int r, float alpha, float *S, void *Y, float *part,
-                             float *spart, hipStream_t stream) {
+                             int n, const void *A, const void *B, int r, float alpha, const MxDropout &drop, float *S,
+                             void *Y, float *part, float *spart, hipStream_t stream) {
     MxGemmParams P{};
     P.X = (const uint16_t *)X;
     P.codes = (const uint8_t *)codes;
@@ -645,11 +668,16 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     P.r = r;
     P.alpha = alpha;
     P.jobs = pl.jobs;
+    P.keep = drop.keep;
+    P.seed = drop.seed;
+    P.offset = drop.offset;
+    P.drop = drop_threshold(drop.p);
     int slot = prof_begin("mxfp4_gemm", stream);
     const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
     if (e != hipSuccess || !pl.finish || Y == nullptr) return e;
-    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)B, alpha, S, (uint16_t *)Y};
+    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)B, alpha, drop_scale(drop.p), S,
+                           (uint16_t *)Y};
     slot = prof_begin("mxfp4_finish", stream);
     hipLaunchKernelGGL(mxfp4_finish_kernel, dim3((unsigned)((n + 127) / 128), (unsigned)((m + 15) / 16)), dim3(256), 0, stream,
                        F);

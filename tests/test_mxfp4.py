@@ -440,6 +440,23 @@ def test_layer_forward_and_backward(case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,k,r", [(1, 136, 8), (40, 1080, 40), (130, 2056, 72), (700, 264, 16)])
+def test_mask_is_written_whole(m, k, r):
+    # every word of the mask, its bits past k among them, whatever the buffer held; p = 0 keeps everything, and
+    # a p whose threshold is zero drops nothing
+    n = 264
+    X, W4, W, A, B, dY = layer_case(m, k, n, r, seed=37)
+    for p in (0.0, 2.0 ** -20, 0.3, 0.9999):
+        keep = torch.full((m + 1, (k + 31) // 32), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+        Y, S, got = lf.lora_mxfp4_linear_fwd(X.cuda(), W4, A.cuda(), B.cuda(), 2.0, p, 11, 24, keep_bits=keep[:m])
+        torch.cuda.synchronize()
+        assert got.data_ptr() == keep.data_ptr() and (keep[m] == 0x5A5A5A5A).all()
+        assert torch.equal(got, lf.lora_dropout_mask(11, 24, m, k, p))
+        want, slack = layer_reference(X, W, A, B, dY, 2.0, p, 11, 24)
+        near("Y", Y, want["Y"], slack["Y"])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m,r,p", [(1, 16, 0.0), (33, 9, 0.0), (33, 64, 0.1), (300, 40, 0.1), (700, 16, 0.0)])
 def test_unaligned_adapter_gives_the_same(m, r, p):
     # A and B one element past a 16-byte boundary: the same sums in the same order
