@@ -6,6 +6,7 @@ only marshals arguments, as the rest of the binding does.  `lora_linear`,
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -13,6 +14,7 @@ import torch
 from ._lib import (_check, _check_table, _elsewhere, _handle, _need, _need_on, _on_device, _scratch, load)
 
 _BF16, _F32 = torch.bfloat16, torch.float32
+_sizes = functools.lru_cache(maxsize=1024)  # a workspace's size follows from the sizes asked for alone
 
 
 class Mxfp4Weight(NamedTuple):
@@ -93,26 +95,32 @@ def lora_mxfp4_dequantize(W: Mxfp4Weight, *, out=None, stream=None):
     return out
 
 
+@_sizes
 def lora_mxfp4_frozen_fwd_workspace_size(m, k, n) -> int:
     return load().lora_mxfp4_frozen_fwd_workspace_size(m, k, n)
 
 
+@_sizes
 def lora_mxfp4_frozen_bwd_workspace_size(m, k, n) -> int:
     return load().lora_mxfp4_frozen_bwd_workspace_size(m, k, n)
 
 
+@_sizes
 def lora_mxfp4_linear_fwd_workspace_size(m, k, n, r) -> int:
     return load().lora_mxfp4_linear_fwd_workspace_size(m, k, n, r)
 
 
+@_sizes
 def lora_mxfp4_linear_bwd_workspace_size(m, k, n, r) -> int:
     return load().lora_mxfp4_linear_bwd_workspace_size(m, k, n, r)
 
 
+@_sizes
 def multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments) -> int:
     return load().multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
 
 
+@_sizes
 def multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments) -> int:
     return load().multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
 
@@ -127,7 +135,7 @@ def lora_mxfp4_frozen_fwd(X, W: Mxfp4Weight, *, Y=None, workspace=None, stream=N
             return lora_mxfp4_frozen_fwd(X, W, Y=Y, workspace=workspace)
     lib = load()
     Y = _out(Y, (m, n), _BF16, "Y", dev)
-    ws, nb, _held = _scratch(lib.lora_mxfp4_frozen_fwd_workspace_size(m, k, n), dev, workspace)
+    ws, nb, _held = _scratch(lora_mxfp4_frozen_fwd_workspace_size(m, k, n), dev, workspace)
     _check(lib.lora_mxfp4_frozen_fwd(X.data_ptr(), codes.data_ptr(), scales.data_ptr(), m, k, n, Y.data_ptr(), ws, nb,
                                      _handle(dev)))
     return Y
@@ -143,7 +151,7 @@ def lora_mxfp4_frozen_bwd(dY, W: Mxfp4Weight, *, dX=None, workspace=None, stream
             return lora_mxfp4_frozen_bwd(dY, W, dX=dX, workspace=workspace)
     lib = load()
     dX = _out(dX, (m, k), _BF16, "dX", dev)
-    ws, nb, _held = _scratch(lib.lora_mxfp4_frozen_bwd_workspace_size(m, k, n), dev, workspace)
+    ws, nb, _held = _scratch(lora_mxfp4_frozen_bwd_workspace_size(m, k, n), dev, workspace)
     _check(lib.lora_mxfp4_frozen_bwd(dY.data_ptr(), codes.data_ptr(), scales.data_ptr(), m, k, n, dX.data_ptr(), ws, nb,
                                      _handle(dev)))
     return dX
@@ -166,7 +174,7 @@ def lora_mxfp4_linear_fwd(X, W: Mxfp4Weight, A, B, alpha: float, p: float, seed:
     S = _out(S, (m, r), _F32, "S", dev)
     if keep_bits is not None or p != 0.0:
         keep_bits = _out(keep_bits, (m, (k + 31) // 32), torch.int32, "keep_bits", dev)
-    ws, nb, _held = _scratch(lib.lora_mxfp4_linear_fwd_workspace_size(m, k, n, r), dev, workspace)
+    ws, nb, _held = _scratch(lora_mxfp4_linear_fwd_workspace_size(m, k, n, r), dev, workspace)
     _check(lib.lora_mxfp4_linear_fwd(X.data_ptr(), codes.data_ptr(), scales.data_ptr(), A.data_ptr(), B.data_ptr(), m, k,
                                      n, r, alpha, p, seed, offset, Y.data_ptr(), S.data_ptr(),
                                      None if keep_bits is None else keep_bits.data_ptr(), ws, nb, _handle(dev)))
@@ -194,7 +202,7 @@ def lora_mxfp4_linear_bwd(dY, X, W: Mxfp4Weight, A, B, S, keep_bits, alpha: floa
     dX = _out(dX, (m, k), _BF16, "dX", dev) if want_dX else None
     dA = _out(dA, (k, r), _BF16, "dA", dev)
     dB = _out(dB, (r, n), _BF16, "dB", dev)
-    ws, nb, _held = _scratch(lib.lora_mxfp4_linear_bwd_workspace_size(m, k, n, r), dev, workspace)
+    ws, nb, _held = _scratch(lora_mxfp4_linear_bwd_workspace_size(m, k, n, r), dev, workspace)
     _check(lib.lora_mxfp4_linear_bwd(dY.data_ptr(), X.data_ptr(), codes.data_ptr(), scales.data_ptr(), A.data_ptr(),
                                      B.data_ptr(), S.data_ptr(), None if keep_bits is None else keep_bits.data_ptr(), m,
                                      k, n, r, alpha, p, None if dX is None else dX.data_ptr(), dA.data_ptr(),
@@ -228,7 +236,7 @@ def multi_lora_mxfp4_linear_fwd(X, W: Mxfp4Weight, adapters: torch.Tensor, num_a
     Y = _out(Y, (m, n), _BF16, "Y", dev)
     S = _out(S, (m, r_max), _F32, "S", dev)
     keep_bits = _out(keep_bits, (m, (k + 31) // 32), torch.int32, "keep_bits", dev)
-    ws, nb, _held = _scratch(lib.multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, nseg), dev, workspace)
+    ws, nb, _held = _scratch(multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, nseg), dev, workspace)
     _check(lib.multi_lora_mxfp4_linear_fwd(X.data_ptr(), codes.data_ptr(), scales.data_ptr(), adapters.data_ptr(),
                                            num_adapters, seg_off.data_ptr(), seg_adapter.data_ptr(), nseg, m, k, n,
                                            r_max, seed, offset, Y.data_ptr(), S.data_ptr(), keep_bits.data_ptr(), ws, nb,
@@ -254,7 +262,7 @@ def multi_lora_mxfp4_linear_bwd(dY, X, W: Mxfp4Weight, adapters: torch.Tensor, n
                                                r_max, dX=dX, workspace=workspace, want_dX=want_dX)
     lib = load()
     dX = _out(dX, (m, k), _BF16, "dX", dev) if want_dX else None
-    ws, nb, _held = _scratch(lib.multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, nseg), dev, workspace)
+    ws, nb, _held = _scratch(multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, nseg), dev, workspace)
     _check(lib.multi_lora_mxfp4_linear_bwd(dY.data_ptr(), X.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                            adapters.data_ptr(), num_adapters, seg_off.data_ptr(), seg_adapter.data_ptr(),
                                            nseg, S.data_ptr(), keep_bits.data_ptr(), m, k, n, r_max,

@@ -127,7 +127,9 @@ def test_sizes():
         assert lib.lora_mxfp4_codes_size(k, n) == want
         assert lib.lora_mxfp4_scales_size(k, n) == want // 16
     assert lib.lora_mxfp4_codes_size(0, 8) == 0 and lib.lora_mxfp4_codes_size(8, -1) == 0
-    assert lf.lora_mxfp4_linear_bwd_workspace_size(0, 64, 64, 8) > 0      # zero dA and dB are still written
+    # without rows the weight is not read: the bf16 layer's scratch alone
+    assert lf.lora_mxfp4_linear_bwd_workspace_size(0, 64, 64, 8) == _lib.lora_linear_bwd_workspace_size(0, 64, 64, 8)
+    assert lf.lora_mxfp4_linear_bwd_workspace_size(8192, 64, 64, 8) > 0
     assert lf.lora_mxfp4_frozen_fwd_workspace_size(0, 64, 64) == 0
     assert lf.lora_mxfp4_frozen_fwd_workspace_size(-1, 64, 64) == 0
 
