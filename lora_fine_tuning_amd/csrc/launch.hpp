@@ -291,20 +291,18 @@ struct MxGemmPlan {
     int SK, jobs;          // > 0: the product's launch also forms S = X A, in SK partial sums, by `jobs` work-groups
     size_t spart_bytes;
 };
-// r == 0: no adapter.  kMxMixed: S comes from F1, and the partial sums go to
-// launch_mxfp4_join.
+// r == 0: no adapter.  kMxMixed: rows in nseg segments, r the largest rank.
 enum MxForm { kMxPlain = 0, kMxMixed = 1 };
 struct MxDropout {
-    float p;
     uint64_t seed, offset;
     uint32_t *keep;  // NULL: no mask is applied or written
 };
-MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form);
-// S and drop.keep: written where the plan forms S (SK > 0), else S is read (r > 0).  Y NULL: the
-// product's partial sums alone (kMxMixed, with r = 0 here).
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form, int nseg = 0);
+// The product and the launch that finishes it.  S and drop.keep: written where the
+// plan forms S (SK > 0), else S is read (src.r > 0).
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
-                             int n, const void *A, const void *B, int r, float alpha, const MxDropout &drop, float *S,
-                             void *Y, float *part, float *spart, hipStream_t stream);
+                             int n, const AdapterSource &src, const MxDropout &drop, float *S, void *Y, float *part,
+                             float *spart, hipStream_t stream);
 
 // dX = dY W'^T (+ scale keep.(dS A^T)) straight from the packed weight
 // (mxfp4_gemm_t.hip).
@@ -319,9 +317,10 @@ hipError_t launch_mxfp4_gemm_t(const MxGemmTPlan &pl, const void *dY, const void
                                int n, void *dX, float *part, hipStream_t stream);
 
 // The partial sums of either product ([KS][m][n]) and the adapters' term
-// (mxfp4_join.hip): up for Y, with segments only; otherwise for dX.
-hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, const float *S, int RS,
-                             const uint32_t *keep, const AdapterSource &src, void *Y, hipStream_t stream);
+// (mxfp4_join.hip): up for Y, with segments only; otherwise for dX.  SK > 0: S is
+// the sum of SK partial sums ([SK][m][RS rounded up to 4]), and written.
+hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, float *S, int RS, int SK,
+                             const float *spart, const uint32_t *keep, const AdapterSource &src, void *Y, hipStream_t stream);
 
 // The layers' low-rank steps alone (api.cpp), in a workspace of the bf16 layer's
 // size.  B1 and B2 write dA, dB and dS (m x r fp32, in the workspace, where

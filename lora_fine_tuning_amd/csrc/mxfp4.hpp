@@ -80,10 +80,9 @@ inline double expanded_us(int64_t m, int64_t out, int64_t depth, double values) 
 // `find`'s answers for the shapes a thread asked for last (a plan takes a few
 // microseconds to find, a call asks twice, and a program's shapes come back).
 template <class Plan, class Find>
-Plan remembered(int64_t m, int64_t k, int64_t n, int tag, Find find) {
+Plan remembered(int64_t m, int64_t k, int64_t n, int64_t tag, Find find) {
     struct Known {
-        int64_t m, k, n;
-        int tag;
+        int64_t m, k, n, tag;
         Plan plan;
     };
     thread_local Known known[64] = {};

@@ -79,7 +79,7 @@ extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, c
     REQ_WORKSPACE(lora_mxfp4_frozen_fwd_workspace_size(m, k, n));
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, 0, kMxPlain);
     if (pl.kind) {
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, MxDropout{}, nullptr, Y,
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, AdapterSource{}, MxDropout{}, nullptr, Y,
                                  (float *)workspace, nullptr, stream), "MXFP4 product launch");
         return LORA_OK;
     }
@@ -101,8 +101,8 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
         HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, dX, (float *)workspace, stream),
                "MXFP4 transposed product launch");
         if (pl.finish)
-            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, nullptr, 0, nullptr,
-                                     AdapterSource{}, dX, stream), "MXFP4 sum launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, nullptr, 0, 0,
+                                     nullptr, nullptr, AdapterSource{}, dX, stream), "MXFP4 sum launch");
         return LORA_OK;
     }
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
@@ -146,8 +146,9 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
     if (pl.kind) {
         char *rest = ws_at(workspace, align_up(pl.part_bytes));
         if (pl.SK == 0) CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, rest, stream));
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, A, B, r, alpha,
-                                 MxDropout{p, seed, offset, keep_bits}, S, Y, (float *)workspace, (float *)rest, stream), "MXFP4 product launch");
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n,
+                                 single_source(A, B, nullptr, nullptr, r, alpha, p), MxDropout{seed, offset, keep_bits}, S,
+                                 Y, (float *)workspace, (float *)rest, stream), "MXFP4 product launch");
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
@@ -188,8 +189,8 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
         if (dX != nullptr) {
             HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
                    "MXFP4 transposed product launch");
-            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, dS, r,
-                                     p == 0.0f ? nullptr : keep_bits, src, dX, stream), "MXFP4 sum launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, r, 0,
+                                     nullptr, p == 0.0f ? nullptr : keep_bits, src, dX, stream), "MXFP4 sum launch");
         }
         return LORA_OK;
     }
@@ -203,9 +204,9 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
 extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                       int32_t num_adapters, int32_t num_segments) {
     if (!sizes_ok(m, k, n) || m == 0 || r_max < 1) return 0;
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed);
-    return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) +
-           multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed, num_segments);
+    const size_t layer = multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    return pl.kind ? align_up(pl.part_bytes) + std::max(pl.spart_bytes, layer) : expanded_bytes(m, k, n) + layer;
 }
 
 extern "C" size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
@@ -234,15 +235,13 @@ extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *co
     REQ_PTR(S, 4);
     REQ_PTR(keep_bits, 4);
     REQ_WORKSPACE(multi_lora_mxfp4_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments));
-    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed);
+    const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed, num_segments);
     if (pl.kind) {
         const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
-        CHECK(multi_forward_s_only(X, src, m, k, seed, offset, S, keep_bits, ws_at(workspace, align_up(pl.part_bytes)),
-                                   stream));
-        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, nullptr, nullptr, 0, 0.f, MxDropout{}, nullptr, nullptr,
-                                 (float *)workspace, nullptr, stream), "MXFP4 product launch");
-        HIPCHK(launch_mxfp4_join(true, (const float *)workspace, pl.KS, (int)m, (int)n, S, r_max, nullptr, src, Y, stream),
-               "MXFP4 sum launch");
+        char *rest = ws_at(workspace, align_up(pl.part_bytes));
+        if (pl.SK == 0) CHECK(multi_forward_s_only(X, src, m, k, seed, offset, S, keep_bits, rest, stream));
+        HIPCHK(launch_mxfp4_gemm(pl, X, codes, scales, (int)m, (int)k, (int)n, src, MxDropout{seed, offset, keep_bits}, S,
+                                 Y, (float *)workspace, (float *)rest, stream), "MXFP4 product launch");
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
@@ -281,8 +280,8 @@ extern "C" lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X
         if (dX != nullptr) {
             HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
                    "MXFP4 transposed product launch");
-            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, dS, r_max, keep_bits, src, dX,
-                                     stream), "MXFP4 sum launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, r_max, 0,
+                                     nullptr, keep_bits, src, dX, stream), "MXFP4 sum launch");
         }
         return LORA_OK;
     }

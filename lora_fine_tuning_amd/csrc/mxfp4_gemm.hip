@@ -51,12 +51,18 @@ struct MxGemmParams {
     const uint16_t *B;   // r x N
     int r;
     float alpha;
-    const uint16_t *A;   // partial sums of S = X A by further work-groups (nullptr: none)
-    float *spart;        // [SK][M][rs], rs = r rounded up to 4
-    int rs, SK, jobs;        // partial sums; work-groups that form them (a multiple of 8)
-    uint32_t *keep;          // their dropout mask, M x ceil(K / 32) words, written here (nullptr: none)
+    // partial sums of S = X A by further work-groups
+    const uint16_t *A;
+    float *spart;     // [SK][M][rs], rs = r rounded up to 4
+    int rs, SK, jobs; // partial sums; work-groups that form them (a multiple of 8)
+    uint32_t *keep;   // their dropout mask, M x ceil(K / 32) words, written here (nullptr: none)
     uint64_t seed, offset;
-    uint32_t drop;           // threshold of the mask's 16-bit numbers
+    uint32_t drop;    // threshold of the mask's 16-bit numbers
+    // rows in segments with an adapter each (nullptr: one adapter); r is then the largest rank
+    const lora_adapter *adapters;
+    const int64_t *seg_off;
+    const int32_t *seg_adapter;
+    int num_adapters, nseg;
 };
 
 constexpr int kSK = 1024;  // k of one partial sum of S
@@ -73,14 +79,15 @@ struct MxTile {
     static constexpr int RED = (WK - 1) * WM * WN * MB * NB * 1024;
     static constexpr int LDS = SPARE + 1024 > RED ? SPARE + 1024 : RED;
     static constexpr int SHARE = 160 * 1024 / LDS < 3 ? 160 * 1024 / LDS : 3;  // work-groups that a CU holds
-    // 16-rank tiles of a job of S (few enough registers for SHARE work-groups a CU)
-    static constexpr int RT = MB > 2 || XR == 4 ? 2 : 4;
+    // 16-rank tiles of a job of S (every operand of it is in registers at once: few
+    // where SHARE work-groups have to fit a CU)
+    static constexpr int RT = SHARE > 2 ? 1 : 2;
     static constexpr bool RIDE = WM == 1;  // the adapter's S rides along, a second launch adds alpha S B
     static_assert(SU <= NW && LDS <= 160 * 1024, "tile does not fit");
 };
 
-// One work-group's share of keep.X A: k from kSK * (job % SK), 128 a wave, the row
-// tile job / SK % tiles_m, and 16 RT ranks.  X's rows and A's columns come straight from memory
+// One work-group's share of keep.X A: 1024 of k (128 a wave), up to TM rows of one
+// adapter and 16 RT ranks.  X's rows and A's columns come straight from memory
 // (8 two-byte loads make a 16-rank operand: A's rows are r values long), every
 // load of a wave before its first use; the waves are added in LDS in wave order.
 // A lane's 8 elements of X are one counter of the dropout mask and one byte of
@@ -91,52 +98,82 @@ __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *sme
     static_assert(T::NW == 8 && T::WM == 1 && MB * RT <= 8 && 8 * MB * RT * 1024 <= T::LDS, "no room for the partial sums");
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int ks = job % P.SK, m0 = job / P.SK % P.tiles_m * T::TM, r0 = job / (P.SK * P.tiles_m) * 16 * RT;
-    if (r0 >= P.r) return;  // (the count is rounded up)
+    const int ks = job % P.SK;
+    int rest = job / P.SK, m0, mend = P.M, r = P.r;
+    const uint16_t *A = P.A;
+    uint32_t drop = P.drop;
+    if (P.adapters != nullptr) {  // a segment's rows in tiles; most segments have fewer than the batch
+        const int seg = rest % P.nseg;
+        rest /= P.nseg;
+        const int which = P.seg_adapter[seg];
+        if (which < 0 || which >= P.num_adapters) return;
+        const lora_adapter ad = P.adapters[which];
+        if (ad.r < 1 || ad.r > P.r) return;
+        const int64_t lo = max((int64_t)0, P.seg_off[seg]) + rest % P.tiles_m * T::TM;
+        mend = (int)min(P.seg_off[seg + 1], (int64_t)P.M);
+        if (lo >= mend) return;
+        m0 = (int)lo;
+        A = (const uint16_t *)ad.A;
+        r = ad.r;
+        drop = drop_threshold(ad.p);
+    } else {
+        m0 = rest % P.tiles_m * T::TM;
+    }
+    const int r0 = rest / P.tiles_m * 16 * RT;
+    if (r0 >= r) return;  // (the count is rounded up)
+    mend = min(mend, m0 + T::TM);
     const int k0 = ks * kSK + wave * (kSK / 8);
-    // rows past M read as zeros; the host keeps A under 2 GiB
-    const __amdgpu_buffer_rsrc_t rX = make_rsrc(P.X + (size_t)m0 * P.K, (uint64_t)min(P.M - m0, T::TM) * P.K * 2u);
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(P.A, (uint64_t)P.K * P.r * 2u);
+    // rows past the end read as zeros; the host keeps A under 2 GiB
+    const __amdgpu_buffer_rsrc_t rX = make_rsrc(P.X + (size_t)m0 * P.K, (uint64_t)(mend - m0) * P.K * 2u);
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, (uint64_t)P.K * r * 2u);
     f32x4_t acc[MB][RT];
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    constexpr int J = kSK / 8 / 32;
+    uint4 x[J][MB];
+    uint32_t h[J][RT][8];
 #pragma unroll
-    for (int j = 0; j < kSK / 8 / 32; ++j) {
+    for (int j = 0; j < J; ++j) {
         const int k = k0 + 32 * j + 8 * lg;
-        uint4 x[MB], w[RT];
 #pragma unroll
         for (int a = 0; a < MB; ++a)
-            x[a] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                       rX, k < P.K ? ((uint32_t)(16 * a + l16) * (uint32_t)P.K + (uint32_t)k) * 2u : kOOB, 0, 0));
+            x[j][a] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                          rX, k < P.K ? ((uint32_t)(16 * a + l16) * (uint32_t)P.K + (uint32_t)k) * 2u : kOOB, 0, 0));
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const int rank = r0 + 16 * t + l16;
-            uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                h[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
-                    rA, rank < P.r && k < P.K ? ((uint32_t)(k + e) * (uint32_t)P.r + (uint32_t)rank) * 2u : kOOB, 0, 0);
-            w[t] = make_uint4(pack2(h[0], h[1]), pack2(h[2], h[3]), pack2(h[4], h[5]), pack2(h[6], h[7]));
+                h[j][t][e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
+                    rA, rank < r && k < P.K ? ((uint32_t)(k + e) * (uint32_t)r + (uint32_t)rank) * 2u : kOOB, 0, 0);
         }
-        if (P.keep != nullptr) {
-            const uint32_t row_bytes = (uint32_t)((P.K + 31) / 32) * 4u;
+    }
+    if (P.keep != nullptr) {
+        const uint32_t row_bytes = (uint32_t)((P.K + 31) / 32) * 4u;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int a = 0; a < MB; ++a) {
-                const int row = m0 + 16 * a + l16;
-                const uint32_t byte =
-                    k < P.K ? keep_byte(P.offset + (uint64_t)row * (uint64_t)P.K + (uint64_t)k, P.seed, P.drop) : 0u;
-                x[a] = apply_keep(x[a], byte);
-                if (r0 == 0 && row < P.M && (uint32_t)k / 8u < row_bytes)
+                const int k = k0 + 32 * j + 8 * lg, row = m0 + 16 * a + l16;
+                uint32_t byte = 0xFFu;
+                if (drop > 0) byte = keep_byte(P.offset + (uint64_t)row * (uint64_t)P.K + (uint64_t)k, P.seed, drop);
+                if (k >= P.K) byte = 0u;
+                x[j][a] = apply_keep(x[j][a], byte);
+                if (r0 == 0 && row < mend && (uint32_t)k / 8u < row_bytes)
                     ((uint8_t *)P.keep)[(size_t)row * row_bytes + k / 8] = (uint8_t)byte;
             }
-        }
-#pragma unroll
-        for (int a = 0; a < MB; ++a)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) acc[a][t] = mfma16x16x32(w[t], x[a], acc[a][t]);
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const uint32_t *q = h[j][t];
+            const uint4 w = make_uint4(pack2(q[0], q[1]), pack2(q[2], q[3]), pack2(q[4], q[5]), pack2(q[6], q[7]));
+#pragma unroll
+            for (int a = 0; a < MB; ++a) acc[a][t] = mfma16x16x32(w, x[j][a], acc[a][t]);
+        }
     f32x4_t *red = (f32x4_t *)smem;
 #pragma unroll
     for (int a = 0; a < MB; ++a)
@@ -149,7 +186,7 @@ __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *sme
 #pragma unroll
     for (int c = 1; c < 8; ++c) sum += red[(c * MB * RT + wave) * 64 + lane];
     const int row = m0 + 16 * (wave / RT) + l16, rank = r0 + 16 * (wave % RT) + 4 * lg;
-    if (row >= P.M) return;
+    if (row >= mend) return;
     if (rank < P.rs) *(f32x4_t *)(P.spart + ((size_t)ks * P.M + row) * P.rs + rank) = sum;  // (zeros past r)
 }
 
@@ -596,13 +633,13 @@ const MxKind kKinds[] = {
 // Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 16.5
 // (16), 300 x 14336 x 4096 45 (48), 1000 x 4096 x 4096 35 (36), 2000 x 4096 x 4096 59
 // (57; expanded 86), 8192 x 4096 x 4096 expanded 201 (192; packed 245).
-static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form) {
+static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form, int nseg) {
     MxGemmPlan best{};
     // (a tile's offsets stay below 2^31 within these)
     if (m <= 0 || k > (1 << 20) || n > (1 << 21) || m > (1 << 19)) return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const double weight = (double)k * n;
-    const double f1 = r > 0 && form == kMxPlain ? 9.0 + (double)m * k * 2 / 4e6 : 0.0;
+    const double f1 = r > 0 ? (form == kMxMixed ? 14.0 : 9.0) + (double)m * k * 2 / 4e6 : 0.0;
     double least = expanded_us(m, n, k, weight) + f1;
     for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
         const MxKind &K = kKinds[kind - 1];
@@ -613,9 +650,11 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form)
         p.tiles_n = (int)cdiv(n, K.tn);
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, stages = cdiv(k, K.kw);
         if (tiles > (1 << 20)) continue;
-        if (r > 0 && K.ranks > 0 && form == kMxPlain) {
+        // a mixed batch's segments take a job for every row tile that they could fill
+        const int64_t jobs = K.ranks > 0 ? cdiv(k, kSK) * p.tiles_m * cdiv(r, K.ranks) * (form == kMxMixed ? nseg : 1) : 0;
+        if (r > 0 && jobs > 0 && (form == kMxPlain || jobs <= 1024)) {
             p.SK = (int)cdiv(k, kSK);
-            p.jobs = (int)cdiv(p.SK * p.tiles_m * cdiv(r, K.ranks), 8) * 8;
+            p.jobs = (int)cdiv(jobs, 8) * 8;
             p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
         }
         for (int want = 1; want <= 16 && want <= stages; ++want) {
@@ -637,13 +676,15 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form)
     return best;
 }
 
-MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form) {
-    return remembered<MxGemmPlan>(m, k, n, 4 * r + (int)form, [&] { return find_plan(m, k, n, r, form); });
+MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form, int nseg) {
+    return remembered<MxGemmPlan>(m, k, n, ((int64_t)nseg << 32) + 4 * r + (int)form,
+                                  [&] { return find_plan(m, k, n, r, form, nseg); });
 }
 
 hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *codes, const void *scales, int m, int k,
-                             int n, const void *A, const void *B, int r, float alpha, const MxDropout &drop, float *S,
-                             void *Y, float *part, float *spart, hipStream_t stream) {
+                             int n, const AdapterSource &src, const MxDropout &drop, float *S, void *Y, float *part,
+                             float *spart, hipStream_t stream) {
+    const int r = src.r;
     MxGemmParams P{};
     P.X = (const uint16_t *)X;
     P.codes = (const uint8_t *)codes;
@@ -660,23 +701,30 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     P.KS = pl.KS;
     P.per = pl.per;
     P.S = r > 0 && !pl.finish ? S : nullptr;
-    P.A = (const uint16_t *)A;
+    P.A = (const uint16_t *)src.A;
     P.spart = spart;
     P.SK = pl.SK;
     P.rs = (r + 3) / 4 * 4;
-    P.B = (const uint16_t *)B;
+    P.B = (const uint16_t *)src.B;
     P.r = r;
-    P.alpha = alpha;
+    P.alpha = src.alpha;
     P.jobs = pl.jobs;
     P.keep = drop.keep;
     P.seed = drop.seed;
     P.offset = drop.offset;
-    P.drop = drop_threshold(drop.p);
+    P.drop = drop_threshold(src.p);
+    P.adapters = src.table;
+    P.seg_off = src.seg_off;
+    P.seg_adapter = src.seg_adapter;
+    P.num_adapters = src.num_adapters;
+    P.nseg = src.num_segments;
     int slot = prof_begin("mxfp4_gemm", stream);
     const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
-    if (e != hipSuccess || !pl.finish || Y == nullptr) return e;
-    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)B, alpha, drop_scale(drop.p), S,
+    if (e != hipSuccess || !pl.finish) return e;
+    if (src.table != nullptr)
+        return launch_mxfp4_join(true, part, pl.KS, m, n, S, r, pl.SK, spart, nullptr, src, Y, stream);
+    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)src.B, src.alpha, drop_scale(src.p), S,
                            (uint16_t *)Y};
     slot = prof_begin("mxfp4_finish", stream);
     hipLaunchKernelGGL(mxfp4_finish_kernel, dim3((unsigned)((n + 127) / 128), (unsigned)((m + 15) / 16)), dim3(256), 0, stream,

@@ -5,7 +5,8 @@
 //   down:  dX = sum_s part_s + s keep.(dS A^T)       (A: N x r, s = 1 / (1 - p))
 //
 // for one adapter (down) or for segments of rows with an adapter each (both; one
-// adapter's up form has S itself to sum and stands with its product).  A
+// adapter's up form stands with its product).  Up, S is given, or it is summed here
+// from the product's partial sums of keep.X A, and the first column tile writes it.  A
 // work-group takes 16 rows of 128 columns, a wave 32 columns (one word of keep a
 // row); it meets the segments of its rows one after the other.  32 ranks are one
 // MFMA step, the scaled S split into bf16 hi + lo.  A lane adds an adapter's sums
@@ -24,8 +25,10 @@ namespace {
 struct MxJoinParams {
     const float *part;  // [KS][M][N]
     int KS, M, N;
-    const float *S;  // M x RS; r == 0 and no table: no adapter
+    float *S;  // M x RS; r == 0 and no table: no adapter
     int RS;
+    int SK;  // > 0: S is summed from spart and written
+    const float *spart;
     const uint16_t *R;  // the adapter's B or A
     int r;
     float scale;
@@ -48,15 +51,32 @@ __global__ __launch_bounds__(256) void mxfp4_join_kernel(MxJoinParams P) {
     const bool live0 = row < P.M && col < P.N, live1 = row < P.M && col + 16 < P.N;
     f32x4_t total[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
 
-    auto adapter = [&](const uint16_t *R, int r, float scale, bool mine) {
+    auto adapter = [&](const uint16_t *R, int r, float scale, float undrop, bool mine) {
         f32x4_t low[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 1
         for (int r0 = 0; r0 < r; r0 += 32) {
             const int rb = r0 + 8 * lg, left = r - rb;  // this lane's ranks rb .. rb+7
-            const float *s = P.S + (size_t)row * P.RS + rb;
+            float *s = P.S + (size_t)row * P.RS + rb;
             float v[8];
+            if (UP && P.SK > 0) {
+                const int rs = (P.RS + 3) & ~3;
+                f32x4_t u[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+                const float *ps = P.spart + (size_t)row * rs + rb;
+#pragma unroll 4
+                for (int c = 0; c < P.SK; ++c) {
+                    if (mine && left > 0) u[0] += *(const f32x4_t *)(ps + (size_t)c * P.M * rs);
+                    if (mine && left > 4) u[1] += *(const f32x4_t *)(ps + (size_t)c * P.M * rs + 4);
+                }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = mine && e < left ? scale * s[e] : 0.f;
+                for (int e = 0; e < 8; ++e) {
+                    const float x = e < left ? undrop * u[e / 4][e % 4] : 0.f;  // (past the rank nothing was written)
+                    if (mine && blockIdx.x == 0 && wave == 0 && rb + e < P.RS) s[e] = x;
+                    v[e] = scale * x;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = mine && e < left ? scale * s[e] : 0.f;
+            }
             uint4 a[2];
             if constexpr (UP) {
                 // rank k's 64 bytes, piece d at d ^ turn(k); the transposing reads give
@@ -103,6 +123,8 @@ __global__ __launch_bounds__(256) void mxfp4_join_kernel(MxJoinParams P) {
                 low[t] = mfma16x16x32(a[t], lo, low[t]);
             }
         }
+        if (UP && P.SK > 0 && blockIdx.x == 0 && wave == 0 && mine)  // S's columns past the rank's last 32
+            for (int c = ((r + 31) & ~31) + lg; c < P.RS; c += 4) P.S[(size_t)row * P.RS + c] = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -124,10 +146,10 @@ __global__ __launch_bounds__(256) void mxfp4_join_kernel(MxJoinParams P) {
             const lora_adapter ad = P.adapters[which];
             if (ad.r < 1 || ad.r > P.RS) continue;
             adapter((const uint16_t *)(UP ? ad.B : ad.A), ad.r, UP ? ad.alpha : drop_scale(ad.p),
-                    row >= lo && row < hi);
+                    drop_scale(ad.p), row >= lo && row < hi);
         }
     } else {
-        adapter(P.R, P.r, P.scale, row < P.M);
+        adapter(P.R, P.r, P.scale, 1.f, row < P.M);
     }
 
     f32x4_t acc[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
@@ -158,8 +180,8 @@ __global__ __launch_bounds__(256) void mxfp4_join_kernel(MxJoinParams P) {
 
 }  // namespace
 
-hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, const float *S, int RS,
-                             const uint32_t *keep, const AdapterSource &src, void *Y, hipStream_t stream) {
+hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, float *S, int RS, int SK,
+                             const float *spart, const uint32_t *keep, const AdapterSource &src, void *Y, hipStream_t stream) {
     MxJoinParams P{};
     P.part = part;
     P.KS = KS;
@@ -167,6 +189,8 @@ hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, c
     P.N = n;
     P.S = S;
     P.RS = RS;
+    P.SK = SK;
+    P.spart = spart;
     P.R = (const uint16_t *)(up ? src.B : src.A);
     P.r = src.r;
     P.scale = up ? src.alpha : drop_scale(src.p);

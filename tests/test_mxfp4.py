@@ -548,6 +548,39 @@ def test_mixed_matches_definition(m):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n,nseg,r_max", [(1, 136, 72, 1, 8), (16, 4104, 264, 16, 64), (40, 1032, 520, 7, 128), (100, 264, 136, 3, 256),
+                                              (128, 2056, 264, 5, 40), (200, 520, 136, 300, 16), (1000, 520, 264, 4, 33)])
+def test_mixed_s_and_mask_are_whole(m, k, n, nseg, r_max):
+    # S of every row, zeros past its rank, and every bit of the mask
+    g = torch.Generator().manual_seed(m + nseg)
+    X, W4, W, _, _, dY = layer_case(m, k, n, 8, seed=260 + m)
+    ranks = [1 + int(torch.randint(0, r_max, (1,), generator=g)) for _ in range(min(nseg, 6))] + [r_max]
+    ps = [(0.0, 0.1, 0.3)[i % 3] for i in range(len(ranks))]
+    As = [bf16_randn((k, r), k ** -0.5, g) for r in ranks]
+    Bs = [bf16_randn((r, n), 0.02 ** 0.5, g) for r in ranks]
+    cuts = torch.randint(0, m + 1, (nseg - 1,), generator=g).sort().values.tolist()
+    seg_off = [0, *cuts, m]
+    seg_ad = torch.randint(0, len(ranks), (nseg,), generator=g).tolist()
+    Ad, Bd = [a.cuda() for a in As], [b.cuda() for b in Bs]  # (a table holds addresses only)
+    table = lf.adapter_table(Ad, Bd, [0.5] * len(ranks), ps)
+    so = torch.tensor(seg_off, dtype=torch.int64, device="cuda")
+    sa = torch.tensor(seg_ad, dtype=torch.int32, device="cuda")
+    S = torch.full((m, r_max), float("nan"), device="cuda")
+    keep = torch.full((m, (k + 31) // 32), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+    Y, S, keep = lf.multi_lora_mxfp4_linear_fwd(X.cuda(), W4, table, len(ranks), so, sa, r_max, 3, 8, S=S, keep_bits=keep)
+    torch.cuda.synchronize()
+    for s, a in enumerate(seg_ad):
+        lo, hi = seg_off[s], seg_off[s + 1]
+        if hi == lo:
+            continue
+        want, slack = layer_reference(X[lo:hi], W, As[a], Bs[a], dY[lo:hi], 0.5, ps[a], 3, 8 + lo * k)
+        near(f"Y[{s}]", Y[lo:hi], want["Y"], slack["Y"])
+        got = f64(S[lo:hi])
+        assert (np.abs(got[:, :ranks[a]] - want["S"]) <= slack["S"] + 1e-30).all() and not got[:, ranks[a]:].any()
+        assert torch.equal(keep[lo:hi], lf.lora_dropout_mask(3, 8 + lo * k, hi - lo, k, ps[a]))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [5, 77, 300])
 def test_mixed_short_segments(m):
     # many segments within one tile of rows, empty ones among them, ranks 1 to 256, unaligned matrices;
