@@ -22,9 +22,11 @@
 // With the shapes for up to 64 rows the adapter rides along: keep and keep.X A
 // are formed by further work-groups of the same launch (partial sums over 1024 of
 // k each), and the finishing launch adds those, writes S and adds alpha S B.  F1
-// took 9 to 14 us before the product.  With the shapes for more rows F1 forms S
-// first, and they add alpha S B in their own epilogue, as rank-deep MFMA steps,
-// where k is not split.
+// took 9 to 14 us before the product.  A mixed batch's segments have such
+// work-groups too, up to 1024 of them (every segment one for each row tile that it
+// could fill, which most leave at once), and mxfp4_join.hip finishes.  With the
+// shapes for more rows F1 forms S first, and they add alpha S B in their own
+// epilogue, as rank-deep MFMA steps, where k is not split.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -151,15 +153,26 @@ __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *sme
         }
     }
     if (P.keep != nullptr) {
+        uint32_t bytes[J][MB];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int a = 0; a < MB; ++a) bytes[j][a] = 0xFFu;
+        if (drop > 0) {  // (one branch: the generators' chains interleave)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int a = 0; a < MB; ++a)
+                    bytes[j][a] = keep_byte(P.offset + (uint64_t)(m0 + 16 * a + l16) * (uint64_t)P.K + (uint64_t)(k0 + 32 * j + 8 * lg),
+                                            P.seed, drop);
+        }
         const uint32_t row_bytes = (uint32_t)((P.K + 31) / 32) * 4u;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int a = 0; a < MB; ++a) {
                 const int k = k0 + 32 * j + 8 * lg, row = m0 + 16 * a + l16;
-                uint32_t byte = 0xFFu;
-                if (drop > 0) byte = keep_byte(P.offset + (uint64_t)row * (uint64_t)P.K + (uint64_t)k, P.seed, drop);
-                if (k >= P.K) byte = 0u;
+                const uint32_t byte = k < P.K ? bytes[j][a] : 0u;
                 x[j][a] = apply_keep(x[j][a], byte);
                 if (r0 == 0 && row < mend && (uint32_t)k / 8u < row_bytes)
                     ((uint8_t *)P.keep)[(size_t)row * row_bytes + k / 8] = (uint8_t)byte;
