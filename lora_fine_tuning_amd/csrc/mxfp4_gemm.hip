@@ -15,9 +15,10 @@
 // NS - 1 stages ahead.  X rows take 256 bytes a chunk; piece 4 g + j (16 bytes)
 // of row i sits at place (4 j + g) ^ (i mod 16).  A 16-byte read serves lanes
 // 0-3, 12-15 and 20-27 (and so on) together: with g in the low bits of the place
-// those 16 lanes fall on 16 different bank ranges (with j there, on 8).  Waves along k are added in LDS in wave order.  Where the tiles would
-// leave CUs idle, work-groups split k further: each slice writes fp32 partial
-// sums and a finishing launch adds them in slice order.
+// those 16 lanes fall on 16 different bank ranges (with j there, on 8).  Waves
+// along k are added in LDS in wave order.  Where the tiles would leave CUs idle,
+// work-groups split k further: each slice writes fp32 partial sums and a finishing
+// launch adds them in slice order.
 //
 // With the shapes for up to 64 rows the adapter rides along: keep and keep.X A
 // are formed by further work-groups of the same launch (partial sums over 1024 of
@@ -112,7 +113,7 @@ __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *sme
         const lora_adapter ad = P.adapters[which];
         if (ad.r < 1 || ad.r > P.r) return;
         const int64_t lo = max((int64_t)0, P.seg_off[seg]) + rest % P.tiles_m * T::TM;
-        mend = (int)min(P.seg_off[seg + 1], (int64_t)P.M);
+        mend = (int)min(max((int64_t)0, P.seg_off[seg + 1]), (int64_t)P.M);
         if (lo >= mend) return;
         m0 = (int)lo;
         A = (const uint16_t *)ad.A;

@@ -581,6 +581,30 @@ def test_mixed_s_and_mask_are_whole(m, k, n, nseg, r_max):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seg_off,seg_ad", [([0, -(1 << 33) + 5, 1 << 40, 20], [0, 1, 0]), ([0, 30, 10, 20], [1, 0, 1]),
+                                            ([-7, 4, 4, 1 << 33], [0, 9, -3]), ([5, 6, 7, 8], [1, 1, 0])])
+def test_bad_segment_tables_stay_in_bounds(seg_off, seg_ad):
+    # offsets out of order, out of range, adapters that are not there: values of those rows are undefined, but
+    # nothing outside the buffers' m rows is written
+    m, k, n = 20, 264, 136
+    g = torch.Generator().manual_seed(8)
+    X, W4, W, _, _, dY = layer_case(m, k, n, 8, seed=8)
+    As = [bf16_randn((k, r), 1.0, g).cuda() for r in (8, 40)]
+    Bs = [bf16_randn((r, n), 1.0, g).cuda() for r in (8, 40)]
+    table = lf.adapter_table(As, Bs, [1.0, 2.0], [0.1, 0.0])
+    so = torch.tensor(seg_off, dtype=torch.int64, device="cuda")
+    sa = torch.tensor(seg_ad, dtype=torch.int32, device="cuda")
+    Y = torch.full((m + 80, n), 5.0, dtype=torch.bfloat16, device="cuda")
+    S = torch.full((m + 80, 40), 5.0, device="cuda")
+    keep = torch.full((m + 80, (k + 31) // 32), 5, dtype=torch.int32, device="cuda")
+    mid = slice(40, 40 + m)
+    lf.multi_lora_mxfp4_linear_fwd(X.cuda(), W4, table, 2, so, sa, 40, 3, 8, Y=Y[mid], S=S[mid], keep_bits=keep[mid])
+    torch.cuda.synchronize()
+    for t in (Y, S, keep):
+        assert (t[:40] == 5).all() and (t[40 + m:] == 5).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [5, 77, 300])
 def test_mixed_short_segments(m):
     # many segments within one tile of rows, empty ones among them, ranks 1 to 256, unaligned matrices;
@@ -713,6 +737,8 @@ def test_captured_mixed_layers_side_by_side(m):
             out = run()
         sides.append((run, stream, graph, out, X, dY))
     for rep in range(3):
+        # (the segment table is read when the kernels run: a replay follows it)
+        so[1] = (m // 2, 0, m)[rep]
         for _, _, _, _, X, dY in sides:
             X.copy_(bf16_randn(X.shape, 1.0, g))
             dY.copy_(bf16_randn(dY.shape, 1.0, g))
