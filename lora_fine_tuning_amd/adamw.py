@@ -185,13 +185,22 @@ class LoraAdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        for group in self.param_groups:
-            calls = {}  # the tensors of one call share a device, types and a step
+        for group in self.param_groups:  # refuse before anything has changed
             for p in group["params"]:
                 if p.grad is None:
                     continue
                 if p.grad.is_sparse:
                     raise ValueError("gradients must be dense")
+                if not p.is_contiguous():
+                    raise ValueError("parameters must be contiguous")
+                held = self.state[p]["m"].numel() if self.state.get(p) else p.numel()
+                if not p.numel() == p.grad.numel() == held:
+                    raise ValueError(f"a parameter had {held} values when its moments were made, now {p.numel()}")
+        for index, group in enumerate(self.param_groups):
+            calls = {}  # the tensors of one call share a device, types and a step
+            for place, p in enumerate(group["params"]):
+                if p.grad is None:
+                    continue
                 st = self.state[p]
                 if not st:
                     st.update(self._new_state(p, group))
@@ -199,49 +208,44 @@ class LoraAdamW(torch.optim.Optimizer):
                 if not group["capturable"]:
                     st["step"] += 1
                     key += (st["step"],)
-                calls.setdefault(key, []).append(p)
+                calls.setdefault(key, []).append((place, p))
             if group["capturable"]:
                 for device in {key[0] for key in calls}:
                     self._counter(group, device).add_(1)
-            for ps in calls.values():
-                self._step(ps, group)
+            for key, ps in calls.items():
+                self._step(group, (index, *key[:4], *(place for place, _ in ps)), [p for _, p in ps])
         return loss
 
-    def _table(self, ps) -> AdamwTable:
-        """The table of these parameters, built at their first step together; later steps
-        read every address anew (gradients are new tensors, parameters may have moved)."""
+    def _table(self, slot, ps) -> AdamwTable:
+        """The table of these parameters.  Its records stay with the optimizer as
+        scratch; every address in them is read anew at each step (gradients are new
+        tensors, parameters may have moved)."""
         states = [self.state[p] for p in ps]
         grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in ps]
         tables = self.__dict__.setdefault("_tables", {})
-        key = tuple(map(id, ps)) + (ps[0].dtype, grads[0].dtype)
-        table = tables.get(key)
-        if table is None:
+        table = tables.get(slot)
+        if table is None or table.records[:, _N].tolist() != [p.numel() for p in ps]:
             each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
             table = adamw_table([p.detach() for p in ps], grads, each("m"), each("v"), m_scales=each("m_scale"),
                                 v_scales=each("v_scale"), masters=each("master"), offsets=each("offset"))
-            table.params = ps  # alive, so that their ids stay theirs
             if len(tables) >= 64:
                 tables.clear()
-            tables[key] = table
+            tables[slot] = table
             return table
         rec = table.records
-        for p, g, st, n in zip(ps, grads, states, rec[:, _N].tolist()):
-            if not p.is_contiguous():
-                raise ValueError("parameters must be contiguous")
-            if not n == p.numel() == g.numel() == st["m"].numel():
-                raise ValueError(f"a parameter had {n} values when its moments were made, now {p.numel()}")
         rec[:, _PARAM] = [p.data_ptr() for p in ps]
         rec[:, _GRAD] = [g.data_ptr() for g in grads]
         for name, col in (("m", _M), ("v", _V), ("m_scale", _M_SCALE), ("v_scale", _V_SCALE), ("master", _MASTER)):
             if name in states[0]:
                 rec[:, col] = [st[name].data_ptr() for st in states]
+        rec[:, _OFFSET] = [st["offset"] for st in states]
         table.tensors = [grads]
         return table
 
-    def _step(self, ps, group) -> None:
+    def _step(self, group, slot, ps) -> None:
         st = self.state[ps[0]]
         at = dict(step_dev=st["step"]) if group["capturable"] else dict(step=st["step"])
-        lora_adamw_step(self._table(ps), lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
+        lora_adamw_step(self._table(slot, ps), lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
                         eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"], **at)
 
     def load_state_dict(self, state_dict) -> None:

@@ -575,6 +575,26 @@ def test_optimizer_refuses_parameters_of_another_size():
 
 
 @pytest.mark.gpu
+def test_optimizer_follows_moved_parameters():
+    # values that move to other memory between steps, and other parameters dropping out and coming back
+    a, b = model(), model()
+    oa, ob = (lf.LoraAdamW(ps, lr=1e-2, seed=2) for ps in (a, b))
+    for t in range(4):
+        for ps in (a, b):
+            gradients(ps, t)
+            if t == 2:
+                ps[1].grad = None
+        for p in b:
+            p.data = p.data.clone()
+            if p.grad is not None:
+                p.grad = torch.stack([p.grad, p.grad], -1)[..., 0]  # (not contiguous)
+        oa.step()
+        ob.step()
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
 def test_one_tensor_past_32_bits():
     # 2^32 values and a bit: its last values step like a small tensor's at the same counters
     n, tail = (1 << 32) + 515, 4099
