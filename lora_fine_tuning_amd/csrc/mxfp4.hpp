@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "device_common.hpp"
@@ -75,6 +76,14 @@ inline hipError_t allow_lds(const void *fn, size_t bytes, std::atomic<uint64_t> 
 inline double expanded_us(int64_t m, int64_t out, int64_t depth, double values) {
     const int64_t tiles = ((m + 255) / 256) * ((out + 255) / 256);
     return 6.0 + values * 2.53 / 6e6 + (double)((tiles + 255) / 256 * ((depth + 63) / 64)) * (tiles <= 128 ? 1.1 : 1.4);
+}
+
+// Microseconds of `groups` work-groups, `slots` at a time, of which each takes `one`
+// and all read the weight's packed bytes once at 6 TB/s between them.
+inline double rounds_us(int64_t groups, int64_t slots, double one, double values) {
+    const int64_t full = groups / slots, rest = groups % slots;
+    const double each = values * 0.53 / 6e6 / (double)groups;
+    return (double)full * std::max(one, each * (double)slots) + (rest > 0 ? std::max(one, each * (double)rest) : 0.0);
 }
 
 // `find`'s answers for the shapes a thread asked for last (a plan takes a few

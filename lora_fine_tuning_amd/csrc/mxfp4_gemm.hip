@@ -640,8 +640,9 @@ const MxKind kKinds[] = {
 
 // The cheapest of the tile shapes, each with k split as far as pays, and of
 // expanding the weight for the bf16 product, by a model of their times:
-//   shape:  3.5 us + rounds (stages x stage time + 1 us), at least the weight's
-//           bytes at 6 TB/s; a finishing launch 3.5 us and its partial sums at 8 TB/s
+//   shape:  3.5 us + rounds of work-groups (stages x stage time + 1 us each, at least
+//           their share of the weight's bytes at 6 TB/s); a finishing launch 3.5 us
+//           and its partial sums at 8 TB/s
 //   expand: expanded_us
 //   S apart: 9 us and X's bytes at 4 TB/s (its work-groups beside a shape's add to the rounds)
 // Measured, model in brackets: 1 x 4096 x 4096 5.6 us (5.9), 48 x 14336 x 4096 16.5
@@ -678,8 +679,7 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form,
             p.finish = p.KS > 1 || (r > 0 && (K.ranks > 0 || form == kMxMixed));
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
             const int64_t groups = tiles * p.KS + p.jobs, slots = 256 * K.share;
-            double t = (double)cdiv(groups, slots) * (p.per * K.stage + 1.0);
-            t = 3.5 + std::max(t, weight * 0.53 / 6e6) + (p.jobs == 0 ? f1 : 0.0);
+            double t = 3.5 + rounds_us(groups, slots, p.per * K.stage + 1.0, weight) + (p.jobs == 0 ? f1 : 0.0);
             if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 8e6;
             if (t < least) {
                 least = t;

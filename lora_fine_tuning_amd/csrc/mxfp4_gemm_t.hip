@@ -314,7 +314,7 @@ static MxGemmTPlan find_plan(int64_t m, int64_t k, int64_t n, int r) {
             if (p.KS != want) continue;
             p.finish = p.KS > 1 || r > 0;
             p.part_bytes = p.finish ? (size_t)p.KS * m * k * sizeof(float) : 0;
-            double t = 3.5 + std::max((double)cdiv(tiles * p.KS, 256) * (p.per * K.stage + 1.0), weight * 0.53 / 6e6);
+            double t = 3.5 + rounds_us(tiles * p.KS, 256, p.per * K.stage + 1.0, weight);
             if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 8e6;
             if (t < least) {
                 least = t;
