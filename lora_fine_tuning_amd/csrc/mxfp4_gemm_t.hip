@@ -299,7 +299,7 @@ static MxGemmTPlan find_plan(int64_t m, int64_t k, int64_t n, int r) {
         return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const double weight = (double)k * n;
-    double least = expanded_us(m, k, n, weight);
+    double least = expanded_us(m, k, n, weight) + (r > 0 ? 8.0 : 0.0);
     for (int kind = 1; kind <= (int)(sizeof(kKindsT) / sizeof(kKindsT[0])); ++kind) {
         const MxKindT &K = kKindsT[kind - 1];
         MxGemmTPlan p{};
