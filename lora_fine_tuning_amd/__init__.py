@@ -1,5 +1,6 @@
 """MI355X (gfx950) LoRA linear layer: Y = XW + alpha * (dropout(X) A) B, forward
-and backward, single-adapter and mixed-adapter batches.
+and backward, single-adapter and mixed-adapter batches, over a frozen W in bf16 or
+in MXFP4, and AdamW over the adapters.
 
 The compute lives in liblora_fused.so (hand-written HIP kernels behind the C ABI
 declared in include/lora_fused.h); this package is its thin Python binding.

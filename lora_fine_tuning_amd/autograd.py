@@ -152,11 +152,12 @@ def multi_lora_linear(X, W, seg_off, seg_adapter, As, Bs, alphas, ps, seed: int 
 
 
 class LoraLinear(torch.nn.Module):
-    """A frozen k x n weight, a tensor (kept in bf16) or an Mxfp4Weight, with
-    one LoRA adapter (A k x r, B r x n; B starts at zero).  Dropout draws from the library's counter-based generator under
-    this module's own seed; each training call advances the counter past the
-    elements it used, so successive calls get fresh masks and a rerun from the
-    same state reproduces them.  In eval mode dropout is off."""
+    """A frozen k x n weight, a tensor (kept in bf16) or an Mxfp4Weight, with one
+    LoRA adapter (A k x r, B r x n; B starts at zero).  Dropout draws from the
+    library's counter-based generator under this module's own seed; each training
+    call advances the counter past the elements it used, so successive calls get
+    fresh masks and a rerun from the same state reproduces them.  In eval mode
+    dropout is off."""
 
     def __init__(self, weight, r: int, alpha: float, p: float = 0.0, seed: int = 0):
         super().__init__()
