@@ -19,7 +19,7 @@
 // stage's conversions while the other half's operands come back took 6 to 10%
 // off.  Measured against expanding the weight for the bf16 product, in us: 1 x
 // 4096 x 4096 10 (85), 16 x 4096 x 14336 17 (265), 128 x 4096 x 4096 19 (86), 512
-// rows 32 (85), 1000 rows 56 (85), 2000 rows 109 (86, and so expanded).
+// rows 32 (85), 1000 rows 56 (85), 2000 rows 109 (86).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -261,6 +261,192 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_t_kernel(MxGemmTParams 
     }
 }
 
+// The shape for many rows: 128 rows and 256 columns of dX, 2 x 4 waves of 64 x 64,
+// 64 n a stage.  Each wave expands one block of rows of W' for the next stage, 4 KiB,
+// into one of two buffers that all waves read, so a code is expanded once for 128
+// rows and its operands are read by two waves.  One barrier a stage: it stands
+// between the writes of a stage's W' and its reads, and the loads of X two stages and
+// of codes three stages ahead.  Bound by LDS, of whose cycles a stage takes about
+// 1900 (32 KiB written at 64 bytes a cycle, 25 KiB by the loads, 64 KiB of X and 64
+// KiB of W' read), against 1024 of the MFMAs.  dX of 1000 x 4096 x 4096 53 us (56 with
+// 128 x 128 tiles), 2000 x 4096 x 4096 75 (86 expanded), 1024 x 4096 x 14336 135
+// (174; 271 expanded); 4096 x 4096 x 4096 154 (105 expanded).  A half's reads moved
+// over the other half's MFMAs, with the second half carried into the next stage,
+// gained nothing.
+struct MxBigT {
+    static constexpr int TM = 128, TN = 256, NWD = 64, NW = 8, MB = 4, NB = 4;
+    static constexpr int XB = 16 * 1024, CB = 9 * 1024;  // X; codes and scales
+    static constexpr int CODES = 3 * XB, WIDE = CODES + 3 * CB, SPARE = WIDE + 2 * 32 * 1024, LDS = SPARE + 1024;
+    static_assert(LDS <= 160 * 1024, "tile does not fit");
+};
+
+__global__ __launch_bounds__(512) void mxfp4_gemm_big_t_kernel(MxGemmTParams P) {
+    using T = MxBigT;
+    constexpr int MB = T::MB, NB = T::NB;
+    extern __shared__ uint4 mxb_smem[];
+    lds_char *smem = (lds_char *)mxb_smem;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wn = wave & 3, wm = wave >> 2;
+
+    const int id = xcd_order(blockIdx.x, P.tiles_m * P.tiles_k * P.KS);
+    int tk = id / P.tiles_m;
+    const int tm = id - tk * P.tiles_m, ks = tk / P.tiles_k;
+    tk -= ks * P.tiles_k;
+    const int m0 = tm * T::TM, c0 = tk * T::TN, kb0 = c0 / 32;
+    const int n0 = ks * P.per * T::NWD, g0 = n0 / 16;
+    const int nit = min(P.per, (P.N - n0 + T::NWD - 1) / T::NWD);  // >= 1: the host sizes the slices
+
+    // the host keeps every offset below 2^31
+    const uint32_t row_bytes = (uint32_t)P.N * 2u, group_bytes = (uint32_t)P.blocks * 256u;
+    const sgpr4_t dX = make_desc(P.X + (size_t)m0 * P.N, (uint32_t)min(P.M - m0, T::TM) * row_bytes);
+    const sgpr4_t dW = make_desc(P.codes, (uint32_t)P.groups * group_bytes);
+    const sgpr4_t dS = make_desc(P.scales, (uint32_t)P.groups * (group_bytes / 16));
+
+    // This wave's loads (kOOB: zeros): of X two, 8 rows of 128 bytes each, piece c (8 n)
+    // of row i at c ^ (i mod 8); of codes one, four blocks of a column group; of scales
+    // wave 0's 32 pieces, block by block of each group.
+    const int xn = n0 + 8 * ((lane & 7) ^ (lane >> 3));
+    uint32_t xo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 16 * wave + 8 * i + (lane >> 3);
+        xo[i] = row < P.M - m0 ? (uint32_t)row * row_bytes + (uint32_t)xn * 2u : kOOB;
+    }
+    const int wg = wave >> 1, wb = 4 * (wave & 1) + lg, sg = (lane & 31) >> 3;
+    const uint32_t wo = kb0 + wb < P.blocks
+        ? (uint32_t)(g0 + wg) * group_bytes + (uint32_t)(kb0 + wb) * 256u + (uint32_t)l16 * 16u : kOOB;
+    const uint32_t so = lane < 32 && kb0 + (lane & 7) < P.blocks
+        ? (uint32_t)(g0 + sg) * (group_bytes / 16) + (uint32_t)(kb0 + (lane & 7)) * 16u : kOOB;
+    auto load_x = [&](int it) {
+        const int dn = it < nit ? it * T::NWD : 0x20000000;  // past every limit
+        const uint32_t base = lds0 + (uint32_t)(it % 3) * T::XB + (uint32_t)wave * 2048u;
+        const bool in = xn + dn < P.N;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) dma16_at(dX, in ? xo[i] : kOOB, (uint32_t)dn * 2u, base + 1024u * i);
+    };
+    auto load_w = [&](int it) {
+        const int dn = it < nit ? it * T::NWD : 0x20000000;
+        const uint32_t dg = it < nit ? (uint32_t)(it * 4) * group_bytes : 0u;
+        const uint32_t base = lds0 + T::CODES + (uint32_t)(it % 3) * T::CB;
+        dma16_at(dW, 16 * (g0 + wg) + dn < P.N ? wo : kOOB, dg, base + (uint32_t)wave * 1024u);
+        dma16_at(dS, 16 * (g0 + sg) + dn < P.N ? so : kOOB, dg / 16u, wave == 0 ? base + 8192u : lds0 + T::SPARE);
+    };
+
+    // The expanded stage: block b's 64 rows of 64 bytes from b * 4096 on, piece d at
+    // d ^ turn(row), as in the kernel above.
+    auto turn = [](int p) { return ((p >> 2) & 3) ^ ((p >> 3) & 2); };
+    uint32_t put[4], get[2];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) put[d] = (uint32_t)(wave * 4096 + lane * 64 + ((d ^ turn(lane)) << 4));
+    // step 0, a block's first column tile, rows 8 lg + (0 .. 3) and + (4 .. 7); the second
+    // tile is at ^ 32, step 1 (32 rows on, of the same turn) at + 2048
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int p = 8 * lg + 4 * e + (l16 >> 2);
+        get[e] = (uint32_t)(wn * 8192 + p * 64 + ((((l16 & 3) >> 1) ^ turn(p)) << 4) + (l16 & 1) * 8);
+    }
+    auto codes = [&](int it, uint4 &q, float &sc) {  // this wave's block of stage it, a lane a row
+        const lds_char *from = smem + T::CODES + it % 3 * T::CB;
+        q = *(const uint4 *)(from + (lg * 2 + (wave >> 2)) * 1024 + (wave & 3) * 256 + l16 * 16);
+        sc = mx_scale(*(const uint8_t *)(from + 8192 + (lg * 8 + wave) * 16 + l16));
+    };
+
+    f32x4_t acc[MB][NB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int t = 0; t < NB; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    load_w(0);
+    load_x(0);
+    load_w(1);
+    load_x(1);
+    load_w(2);
+    wait_vmcnt_lds<8>();  // codes of stage 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    {
+        uint4 q;
+        float sc;
+        codes(0, q, sc);
+        const uint32_t part[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int d = 0; d < 4; ++d) *(uint4 *)(smem + T::WIDE + put[d]) = mx_frag(part[d], sc);
+    }
+    for (int it = 0; it < nit; ++it) {
+        // X of this stage and the codes of the next have landed, this wave has written its block
+        wait_vmcnt_lds<4>();
+        asm volatile("" ::: "memory");  // keep LDS accesses and loads into LDS on their side of the barrier
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const lds_char *sx = smem + it % 3 * T::XB + (wm * 64 + l16) * 128;
+        const lds_char *sw = smem + T::WIDE + (it & 1) * 32768;
+        uint4 q, x[2][MB], w[2][NB];
+        float sc;
+        auto read = [&](int s) {
+#pragma unroll
+            for (int a = 0; a < MB; ++a) x[s][a] = *(const uint4 *)(sx + a * 2048 + (((4 * s + lg) ^ (l16 & 7)) << 4));
+#pragma unroll
+            for (int t = 0; t < NB; ++t) {
+                const uint32_t at = 4096 * (t >> 1) + 2048 * s, flip = 32 * (t & 1);
+                const uint2 w0 = lds_read_tr4(sw + at + (get[0] ^ flip)), w1 = lds_read_tr4(sw + at + (get[1] ^ flip));
+                w[s][t] = make_uint4(w0.x, w0.y, w1.x, w1.y);
+            }
+        };
+        codes(it + 1, q, sc);
+        read(0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(it + 2);  // over stage it - 1's X
+        load_w(it + 3);  // over this stage's codes
+        read(1);
+        __builtin_amdgcn_sched_barrier(0);
+        // the next stage's block between this one's MFMAs
+        lds_char *to = smem + T::WIDE + ((it + 1) & 1) * 32768;
+        const uint32_t part[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < NB; ++t) {
+#pragma unroll
+                for (int a = 0; a < MB; ++a) acc[a][t] = mfma16x16x32(w[s][t], x[s][a], acc[a][t]);
+                if (t & 1) *(uint4 *)(to + put[2 * s + (t >> 1)]) = mx_frag(part[2 * s + (t >> 1)], sc);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+    wait_vmcnt<0>();  // (the last loads fill zeros)
+
+    const bool direct = P.part == nullptr;
+    const int rows = min(P.M - m0, T::TM);
+    const __amdgpu_buffer_rsrc_t rY =
+        direct ? make_rsrc(P.Y + (size_t)m0 * P.K, (uint64_t)rows * P.K * 2u)
+               : make_rsrc(P.part + ((size_t)ks * P.M + m0) * P.K, (uint64_t)rows * P.K * 4u);
+#pragma unroll
+    for (int a = 0; a < MB; ++a) {
+        const uint32_t row = (uint32_t)(wm * 64 + a * 16 + l16);
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+            const int col = c0 + 64 * wn + 16 * t + 4 * lg;
+            const uint32_t at = row < (uint32_t)rows && col < P.K ? row * (uint32_t)P.K + (uint32_t)col : kOOB / 4;
+            if (direct)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2_t{pack_bf16x2(acc[a][t][0], acc[a][t][1]), pack_bf16x2(acc[a][t][2], acc[a][t][3])}, rY, at * 2u, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[a][t]), rY, at * 4u, 0, 0);
+        }
+    }
+}
+
+hipError_t launch_big(const MxGemmTParams &P, hipStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds((const void *)mxfp4_gemm_big_t_kernel, MxBigT::LDS, done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(mxfp4_gemm_big_t_kernel, dim3((unsigned)(P.tiles_m * P.tiles_k * P.KS)), dim3(512), MxBigT::LDS, stream,
+                       P);
+    return hipGetLastError();
+}
+
 template <class T>
 hipError_t launch_tt(const MxGemmTParams &P, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
@@ -273,12 +459,12 @@ hipError_t launch_tt(const MxGemmTParams &P, hipStream_t stream) {
 
 struct MxKindT {
     hipError_t (*launch)(const MxGemmTParams &, hipStream_t);
-    int tm, nwd;
+    int tm, tn, nwd;
     float stage;  // microseconds a stage takes a work-group when a full round of them runs
 };
 template <class T>
 constexpr MxKindT kind_t(float stage) {
-    return MxKindT{launch_tt<T>, T::TM, T::NWD, stage};
+    return MxKindT{launch_tt<T>, T::TM, T::TN, T::NWD, stage};
 }
 const MxKindT kKindsT[] = {
     kind_t<MxTileT<1, 2, 1, 16, 3>>(1.13f),   // 16 rows
@@ -286,6 +472,7 @@ const MxKindT kKindsT[] = {
     kind_t<MxTileT<1, 2, 3, 48, 3>>(1.45f),   // 48
     kind_t<MxTileT<1, 2, 4, 64, 2>>(1.70f),   // 64
     kind_t<MxTileT<2, 1, 4, 128, 2>>(1.60f),  // 128
+    MxKindT{launch_big, MxBigT::TM, MxBigT::TN, MxBigT::NWD, 1.06f},
 };
 
 }  // namespace
@@ -305,7 +492,7 @@ static MxGemmTPlan find_plan(int64_t m, int64_t k, int64_t n, int r) {
         MxGemmTPlan p{};
         p.kind = kind;
         p.tiles_m = (int)cdiv(m, K.tm);
-        p.tiles_k = (int)cdiv(k, 128);
+        p.tiles_k = (int)cdiv(k, K.tn);
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_k, stages = cdiv(n, K.nwd);
         if (tiles > (1 << 20)) continue;
         for (int want = 1; want <= 16 && want <= stages; ++want) {

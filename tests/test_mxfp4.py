@@ -370,7 +370,8 @@ def test_frozen_forward_and_backward(m, k, n):
 
 
 # sums split over many work-groups, and every number of row tiles, in both directions
-DEEP = [(1, 4096, 4104), (9, 1288, 8200), (24, 4096, 2048), (70, 2568, 4096), (128, 1024, 6152), (400, 776, 2056), (1100, 1288, 1032)]
+DEEP = [(1, 4096, 4104), (9, 1288, 8200), (24, 4096, 2048), (70, 2568, 4096), (128, 1024, 6152), (400, 776, 2056), (1100, 1288, 1032),
+        (999, 4104, 2056), (1500, 2056, 1032), (1900, 1800, 776)]
 
 
 @pytest.mark.gpu
@@ -389,6 +390,7 @@ LAYER = [
     (65, 1032, 264, 7, 1.0, 0.0), (100, 4104, 136, 31, -2.0, 0.0), (128, 2056, 520, 66, 0.5, 0.0), (128, 264, 72, 255, 1.0, 0.0),
     # more rows, and a contraction split over work-groups in both directions
     (1030, 520, 136, 16, 2.0, 0.0), (2, 8200, 4104, 16, 2.0, 0.1), (30, 4104, 8200, 12, 2.0, 0.0),
+    (1400, 2056, 1288, 40, 2.0, 0.1),
 ]
 
 
