@@ -103,10 +103,12 @@ def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=
         raise ValueError("offsets must be one multiple of 8 (>= 0) per parameter")
     rec[:, _N], rec[:, _OFFSET] = numels, np.asarray(offsets, dtype=np.uint64)
     # the device last, so that host tests can reach every other check with CPU tensors
+    index = params[0].get_device()
     for ts in tensors:
-        for t in ts:
-            if t.device != device or not t.is_cuda:
-                raise ValueError(f"a tensor is on {t.device}: all must be on one GPU ({device})")
+        places = [t.get_device() for t in ts]
+        if index < 0 or places.count(index) != len(places):
+            other = next((t for t, i in zip(ts, places) if i < 0 or i != index), ts[0])
+            raise ValueError(f"a tensor is on {other.device}: all must be on one GPU ({device})")
     _apart(rec, widths)
     return AdamwTable(rec, tensors, device, pt == torch.bfloat16, gt == torch.bfloat16, 8 if held8 else 32)
 
@@ -185,46 +187,55 @@ class LoraAdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        live = []
         for group in self.param_groups:  # refuse before anything has changed
-            for p in group["params"]:
-                if p.grad is None:
-                    continue
-                if p.grad.is_sparse:
-                    raise ValueError("gradients must be dense")
-                if not p.is_contiguous():
-                    raise ValueError("parameters must be contiguous")
-                held = self.state[p]["m"].numel() if self.state.get(p) else p.numel()
-                if not p.numel() == p.grad.numel() == held:
-                    raise ValueError(f"a parameter had {held} values when its moments were made, now {p.numel()}")
-        for index, group in enumerate(self.param_groups):
+            places = [i for i, p in enumerate(group["params"]) if p.grad is not None]
+            ps = [group["params"][i] for i in places]
+            gs = [p.grad for p in ps]
+            if any(g.is_sparse for g in gs):
+                raise ValueError("gradients must be dense")
+            if not all(map(torch.Tensor.is_contiguous, ps)):
+                raise ValueError("parameters must be contiguous")
+            numels = list(map(torch.Tensor.numel, ps))
+            known = [self.state.get(p) for p in ps]
+            held = [st["m"].numel() if st else n for st, n in zip(known, numels)]
+            if not numels == held == list(map(torch.Tensor.numel, gs)):
+                n, had = next(((n, h) for n, h in zip(numels, held) if n != h), (None, None))
+                raise ValueError(f"a parameter had {had} values when its moments were made, now {n}" if had is not None
+                                 else "a gradient and its parameter have different sizes")
+            live.append((group, places, ps, gs, numels))
+        for index, (group, places, ps, gs, numels) in enumerate(live):
+            states = [self.state[p] for p in ps]
             calls = {}  # the tensors of one call share a device, types and a step
-            for place, p in enumerate(group["params"]):
-                if p.grad is None:
-                    continue
-                st = self.state[p]
+            for i, (p, g, st) in enumerate(zip(ps, gs, states)):
                 if not st:
                     st.update(self._new_state(p, group))
-                key = (p.device, p.dtype, p.grad.dtype, "master" in st)
+                key = (p.get_device(), p.dtype, g.dtype, "master" in st)
                 if not group["capturable"]:
                     st["step"] += 1
                     key += (st["step"],)
-                calls.setdefault(key, []).append((place, p))
+                calls.setdefault(key, []).append(i)
             if group["capturable"]:
-                for device in {key[0] for key in calls}:
+                for device in {ps[at[0]].device for at in calls.values()}:
                     self._counter(group, device).add_(1)
-            for key, ps in calls.items():
-                self._step(group, (index, *key[:4], *(place for place, _ in ps)), [p for _, p in ps])
+            for key, at in calls.items():
+                pick = (lambda xs: xs) if len(at) == len(ps) else (lambda xs, at=at: [xs[i] for i in at])
+                table = self._table((index, *key[:4], *pick(places)), pick(ps), pick(gs), pick(states), pick(numels))
+                step = states[at[0]]["step"]
+                lora_adamw_step(table, lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
+                                eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"],
+                                **(dict(step_dev=step) if group["capturable"] else dict(step=step)))
         return loss
 
-    def _table(self, slot, ps) -> AdamwTable:
+    def _table(self, slot, ps, grads, states, numels) -> AdamwTable:
         """The table of these parameters.  Its records stay with the optimizer as
         scratch; every address in them is read anew at each step (gradients are new
         tensors, parameters may have moved)."""
-        states = [self.state[p] for p in ps]
-        grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in ps]
+        if not all(map(torch.Tensor.is_contiguous, grads)):
+            grads = [g.contiguous() for g in grads]
         tables = self.__dict__.setdefault("_tables", {})
         table = tables.get(slot)
-        if table is None or table.records[:, _N].tolist() != [p.numel() for p in ps]:
+        if table is None or table.records[:, _N].tolist() != numels:
             each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
             table = adamw_table([p.detach() for p in ps], grads, each("m"), each("v"), m_scales=each("m_scale"),
                                 v_scales=each("v_scale"), masters=each("master"), offsets=each("offset"))
@@ -232,21 +243,15 @@ class LoraAdamW(torch.optim.Optimizer):
                 tables.clear()
             tables[slot] = table
             return table
-        rec = table.records
-        rec[:, _PARAM] = [p.data_ptr() for p in ps]
-        rec[:, _GRAD] = [g.data_ptr() for g in grads]
+        rec, address = table.records, torch.Tensor.data_ptr
+        rec[:, _PARAM] = list(map(address, ps))
+        rec[:, _GRAD] = list(map(address, grads))
         for name, col in (("m", _M), ("v", _V), ("m_scale", _M_SCALE), ("v_scale", _V_SCALE), ("master", _MASTER)):
             if name in states[0]:
-                rec[:, col] = [st[name].data_ptr() for st in states]
+                rec[:, col] = [address(st[name]) for st in states]
         rec[:, _OFFSET] = [st["offset"] for st in states]
         table.tensors = [grads]
         return table
-
-    def _step(self, group, slot, ps) -> None:
-        st = self.state[ps[0]]
-        at = dict(step_dev=st["step"]) if group["capturable"] else dict(step=st["step"])
-        lora_adamw_step(self._table(slot, ps), lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
-                        eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"], **at)
 
     def load_state_dict(self, state_dict) -> None:
         """The moments keep their own types (torch's loader would cast them to
