@@ -200,7 +200,7 @@ def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor]):
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace

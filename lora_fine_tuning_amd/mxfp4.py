@@ -42,6 +42,10 @@ def _need_weight(W: Mxfp4Weight):
         raise TypeError(f"W must be an Mxfp4Weight, got {type(W).__name__}")
     codes, scales, k, n = W
     groups, blocks = (n + 15) // 16, (k + 127) // 128 * 4
+    if (codes.shape == (groups, blocks, 16, 16) and scales.shape == (groups, blocks, 16) and codes.is_cuda
+            and codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_contiguous()
+            and scales.is_contiguous() and scales.get_device() == codes.get_device()):
+        return codes, scales, k, n, codes.device
     if codes.shape != (groups, blocks, 16, 16) or scales.shape != (groups, blocks, 16):
         raise ValueError(f"W.codes {tuple(codes.shape)} and W.scales {tuple(scales.shape)} do not hold a {k} x {n} "
                          f"weight ({(groups, blocks, 16, 16)} and {(groups, blocks, 16)} do)")
@@ -63,8 +67,9 @@ def _rank(A) -> int:
 
 
 def _out(t, shape, dtype, name: str, dev):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+    if t is None:  # (with strides the call takes 1.2 us, without 1.6)
+        strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * 256, 256, 16, 1) if len(shape) == 4 else (shape[1] * 16, 16, 1)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
     _need_on(t, shape, dtype, name, dev)
     return t
 
