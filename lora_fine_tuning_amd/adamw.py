@@ -32,15 +32,15 @@ def _column(ts: Sequence[torch.Tensor], name: str, count: int, dtypes, numels=No
     dtype = ts[0].dtype if count else dtypes[0]
     if dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
-    if any(t.dtype is not dtype for t in ts):
+    if {t.dtype for t in ts} - {dtype}:
         i = next(i for i, t in enumerate(ts) if t.dtype != dtype)
         raise TypeError(f"{name}[{i}] is {ts[i].dtype}, {name}[0] {dtype}")
-    if not all(t.is_contiguous() for t in ts):
+    if not all(map(torch.Tensor.is_contiguous, ts)):
         raise ValueError(f"{name}[{next(i for i, t in enumerate(ts) if not t.is_contiguous())}] must be contiguous")
-    if numels is not None and [t.numel() for t in ts] != numels:
+    if numels is not None and list(map(torch.Tensor.numel, ts)) != numels:
         i = next(i for i, t in enumerate(ts) if t.numel() != numels[i])
         raise ValueError(f"{name}[{i}] must have {numels[i]} values, got {ts[i].numel()}")
-    return [t.data_ptr() for t in ts], dtype
+    return list(map(torch.Tensor.data_ptr, ts)), dtype
 
 
 def _apart(records, widths) -> None:
@@ -69,7 +69,7 @@ def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=
     if count == 0:
         raise ValueError("params must not be empty")
     device = params[0].device
-    numels = [p.numel() for p in params]
+    numels = list(map(torch.Tensor.numel, params))
     held8 = ms[0].dtype == torch.float8_e4m3fn if ms else False
     moment = (torch.float8_e4m3fn,) if held8 else (torch.float32,)
     f32, either = (torch.float32,), (torch.float32, torch.bfloat16)
@@ -99,13 +99,13 @@ def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=
     if offsets is None:
         padded = [(e + 7) // 8 * 8 for e in numels]
         offsets = np.concatenate([[0], np.cumsum(padded)[:-1]])
-    elif len(offsets) != count or any(int(o) % 8 or int(o) < 0 for o in offsets):
+    elif len(offsets) != count or any(o < 0 or o % 8 for o in map(int, offsets)):
         raise ValueError("offsets must be one multiple of 8 (>= 0) per parameter")
     rec[:, _N], rec[:, _OFFSET] = numels, np.asarray(offsets, dtype=np.uint64)
     # the device last, so that host tests can reach every other check with CPU tensors
     index = params[0].get_device()
     for ts in tensors:
-        places = [t.get_device() for t in ts]
+        places = list(map(torch.Tensor.get_device, ts))
         if index < 0 or places.count(index) != len(places):
             other = next((t for t, i in zip(ts, places) if i < 0 or i != index), ts[0])
             raise ValueError(f"a tensor is on {other.device}: all must be on one GPU ({device})")
@@ -189,8 +189,7 @@ class LoraAdamW(torch.optim.Optimizer):
                 loss = closure()
         live = []
         for group in self.param_groups:  # refuse before anything has changed
-            places = [i for i, p in enumerate(group["params"]) if p.grad is not None]
-            ps = [group["params"][i] for i in places]
+            ps = [p for p in group["params"] if p.grad is not None]
             gs = [p.grad for p in ps]
             if any(g.is_sparse for g in gs):
                 raise ValueError("gradients must be dense")
@@ -203,14 +202,14 @@ class LoraAdamW(torch.optim.Optimizer):
                 n, had = next(((n, h) for n, h in zip(numels, held) if n != h), (None, None))
                 raise ValueError(f"a parameter had {had} values when its moments were made, now {n}" if had is not None
                                  else "a gradient and its parameter have different sizes")
-            live.append((group, places, ps, gs, numels))
-        for index, (group, places, ps, gs, numels) in enumerate(live):
+            live.append((group, ps, gs))
+        for group, ps, gs in live:
             states = [self.state[p] for p in ps]
             calls = {}  # the tensors of one call share a device, types and a step
             for i, (p, g, st) in enumerate(zip(ps, gs, states)):
                 if not st:
                     st.update(self._new_state(p, group))
-                key = (p.get_device(), p.dtype, g.dtype, "master" in st)
+                key = (p.get_device(), p.dtype, g.dtype, "master" in st, st["m"].dtype)
                 if not group["capturable"]:
                     st["step"] += 1
                     key += (st["step"],)
@@ -218,47 +217,30 @@ class LoraAdamW(torch.optim.Optimizer):
             if group["capturable"]:
                 for device in {ps[at[0]].device for at in calls.values()}:
                     self._counter(group, device).add_(1)
-            for key, at in calls.items():
+            for at in calls.values():
                 pick = (lambda xs: xs) if len(at) == len(ps) else (lambda xs, at=at: [xs[i] for i in at])
-                table = self._table((index, *key[:4], *pick(places)), pick(ps), pick(gs), pick(states), pick(numels))
+                table = self._table(pick(ps), pick(gs), pick(states))
                 step = states[at[0]]["step"]
                 lora_adamw_step(table, lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
                                 eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"],
                                 **(dict(step_dev=step) if group["capturable"] else dict(step=step)))
         return loss
 
-    def _table(self, slot, ps, grads, states, numels) -> AdamwTable:
-        """The table of these parameters.  Its records stay with the optimizer as
-        scratch; every address in them is read anew at each step (gradients are new
-        tensors, parameters may have moved)."""
+    @staticmethod
+    def _table(ps, grads, states) -> AdamwTable:
+        """The table of these parameters, made anew at each step: between two steps
+        any tensor may have moved, and the state's may have been replaced."""
+        each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
         if not all(map(torch.Tensor.is_contiguous, grads)):
             grads = [g.contiguous() for g in grads]
-        tables = self.__dict__.setdefault("_tables", {})
-        table = tables.get(slot)
-        if table is None or table.records[:, _N].tolist() != numels:
-            each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
-            table = adamw_table([p.detach() for p in ps], grads, each("m"), each("v"), m_scales=each("m_scale"),
-                                v_scales=each("v_scale"), masters=each("master"), offsets=each("offset"))
-            if len(tables) >= 64:
-                tables.clear()
-            tables[slot] = table
-            return table
-        rec, address = table.records, torch.Tensor.data_ptr
-        rec[:, _PARAM] = list(map(address, ps))
-        rec[:, _GRAD] = list(map(address, grads))
-        for name, col in (("m", _M), ("v", _V), ("m_scale", _M_SCALE), ("v_scale", _V_SCALE), ("master", _MASTER)):
-            if name in states[0]:
-                rec[:, col] = [address(st[name]) for st in states]
-        rec[:, _OFFSET] = [st["offset"] for st in states]
-        table.tensors = [grads]
-        return table
+        return adamw_table(ps, grads, each("m"), each("v"), m_scales=each("m_scale"), v_scales=each("v_scale"),
+                           masters=each("master"), offsets=each("offset"))
 
     def load_state_dict(self, state_dict) -> None:
         """The moments keep their own types (torch's loader would cast them to
         the parameters')."""
         saved = state_dict["state"]
         super().load_state_dict(dict(state_dict, state={}))
-        self.__dict__.pop("_tables", None)
         for group, old in zip(self.param_groups, state_dict["param_groups"]):
             for p, i in zip(group["params"], old["params"]):
                 if i not in saved:
