@@ -112,10 +112,10 @@ __device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *sme
         if (which < 0 || which >= P.num_adapters) return;
         const lora_adapter ad = P.adapters[which];
         if (ad.r < 1 || ad.r > P.r) return;
-        const int64_t lo = max((int64_t)0, P.seg_off[seg]) + rest % P.tiles_m * T::TM;
+        // (clamped before anything is added: an offset may be any int64)
+        m0 = (int)min(max((int64_t)0, P.seg_off[seg]), (int64_t)P.M) + rest % P.tiles_m * T::TM;
         mend = (int)min(max((int64_t)0, P.seg_off[seg + 1]), (int64_t)P.M);
-        if (lo >= mend) return;
-        m0 = (int)lo;
+        if (m0 >= mend) return;
         A = (const uint16_t *)ad.A;
         r = ad.r;
         drop = drop_threshold(ad.p);
