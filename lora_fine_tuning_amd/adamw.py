@@ -12,6 +12,7 @@ import torch
 from ._lib import _check, _elsewhere, _handle, _on_device, load
 
 BLOCK = 256  # values that share a scale of the 8-bit moments
+MOST = ((1 << 24) - 1) * 2048  # values of one tensor (a launch's work-groups, 2048 values each)
 _PARAM, _GRAD, _MASTER, _M, _V, _M_SCALE, _V_SCALE, _N, _OFFSET = range(9)
 
 
@@ -40,7 +41,7 @@ def _column(ts: Sequence[torch.Tensor], name: str, count: int, dtypes, numels=No
     if numels is not None and list(map(torch.Tensor.numel, ts)) != numels:
         i = next(i for i, t in enumerate(ts) if t.numel() != numels[i])
         raise ValueError(f"{name}[{i}] must have {numels[i]} values, got {ts[i].numel()}")
-    return list(map(torch.Tensor.data_ptr, ts)), dtype
+    return np.fromiter(map(torch.Tensor.data_ptr, ts), np.uint64, count), dtype
 
 
 def _apart(records, widths) -> None:
@@ -70,6 +71,8 @@ def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=
         raise ValueError("params must not be empty")
     device = params[0].device
     numels = list(map(torch.Tensor.numel, params))
+    if max(numels) > MOST:
+        raise ValueError(f"params[{numels.index(max(numels))}] has {max(numels)} values, more than {MOST}")
     held8 = ms[0].dtype == torch.float8_e4m3fn if ms else False
     moment = (torch.float8_e4m3fn,) if held8 else (torch.float32,)
     f32, either = (torch.float32,), (torch.float32, torch.bfloat16)
@@ -99,9 +102,11 @@ def adamw_table(params, grads, ms, vs, *, m_scales=None, v_scales=None, masters=
     if offsets is None:
         padded = [(e + 7) // 8 * 8 for e in numels]
         offsets = np.concatenate([[0], np.cumsum(padded)[:-1]])
-    elif len(offsets) != count or any(o < 0 or o % 8 for o in map(int, offsets)):
-        raise ValueError("offsets must be one multiple of 8 (>= 0) per parameter")
-    rec[:, _N], rec[:, _OFFSET] = numels, np.asarray(offsets, dtype=np.uint64)
+    elif len(offsets) != count or min(offsets) < 0 or max(offsets) >= 1 << 64:
+        raise ValueError(f"offsets must be one per parameter ({count}), each in [0, 2^64)")
+    rec[:, _N], rec[:, _OFFSET] = numels, offsets
+    if (rec[:, _OFFSET] & np.uint64(7)).any():
+        raise ValueError("each offset must be a multiple of 8")
     # the device last, so that host tests can reach every other check with CPU tensors
     index = params[0].get_device()
     for ts in tensors:
@@ -123,12 +128,21 @@ def lora_adamw_step(table: AdamwTable, *, lr: float, beta1: float = 0.9, beta2: 
             return lora_adamw_step(table, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
                                    step=step, step_dev=step_dev, seed=seed)
     if step_dev is not None:
-        if step_dev.dtype != torch.int64 or step_dev.numel() != 1 or step_dev.device != table.device:
-            raise ValueError(f"step_dev must be one int64 on {table.device}")
+        _need_counter(step_dev, table.device)
         step_dev = step_dev.data_ptr()
     _check(load().lora_adamw_step(table.address, len(table.records), table.param_bf16, table.grad_bf16,
                                   table.state_bits, lr, beta1, beta2, eps, weight_decay, step, step_dev,
                                   seed % (1 << 64), _handle(table.device)))
+
+
+def _need_counter(counter: torch.Tensor, device) -> None:
+    if counter.dtype != torch.int64 or counter.numel() != 1 or counter.device != device:
+        raise ValueError(f"step_dev must be one int64 on {device}")
+
+
+def _hyper_allowed(lr, beta1, beta2, eps, weight_decay, seed) -> None:
+    """The library's own checks of a step's numbers, by a call on no tensors."""
+    _check(load().lora_adamw_step(None, 0, 0, 0, 32, lr, beta1, beta2, eps, weight_decay, 1, None, seed % (1 << 64), None))
 
 
 class LoraAdamW(torch.optim.Optimizer):
@@ -165,12 +179,10 @@ class LoraAdamW(torch.optim.Optimizer):
                 return at
         return torch.zeros(1, dtype=torch.int64, device=device)
 
-    def _new_state(self, p: torch.Tensor, group) -> dict:
+    @staticmethod
+    def _new_state(p: torch.Tensor, group, step, offset: int) -> dict:
         n, dev = p.numel(), p.device
-        # counters of the random rounding: past every other parameter's
-        ends = [st["offset"] + st["m"].numel() for st in self.state.values() if st]
-        st = {"step": self._counter(group, dev) if group["capturable"] else 0,
-              "offset": -(-max(ends, default=0) // BLOCK) * BLOCK}
+        st = {"step": step, "offset": offset}
         if group["state_bits"] == 8:
             st["m"], st["v"] = (torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
                                 for _ in range(2))
@@ -187,54 +199,79 @@ class LoraAdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        live = []
-        for group in self.param_groups:  # refuse before anything has changed
-            ps = [p for p in group["params"] if p.grad is not None]
-            gs = [p.grad for p in ps]
-            if any(g.is_sparse for g in gs):
-                raise ValueError("gradients must be dense")
-            if not all(map(torch.Tensor.is_contiguous, ps)):
-                raise ValueError("parameters must be contiguous")
-            numels = list(map(torch.Tensor.numel, ps))
-            known = [self.state.get(p) for p in ps]
-            held = [st["m"].numel() if st else n for st, n in zip(known, numels)]
-            if not numels == held == list(map(torch.Tensor.numel, gs)):
-                n, had = next(((n, h) for n, h in zip(numels, held) if n != h), (None, None))
-                raise ValueError(f"a parameter had {had} values when its moments were made, now {n}" if had is not None
-                                 else "a gradient and its parameter have different sizes")
-            live.append((group, ps, gs))
-        for group, ps, gs in live:
-            states = [self.state[p] for p in ps]
-            calls = {}  # the tensors of one call share a device, types and a step
-            for i, (p, g, st) in enumerate(zip(ps, gs, states)):
-                if not st:
-                    st.update(self._new_state(p, group))
-                key = (p.get_device(), p.dtype, g.dtype, "master" in st, st["m"].dtype)
-                if not group["capturable"]:
-                    st["step"] += 1
-                    key += (st["step"],)
-                calls.setdefault(key, []).append(i)
-            if group["capturable"]:
-                for device in {ps[at[0]].device for at in calls.values()}:
-                    self._counter(group, device).add_(1)
-            for at in calls.values():
-                pick = (lambda xs: xs) if len(at) == len(ps) else (lambda xs, at=at: [xs[i] for i in at])
-                table = self._table(pick(ps), pick(gs), pick(states))
-                step = states[at[0]]["step"]
-                lora_adamw_step(table, lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1],
-                                eps=group["eps"], weight_decay=group["weight_decay"], seed=group["seed"],
-                                **(dict(step_dev=step) if group["capturable"] else dict(step=step)))
+        calls, fresh, counters = self._calls()  # refuses before anything has changed
+        self.state.update(fresh)
+        for counter in counters:
+            counter.add_(1)
+        for table, states, t, hyper in calls:
+            if isinstance(t, torch.Tensor):
+                lora_adamw_step(table, step_dev=t, **hyper)
+            else:
+                for st in states:
+                    st["step"] = t
+                lora_adamw_step(table, step=t, **hyper)
         return loss
+
+    def _calls(self):
+        """What a step does, with every check and no change: its calls, each a table,
+        the states, their step (a number, or the counter on the device) and the
+        hyperparameters; the states of parameters that have none; the counters."""
+        calls, fresh, counters, shared = [], {}, {}, {}
+        end = None  # of the random rounding's counters that are taken
+        for index, group in enumerate(self.param_groups):
+            hyper = dict(lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1], eps=group["eps"],
+                         weight_decay=group["weight_decay"], seed=group["seed"])
+            on_device = bool(group["capturable"])
+            kinds = {}  # the tensors of one call share a device, types and a step
+            for p in group["params"]:
+                g = p.grad
+                if g is None:
+                    continue
+                st = self.state.get(p)
+                if not st:
+                    step = 0
+                    if on_device:
+                        step = shared.get((index, p.device))
+                        if step is None:
+                            step = shared[index, p.device] = self._counter(group, p.device)
+                    if end is None:
+                        end = max((st["offset"] + st["m"].numel() for st in self.state.values() if st), default=0)
+                    st = fresh[p] = self._new_state(p, group, step, -(-end // BLOCK) * BLOCK)
+                    end = st["offset"] + p.numel()
+                t = st["step"]
+                if isinstance(t, torch.Tensor) != on_device:
+                    raise ValueError("capturable was changed after a parameter's first step (a loaded state follows it)")
+                key = (p.get_device(), p.dtype, g.dtype, "master" in st, st["m"].dtype, id(t) if on_device else t)
+                kinds.setdefault(key, []).append((p, g, st))
+            if kinds:
+                _hyper_allowed(**hyper)
+            for members in kinds.values():
+                ps, gs, states = map(list, zip(*members))
+                t = states[0]["step"]
+                calls.append((self._table(ps, gs, states), states, t if on_device else t + 1, hyper))
+                if on_device:
+                    _need_counter(t, ps[0].device)
+                    counters[id(t)] = t
+        return calls, fresh, list(counters.values())
 
     @staticmethod
     def _table(ps, grads, states) -> AdamwTable:
         """The table of these parameters, made anew at each step: between two steps
         any tensor may have moved, and the state's may have been replaced."""
-        each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
+        if {g.layout for g in grads} != {torch.strided}:
+            raise ValueError("gradients must be dense")
         if not all(map(torch.Tensor.is_contiguous, grads)):
             grads = [g.contiguous() for g in grads]
-        return adamw_table(ps, grads, each("m"), each("v"), m_scales=each("m_scale"), v_scales=each("v_scale"),
-                           masters=each("master"), offsets=each("offset"))
+        each = lambda name: [st[name] for st in states] if name in states[0] else None  # noqa: E731
+        try:
+            return adamw_table(ps, grads, each("m"), each("v"), m_scales=each("m_scale"), v_scales=each("v_scale"),
+                               masters=each("master"), offsets=each("offset"))
+        except ValueError:
+            for p, st in zip(ps, states):
+                if p.numel() != st["m"].numel():
+                    raise ValueError(f"a parameter had {st['m'].numel()} values when its moments were made, "
+                                     f"now {p.numel()}") from None
+            raise
 
     def load_state_dict(self, state_dict) -> None:
         """The moments keep their own types (torch's loader would cast them to

@@ -103,3 +103,139 @@ def test_state_that_was_replaced_is_read_anew(launches, monkeypatch):
     ps[0].data, ps[1].data = both[:40], both[38:45]
     with pytest.raises(ValueError, match="share memory"):
         opt.step()
+
+
+# ---- a refused step ------------------------------------------------------------------------------
+
+def everything(opt):
+    """The optimizer's state and parameters, copied."""
+    held = {id(p): {k: (x.clone() if isinstance(x, torch.Tensor) else x) for k, x in st.items()}
+            for p, st in opt.state.items()}
+    return held, [p.detach().clone() for g in opt.param_groups for p in g["params"]]
+
+
+def same(a, b):
+    assert a[0].keys() == b[0].keys()
+    for p, st in a[0].items():
+        assert st.keys() == b[0][p].keys()
+        for name, x in st.items():
+            y = b[0][p][name]
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)) if isinstance(x, torch.Tensor) else x == y, name
+    assert all(torch.equal(x, y) for x, y in zip(a[1], b[1]))
+
+
+def bad_type(opt, p):
+    p.data = p.data.to(torch.float16)
+    p.grad = torch.ones_like(p)
+
+
+def bad_size(opt, p):
+    p.grad = None
+    p.data = p.data[:-1].clone()
+    p.grad = torch.ones_like(p)
+
+
+def bad_layout(opt, p):
+    p.grad = None
+    p.data = torch.zeros(14, dtype=p.dtype)[::2]
+    p.grad = torch.ones(7, dtype=p.dtype)
+
+
+def bad_gradient(opt, p):
+    p.grad = torch.ones_like(p).to_sparse()
+
+
+def shared_memory(opt, p):
+    p.data = opt.param_groups[1]["params"][1].data[3:10]
+    p.grad = torch.ones_like(p)
+
+
+def bad_rate(opt, p):
+    opt.param_groups[1]["lr"] = float("nan")
+
+
+def bad_decay(opt, p):
+    opt.param_groups[1]["weight_decay"] = float("inf")
+
+
+def bad_betas(opt, p):
+    opt.param_groups[1]["betas"] = (0.9, 1.0)
+
+
+def bad_eps(opt, p):
+    opt.param_groups[1]["eps"] = -1.0
+
+
+def bad_seed(opt, p):
+    opt.param_groups[1]["seed"] = "x"
+
+
+def counter_elsewhere(opt, p):
+    opt.param_groups[1]["capturable"] = not opt.param_groups[1]["capturable"]
+
+
+SPOILERS = [bad_type, bad_size, bad_layout, bad_gradient, shared_memory, bad_rate, bad_decay, bad_betas, bad_eps, bad_seed,
+            counter_elsewhere]
+
+
+# (before the first step there is no size and no kind of count to differ from)
+@pytest.mark.parametrize("capturable", [False, True])
+@pytest.mark.parametrize("before,spoil", [(steps, f) for steps in (0, 2) for f in SPOILERS
+                                          if steps or f not in (bad_size, counter_elsewhere)])
+def test_a_refused_step_changes_nothing(launches, spoil, capturable, before):
+    # the second group's first parameter, or its numbers, are at fault: the first group is not stepped either,
+    # no state is made and no count moves
+    a, b = parameters(), parameters((7, 40))
+    opt = lf.LoraAdamW([dict(params=a), dict(params=b)], capturable=capturable)
+    for _ in range(before):
+        opt.step()
+    made = len(launches)
+    spoil(opt, b[0])
+    kept = everything(opt)
+    for _ in range(2):
+        with pytest.raises(Exception):
+            opt.step()
+        same(kept, everything(opt))
+    assert len(launches) == made
+
+
+def test_a_parameter_on_the_host_is_refused_before_it_gets_state(launches, monkeypatch):
+    a, b = parameters(), parameters()
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: -1 if self is b[1] else 0)
+    opt = lf.LoraAdamW([dict(params=a), dict(params=b)])
+    for _ in range(2):
+        with pytest.raises(ValueError, match="GPU"):
+            opt.step()
+        assert not opt.state and not launches
+    # moved, it takes its first step
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    opt.step()
+    assert [kw["step"] for _, kw in launches] == [1, 1]
+
+
+def test_steps_and_counters_advance_once_a_step(launches):
+    a, b = parameters(), parameters((5, 6, 7))
+    opt = lf.LoraAdamW([dict(params=a, capturable=True), dict(params=b)])
+    for t in range(1, 4):
+        b[1].grad = None if t == 2 else torch.ones_like(b[1])
+        opt.step()
+        assert int(opt.state[a[0]]["step"]) == t and opt.state[a[0]]["step"] is opt.state[a[1]]["step"]
+        assert [opt.state[p]["step"] for p in b] == [t, t - (t >= 2), t]
+    # parameters whose steps differ have a call each
+    assert [len(table.records) for table, _ in launches] == [2, 3, 2, 2, 2, 2, 1]
+    spans = sorted((opt.state[p]["offset"], p.numel()) for p in a + b)
+    assert all(x + n <= y for (x, n), (y, _) in zip(spans, spans[1:]))
+
+
+def test_a_tensor_of_too_many_values_is_refused(monkeypatch):
+    many = torch.zeros(1).expand(adamw.MOST + 1)
+    with pytest.raises(ValueError, match="values, more than"):
+        lf.adamw_table([many], [many], [many], [many])
+
+
+@pytest.mark.parametrize("offsets,said", [([8], "one per parameter"), ([0, -8], "offsets"), ([0, 4], "multiple of 8"),
+                                          ([0, 1 << 64], "offsets"), (np.array([0, -8]), "offsets")])
+def test_offsets_are_checked(offsets, said):
+    z = [torch.zeros(8) for _ in range(8)]
+    with pytest.raises(ValueError, match=said):
+        lf.adamw_table(z[:2], z[2:4], z[4:6], z[6:], offsets=offsets)
