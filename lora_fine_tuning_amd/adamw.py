@@ -154,6 +154,8 @@ class LoraAdamW(torch.optim.Optimizer):
     its last place).  seed: of the 8-bit moments' random rounding.  capturable:
     the step number lives on the device, so that a captured step() counts on in
     every replay; the group's learning rate and decay are those of the capture.
+    A step is captured with it only, and after each parameter's first one, which
+    makes its state.
 
     Parameters are contiguous GPU tensors, fp32 or bf16.  A parameter without a
     gradient is left out of a step (the shared counter of a capturable group goes
@@ -217,6 +219,7 @@ class LoraAdamW(torch.optim.Optimizer):
         the states, their step (a number, or the counter on the device) and the
         hyperparameters; the states of parameters that have none; the counters."""
         calls, fresh, counters, shared = [], {}, {}, {}
+        capturing = torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
         end = None  # of the random rounding's counters that are taken
         for index, group in enumerate(self.param_groups):
             hyper = dict(lr=float(group["lr"]), beta1=group["betas"][0], beta2=group["betas"][1], eps=group["eps"],
@@ -227,8 +230,13 @@ class LoraAdamW(torch.optim.Optimizer):
                 g = p.grad
                 if g is None:
                     continue
+                if capturing and not on_device:
+                    raise ValueError("a captured step needs capturable=True: its replays would repeat one step's number")
                 st = self.state.get(p)
                 if not st:
+                    if capturing:
+                        raise ValueError("a parameter's first step cannot be captured: every replay would begin "
+                                         "with empty moments again (take a step before the capture)")
                     step = 0
                     if on_device:
                         step = shared.get((index, p.device))

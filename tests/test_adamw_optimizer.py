@@ -239,3 +239,60 @@ def test_offsets_are_checked(offsets, said):
     z = [torch.zeros(8) for _ in range(8)]
     with pytest.raises(ValueError, match=said):
         lf.adamw_table(z[:2], z[2:4], z[4:6], z[6:], offsets=offsets)
+
+
+# ---- a captured step -----------------------------------------------------------------------------
+
+def capture(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+
+
+def test_a_first_step_is_not_captured(launches, monkeypatch):
+    # its replays would make the state anew each time: moments of zero, step 1, the parameter as master
+    ps = parameters()
+    opt = lf.LoraAdamW(ps[:1], capturable=True)
+    opt.step()
+    opt.param_groups[0]["params"].append(ps[1])
+    kept = everything(opt)
+    capture(monkeypatch)
+    with pytest.raises(ValueError, match="first step"):
+        opt.step()
+    same(kept, everything(opt))
+    ps[1].grad = None
+    opt.step()
+    assert len(launches) == 2 and ps[1] not in opt.state
+
+
+def test_a_step_counted_on_the_host_is_not_captured(launches, monkeypatch):
+    ps = parameters()
+    opt = lf.LoraAdamW(ps)
+    opt.step()
+    capture(monkeypatch)
+    with pytest.raises(ValueError, match="capturable"):
+        opt.step()
+    assert len(launches) == 1 and opt.state[ps[0]]["step"] == 1
+
+
+@pytest.mark.gpu
+def test_a_refused_capture_leaves_the_optimizer_usable():
+    p = torch.nn.Parameter(torch.ones(300, device="cuda", dtype=torch.bfloat16))
+    opt = lf.LoraAdamW([p], lr=1e-2, capturable=True)
+    p.grad = torch.ones_like(p)
+    x = torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        with pytest.raises(ValueError, match="first step"):
+            opt.step()
+    assert not opt.state
+    opt.step()
+    graph2 = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph2):
+        opt.step()
+    for rep in range(3):
+        graph2.replay()
+        torch.cuda.synchronize()
+        assert int(opt.state[p]["step"]) == rep + 2
