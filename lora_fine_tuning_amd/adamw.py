@@ -122,7 +122,8 @@ def lora_adamw_step(table: AdamwTable, *, lr: float, beta1: float = 0.9, beta2: 
                     weight_decay: float = 0.0, step: int = 0, step_dev: Optional[torch.Tensor] = None, seed: int = 0,
                     stream=None) -> None:
     """One step (the step-th, from 1; or the one whose number the int64 device
-    tensor step_dev holds) over the table's tensors, in place."""
+    tensor step_dev holds) over the table's tensors, in place.  Autograd does not
+    see the change (torch.autograd.graph.increment_version tells it; LoraAdamW does)."""
     if _elsewhere(table.device, stream):
         with _on_device(table.device, stream):
             return lora_adamw_step(table, lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
@@ -205,19 +206,21 @@ class LoraAdamW(torch.optim.Optimizer):
         self.state.update(fresh)
         for counter in counters:
             counter.add_(1)
-        for table, states, t, hyper in calls:
+        for table, ps, states, t, hyper in calls:
             if isinstance(t, torch.Tensor):
                 lora_adamw_step(table, step_dev=t, **hyper)
             else:
                 for st in states:
                     st["step"] = t
                 lora_adamw_step(table, step=t, **hyper)
+            # a backward through a graph from before the step is refused, as after any in-place change
+            torch.autograd.graph.increment_version(ps)
         return loss
 
     def _calls(self):
         """What a step does, with every check and no change: its calls, each a table,
-        the states, their step (a number, or the counter on the device) and the
-        hyperparameters; the states of parameters that have none; the counters."""
+        the parameters, their states and step (a number, or the counter on the device)
+        and the hyperparameters; the states of parameters that have none; the counters."""
         calls, fresh, counters, shared = [], {}, {}, {}
         capturing = torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
         end = None  # of the random rounding's counters that are taken
@@ -256,7 +259,7 @@ class LoraAdamW(torch.optim.Optimizer):
             for members in kinds.values():
                 ps, gs, states = map(list, zip(*members))
                 t = states[0]["step"]
-                calls.append((self._table(ps, gs, states), states, t if on_device else t + 1, hyper))
+                calls.append((self._table(ps, gs, states), ps, states, t if on_device else t + 1, hyper))
                 if on_device:
                     _need_counter(t, ps[0].device)
                     counters[id(t)] = t

@@ -296,3 +296,34 @@ def test_a_refused_capture_leaves_the_optimizer_usable():
         graph2.replay()
         torch.cuda.synchronize()
         assert int(opt.state[p]["step"]) == rep + 2
+
+
+# ---- autograd ------------------------------------------------------------------------------------
+
+def test_autograd_sees_a_step(launches):
+    ps = parameters()
+    opt = lf.LoraAdamW(ps)
+    ps[1].grad = None
+    squares = [p.square().sum() for p in ps]
+    versions = [p._version for p in ps]
+    opt.step()
+    assert [p._version > v for p, v in zip(ps, versions)] == [True, False]
+    with pytest.raises(RuntimeError, match="inplace"):
+        squares[0].backward()
+    squares[1].backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_backward_from_before_a_step_is_refused(capturable):
+    W = torch.randn(72, 40, device="cuda").bfloat16()
+    layer = lf.LoraLinear(W, 8, 2.0)
+    opt = lf.LoraAdamW(layer.parameters(), capturable=capturable)
+    X = torch.randn(5, 72, device="cuda").bfloat16().requires_grad_()
+    layer(X).sum().backward()
+    stale = layer(X).sum()
+    opt.step()
+    with pytest.raises(RuntimeError, match="inplace"):
+        stale.backward()
+    layer(X).sum().backward()  # and one from after it runs
+    opt.step()
