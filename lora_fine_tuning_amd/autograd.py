@@ -127,15 +127,17 @@ class MultiLoraLinearFunction(torch.autograd.Function):
         st = _adapter_set(As, Bs, alphas, ps)
         fwd = mxfp4.multi_lora_mxfp4_linear_fwd if isinstance(W, Mxfp4Weight) else _lib.multi_lora_linear_fwd
         Y, S, keep = fwd(X, W, st.table, st.num, seg_off, seg_adapter, st.r_max, seed, offset)
-        ctx.save_for_backward(X, seg_off, seg_adapter, S, keep, *_weight_tensors(W))
-        ctx.adapter_set = st
+        # the table holds A's and B's addresses alone: saved, they live on and are guarded against changes
+        held = _weight_tensors(W)
+        ctx.save_for_backward(X, seg_off, seg_adapter, S, keep, *held, *AB)
+        ctx.adapter_set, ctx.held = st, len(held)
         return Y
 
     @staticmethod
     def backward(ctx, dY):
-        X, seg_off, seg_adapter, S, keep, *held = ctx.saved_tensors
+        X, seg_off, seg_adapter, S, keep, *rest = ctx.saved_tensors
         st = ctx.adapter_set
-        W = _weight_again(held, st.k, st.n)
+        W = _weight_again(rest[:ctx.held], st.k, st.n)
         bwd = mxfp4.multi_lora_mxfp4_linear_bwd if isinstance(W, Mxfp4Weight) else _lib.multi_lora_linear_bwd
         dAs, dBs = st.gradient_buffers()
         dX = bwd(dY.contiguous(), X, W, st.table, st.num, seg_off, seg_adapter, S, keep, st.r_max,

@@ -1,0 +1,91 @@
+"""The mixed-adapter layer's autograd function keeps the adapters' matrices for its
+backward: the device table that the backward reads holds their addresses alone."""
+import gc
+import weakref
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import lora_fine_tuning_amd as lf
+from lora_fine_tuning_amd import _lib, autograd, mxfp4
+from parity import bf16_randn
+
+K, N, RANKS = 72, 40, (8, 3)
+
+
+@pytest.fixture(params=[False, True], ids=["bf16", "mxfp4"])
+def weight(request, monkeypatch):
+    """W on the CPU, with the library's calls replaced."""
+    def table(As, Bs, alphas, ps):
+        sizes = [[t.shape for t in ts] for ts in (As, Bs)]  # (as the real one, it holds no tensor)
+        return SimpleNamespace(table=None, num=len(As), r_max=max(RANKS), k=K, n=N, gradient_buffers=lambda: [
+            [torch.ones(z, dtype=torch.bfloat16) for z in zs] for zs in sizes])
+
+    def fwd(X, W, *rest):
+        m = X.shape[0]
+        return torch.zeros(m, N, dtype=X.dtype), torch.zeros(m, max(RANKS)), torch.zeros(m, 3, dtype=torch.int32)
+
+    monkeypatch.setattr(autograd, "_adapter_set", table)
+    for module, name in ((_lib, "multi_lora_linear"), (mxfp4, "multi_lora_mxfp4_linear")):
+        monkeypatch.setattr(module, name + "_fwd", fwd)
+        monkeypatch.setattr(module, name + "_bwd", lambda dY, X, W, *rest, want_dX: torch.zeros_like(X))
+    if request.param:
+        return lf.Mxfp4Weight(torch.zeros(3, 4, 16, 16, dtype=torch.uint8), torch.zeros(3, 4, 16, dtype=torch.uint8), K, N)
+    return torch.zeros(K, N, dtype=torch.bfloat16)
+
+
+def call(W, As, Bs):
+    so, sa = torch.tensor([0, 2, 5]), torch.tensor([0, 1], dtype=torch.int32)
+    return lf.multi_lora_linear(torch.ones(5, K, dtype=torch.bfloat16), W, so, sa, As, Bs, [1.0, 2.0], [0.0, 0.0])
+
+
+def test_matrices_made_for_the_call_live_until_the_backward(weight):
+    # adapters trained in fp32 and cast for the call: nothing but the graph holds the casts
+    leaves = [torch.randn(s, requires_grad=True) for r in RANKS for s in ((K, r), (r, N))]
+    casts = [t.bfloat16() for t in leaves]
+    watch = [weakref.ref(t) for t in casts]
+    y = call(weight, casts[0::2], casts[1::2])
+    del casts
+    gc.collect()
+    assert all(w() is not None for w in watch)
+    y.sum().backward()
+    assert all(t.grad is not None and t.grad.shape == t.shape for t in leaves)
+    del y
+    gc.collect()
+    assert all(w() is None for w in watch)
+
+
+def test_a_change_between_forward_and_backward_is_refused(weight):
+    leaves = [torch.randn(s).bfloat16().requires_grad_() for r in RANKS for s in ((K, r), (r, N))]
+    y = call(weight, leaves[0::2], leaves[1::2])
+    with torch.no_grad():
+        leaves[3].add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients_of_adapters_cast_for_the_call(packed):
+    g = torch.Generator().manual_seed(3)
+    X, dY = bf16_randn((50, K), 1.0, g).cuda(), bf16_randn((50, N), 1.0, g).cuda()
+    W = bf16_randn((K, N), K ** -0.5, g).cuda()
+    W = lf.lora_mxfp4_quantize(W) if packed else W
+    so = torch.tensor([0, 20, 50], dtype=torch.int64, device="cuda")
+    sa = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    values = [bf16_randn(s, 0.2, g).cuda() for r in RANKS for s in ((K, r), (r, N))]
+    grads = []
+    for cast in (False, True):
+        leaves = [(v.float() if cast else v.clone()).requires_grad_() for v in values]
+        x = X.clone().requires_grad_()
+        used = [t.bfloat16() for t in leaves] if cast else leaves
+        y = lf.multi_lora_linear(x, W, so, sa, used[0::2], used[1::2], [2.0, 0.5], [0.0, 0.0])
+        del used
+        others = [torch.full_like(v, 9.0) for v in values]  # (these would take memory that was given back)
+        y.backward(dY)
+        torch.cuda.synchronize()
+        grads.append([x.grad, *(t.grad.bfloat16() for t in leaves)])
+        del others
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
