@@ -350,8 +350,9 @@ lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const voi
 /* ---- optimizer ------------------------------------------------------------
  * One AdamW step over many tensors (the adapters' A and B of a model):
  *   m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2
- *   w = w (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32 (each constant, 1 - beta among them, rounded from its double), everything
+ *   w = w - (lr weight_decay w + lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ * in fp32 (each constant, 1 - beta and lr weight_decay among them, rounded from its
+ * double; the two terms are added before w takes them, in one rounding), everything
  * updated in place.
  *
  * Types: param is fp32, or bf16 (param_bf16 = 1) with or without an fp32

@@ -1,0 +1,57 @@
+"""The AdamW step's arithmetic where single roundings add up: many steps' worth of small
+decays, and epsilons at the end of fp32's range.  References in 64 bits from the formulas."""
+import numpy as np
+import pytest
+import torch
+
+import lora_fine_tuning_amd as lf
+from parity import log
+
+
+def f64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("master", [True, False])
+@pytest.mark.parametrize("lr,wd", [(1e-3, 1e-2), (1e-4, 1e-2), (1e-5, 1e-2), (2e-6, 1e-2), (1e-6, 1e-2)])
+@pytest.mark.parametrize("n", [1 << 18, (1 << 18) + 777])
+def test_small_decays_are_not_lost(lr, wd, master, n):
+    # w in [1/2, 1), where fp32's step is 2^-24, and updates of both signs far larger than a step: each w is
+    # rounded by an even draw from half a step up and down, 2^-24 / sqrt(12) as a standard deviation.  Over n
+    # values the mean is off by 5 / sqrt(n) of that, and by the decay's and the update's own roundings:
+    # 2^-23 of the mean decay, and of the update m / sqrt(v) (2^-20 with its root, quotient and products, of
+    # mixed signs) no more than 2^-20 of its mean over 1
+    log(f"lr={lr} wd={wd} master={master} n={n}")
+    g = torch.Generator().manual_seed(int(lr * 1e7))
+    w = 0.5 + 0.5 * torch.rand(n, generator=g)
+    grad = torch.randn(n, generator=g)
+    m, v = 0.3 * torch.randn(n, generator=g), 0.5 + torch.rand(n, generator=g)
+    param = w.bfloat16().cuda() if master else w.cuda()
+    held = w.cuda() if master else param
+    ms, vs = m.cuda(), v.cuda()
+    table = lf.adamw_table([param], [grad.cuda()], [ms], [vs], masters=[held] if master else None)
+    lf.lora_adamw_step(table, lr=lr, weight_decay=wd, step=50)
+    torch.cuda.synchronize()
+    m2, v2 = 0.9 * f64(m) + 0.1 * f64(grad), 0.999 * f64(v) + 0.001 * f64(grad) ** 2
+    up = lr * m2 / (1 - 0.9 ** 50) / (np.sqrt(v2 / (1 - 0.999 ** 50)) + 1e-8)
+    want = f64(w) - lr * wd * f64(w) - up
+    bound = 5 * 2.0 ** -24 / np.sqrt(12 * n) + 2.0 ** -23 * lr * wd + 2.0 ** -20 * (lr * 5 / np.sqrt(n) + abs(up.mean()))
+    off = (f64(held) - want).mean()
+    assert abs(off) <= bound, (off, bound, lr * wd * f64(w).mean())
+    if lr * wd <= 1e-7:  # the bound is a small part of the decay itself
+        assert bound < 0.02 * lr * wd
+
+
+@pytest.mark.gpu
+def test_infinite_parameters_stay_infinite():
+    for n in (2048, 300):
+        for wd in (0.0, 0.1):
+            w = torch.ones(n, device="cuda")
+            w[3], w[5], w[7] = float("inf"), -float("inf"), float("nan")
+            z = [torch.zeros(n, device="cuda") for _ in range(2)]
+            lf.lora_adamw_step(lf.adamw_table([w], [torch.ones(n, device="cuda")], z[:1], z[1:]), lr=1e-2,
+                               weight_decay=wd, step=1)
+            torch.cuda.synchronize()
+            assert w[3] == float("inf") and w[5] == -float("inf") and torch.isnan(w[7])
+            assert torch.isfinite(w).sum() == n - 3
