@@ -372,7 +372,8 @@ lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const voi
  * with disjoint ranges [offset, offset + n) draw independently.
  *
  * An infinite or NaN gradient makes its own w and moments NaN (or infinite)
- * and nothing else.
+ * and nothing else.  eps is 0 or at least 2^-126, the smallest normal float; with
+ * eps = 0 a value whose gradients were all zero becomes NaN, as 0 / 0 does.
  *
  * t = step (>= 1) or, where step_dev is not NULL, the int64 it points to on
  * the device, read when the kernels run (a captured call then follows the

@@ -21,6 +21,8 @@ extern "C" lora_status lora_adamw_step(const lora_adamw_tensor *tensors, int32_t
             lr, weight_decay);
     REQUIRE(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1, "betas (%g, %g) must be in [0, 1)", beta1, beta2);
     REQUIRE(eps >= 0 && std::isfinite(eps), "eps = %g must be finite and >= 0", eps);
+    // (the reciprocal takes a subnormal for zero: 0 / eps would be NaN where v is zero)
+    REQUIRE(eps == 0 || eps >= 0x1p-126, "eps = %g must be 0 or at least 2^-126", eps);
     REQUIRE(step_dev != nullptr || step >= 1, "step = %lld must be >= 1", (long long)step);
     REQUIRE(aligned(step_dev, 8), "step_dev must be 8-byte aligned");
     bool master = false;

@@ -55,3 +55,40 @@ def test_infinite_parameters_stay_infinite():
             torch.cuda.synchronize()
             assert w[3] == float("inf") and w[5] == -float("inf") and torch.isnan(w[7])
             assert torch.isfinite(w).sum() == n - 3
+
+
+def test_subnormal_epsilons_are_refused():
+    import os
+
+    from lora_fine_tuning_amd import _lib
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("library not built")
+    lib = _lib.load()
+
+    def call(eps):
+        return lib.lora_adamw_step(None, 0, 1, 1, 8, 1e-3, 0.9, 0.999, eps, 0.0, 1, None, 0, None)
+
+    for eps in (1e-40, 1e-300, 2.0 ** -127, float(np.nextafter(2.0 ** -126, 0))):
+        assert call(eps) == -1, eps
+        assert b"eps" in lib.lora_last_error_message()
+    for eps in (0.0, 2.0 ** -126, 1e-8, 1.0):
+        assert call(eps) == 0, eps
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2048, 300])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_parameter_without_gradients_so_far(n, bits):
+    # moments of zero and a gradient of zero (an adapter's A while B is zero): only the decay moves w, down to
+    # the smallest eps, and eps = 0 is 0 / 0
+    F8 = torch.float8_e4m3fn
+    for eps in (2.0 ** -126, 1e-8, 0.0):
+        w, g = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda")
+        m, v = (torch.zeros(n, dtype=torch.uint8 if bits == 8 else torch.float32, device="cuda") for _ in range(2))
+        scales = [torch.zeros(-(-n // 256), device="cuda") for _ in range(2)]
+        kw = dict(m_scales=scales[:1], v_scales=scales[1:]) if bits == 8 else {}
+        table = lf.adamw_table([w], [g], [m.view(F8) if bits == 8 else m], [v.view(F8) if bits == 8 else v], **kw)
+        lf.lora_adamw_step(table, lr=0.5, weight_decay=0.25, eps=eps, step=1)
+        torch.cuda.synchronize()
+        assert (w == 0.875).all() if eps else torch.isnan(w).all()
+        assert not m.any() and not v.any()
