@@ -49,6 +49,12 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
     return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && k * n < (1LL << 46);
 }
 
+// What the workspace queries take for a layer: ranks that a layer can have, counts
+// that a plan can be sized by.
+static bool ranks_ok(int32_t r, int32_t num_adapters, int32_t num_segments) {
+    return r >= 1 && r <= 256 && num_adapters >= 0 && num_segments >= 0;
+}
+
 #define REQ_WORKSPACE(need)                                                                            \
     do {                                                                                               \
         if (workspace_bytes < (need))                                                                  \
@@ -110,14 +116,14 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
 }
 
 extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
-    if (!sizes_ok(m, k, n) || m == 0 || r < 1) return 0;
+    if (!sizes_ok(m, k, n) || m == 0 || !ranks_ok(r, 0, 0)) return 0;
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, r, kMxPlain);
     if (!pl.kind) return expanded_bytes(m, k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
     return align_up(pl.part_bytes) + std::max(pl.spart_bytes, lora_linear_fwd_workspace_size(m, k, n, r));
 }
 
 extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
-    if (!sizes_ok(m, k, n) || r < 1) return 0;
+    if (!sizes_ok(m, k, n) || !ranks_ok(r, 0, 0)) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
     return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) + lora_linear_bwd_workspace_size(m, k, n, r);
 }
@@ -203,7 +209,7 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
 
 extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                       int32_t num_adapters, int32_t num_segments) {
-    if (!sizes_ok(m, k, n) || m == 0 || r_max < 1) return 0;
+    if (!sizes_ok(m, k, n) || m == 0 || !ranks_ok(r_max, num_adapters, num_segments)) return 0;
     const MxGemmPlan pl = mx_gemm_plan(m, k, n, r_max, kMxMixed, num_segments);
     const size_t layer = multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
     return pl.kind ? align_up(pl.part_bytes) + std::max(pl.spart_bytes, layer) : expanded_bytes(m, k, n) + layer;
@@ -211,7 +217,7 @@ extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int6
 
 extern "C" size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                       int32_t num_adapters, int32_t num_segments) {
-    if (!sizes_ok(m, k, n) || r_max < 1) return 0;
+    if (!sizes_ok(m, k, n) || !ranks_ok(r_max, num_adapters, num_segments)) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r_max);
     return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) +
            multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);

@@ -691,7 +691,7 @@ static MxGemmPlan find_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form,
 }
 
 MxGemmPlan mx_gemm_plan(int64_t m, int64_t k, int64_t n, int r, MxForm form, int nseg) {
-    return remembered<MxGemmPlan>(m, k, n, ((int64_t)nseg << 32) + 4 * r + (int)form,
+    return remembered<MxGemmPlan>(m, k, n, nseg * (1LL << 32) + 4 * r + (int)form,
                                   [&] { return find_plan(m, k, n, r, form, nseg); });
 }
 
