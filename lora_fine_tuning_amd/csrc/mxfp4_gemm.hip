@@ -614,26 +614,27 @@ hipError_t launch_t(const MxGemmParams &P, hipStream_t stream) {
 // takes a work-group when a full round of them runs (measured at k = 14336 and
 // 28672, 2.4 GHz); `share`: work-groups that a CU holds.
 struct MxKind {
+    const char *name;  // in the timing pool
     hipError_t (*launch)(const MxGemmParams &, hipStream_t);
-    int tm, tn, kw, ranks;  // ranks: of one job of S, 0 where S does not ride along
+    int tm, tn, kw, ranks;  // rows and columns of a tile; ranks: of one job of S, 0 where S does not ride along
     float stage;
     int share;
 };
 template <class T>
-constexpr MxKind kind_of(float stage) {
-    return MxKind{launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? 16 * T::RT : 0, stage, T::SHARE};
+constexpr MxKind kind_of(const char *name, float stage) {
+    return MxKind{name, launch_t<T>, T::TM, T::TN, T::KW, T::RIDE ? 16 * T::RT : 0, stage, T::SHARE};
 }
 const MxKind kKinds[] = {
-    kind_of<MxTile<1, 1, 8, 1, 1, 4, 3>>(0.36f),   // 4 rows x 16 columns
-    kind_of<MxTile<1, 2, 4, 1, 1, 4, 3>>(0.31f),   // 4 x 32
-    kind_of<MxTile<1, 1, 8, 1, 1, 16, 3>>(0.60f),  // 16 x 16
-    kind_of<MxTile<1, 2, 4, 1, 2, 16, 3>>(0.53f),  // 16 x 64
-    kind_of<MxTile<1, 2, 4, 2, 1, 32, 3>>(0.61f),  // 32 x 32
-    kind_of<MxTile<1, 4, 2, 2, 2, 32, 3>>(0.67f),  // 32 x 128
-    kind_of<MxTile<1, 4, 2, 3, 2, 48, 3>>(0.78f),  // 48 x 128
-    kind_of<MxTile<1, 4, 2, 4, 2, 64, 3>>(1.00f),  // 64 x 128
-    kind_of<MxTile<2, 4, 1, 2, 4, 64, 3>>(0.98f),  // 64 x 256
-    kind_of<MxTile<2, 4, 1, 4, 4, 128, 3>>(1.65f), // 128 x 256
+    kind_of<MxTile<1, 1, 8, 1, 1, 4, 3>>("mxfp4_gemm 4x16", 0.36f),
+    kind_of<MxTile<1, 2, 4, 1, 1, 4, 3>>("mxfp4_gemm 4x32", 0.31f),
+    kind_of<MxTile<1, 1, 8, 1, 1, 16, 3>>("mxfp4_gemm 16x16", 0.60f),
+    kind_of<MxTile<1, 2, 4, 1, 2, 16, 3>>("mxfp4_gemm 16x64", 0.53f),
+    kind_of<MxTile<1, 2, 4, 2, 1, 32, 3>>("mxfp4_gemm 32x32", 0.61f),
+    kind_of<MxTile<1, 4, 2, 2, 2, 32, 3>>("mxfp4_gemm 32x128", 0.67f),
+    kind_of<MxTile<1, 4, 2, 3, 2, 48, 3>>("mxfp4_gemm 48x128", 0.78f),
+    kind_of<MxTile<1, 4, 2, 4, 2, 64, 3>>("mxfp4_gemm 64x128", 1.00f),
+    kind_of<MxTile<2, 4, 1, 2, 4, 64, 3>>("mxfp4_gemm 64x256", 0.98f),
+    kind_of<MxTile<2, 4, 1, 4, 4, 128, 3>>("mxfp4_gemm 128x256", 1.65f),
 };
 
 }  // namespace
@@ -732,7 +733,7 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     P.seg_adapter = src.seg_adapter;
     P.num_adapters = src.num_adapters;
     P.nseg = src.num_segments;
-    int slot = prof_begin("mxfp4_gemm", stream);
+    int slot = prof_begin(kKinds[pl.kind - 1].name, stream);
     const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
     if (e != hipSuccess || !pl.finish) return e;

@@ -458,21 +458,22 @@ hipError_t launch_tt(const MxGemmTParams &P, hipStream_t stream) {
 }
 
 struct MxKindT {
+    const char *name;  // in the timing pool
     hipError_t (*launch)(const MxGemmTParams &, hipStream_t);
     int tm, tn, nwd;
     float stage;  // microseconds a stage takes a work-group when a full round of them runs
 };
 template <class T>
-constexpr MxKindT kind_t(float stage) {
-    return MxKindT{launch_tt<T>, T::TM, T::TN, T::NWD, stage};
+constexpr MxKindT kind_t(const char *name, float stage) {
+    return MxKindT{name, launch_tt<T>, T::TM, T::TN, T::NWD, stage};
 }
 const MxKindT kKindsT[] = {
-    kind_t<MxTileT<1, 2, 1, 16, 3>>(1.13f),   // 16 rows
-    kind_t<MxTileT<1, 2, 2, 32, 3>>(1.27f),   // 32
-    kind_t<MxTileT<1, 2, 3, 48, 3>>(1.45f),   // 48
-    kind_t<MxTileT<1, 2, 4, 64, 2>>(1.70f),   // 64
-    kind_t<MxTileT<2, 1, 4, 128, 2>>(1.60f),  // 128
-    MxKindT{launch_big, MxBigT::TM, MxBigT::TN, MxBigT::NWD, 1.06f},
+    kind_t<MxTileT<1, 2, 1, 16, 3>>("mxfp4_gemm_t 16x128", 1.13f),
+    kind_t<MxTileT<1, 2, 2, 32, 3>>("mxfp4_gemm_t 32x128", 1.27f),
+    kind_t<MxTileT<1, 2, 3, 48, 3>>("mxfp4_gemm_t 48x128", 1.45f),
+    kind_t<MxTileT<1, 2, 4, 64, 2>>("mxfp4_gemm_t 64x128", 1.70f),
+    kind_t<MxTileT<2, 1, 4, 128, 2>>("mxfp4_gemm_t 128x128", 1.60f),
+    MxKindT{"mxfp4_gemm_t 128x256", launch_big, MxBigT::TM, MxBigT::TN, MxBigT::NWD, 1.06f},
 };
 
 }  // namespace
@@ -533,7 +534,7 @@ hipError_t launch_mxfp4_gemm_t(const MxGemmTPlan &pl, const void *dY, const void
     P.tiles_k = pl.tiles_k;
     P.KS = pl.KS;
     P.per = pl.per;
-    const int slot = prof_begin("mxfp4_gemm_t", stream);
+    const int slot = prof_begin(kKindsT[pl.kind - 1].name, stream);
     const hipError_t e = kKindsT[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
     return e;
