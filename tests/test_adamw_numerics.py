@@ -1,5 +1,5 @@
 """The AdamW step's arithmetic where single roundings add up: many steps' worth of small
-decays, and epsilons at the end of fp32's range.  References in 64 bits from the formulas."""
+decays, epsilons at the end of fp32's range, corrections formed on the device.  References in 64 bits from the formulas."""
 import numpy as np
 import pytest
 import torch
@@ -92,3 +92,44 @@ def test_a_parameter_without_gradients_so_far(n, bits):
         torch.cuda.synchronize()
         assert (w == 0.875).all() if eps else torch.isnan(w).all()
         assert not m.any() and not v.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_replays_follow_the_formulas(bits):
+    # a captured step against the reference of the plain one, replay by replay
+    from test_adamw import HYPER, Tensors
+    lr, wd, E = HYPER["lr"], HYPER["weight_decay"], 2.0 ** -24
+    T = Tensors([700, 5000], bits, torch.bfloat16, torch.bfloat16, True, seed=6)
+    counter = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def run():
+        counter.add_(1)
+        lf.lora_adamw_step(T.table, step_dev=counter, seed=4, **HYPER)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for rep in range(3):
+        for i, grad in enumerate(T.g):
+            grad.copy_(torch.randn(grad.numel(), generator=torch.Generator().manual_seed(rep * 10 + i)))
+        torch.cuda.synchronize()
+        before = [T.before(i) for i in range(2)]
+        graph.replay()
+        torch.cuda.synchronize()
+        t = int(counter)
+        assert t == rep + 2
+        # 1 - beta^t is formed on the device from fp32 logarithms (2^-23 of themselves) and t: the exponent is off
+        # by 2^-22 of itself, and 1 - beta^t, at least half of t |ln beta| here, by 2^-21 of itself at most; with the
+        # root half of that, and the quotient, the update moves by 2^-20 of itself
+        for (w, g, m, v), master in zip(before, T.master):
+            m2, v2 = 0.9 * m + 0.1 * g, 0.999 * v + 0.001 * g * g
+            rate = lr / (1 - 0.9 ** t) / (np.sqrt(v2 / (1 - 0.999 ** t)) + 1e-8)
+            want = w - lr * wd * w - rate * m2
+            slack = 4 * E * np.abs(w) + (2.0 ** -20 + 24 * E) * rate * np.abs(m2) + 8 * E * rate * (np.abs(m) + np.abs(g))
+            assert (np.abs(f64(master) - want) <= slack).all()

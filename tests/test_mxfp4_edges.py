@@ -1,12 +1,12 @@
 """Calls over an MXFP4 weight that the documentation allows and that reach further than the
-layers' own tests: segment tables with any content.
+layers' own tests: segment tables with any content, matrices at any address.
 
 The references and tolerances are those of test_mxfp4.py."""
 import pytest
 import torch
 
 import lora_fine_tuning_amd as lf
-from parity import bf16_randn, log
+from parity import bf16_randn, log, offset_view
 from test_mxfp4 import layer_case, layer_reference, near
 
 LAST = (1 << 63) - 1
@@ -46,3 +46,53 @@ def test_segment_offsets_may_be_any_number(m, ends):
     if ends[0] > 0:
         want, slack = layer_reference(X[10:], W, As[1].cpu(), Bs[1].cpu(), dY[10:], 2.0, 0.0, 3, 8 + 10 * k)
         near("Y", Y[50:40 + m], want["Y"], slack["Y"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [20, 100, 1000])
+@pytest.mark.parametrize("seg_off,seg_ad", [([0, 10, LAST, LAST, LAST], [0, 1, 0, 1]), ([0, -(1 << 33) + 5, 1 << 40, 20], [0, 1, 0]),
+                                            ([0, 30, 10, 20], [1, 0, 1]), ([-7, 4, 4, 1 << 33], [0, 9, -3]),
+                                            ([5, 6, 7, 8], [1, 1, 0])])
+def test_bad_segment_tables_stay_in_bounds_backward(m, seg_off, seg_ad):
+    # the same tables as the forward's: values of rows that are not in order are undefined, but nothing outside
+    # the m rows of dX, and of the gradients nothing beside dA and dB, is written
+    k, n = 264, 136
+    log(f"m={m} {seg_off} {seg_ad}")
+    X, W4, _, _, _, dY = layer_case(m, k, n, 8, seed=8)
+    g = torch.Generator().manual_seed(8)
+    As = [bf16_randn((k, r), 1.0, g).cuda() for r in (8, 40)]
+    Bs = [bf16_randn((r, n), 1.0, g).cuda() for r in (8, 40)]
+    flat = torch.full((sum(t.numel() + 16 for t in (*As, *Bs)) + 16,), 5.0, dtype=torch.bfloat16, device="cuda")
+    own, at, grads = torch.zeros_like(flat, dtype=torch.bool), 16, []
+    for t in (*As, *Bs):
+        grads.append(flat[at:at + t.numel()].view(t.shape))
+        own[at:at + t.numel()] = True
+        at += t.numel() + 16
+    table = lf.adapter_table(As, Bs, [1.0, 2.0], [0.1, 0.0], grads[:2], grads[2:])
+    so = torch.tensor(seg_off, dtype=torch.int64, device="cuda")
+    sa = torch.tensor(seg_ad, dtype=torch.int32, device="cuda")
+    S = torch.zeros((m, 40), device="cuda")
+    keep = torch.full((m, (k + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    dX = torch.full((m + 80, k), 5.0, dtype=torch.bfloat16, device="cuda")
+    lf.multi_lora_mxfp4_linear_bwd(dY.cuda(), X.cuda(), W4, table, 2, so, sa, S, keep, 40, dX=dX[40:40 + m])
+    torch.cuda.synchronize()
+    assert (dX[:40] == 5).all() and (dX[40 + m:] == 5).all()
+    assert (flat[~own] == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n,r,p", [(1, 1032, 520, 16, 0.0), (33, 1032, 520, 9, 0.0), (33, 1032, 520, 64, 0.1),
+                                       (300, 1032, 520, 40, 0.1), (700, 1032, 520, 16, 0.0), (1003, 4184, 1144, 33, 0.1),
+                                       (5010, 136, 376, 200, 0.0)])
+def test_unaligned_adapter_gives_the_same_bits(m, k, n, r, p):
+    # over the packed weight the kernels take A and B at any address alike: the same sums in the same order
+    # (the bf16 layer, which runs over an expanded weight, has a form of its own for aligned matrices of ranks 33 to 128)
+    X, W4, _, A, B, dY = layer_case(m, k, n, r, seed=31)
+    X, dY = X.cuda(), dY.cuda()
+
+    def run(A, B):
+        Y, S, keep = lf.lora_mxfp4_linear_fwd(X, W4, A, B, 2.0, p, 3, 0)
+        return (Y, S, *lf.lora_mxfp4_linear_bwd(dY, X, W4, A, B, S, keep, 2.0, p))
+
+    for name, a, b in zip(("Y", "S", "dX", "dA", "dB"), run(A.cuda(), B.cuda()), run(offset_view(A), offset_view(B))):
+        assert torch.equal(a, b), name
