@@ -94,7 +94,6 @@ __device__ __forceinline__ AdamwKernelTensor unpack_record(const AdamwRecord &r)
 }
 
 constexpr float kTop = 448.f;           // largest e4m3
-constexpr float kLeast = 0.001953125f;  // smallest e4m3, 2^-9
 constexpr float kTiny = 7.888609e-31f;  // 2^-100
 constexpr float kLargest = 3.402823466e38f;
 
@@ -118,9 +117,9 @@ struct AdamwStep {
     }
 };
 
-// x / scale (inv = 1 / scale) to one of its two e4m3 neighbours, the upper one
-// where the fraction of a step and r / 65536 make 1 or more; `least` for a
-// positive value that came out as zero.
+// x / scale (inv = 1 / scale) to one of its two e4m3 neighbours, the upper one in
+// magnitude where the fraction of a step and r / 65536 make 1 or more, with r in
+// the high half of `r16_high`.
 __device__ __forceinline__ uint32_t e4m3_at_random(float x, float inv, uint32_t r16_high) {
     const float y = __builtin_copysignf(fminf(fabsf(x) * inv, kTop), x);
     return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y, (int)r16_high, 0, 0) & 255u;

@@ -19,7 +19,8 @@
 // stage's conversions while the other half's operands come back took 6 to 10%
 // off.  Measured against expanding the weight for the bf16 product, in us: 1 x
 // 4096 x 4096 10 (85), 16 x 4096 x 14336 17 (265), 128 x 4096 x 4096 19 (86), 512
-// rows 32 (85), 1000 rows 56 (85), 2000 rows 109 (86).
+// rows 32 (85).  For more rows the second kernel below shares the expanded blocks:
+// 1000 rows 53 (56 with this one's 128-row tile), 2000 rows 75 (109).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -479,8 +480,10 @@ const MxKindT kKindsT[] = {
 }  // namespace
 
 // The cheapest of the tile shapes and of expanding the weight, by the forward
-// product's model (which says 10, 16, 17, 32, 56 and 108 us for the packed shapes
-// measured above, and 99 us for their 4096 x 4096 expanded).
+// product's model (which says 10, 16, 17, 32, 50 and 72 us for the packed shapes
+// measured above, and 84 us for up to 2000 rows of 4096 x 4096 expanded).  The
+// 128 x 256 tile is for many rows; where the contraction is short (up to about ten of
+// its 64-deep stages) the model takes it for few rows too, for a microsecond.
 static MxGemmTPlan find_plan(int64_t m, int64_t k, int64_t n, int r) {
     MxGemmTPlan best{};
     if (m <= 0 || k > (1 << 20) || n > (1 << 20) || m > (1 << 19) || mx_groups(n) * mx_blocks(k) * 256 >= (1LL << 31))

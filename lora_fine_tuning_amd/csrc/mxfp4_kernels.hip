@@ -38,46 +38,37 @@ struct MxShape {
     int64_t kb, n16;  // blocks of 32 rows (a multiple of 4), groups of 16 columns
 };
 
-// One thread: one block of 32 rows of COLS columns, whose maxima stay inside the
-// thread.  Reads 2 COLS bytes of each row and writes 16 COLS bytes of codes; the
-// lanes of a wave are neighbours in both.  HBM-bound: 2 bytes in and 0.53 out an
-// element.  28672 x 8192, right after a pass that wrote 470 MB: 140 us with two
-// columns a thread (4.3 TB/s), 153 with four, 166 with eight (whose stores touch 64
-// lines an instruction); after a pass that read, 108 us (5.5 TB/s).
-template <int COLS>
+// One thread: one block of 32 rows of two columns, whose maxima stay inside the
+// thread.  Reads 4 bytes of each row and writes 32 bytes of codes; the lanes of a
+// wave are neighbours in both.  HBM-bound: 2 bytes in and 0.53 out an element.
+// 28672 x 8192, right after a pass that wrote 470 MB: 140 us with two columns a
+// thread (4.3 TB/s), 153 with four, 166 with eight (whose stores touch 64 lines an
+// instruction); after a pass that read, 108 us (5.5 TB/s).
 __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const uint16_t *W, MxShape S, uint8_t *codes,
                                                              uint8_t *scales) {
-    constexpr int NW = COLS / 2;  // words of a row
-    const int64_t nc = S.n16 * 16 / COLS, items = S.kb * nc;
+    const int64_t nc = S.n16 * 8, items = S.kb * nc;
     for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
         const int64_t kb = it / nc, cc = it - kb * nc;
-        const int64_t col = cc * COLS, row0 = kb * 32;
-        uint32_t r[32][NW];
+        const int64_t col = cc * 2, row0 = kb * 32;
+        uint32_t r[32];
         const int rows = col < S.n ? (int)min((int64_t)32, max((int64_t)0, S.k - row0)) : 0;
         const uint16_t *src = W + row0 * S.n + col;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-#pragma unroll
-            for (int w = 0; w < NW; ++w) r[i][w] = 0u;
-            if (i < rows) __builtin_memcpy(r[i], __builtin_assume_aligned(src + i * S.n, 2 * COLS), 2 * COLS);
-        }
+        for (int i = 0; i < 32; ++i) r[i] = i < rows ? *(const uint32_t *)(src + i * S.n) : 0u;
         // bf16 magnitudes order as their bit patterns
-        u16x2_t top[NW] = {};
+        u16x2_t top = {};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                top[w] = __builtin_elementwise_max(top[w], __builtin_bit_cast(u16x2_t, r[i][w] & 0x7FFF7FFFu));
+        for (int i = 0; i < 32; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, r[i] & 0x7FFF7FFFu));
         const int64_t at = ((col >> 4) * S.kb + kb) * 16 + (col & 15);
-        uint32_t sb[(COLS + 3) / 4] = {};
+        uint32_t sb = 0u;
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
+        for (int c = 0; c < 2; ++c) {
             // With the exponent field E and 7 mantissa bits M of the largest
             // magnitude, s = E - 2, one more from M = 96 (1.75) on: the largest
             // over 2^(s-127) lies in [3.5, 7) and rounds to 4 or 6, so nothing is
             // clipped by more than the half step of that part of the grid.  The
             // clamps keep every W' a normal finite bf16.
-            const uint32_t b = top[c >> 1][c & 1];
+            const uint32_t b = top[c];
             uint32_t s = (b + 32u) >> 7;
             s = s < 4u ? 2u : min(s - 2u, 252u);
             if (b == 0u) s = 127u;
@@ -86,18 +77,18 @@ __global__ __launch_bounds__(256) void mxfp4_quantize_kernel(const uint16_t *W, 
             uint32_t q[4];
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+                const uint32_t sel = c ? 0x07060302u : 0x05040100u;
                 uint32_t o = 0u;
-                o = mx_code<0>(o, __builtin_amdgcn_perm(r[8 * d + 1][c >> 1], r[8 * d][c >> 1], sel), scale);
-                o = mx_code<1>(o, __builtin_amdgcn_perm(r[8 * d + 3][c >> 1], r[8 * d + 2][c >> 1], sel), scale);
-                o = mx_code<2>(o, __builtin_amdgcn_perm(r[8 * d + 5][c >> 1], r[8 * d + 4][c >> 1], sel), scale);
-                o = mx_code<3>(o, __builtin_amdgcn_perm(r[8 * d + 7][c >> 1], r[8 * d + 6][c >> 1], sel), scale);
+                o = mx_code<0>(o, __builtin_amdgcn_perm(r[8 * d + 1], r[8 * d], sel), scale);
+                o = mx_code<1>(o, __builtin_amdgcn_perm(r[8 * d + 3], r[8 * d + 2], sel), scale);
+                o = mx_code<2>(o, __builtin_amdgcn_perm(r[8 * d + 5], r[8 * d + 4], sel), scale);
+                o = mx_code<3>(o, __builtin_amdgcn_perm(r[8 * d + 7], r[8 * d + 6], sel), scale);
                 q[d] = bad ? 0u : o;
             }
             *(uint4 *)(codes + (at + c) * 16) = make_uint4(q[0], q[1], q[2], q[3]);
-            sb[c >> 2] |= (bad ? 255u : s) << (8 * (c & 3));
+            sb |= (bad ? 255u : s) << (8 * c);
         }
-        __builtin_memcpy(__builtin_assume_aligned(scales + at, COLS), sb, COLS);
+        *(uint16_t *)(scales + at) = (uint16_t)sb;
     }
 }
 
@@ -152,9 +143,7 @@ unsigned mx_grid(int64_t items) { return (unsigned)std::min<int64_t>((items + 25
 hipError_t launch_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *codes, void *scales, hipStream_t stream) {
     const MxShape s = mx_shape(k, n);
     const int slot = prof_begin("mxfp4_quantize", stream);
-    constexpr int cols = 2;
-    hipLaunchKernelGGL(mxfp4_quantize_kernel<cols>, dim3(mx_grid(s.kb * s.n16 * 16 / cols)), dim3(256), 0, stream,
-                       (const uint16_t *)W, s, (uint8_t *)codes, (uint8_t *)scales);
+    hipLaunchKernelGGL(mxfp4_quantize_kernel, dim3(mx_grid(s.kb * s.n16 * 8)), dim3(256), 0, stream, (const uint16_t *)W, s, (uint8_t *)codes, (uint8_t *)scales);
     prof_end(slot, stream);
     return hipGetLastError();
 }

@@ -285,3 +285,24 @@ def test_mixed(case):
     for a in range(3):
         near(f"dA[{a}]", dAs[a], sums[a]["dA"], slacks[a]["dA"])
         near(f"dB[{a}]", dBs[a], sums[a]["dB"], slacks[a]["dB"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n,r", [(1 << 19, 72, 40, 8), ((1 << 19) + 5, 72, 40, 8), (3, 1 << 20, 24, 5), (3, (1 << 20) + 8, 24, 5),
+                                     (3, 24, 1 << 20, 5), (3, 24, (1 << 21) + 8, 5)])
+def test_sizes_around_the_packed_products_limits(m, k, n, r):
+    # up to 2^19 rows, 2^20 of k and 2^21 columns (2^20 in the backward) the packed weight is read, past them it
+    # is expanded
+    log(f"limits m={m} k={k} n={n}")
+    X, W4, W, dY, g = inputs(m, k, n, seed=5)
+    A, B = bf16_randn((k, r), k ** -0.5, g).cuda(), bf16_randn((r, n), 0.02 ** 0.5, g).cuda()
+    with Ran() as ran:
+        Y, S, _ = lf.lora_mxfp4_linear_fwd(X, W4, A, B, 2.0, 0.0)
+        dX, dA, dB = lf.lora_mxfp4_linear_bwd(dY, X, W4, A, B, S, None, 2.0, 0.0)
+        torch.cuda.synchronize()
+    past = m > 1 << 19 or k > 1 << 20 or n > 1 << 21
+    assert not past or not (ran.forward or ran.backward) and ran.expanded == 2
+    want, slack = layer(X, W, A, B, dY, 2.0, 0.0, torch.ones((), dtype=F64, device="cuda"))
+    assert ((S.to(F64) - want["S"]).abs() <= slack["S"] + 1e-30).all()
+    for name, t in (("Y", Y), ("dX", dX), ("dA", dA), ("dB", dB)):
+        near(name, t, want[name], slack[name])
