@@ -420,7 +420,8 @@ lora_status lora_frozen_bwd(const void *dY, const void *W, int64_t m, int64_t k,
  * `name_substring`, the number of launches and their summed duration in
  * milliseconds since the last reset.  Event pairs come from a pool created by
  * lora_profiling_enable(1) (capacity events per kernel launch slot); launches
- * beyond the capacity are not timed. */
+ * beyond the capacity are not timed.  The products over an MXFP4 weight carry
+ * their tile ("mxfp4_gemm 64x128", "mxfp4_gemm_t 128x256"). */
 lora_status lora_profiling_enable(int32_t enable, int32_t capacity);
 lora_status lora_profiling_reset(void);
 lora_status lora_profiling_query(const char *name_substring, int64_t *launches, double *total_ms);
