@@ -172,7 +172,10 @@ lora_status lora_linear_bwd_noalloc(const void *dY, const void *X, const void *W
 /* Segments: rows [seg_off[s], seg_off[s+1]) use adapter seg_adapter[s];
  * seg_off (int64, num_segments+1 entries) and seg_adapter (int32) are device
  * arrays; segments must be ordered, contiguous and cover [0, m); empty
- * segments are allowed.  r_max >= every adapter's r is the row stride of S. */
+ * segments are allowed.  r_max >= every adapter's r is the row stride of S.
+ * Adapters are added to tiles of 128 rows with zeros in the rows of others: an
+ * infinity or NaN in one adapter's A or B can make rows of its neighbours in
+ * a tile NaN (finite adapters never touch each other's rows). */
 size_t multi_lora_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                      int32_t num_adapters, int32_t num_segments);
 
