@@ -127,10 +127,11 @@ class MultiLoraLinearFunction(torch.autograd.Function):
         st = _adapter_set(As, Bs, alphas, ps)
         fwd = mxfp4.multi_lora_mxfp4_linear_fwd if isinstance(W, Mxfp4Weight) else _lib.multi_lora_linear_fwd
         Y, S, keep = fwd(X, W, st.table, st.num, seg_off, seg_adapter, st.r_max, seed, offset)
-        # the table holds A's and B's addresses alone: saved, they live on and are guarded against changes
+        # the table holds A's and B's addresses alone: saved, they are guarded against changes, and kept here
+        # they live on where a hook packs saved tensors away
         held = _weight_tensors(W)
         ctx.save_for_backward(X, seg_off, seg_adapter, S, keep, *held, *AB)
-        ctx.adapter_set, ctx.held = st, len(held)
+        ctx.adapter_set, ctx.held, ctx.adapters = st, len(held), AB
         return Y
 
     @staticmethod

@@ -65,6 +65,21 @@ def test_a_change_between_forward_and_backward_is_refused(weight):
         y.sum().backward()
 
 
+def test_matrices_live_where_saved_tensors_are_packed_away(weight):
+    # (as torch.autograd.graph.save_on_cpu does: the backward gets copies at other addresses)
+    casts = [torch.randn(s).bfloat16().requires_grad_() * 1 for r in RANKS for s in ((K, r), (r, N))]
+    watch = [weakref.ref(t) for t in casts]
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), lambda t: t):
+        y = call(weight, casts[0::2], casts[1::2])
+    del casts
+    gc.collect()
+    assert all(w() is not None for w in watch)
+    y.sum().backward()
+    del y
+    gc.collect()
+    assert all(w() is None for w in watch)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("packed", [False, True])
 def test_gradients_of_adapters_cast_for_the_call(packed):
