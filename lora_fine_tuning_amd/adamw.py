@@ -169,6 +169,8 @@ class LoraAdamW(torch.optim.Optimizer):
             raise ValueError(f"state_bits = {state_bits} must be 8 or 32")
         if not lr >= 0.0 or not weight_decay >= 0.0 or not eps >= 0.0:
             raise ValueError(f"lr = {lr}, weight_decay = {weight_decay} and eps = {eps} must be >= 0")
+        if 0.0 < eps < 2.0 ** -126:
+            raise ValueError(f"eps = {eps} must be 0 or at least 2^-126")
         if not all(0.0 <= b < 1.0 for b in betas):
             raise ValueError(f"betas = {betas} must be in [0, 1)")
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,

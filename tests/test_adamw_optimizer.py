@@ -327,3 +327,11 @@ def test_a_backward_from_before_a_step_is_refused(capturable):
         stale.backward()
     layer(X).sum().backward()  # and one from after it runs
     opt.step()
+
+
+# ---- hyperparameters -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("eps", [1e-40, 2.0 ** -127, -1.0, float("nan")])
+def test_epsilons_that_the_library_refuses_are_refused_at_once(eps):
+    with pytest.raises(ValueError, match="eps"):
+        lf.LoraAdamW(parameters(), eps=eps)
