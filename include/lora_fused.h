@@ -350,6 +350,130 @@ lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const voi
                                         int64_t m, int64_t k, int64_t n, int32_t r_max, void *dX,
                                         void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- frozen weights of 4-bit integers in groups of rows --------------------
+ * The frozen W may also be held as 4-bit integers q with one scale s and one
+ * zero z for `group` rows of a column, W'[i][j] = s (q - z), which is how
+ * integer-quantised checkpoints hold it.  group is 32, 64 or a multiple of
+ * 128 (k or more rows: one scale a column).
+ *
+ * Storage, N16 = ceil(n / 16) and K128 = ceil(k / 128):
+ *   codes   [N16][K128][4][16][16] bytes: word d (little-endian) of the 16
+ *           bytes of (c, t, g, j) holds rows i .. i+7, i = 128t + 32d + 8g, of
+ *           column 16c + j; rows i, i+2, i+4, i+6 in its low four nibbles
+ *           from the lowest up, i+1, i+3, i+5, i+7 in its high four
+ *   scales  [N16][G][16] words: the bits of s as a float with its last 8 bits
+ *           zero, and z (0 .. 255) in those 8, of column 16c + j;
+ *           G = 128 K128 / group for groups of 32 or 64, else ceil(k / group)
+ * both 16-byte aligned, lora_int4_codes_size() and lora_int4_scales_size()
+ * bytes.  s has 16 significant bits: a bf16's or an fp16's exactly.  Padding
+ * columns and rows hold code 0, padding columns and groups the word 0.
+ *
+ * lora_int4_quantize makes both from a bf16 W, to the nearest code (ties of
+ * w / s to even, then clamped to 0 .. 15):
+ *   symmetric = 0: lo and hi the group's smallest and largest value and 0,
+ *                  s = (hi - lo) / 15, z = -lo / s to the nearest integer
+ *   symmetric = 1: s = max |w| / 7, z = 8
+ * s rounded to 16 significant bits and at least 2^-120; a group of zeros has
+ * s = 1, one with an infinity or a NaN has s = NaN: all its values then are.
+ *
+ * lora_int4_pack makes both from a checkpoint's: Q (k x n bytes, the code in
+ * the low four bits), group_scales (ceil(k / group) x n of scale_type 0: fp32,
+ * rounded to 16 significant bits, 1: bf16, 2: fp16; an infinity reads as NaN)
+ * and zeros (ceil(k / group) x n bytes; NULL: every zero is 8); Q and
+ * group_scales 4-byte aligned. */
+size_t lora_int4_codes_size(int64_t k, int64_t n);
+size_t lora_int4_scales_size(int64_t k, int64_t n, int64_t group);
+lora_status lora_int4_quantize(const void *W, int64_t k, int64_t n, int64_t group, int32_t symmetric, void *codes,
+                               void *scales, hipStream_t stream);
+lora_status lora_int4_pack(const void *Q, const void *group_scales, int32_t scale_type, const void *zeros, int64_t k,
+                           int64_t n, int64_t group, void *codes, void *scales, hipStream_t stream);
+/* W' as row-major k x n bf16, each value rounded to the nearest. */
+lora_status lora_int4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, int64_t group, void *W,
+                                 hipStream_t stream);
+
+/* The frozen layer and the LoRA layers over W': as lora_frozen_fwd / _bwd,
+ * lora_linear_fwd / _bwd and multi_lora_linear_fwd / _bwd, with the same
+ * arguments, outputs, checks and errors. */
+size_t lora_int4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group);
+lora_status lora_int4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t group, int64_t m,
+                                 int64_t k, int64_t n, void *Y, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+size_t lora_int4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group);
+lora_status lora_int4_frozen_bwd(const void *dY, const void *codes, const void *scales, int64_t group, int64_t m,
+                                 int64_t k, int64_t n, void *dX, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+size_t lora_int4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r);
+lora_status lora_int4_linear_fwd(const void *X, const void *codes, const void *scales, int64_t group, const void *A,
+                                 const void *B, int64_t m, int64_t k, int64_t n, int32_t r, float alpha, float p,
+                                 uint64_t seed, uint64_t offset, void *Y, float *S, uint32_t *keep_bits,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t lora_int4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r);
+lora_status lora_int4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales, int64_t group,
+                                 const void *A, const void *B, const float *S, const uint32_t *keep_bits, int64_t m,
+                                 int64_t k, int64_t n, int32_t r, float alpha, float p, void *dX, void *dA, void *dB,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t multi_lora_int4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max,
+                                          int32_t num_adapters, int32_t num_segments);
+lora_status multi_lora_int4_linear_fwd(const void *X, const void *codes, const void *scales, int64_t group,
+                                       const lora_adapter *adapters, int32_t num_adapters, const int64_t *seg_off,
+                                       const int32_t *seg_adapter, int32_t num_segments, int64_t m, int64_t k,
+                                       int64_t n, int32_t r_max, uint64_t seed, uint64_t offset, void *Y, float *S,
+                                       uint32_t *keep_bits, void *workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+size_t multi_lora_int4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max,
+                                          int32_t num_adapters, int32_t num_segments);
+lora_status multi_lora_int4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales,
+                                       int64_t group, const lora_adapter *adapters, int32_t num_adapters,
+                                       const int64_t *seg_off, const int32_t *seg_adapter, int32_t num_segments,
+                                       const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                                       int32_t r_max, void *dX, void *workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+
+/* ---- the layer's input saved in 8 bits (MXINT8) -----------------------------
+ * X is all that the backward keeps of a layer that grows with tokens times
+ * width, and it is read for dA alone.  It may be saved as 8-bit integers in
+ * blocks of 32 along each row with one power-of-two scale byte s each,
+ * X'[i][32b + j] = c 2^(s - 127), 0.52 of its bf16 bytes.  Every X' is exactly
+ * a bf16.
+ *
+ * Storage, KB = 4 ceil(k / 128): codes [m][KB][32] int8 (16-byte aligned) and
+ * scales [m][KB] bytes (4-byte aligned).  Padding holds codes 0, scales 127.
+ *
+ * lora_mxint8_quantize: with a the block's largest magnitude, the scale is
+ * 2^e, e = floor(log2 a) - 6 clamped to [-120, 121], and each code the nearest
+ * to x / 2^e (ties to even): |x - x'| <= 2^(e-1).  A block of zeros gets
+ * s = 127, and a block with an infinity or a NaN s = 255: all its values then
+ * read as NaN.  Other bytes that are not written by it read as the powers of
+ * two they stand for. */
+size_t lora_mxint8_codes_size(int64_t m, int64_t k);
+size_t lora_mxint8_scales_size(int64_t m, int64_t k);
+lora_status lora_mxint8_quantize(const void *X, int64_t m, int64_t k, void *codes, void *scales, hipStream_t stream);
+/* X' as row-major m x k bf16 (exact). */
+lora_status lora_mxint8_dequantize(const void *codes, const void *scales, int64_t m, int64_t k, void *X,
+                                   hipStream_t stream);
+
+/* lora_linear_bwd and multi_lora_linear_bwd with X' in place of X (S and
+ * keep_bits are the forward's, which ran on X): dA = s (keep (.) X')^T dS, and
+ * dX and dB as before.  The weight is W (kind LORA_WEIGHT_BF16; W_scales and
+ * group are not read), the codes and scales of an MXFP4 weight (group is not
+ * read) or those of 4-bit integers.  Other arguments, outputs, checks and
+ * errors as there. */
+typedef enum { LORA_WEIGHT_BF16 = 0, LORA_WEIGHT_MXFP4 = 1, LORA_WEIGHT_INT4 = 2 } lora_weight_kind;
+size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r);
+lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind,
+                                   const void *W, const void *W_scales, int64_t group, const void *A, const void *B,
+                                   const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                                   int32_t r, float alpha, float p, void *dX, void *dA, void *dB, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n,
+                                            int32_t r_max, int32_t num_adapters, int32_t num_segments);
+lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind,
+                                         const void *W, const void *W_scales, int64_t group,
+                                         const lora_adapter *adapters, int32_t num_adapters, const int64_t *seg_off,
+                                         const int32_t *seg_adapter, int32_t num_segments, const float *S,
+                                         const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                         void *dX, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ---- optimizer ------------------------------------------------------------
  * One AdamW step over many tensors (the adapters' A and B of a model):
  *   m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2

@@ -39,6 +39,14 @@ EXPORTS = [
     "lora_mxfp4_linear_bwd_workspace_size", "lora_mxfp4_linear_bwd", "multi_lora_mxfp4_fwd_workspace_size",
     "multi_lora_mxfp4_linear_fwd", "multi_lora_mxfp4_bwd_workspace_size", "multi_lora_mxfp4_linear_bwd",
     "lora_adamw_step",
+    "lora_int4_codes_size", "lora_int4_scales_size", "lora_int4_quantize", "lora_int4_pack", "lora_int4_dequantize",
+    "lora_int4_frozen_fwd_workspace_size", "lora_int4_frozen_fwd", "lora_int4_frozen_bwd_workspace_size",
+    "lora_int4_frozen_bwd", "lora_int4_linear_fwd_workspace_size", "lora_int4_linear_fwd",
+    "lora_int4_linear_bwd_workspace_size", "lora_int4_linear_bwd", "multi_lora_int4_fwd_workspace_size",
+    "multi_lora_int4_linear_fwd", "multi_lora_int4_bwd_workspace_size", "multi_lora_int4_linear_bwd",
+    "lora_mxint8_codes_size", "lora_mxint8_scales_size", "lora_mxint8_quantize", "lora_mxint8_dequantize",
+    "lora_mxint8_linear_bwd_workspace_size", "lora_mxint8_linear_bwd", "multi_lora_mxint8_bwd_workspace_size",
+    "multi_lora_mxint8_linear_bwd",
 ]
 
 
@@ -119,6 +127,37 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "multi_lora_mxfp4_linear_bwd": (I32, [P, P, P, P, P, I32, P, P, I32, P, P, I64, I64, I64, I32,
                                               P, P, SZ, P]),
         "lora_adamw_step": (I32, [P, I32, I32, I32, I32, F64, F64, F64, F64, F64, I64, P, U64, P]),
+        "lora_int4_codes_size": (SZ, [I64, I64]),
+        "lora_int4_scales_size": (SZ, [I64, I64, I64]),
+        "lora_int4_quantize": (I32, [P, I64, I64, I64, I32, P, P, P]),
+        "lora_int4_pack": (I32, [P, P, I32, P, I64, I64, I64, P, P, P]),
+        "lora_int4_dequantize": (I32, [P, P, I64, I64, I64, P, P]),
+        "lora_int4_frozen_fwd_workspace_size": (SZ, [I64, I64, I64, I64]),
+        "lora_int4_frozen_bwd_workspace_size": (SZ, [I64, I64, I64, I64]),
+        "lora_int4_frozen_fwd": (I32, [P, P, P, I64, I64, I64, I64, P, P, SZ, P]),
+        "lora_int4_frozen_bwd": (I32, [P, P, P, I64, I64, I64, I64, P, P, SZ, P]),
+        "lora_int4_linear_fwd_workspace_size": (SZ, [I64, I64, I64, I64, I32]),
+        "lora_int4_linear_bwd_workspace_size": (SZ, [I64, I64, I64, I64, I32]),
+        "lora_int4_linear_fwd": (I32, [P, P, P, I64, P, P, I64, I64, I64, I32, F32, F32, U64, U64, P, P, P,
+                                       P, SZ, P]),
+        "lora_int4_linear_bwd": (I32, [P, P, P, P, I64, P, P, P, P, I64, I64, I64, I32, F32, F32, P, P, P,
+                                       P, SZ, P]),
+        "multi_lora_int4_fwd_workspace_size": (SZ, [I64, I64, I64, I64, I32, I32, I32]),
+        "multi_lora_int4_bwd_workspace_size": (SZ, [I64, I64, I64, I64, I32, I32, I32]),
+        "multi_lora_int4_linear_fwd": (I32, [P, P, P, I64, P, I32, P, P, I32, I64, I64, I64, I32, U64, U64,
+                                             P, P, P, P, SZ, P]),
+        "multi_lora_int4_linear_bwd": (I32, [P, P, P, P, I64, P, I32, P, P, I32, P, P, I64, I64, I64, I32,
+                                             P, P, SZ, P]),
+        "lora_mxint8_codes_size": (SZ, [I64, I64]),
+        "lora_mxint8_scales_size": (SZ, [I64, I64]),
+        "lora_mxint8_quantize": (I32, [P, I64, I64, P, P, P]),
+        "lora_mxint8_dequantize": (I32, [P, P, I64, I64, P, P]),
+        "lora_mxint8_linear_bwd_workspace_size": (SZ, [I32, I64, I64, I64, I64, I32]),
+        "lora_mxint8_linear_bwd": (I32, [P, P, P, I32, P, P, I64, P, P, P, P, I64, I64, I64, I32, F32, F32, P,
+                                         P, P, P, SZ, P]),
+        "multi_lora_mxint8_bwd_workspace_size": (SZ, [I32, I64, I64, I64, I64, I32, I32, I32]),
+        "multi_lora_mxint8_linear_bwd": (I32, [P, P, P, I32, P, P, I64, P, I32, P, P, I32, P, P, I64, I64, I64,
+                                               I32, P, P, SZ, P]),
         "lora_status_string": (ctypes.c_char_p, [I32]),
         "lora_last_error_message": (ctypes.c_char_p, []),
     }

@@ -282,6 +282,20 @@ hipError_t launch_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *code
 hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, void *W,
                                    hipStream_t stream);
 
+// Inputs saved in 8 bits: blocks of 32 of the padded k (mxint8_kernels.hip).
+inline int64_t i8_blocks(int64_t k) { return (k + 127) / 128 * 4; }
+hipError_t launch_mxint8_quantize(const void *X, int64_t m, int64_t k, void *codes, void *scales, hipStream_t stream);
+hipError_t launch_mxint8_dequantize(const void *codes, const void *scales, int64_t m, int64_t k, void *X, hipStream_t stream);
+
+// Weights as 4-bit integers in groups of rows (int4_kernels.hip).  scale_type of
+// given scales: 0 fp32, 1 bf16, 2 fp16; zeros may be NULL (all 8).
+hipError_t launch_int4_quantize(const void *W, int64_t k, int64_t n, int64_t group, bool symmetric, void *codes, void *scales,
+                                hipStream_t stream);
+hipError_t launch_int4_pack(const void *Q, const void *scales_in, int scale_type, const void *zeros, int64_t k, int64_t n, int64_t group,
+                            void *codes, void *scales, hipStream_t stream);
+hipError_t launch_int4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, int64_t group, void *W,
+                                  hipStream_t stream);
+
 // Y = X W' (+ alpha S B) straight from the packed weight (mxfp4_gemm.hip).
 struct MxGemmPlan {
     int kind;  // tile shape; 0: not for this shape

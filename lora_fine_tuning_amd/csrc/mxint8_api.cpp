@@ -1,0 +1,147 @@
+// C-ABI entry points for a layer's input saved in 8 bits (MXINT8), and the layer's
+// backward from it in both adapter forms, over a frozen weight in any of its forms.
+#include <hip/hip_runtime.h>
+
+#include "api_checks.hpp"
+#include "launch.hpp"
+#include "lora_fused.h"
+
+using namespace lora;
+
+static lora_status check_input(int64_t m, int64_t k, const void *codes, const void *scales) {
+    CHECK(check_shape(m, k, 8));
+    if (m == 0) return LORA_OK;
+    REQ_PTR(codes, 16);
+    REQ_PTR(scales, 4);
+    return LORA_OK;
+}
+
+extern "C" size_t lora_mxint8_codes_size(int64_t m, int64_t k) {
+    if (m < 0 || k <= 0 || m >= (1LL << 31) || k >= (1LL << 31)) return 0;
+    return (size_t)m * (size_t)i8_blocks(k) * 32;
+}
+
+extern "C" size_t lora_mxint8_scales_size(int64_t m, int64_t k) { return lora_mxint8_codes_size(m, k) / 32; }
+
+extern "C" lora_status lora_mxint8_quantize(const void *X, int64_t m, int64_t k, void *codes, void *scales, hipStream_t stream) {
+    CHECK(check_input(m, k, codes, scales));
+    if (m == 0) return LORA_OK;
+    REQ_PTR(X, 16);
+    HIPCHK(launch_mxint8_quantize(X, m, k, codes, scales, stream), "MXINT8 quantise launch");
+    return LORA_OK;
+}
+
+extern "C" lora_status lora_mxint8_dequantize(const void *codes, const void *scales, int64_t m, int64_t k, void *X, hipStream_t stream) {
+    CHECK(check_input(m, k, codes, scales));
+    if (m == 0) return LORA_OK;
+    REQ_PTR(X, 16);
+    HIPCHK(launch_mxint8_dequantize(codes, scales, m, k, X, stream), "MXINT8 dequantise launch");
+    return LORA_OK;
+}
+
+// The expanded input sits at the start of the workspace, the layer's own after it.
+static size_t input_bytes(int64_t m, int64_t k) { return align_up((size_t)m * (size_t)k * 2); }
+
+static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
+    return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && m * k < (1LL << 46) && k * n < (1LL << 46);
+}
+
+static lora_status check_weight(int32_t kind, const void *W, const void *W_scales, int64_t group) {
+    REQUIRE(kind == LORA_WEIGHT_BF16 || kind == LORA_WEIGHT_MXFP4 || kind == LORA_WEIGHT_INT4, "weight kind %d is unknown", kind);
+    REQ_PTR(W, 16);
+    if (kind != LORA_WEIGHT_BF16) REQ_PTR(W_scales, 16);
+    REQUIRE(kind != LORA_WEIGHT_INT4 || lora_int4_scales_size(128, 8, group) > 0, "group = %lld must be 32, 64 or a multiple of 128",
+            (long long)group);
+    return LORA_OK;
+}
+
+// What both backward calls read and write a row at a time.
+static lora_status check_rows(int64_t m, const void *dY, const float *S, const uint32_t *keep_bits, bool keep_needed, const void *dX) {
+    if (m == 0) return LORA_OK;
+    REQ_PTR(dY, 16);
+    REQ_PTR(S, 4);
+    REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
+    REQUIRE(keep_bits != nullptr || !keep_needed, "keep_bits may be NULL only for one adapter with p == 0");
+    REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
+    return LORA_OK;
+}
+
+extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r) {
+    if (!sizes_ok(m, k, n) || r < 1 || r > 256) return 0;
+    const size_t layer = kind == LORA_WEIGHT_BF16    ? lora_linear_bwd_workspace_size(m, k, n, r)
+                         : kind == LORA_WEIGHT_MXFP4 ? lora_mxfp4_linear_bwd_workspace_size(m, k, n, r)
+                                                     : lora_int4_linear_bwd_workspace_size(m, k, n, group, r);
+    return input_bytes(m, k) + layer;
+}
+
+extern "C" size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r_max,
+                                                       int32_t num_adapters, int32_t num_segments) {
+    if (!sizes_ok(m, k, n) || r_max < 1 || r_max > 256 || num_adapters < 1 || num_segments < 0) return 0;
+    const size_t layer = kind == LORA_WEIGHT_BF16    ? multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
+                         : kind == LORA_WEIGHT_MXFP4 ? multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
+                                                     : multi_lora_int4_bwd_workspace_size(m, k, n, group, r_max, num_adapters, num_segments);
+    return input_bytes(m, k) + layer;
+}
+
+// The layer's backward over a weight of either kind.
+static lora_status layer_bwd(int32_t kind, const void *W, const void *W_scales, int64_t group, const void *dY, const void *X,
+                             const void *A, const void *B, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                             int32_t r, float alpha, float p, void *dX, void *dA, void *dB, void *workspace, size_t bytes,
+                             hipStream_t stream) {
+    if (kind == LORA_WEIGHT_BF16)
+        return lora_linear_bwd(dY, X, W, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB, workspace, bytes, stream);
+    if (kind == LORA_WEIGHT_MXFP4)
+        return lora_mxfp4_linear_bwd(dY, X, W, W_scales, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB, workspace, bytes, stream);
+    return lora_int4_linear_bwd(dY, X, W, W_scales, group, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB, workspace, bytes, stream);
+}
+
+extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind, const void *W,
+                                              const void *W_scales, int64_t group, const void *A, const void *B, const float *S,
+                                              const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r, float alpha, float p,
+                                              void *dX, void *dA, void *dB, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(kind, W, W_scales, group));
+    CHECK(check_input(m, k, x_codes, x_scales));
+    CHECK(check_rank(r));
+    CHECK(check_p(p));
+    CHECK(check_b_size(r, k, n));
+    REQ_PTR(A, 2);
+    REQ_PTR(B, 2);
+    REQ_PTR(dA, 2);
+    REQ_PTR(dB, 2);
+    CHECK(check_rows(m, dY, S, keep_bits, p != 0.0f, dX));
+    const size_t need = lora_mxint8_linear_bwd_workspace_size(kind, group, m, k, n, r), w = input_bytes(m, k);
+    if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (need > 0) REQ_PTR(workspace, 16);
+    if (m > 0) HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
+    return layer_bwd(kind, W, W_scales, group, dY, workspace, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
+                     ws_at(workspace, w), workspace_bytes - w, stream);
+}
+
+extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind, const void *W,
+                                                    const void *W_scales, int64_t group, const lora_adapter *adapters,
+                                                    int32_t num_adapters, const int64_t *seg_off, const int32_t *seg_adapter,
+                                                    int32_t num_segments, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
+                                                    int64_t n, int32_t r_max, void *dX, void *workspace, size_t workspace_bytes,
+                                                    hipStream_t stream) {
+    CHECK(check_shape(m, k, n));
+    CHECK(check_weight(kind, W, W_scales, group));
+    CHECK(check_input(m, k, x_codes, x_scales));
+    // (the forward on no rows makes the checks of the adapter and segment tables, and enqueues nothing)
+    CHECK(multi_lora_linear_fwd(nullptr, W, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max, 0, 0, nullptr,
+                                nullptr, nullptr, nullptr, 0, stream));
+    CHECK(check_rows(m, dY, S, keep_bits, true, dX));
+    const size_t need = multi_lora_mxint8_bwd_workspace_size(kind, group, m, k, n, r_max, num_adapters, num_segments), w = input_bytes(m, k);
+    if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (need > 0) REQ_PTR(workspace, 16);
+    if (m > 0) HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
+    char *rest = ws_at(workspace, w);
+    if (kind == LORA_WEIGHT_BF16)
+        return multi_lora_linear_bwd(dY, workspace, W, adapters, num_adapters, seg_off, seg_adapter, num_segments, S, keep_bits, m, k, n,
+                                     r_max, dX, rest, workspace_bytes - w, stream);
+    if (kind == LORA_WEIGHT_MXFP4)
+        return multi_lora_mxfp4_linear_bwd(dY, workspace, W, W_scales, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
+                                           keep_bits, m, k, n, r_max, dX, rest, workspace_bytes - w, stream);
+    return multi_lora_int4_linear_bwd(dY, workspace, W, W_scales, group, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
+                                      keep_bits, m, k, n, r_max, dX, rest, workspace_bytes - w, stream);
+}

@@ -1,0 +1,728 @@
+"""Frozen weights of 4-bit integers in groups of rows: packing, and the layers over them.
+
+The reference is written here from the format's definition, in 64 bits with
+numpy; it shares nothing with the library.
+
+Tolerances, derived (half a step of bf16 is 2^-8 of a value, of fp32 2^-24):
+* packing is exact, unpacking to the nearest bf16 of s (q - z), which fp32 holds
+  exactly (16 and 8 significant bits).
+* a product's entry is an fp32 sum rounded once to bf16: half a bf16 step, and
+  2^-24 of the terms' magnitudes for each addition.  Up to FEW rows the terms are
+  x (16 + q) and x (16 + z), so their magnitudes are |x| s (32 + q + z), and there
+  are k + 16 additions to count with the scales' products; the weight itself is
+  not rounded.  With more rows, and in the backward, the weight is the bf16 one
+  that lora_int4_dequantize gives, and the terms x W'.
+* the LoRA term adds what test_mxfp4.layer_reference derives.
+"""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import lora_fine_tuning_amd as lf
+from lora_fine_tuning_amd import _lib
+from parity import bf16_randn, log, offset_view
+from test_mxfp4 import f64, layer_reference, near
+
+HALF = 2.0 ** -24
+FAKE = 0x10000  # aligned, never dereferenced
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
+FEW = 0  # rows up to which the weight is not rounded
+
+
+# ---- the format, from its definition ---------------------------------------------------------
+
+def short(s):
+    """s > 0 rounded to 16 significant bits, ties to even."""
+    e = np.floor(np.log2(s))
+    e -= 2.0 ** e > s
+    e += 2.0 ** (e + 1) <= s
+    return np.rint(s / 2.0 ** (e - 15)) * 2.0 ** (e - 15)
+
+
+def ref_quantize(W, group, symmetric):
+    """(codes (k, n), scales (G, n) with NaN for marked groups, zeros (G, n))."""
+    k, n = W.shape
+    G = -(-k // group)
+    q, s, z = np.zeros((k, n), np.uint8), np.ones((G, n)), np.zeros((G, n))
+    for b in range(G):
+        w = W[b * group:(b + 1) * group]
+        bad = ~np.isfinite(w).all(0)
+        w = np.where(np.isfinite(w), w, 0.0)
+        lo, hi = np.minimum(w.min(0), 0), np.maximum(w.max(0), 0)
+        span = np.maximum(hi, -lo) / 7 if symmetric else (hi - lo) / 15
+        some = span > 0
+        s[b, some] = short(np.maximum(span[some], 2.0 ** -120))
+        z[b] = 8 if symmetric else np.rint(-lo / s[b])
+        q[b * group:(b + 1) * group] = np.where(bad, 0, np.clip(np.rint(w / s[b]) + z[b], 0, 15))
+        s[b, bad], z[b, bad] = np.nan, 0
+    return q, s, z
+
+
+def values(q, s, z, group):
+    """s (q - z) in 64 bits."""
+    which = np.arange(q.shape[0]) // group
+    return s[which] * (q.astype(float) - z[which])
+
+
+def rounded(W):
+    return f64(torch.from_numpy(W).float().bfloat16())
+
+
+def stored(q, s, z, group, device="cuda"):
+    """An Int4Weight from plain codes, scales and zeros, word by word."""
+    k, n = q.shape
+    wide, deep = -(-n // 16), -(-k // 128)
+    full = np.zeros((deep * 128, wide * 16), np.uint32)
+    full[:k, :n] = q
+    rows = full.reshape(deep, 4, 4, 8, wide, 16)  # t, d, g, row, c, j
+    word = np.zeros((deep, 4, 4, wide, 16), np.uint32)
+    for e in range(8):
+        word |= rows[:, :, :, e] << np.uint32(4 * (e // 2 + 4 * (e % 2)))
+    codes = np.ascontiguousarray(word.transpose(3, 0, 2, 4, 1)).view(np.uint8).reshape(wide, deep, 4, 16, 16)
+    G = deep * 128 // group if group < 128 else s.shape[0]
+    bits = np.zeros((G, wide * 16), np.uint32)
+    f = s.astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        bits[:s.shape[0], :n] = np.where(np.isnan(f), np.uint32(0x7FC00000), f.view(np.uint32)) | z.astype(np.uint32)
+    scales = np.ascontiguousarray(bits.reshape(G, wide, 16).transpose(1, 0, 2)).view(np.int32)
+    return lf.Int4Weight(torch.from_numpy(codes).to(device), torch.from_numpy(scales).to(device), k, n, group)
+
+
+def test_reference_round_trip():
+    # the definition itself: a value is off by half a scale, but for the clamped ends, and values on the grid are exact
+    rng = np.random.default_rng(0)
+    W = f64(torch.from_numpy(rng.standard_normal((192, 24))).bfloat16())
+    for group, sym in ((32, False), (64, True), (128, False)):
+        q, s, z = ref_quantize(W, group, sym)
+        V = values(q, s, z, group)
+        step = s[np.arange(192) // group]
+        assert (np.abs(V - W) <= 0.5001 * step * (1 if sym else 2)).all()
+        q2, s2, z2 = q, s, z
+        assert np.array_equal(values(q2, s2, z2, group), V)
+
+
+# ---- refusals (host) ---------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def lib():
+    if torch.cuda.is_available():
+        pytest.skip("host-only checks; a GPU is visible")
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("library not built")
+    return _lib.load()
+
+
+def test_sizes():
+    lib = _lib.load()
+    for k, n, group, codes, scales in ((8, 8, 32, 1024, 4 * 64), (128, 16, 128, 1024, 64), (136, 24, 64, 4 * 1024, 2 * 4 * 64),
+                                       (300 * 8, 16, 256, 19 * 1024, 10 * 64), (4096, 14336, 128, 32 * 896 * 1024, 32 * 896 * 64)):
+        assert lib.lora_int4_codes_size(k, n) == codes and lib.lora_int4_scales_size(k, n, group) == scales
+    for group in (0, -32, 16, 96, 100, 192, 1 << 31):
+        assert lib.lora_int4_scales_size(256, 64, group) == 0
+        assert lib.lora_int4_frozen_fwd_workspace_size(4, 256, 64, group) == 0
+    assert lib.lora_int4_codes_size(0, 8) == 0 and lib.lora_int4_codes_size(8, -1) == 0
+    assert lf.lora_int4_linear_bwd_workspace_size(0, 64, 64, 32, 8) == _lib.lora_linear_bwd_workspace_size(0, 64, 64, 8)
+    assert lf.lora_int4_frozen_fwd_workspace_size(0, 64, 64, 32) == 0
+    assert lf.lora_int4_frozen_fwd_workspace_size(-1, 64, 64, 32) == 0
+    assert lf.lora_int4_linear_fwd_workspace_size(64, 64, 64, 32, 0) == lf.lora_int4_linear_fwd_workspace_size(64, 64, 64, 32, 257) == 0
+    assert lf.multi_lora_int4_fwd_workspace_size(64, 64, 64, 32, 8, -1, 2) == 0
+
+
+def test_pack_rejects(lib):
+    F = FAKE
+    for kw in (dict(W=None), dict(k=60), dict(n=20), dict(k=0), dict(W=F + 8), dict(codes=F + 8), dict(scales=F + 8), dict(scales=None),
+               dict(k=1 << 30, n=1 << 30), dict(group=16), dict(group=96), dict(group=0), dict(group=-128), dict(group=1 << 31)):
+        a = {**dict(W=F, k=64, n=64, group=32, codes=F, scales=F), **kw}
+        assert lib.lora_int4_quantize(a["W"], a["k"], a["n"], a["group"], 0, a["codes"], a["scales"], None) == INVALID, kw
+        assert lib.lora_int4_dequantize(a["codes"], a["scales"], a["k"], a["n"], a["group"], a["W"], None) == INVALID, kw
+        assert lib.lora_int4_pack(a["W"] and a["W"] - 7, F, 1, None, a["k"], a["n"], a["group"], a["codes"], a["scales"], None) == INVALID, kw
+    assert lib.lora_int4_pack(F, F, 3, None, 64, 64, 32, F, F, None) == INVALID
+    assert lib.lora_int4_pack(F, None, 1, None, 64, 64, 32, F, F, None) == INVALID
+    assert lib.lora_int4_pack(F, F + 2, 1, None, 64, 64, 32, F, F, None) == INVALID
+
+
+def test_layer_rejects(lib):
+    F, big = FAKE, 1 << 40
+    fz = lib.lora_int4_frozen_fwd
+    assert fz(F, F, F, 32, 4, 60, 64, F, F, big, None) == INVALID
+    assert fz(F, F, F, 48, 4, 64, 64, F, F, big, None) == INVALID
+    assert fz(F, F, F, 32, -1, 64, 64, F, F, big, None) == INVALID
+    assert fz(None, F, F, 32, 4, 64, 64, F, F, big, None) == INVALID
+    assert fz(F + 8, F, F, 32, 4, 64, 64, F, F, big, None) == INVALID
+    assert fz(F, F, F + 4, 32, 4, 64, 64, F, F, big, None) == INVALID
+    assert fz(None, F, F, 32, 0, 64, 64, None, None, 0, None) == 0
+    assert lib.lora_int4_frozen_bwd(F, F, F, 32, 4, 64, 64, None, F, big, None) == INVALID
+    need = lib.lora_int4_frozen_bwd_workspace_size(4096, 4096, 4096, 128)
+    assert need and lib.lora_int4_frozen_bwd(F, F, F, 128, 4096, 4096, 4096, F, F, need - 1, None) == WORKSPACE
+
+    def fwd(**kw):
+        a = dict(X=F, c=F, s=F, group=32, A=F, B=F, m=64, k=64, n=64, r=8, p=0.1, off=0, Y=F, S=F, keep=F, ws=F, wsb=big)
+        a.update(kw)
+        return lib.lora_int4_linear_fwd(a["X"], a["c"], a["s"], a["group"], a["A"], a["B"], a["m"], a["k"], a["n"], a["r"], 1.0,
+                                        a["p"], 0, a["off"], a["Y"], a["S"], a["keep"], a["ws"], a["wsb"], None)
+
+    for kw in (dict(X=None), dict(c=None), dict(c=F + 8), dict(s=None), dict(A=None), dict(B=None), dict(Y=None), dict(group=33),
+               dict(S=None), dict(r=0), dict(r=257), dict(p=1.0), dict(p=-0.1), dict(off=4), dict(keep=None),
+               dict(k=12), dict(n=12), dict(S=F + 2), dict(keep=F + 2), dict(p=float("nan"))):
+        assert fwd(**kw) == INVALID, kw
+    need = lib.lora_int4_linear_fwd_workspace_size(512, 4096, 4096, 128, 256)
+    assert need > 0 and fwd(m=512, k=4096, n=4096, group=128, r=256, wsb=need - 1) == WORKSPACE
+    assert fwd(r=256, n=1 << 22) == UNSUPPORTED
+    assert fwd(m=0, X=None, Y=None, S=None, keep=None, ws=None, wsb=0) == 0
+
+    def bwd(**kw):
+        a = dict(dY=F, X=F, c=F, s=F, group=64, A=F, B=F, S=F, keep=F, m=64, k=64, n=64, r=8, p=0.1, dX=F, dA=F, dB=F, ws=F,
+                 wsb=big)
+        a.update(kw)
+        return lib.lora_int4_linear_bwd(a["dY"], a["X"], a["c"], a["s"], a["group"], a["A"], a["B"], a["S"], a["keep"], a["m"],
+                                        a["k"], a["n"], a["r"], 1.0, a["p"], a["dX"], a["dA"], a["dB"], a["ws"], a["wsb"], None)
+
+    for kw in (dict(dY=None), dict(X=None), dict(c=None), dict(s=F + 1), dict(dA=None), dict(dB=None), dict(S=None), dict(group=-1),
+               dict(keep=None), dict(r=300), dict(p=1.5), dict(dX=F + 2), dict(k=20), dict(ws=None)):
+        assert bwd(**kw) == INVALID, kw
+    assert bwd(wsb=0) == WORKSPACE and bwd(dX=None, wsb=0) == WORKSPACE
+    assert bwd(r=256, k=1 << 22) == UNSUPPORTED
+
+    mf, mb = lib.multi_lora_int4_linear_fwd, lib.multi_lora_int4_linear_bwd
+    assert mf(F, F, F, 32, F, 0, F, F, 1, 64, 64, 64, 16, 0, 0, F, F, F, F, big, None) == INVALID
+    assert mf(F, F, F, 31, F, 2, F, F, 1, 64, 64, 64, 16, 0, 0, F, F, F, F, big, None) == INVALID
+    assert mf(F, F, F, 32, F, 2, F, F, 0, 64, 64, 64, 16, 0, 0, F, F, F, F, big, None) == INVALID
+    assert mf(F, F, F, 32, F, 2, F, F, 1, 64, 64, 64, 16, 0, 0, F, F, None, F, big, None) == INVALID
+    assert mf(F, F, F, 32, F, 2, F, F, 1, 64, 64, 64, 16, 0, 4, F, F, F, F, big, None) == INVALID
+    assert mf(F, F, F, 32, F, 2, F, F, 1, 64, 64, 64, 16, 0, 0, F, F, F, F, 0, None) == WORKSPACE
+    assert mb(F, F, F, F, 32, F, 2, F, F, 1, F, F, 64, 64, 64, 300, F, F, big, None) == INVALID
+    assert mb(F, F, F, F, 32, F, 2, F, F, 1, F, None, 64, 64, 64, 16, F, F, big, None) == INVALID
+    assert mb(F, F, F, F, 32, F, 2, F, F, 1, F, F, 64, 64, 64, 16, F, F, 0, None) == WORKSPACE
+
+
+def test_binding_rejects():
+    # everything but the device is checked on CPU tensors too
+    W = stored(np.zeros((64, 64), np.uint8), np.ones((2, 64)), np.zeros((2, 64)), 32, "cpu")
+    X = torch.zeros(3, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="Int4Weight"):
+        lf.lora_int4_frozen_fwd(X, X)
+    with pytest.raises(TypeError, match="uint8"):
+        lf.lora_int4_frozen_fwd(X, W._replace(codes=W.codes.int()))
+    with pytest.raises(ValueError, match="do not hold"):
+        lf.lora_int4_frozen_fwd(X, W._replace(group=64))
+    with pytest.raises(ValueError, match="group"):
+        lf.lora_int4_frozen_fwd(X, W._replace(group=48))
+    with pytest.raises(ValueError, match="device"):
+        lf.lora_int4_frozen_fwd(X, W)
+    with pytest.raises(TypeError, match="bfloat16"):
+        lf.lora_int4_quantize(X.float())
+    with pytest.raises(TypeError, match="uint8"):
+        lf.lora_int4_pack(X, X, group=32)
+
+
+# ---- packing (GPU) --------------------------------------------------------------------------------
+
+def check_quantize(W, group, symmetric):
+    k, n = W.shape
+    q, s, z = ref_quantize(f64(W), group, symmetric)
+    got = lf.lora_int4_quantize(W.cuda(), group, symmetric=symmetric)
+    want = stored(q, s, z, group)
+    torch.cuda.synchronize()
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    back = lf.lora_int4_dequantize(got)
+    assert back.shape == (k, n)
+    ref = torch.from_numpy(rounded(values(q, s, z, group))).bfloat16()
+    nan = torch.isnan(ref)
+    assert torch.equal(torch.isnan(back.cpu()), nan) and torch.equal(back.cpu()[~nan], ref[~nan])
+
+
+PACK = [(8, 8, 32), (32, 16, 64), (40, 24, 128), (128, 256, 32), (136, 8, 64), (1000, 1032, 32), (264, 520, 128), (2048, 4104, 64),
+        (520, 72, 256), (904, 136, 384), (264, 24, 1024), (1032, 200, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("symmetric", [False, True])
+@pytest.mark.parametrize("k,n,group", PACK)
+def test_quantize_matches_definition(k, n, group, symmetric):
+    log(f"quantize {k}x{n} group {group}")
+    check_quantize(bf16_randn((k, n), k ** -0.5, torch.Generator().manual_seed(k + n)), group, symmetric)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("symmetric", [False, True])
+@pytest.mark.parametrize("group", [32, 128, 256])
+def test_quantize_special_values(group, symmetric):
+    # ties, zeros of both signs, one sign alone, subnormals, the largest values, marked groups
+    k, n = 392, 40
+    W = bf16_randn((k, n), 1.0, torch.Generator().manual_seed(1))
+    grid = torch.arange(k) % 15
+    W[:, 0] = (grid - 7).bfloat16() / 2                     # halves of a scale of 1 where 7 is the largest
+    W[3, 0] = 7.0
+    W[:, 1] = 0.0
+    W[:, 2] = -0.0
+    W[:, 3] = W[:, 3].abs()
+    W[:, 4] = -W[:, 4].abs()
+    W[:, 5] = 2.0 ** -133
+    W[:, 6] = 3.3895313892515355e38
+    W[::2, 7] = -3.3895313892515355e38
+    W[1::2, 7] = 3.3895313892515355e38
+    W[:, 8] = 0.0
+    W[77, 8] = -1.5
+    W[40, 9], W[300, 10], W[391, 11] = float("inf"), float("nan"), -float("inf")
+    W[:, 12] = (grid.bfloat16() + 0.5)
+    W[:, 13] = 1.0
+    W[::3, 14] = 2.0 ** -130
+    check_quantize(W, group, symmetric)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("k,n,group,zeros", [(8, 8, 32, True), (264, 72, 64, False), (520, 136, 128, True), (904, 40, 256, True),
+                                             (1032, 776, 32, False)])
+def test_pack_keeps_a_checkpoint(k, n, group, zeros, dtype):
+    rng = np.random.default_rng(k)
+    G = -(-k // group)
+    q = rng.integers(0, 16, (k, n)).astype(np.uint8)
+    s = torch.from_numpy(rng.standard_normal((G, n)) * 0.02).to(dtype)
+    z = rng.integers(0, 17, (G, n)).astype(np.uint8) if zeros else np.full((G, n), 8, np.uint8)
+    z[0, 0] = 255 if zeros else 8
+    held = f64(s)
+    if dtype is torch.float32:
+        held = np.sign(held) * short(np.abs(held))
+    got = lf.lora_int4_pack(torch.from_numpy(q).cuda(), s.cuda(), torch.from_numpy(z).cuda() if zeros else None, group=group)
+    want = stored(q, held, z, group)
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    assert np.array_equal(f64(lf.lora_int4_dequantize(got)), rounded(values(q, held, z, group)))
+
+
+# ---- the layers (GPU) -------------------------------------------------------------------------------
+
+def case(m, k, n, r, group, seed):
+    """(X, weight, (W' in 64 bits, W' in bf16, magnitudes of the few-row terms), A, B, dY)."""
+    g = torch.Generator().manual_seed(seed)
+    X = bf16_randn((m, k), 1.0, g)
+    q, s, z = ref_quantize(f64(bf16_randn((k, n), k ** -0.5, g)), group, seed % 2 == 0)
+    A, B, dY = bf16_randn((k, r), k ** -0.5, g), bf16_randn((r, n), 0.02 ** 0.5, g), bf16_randn((m, n), 1.0, g)
+    W = values(q, s, z, group)
+    which = np.arange(k) // group
+    return X, stored(q, s, z, group), (W, rounded(W), s[which] * (32.0 + q + z[which])), A, B, dY
+
+
+def product(m, x, W):
+    """(Y = X W', its slack) for m rows of a call."""
+    k = x.shape[1]
+    if m <= FEW:
+        return x @ W[0], (k + 16) * HALF * (np.abs(x) @ W[2])
+    return x @ W[1], k * HALF * (np.abs(x) @ np.abs(W[1]))
+
+
+def reference(X, W, A, B, dY, alpha, p, seed, offset, rows):
+    """layer_reference over the weight that a call of `rows` rows uses, forward and backward."""
+    want, slack = layer_reference(X, W[1], A, B, dY, alpha, p, seed, offset)
+    if rows <= FEW:
+        x = f64(X)
+        want["Y"] = want["Y"] + x @ (W[0] - W[1])
+        slack["Y"] = slack["Y"] + product(rows, x, W)[1]
+    return want, slack
+
+
+FROZEN = [(1, 8, 8, 32), (1, 128, 16, 128), (2, 40, 24, 32), (1, 4096, 264, 128), (3, 1032, 520, 64), (7, 136, 8, 32), (15, 264, 136, 128),
+          (16, 520, 1032, 32), (17, 392, 72, 64), (31, 2056, 104, 128), (33, 640, 200, 256), (48, 1000, 312, 32), (64, 4104, 96, 128),
+          (65, 256, 264, 64), (100, 904, 136, 128), (129, 136, 264, 32), (513, 264, 1032, 64), (1030, 400, 776, 384)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n,group", FROZEN)
+def test_frozen_forward_and_backward(m, k, n, group):
+    log(f"frozen m={m} k={k} n={n} group={group}")
+    X, W4, W, _, _, dY = case(m, k, n, 8, group, seed=m + k + n)
+    Yb = torch.full((m + 3, n), 5.0, dtype=torch.bfloat16, device="cuda")  # rows behind the last stay as they were
+    dXb = torch.full((m + 3, k), 5.0, dtype=torch.bfloat16, device="cuda")
+    lf.lora_int4_frozen_fwd(X.cuda(), W4, Y=Yb[:m])
+    lf.lora_int4_frozen_bwd(dY.cuda(), W4, dX=dXb[:m])
+    torch.cuda.synchronize()
+    assert (Yb[m:] == 5).all() and (dXb[m:] == 5).all()
+    dy = f64(dY)
+    near("Y", Yb[:m], *product(m, f64(X), W))
+    near("dX", dXb[:m], dy @ W[1].T, n * HALF * (np.abs(dy) @ np.abs(W[1]).T))
+
+
+DEEP = [(1, 4096, 4104, 128), (1, 14336, 1032, 32), (4, 8200, 264, 64), (9, 1288, 8200, 64), (24, 4096, 2048, 32), (40, 14336, 520, 128),
+        (64, 2056, 4104, 128), (50, 28672, 72, 1024), (2, 16, 14336, 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n,group", DEEP)
+def test_frozen_deep(m, k, n, group):
+    test_frozen_forward_and_backward(m, k, n, group)
+
+
+LAYER = [
+    # m, k, n, r, group, alpha, p
+    (1, 4096, 520, 16, 128, 2.0, 0.0), (1, 264, 136, 5, 32, -0.7, 0.0), (1, 72, 40, 1, 64, 2.0, 0.3), (2, 1032, 264, 64, 128, 0.5, 0.0),
+    (5, 2056, 136, 200, 64, 1.0, 0.0), (16, 520, 1032, 8, 32, 2.0, 0.1), (17, 136, 72, 33, 128, 1.0, 0.0), (40, 1288, 264, 128, 64, 0.5, 0.0),
+    (48, 392, 520, 256, 32, 1.0, 0.05), (63, 264, 264, 13, 128, 2.0, 0.0), (64, 2056, 1032, 64, 128, 0.5, 0.1), (100, 904, 392, 32, 32, 2.0, 0.2),
+    (333, 1032, 776, 5, 64, 2.0, 0.2), (520, 400, 264, 130, 128, 0.5, 0.1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("at", range(len(LAYER)))
+def test_layer_forward_and_backward(at):
+    m, k, n, r, group, alpha, p = LAYER[at]
+    log(f"layer m={m} k={k} n={n} r={r} group={group} p={p}")
+    X, W4, W, A, B, dY = case(m, k, n, r, group, seed=900 + at)
+    Xd, Ad, Bd = X.cuda(), A.cuda(), B.cuda()
+    Y, S, keep = lf.lora_int4_linear_fwd(Xd, W4, Ad, Bd, alpha, p, 7, 16)
+    dX, dA, dB = lf.lora_int4_linear_bwd(dY.cuda(), Xd, W4, Ad, Bd, S, keep, alpha, p)
+    torch.cuda.synchronize()
+    if p > 0:
+        assert torch.equal(keep, lf.lora_dropout_mask(7, 16, m, k, p))
+    want, slack = reference(X, W, A, B, dY, alpha, p, 7, 16, m)
+    assert (np.abs(f64(S) - want["S"]) <= slack["S"] + 1e-30).all()
+    for name, t in (("Y", Y), ("dX", dX), ("dA", dA), ("dB", dB)):
+        near(name, t, want[name], slack[name])
+    none, dA2, dB2 = lf.lora_int4_linear_bwd(dY.cuda(), Xd, W4, Ad, Bd, S, keep, alpha, p, want_dX=False)
+    assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,r", [(1, 136, 8), (40, 1080, 40), (64, 2056, 72), (130, 264, 16)])
+def test_mask_is_written_whole(m, k, r):
+    X, W4, W, A, B, dY = case(m, k, 264, r, 32, seed=37)
+    for p in (0.0, 2.0 ** -20, 0.3, 0.9999):
+        keep = torch.full((m + 1, (k + 31) // 32), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+        Y, S, got = lf.lora_int4_linear_fwd(X.cuda(), W4, A.cuda(), B.cuda(), 2.0, p, 11, 24, keep_bits=keep[:m])
+        torch.cuda.synchronize()
+        assert got.data_ptr() == keep.data_ptr() and (keep[m] == 0x5A5A5A5A).all()
+        assert torch.equal(got, lf.lora_dropout_mask(11, 24, m, k, p))
+        want, slack = reference(X, W, A, B, dY, 2.0, p, 11, 24, m)
+        near("Y", Y, want["Y"], slack["Y"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,r,p", [(1, 16, 0.0), (33, 9, 0.0), (33, 64, 0.1), (300, 40, 0.1)])
+def test_unaligned_adapter_gives_the_same(m, r, p):
+    X, W4, W, A, B, dY = case(m, 1032, 520, r, 128, seed=31)
+    A1, B1 = offset_view(A), offset_view(B)
+    Y, S, keep = lf.lora_int4_linear_fwd(X.cuda(), W4, A1, B1, 2.0, p, 3, 0)
+    dX, dA, dB = lf.lora_int4_linear_bwd(dY.cuda(), X.cuda(), W4, A1, B1, S, keep, 2.0, p)
+    want, slack = reference(X, W, A, B, dY, 2.0, p, 3, 0, m)
+    for name, t in (("Y", Y), ("dX", dX), ("dA", dA), ("dB", dB)):
+        near(name, t, want[name], slack[name])
+    assert (np.abs(f64(S) - want["S"]) <= slack["S"] + 1e-30).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n,nseg,r_max,group", [(1, 136, 72, 1, 8, 32), (16, 4104, 264, 16, 64, 128), (40, 1032, 520, 7, 128, 64),
+                                                    (64, 264, 136, 3, 256, 32), (50, 2056, 264, 80, 40, 128), (200, 520, 136, 300, 16, 64)])
+def test_mixed_matches_definition(m, k, n, nseg, r_max, group):
+    # every output of every segment, empty segments and an adapter without rows among them; S past its rank is zero
+    g = torch.Generator().manual_seed(m + nseg)
+    X, W4, W, _, _, dY = case(m, k, n, 8, group, seed=260 + m)
+    ranks = [1 + int(torch.randint(0, r_max, (1,), generator=g)) for _ in range(min(nseg, 5))] + [r_max, 7]
+    used = len(ranks) - 1  # the last has no rows
+    ps = [(0.0, 0.1, 0.3)[i % 3] for i in range(len(ranks))]
+    alphas = [(0.5, 2.0, -1.0)[i % 3] for i in range(len(ranks))]
+    As = [bf16_randn((k, r), k ** -0.5, g) for r in ranks]
+    Bs = [bf16_randn((r, n), 0.02 ** 0.5, g) for r in ranks]
+    cuts = torch.randint(0, m + 1, (nseg - 1,), generator=g).sort().values.tolist()
+    seg_off, seg_ad = [0, *cuts, m], torch.randint(0, used, (nseg,), generator=g).tolist()
+    Ad, Bd = [a.cuda() for a in As], [b.cuda() for b in Bs]
+    dAs, dBs = [torch.full_like(a, 7.0) for a in Ad], [torch.full_like(b, 7.0) for b in Bd]
+    table = lf.adapter_table(Ad, Bd, alphas, ps, dAs, dBs)
+    so = torch.tensor(seg_off, dtype=torch.int64, device="cuda")
+    sa = torch.tensor(seg_ad, dtype=torch.int32, device="cuda")
+    rm = max(ranks)
+    S = torch.full((m, rm), float("nan"), device="cuda")
+    keep = torch.full((m, (k + 31) // 32), 0x5A5A5A5A, dtype=torch.int32, device="cuda")
+    Yb = torch.full((m + 2, n), 5.0, dtype=torch.bfloat16, device="cuda")
+    Y, S, keep = lf.multi_lora_int4_linear_fwd(X.cuda(), W4, table, len(ranks), so, sa, rm, 3, 8, Y=Yb[:m], S=S, keep_bits=keep)
+    dX = lf.multi_lora_int4_linear_bwd(dY.cuda(), X.cuda(), W4, table, len(ranks), so, sa, S, keep, rm)
+    torch.cuda.synchronize()
+    assert (Yb[m:] == 5).all()
+    sums = {}
+    for s, a in enumerate(seg_ad):
+        lo, hi = seg_off[s], seg_off[s + 1]
+        if hi == lo:
+            continue
+        want, slack = reference(X[lo:hi], W, As[a], Bs[a], dY[lo:hi], alphas[a], ps[a], 3, 8 + lo * k, m)
+        near(f"Y[{s}]", Y[lo:hi], want["Y"], slack["Y"])
+        near(f"dX[{s}]", dX[lo:hi], want["dX"], slack["dX"])
+        got = f64(S[lo:hi])
+        assert (np.abs(got[:, :ranks[a]] - want["S"]) <= slack["S"] + 1e-30).all() and not got[:, ranks[a]:].any()
+        assert torch.equal(keep[lo:hi], lf.lora_dropout_mask(3, 8 + lo * k, hi - lo, k, ps[a]))
+        for name in ("dA", "dB"):
+            w, e = sums.get((name, a), (0.0, 0.0))
+            # (the other segments' sums are added: their roundings and one more for each segment)
+            sums[name, a] = w + want[name], e + slack[name] + (nseg + 1) * HALF * np.abs(want[name])
+    for (name, a), (w, e) in sums.items():
+        near(f"{name}[{a}]", (dAs if name == "dA" else dBs)[a], w, e)
+    assert not dAs[-1].any() and not dBs[-1].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seg_off,seg_ad", [([0, -(1 << 33) + 5, 1 << 40, 20], [0, 1, 0]), ([0, 30, 10, 20], [1, 0, 1]),
+                                            ([-7, 4, 4, 1 << 33], [0, 9, -3]), ([5, 6, 7, 8], [1, 1, 0])])
+def test_bad_segment_tables_stay_in_bounds(seg_off, seg_ad):
+    m, k, n = 20, 264, 136
+    g = torch.Generator().manual_seed(8)
+    X, W4, _, _, _, dY = case(m, k, n, 8, 32, seed=8)
+    As = [bf16_randn((k, r), 1.0, g).cuda() for r in (8, 40)]
+    Bs = [bf16_randn((r, n), 1.0, g).cuda() for r in (8, 40)]
+    table = lf.adapter_table(As, Bs, [1.0, 2.0], [0.1, 0.0])
+    so = torch.tensor(seg_off, dtype=torch.int64, device="cuda")
+    sa = torch.tensor(seg_ad, dtype=torch.int32, device="cuda")
+    Y = torch.full((m + 80, n), 5.0, dtype=torch.bfloat16, device="cuda")
+    S = torch.full((m + 80, 40), 5.0, device="cuda")
+    keep = torch.full((m + 80, (k + 31) // 32), 5, dtype=torch.int32, device="cuda")
+    mid = slice(40, 40 + m)
+    lf.multi_lora_int4_linear_fwd(X.cuda(), W4, table, 2, so, sa, 40, 3, 8, Y=Y[mid], S=S[mid], keep_bits=keep[mid])
+    torch.cuda.synchronize()
+    for t in (Y, S, keep):
+        assert (t[:40] == 5).all() and (t[40 + m:] == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 5, 40, 200])
+def test_infinities_stay_in_their_rows_and_columns(m):
+    # a marked group makes its column NaN; an infinite or NaN input makes its row infinite or NaN, and no other
+    k, n = 392, 72
+    g = torch.Generator().manual_seed(3)
+    W = bf16_randn((k, n), 1.0, g)
+    W[300, 5] = float("inf")
+    W4 = lf.lora_int4_quantize(W.cuda(), 128)
+    X = bf16_randn((m, k), 1.0, g).cuda()
+    Y = lf.lora_int4_frozen_fwd(X, W4)
+    bad = torch.isnan(Y).cpu()
+    assert bad[:, 5].all() and not bad[:, :5].any() and not bad[:, 6:].any()
+    if m > 1:
+        X2 = X.clone()
+        X2[m // 2, 17], X2[m - 1, 18] = float("inf"), float("nan")
+        Y2 = lf.lora_int4_frozen_fwd(X2, W4)
+        rows = torch.ones(m, dtype=torch.bool)
+        rows[m // 2] = rows[m - 1] = False
+        assert torch.equal(torch.nan_to_num(Y2[rows.cuda()].float()), torch.nan_to_num(Y[rows.cuda()].float()))
+        assert not torch.isfinite(Y2[m // 2].float()).any() and torch.isnan(Y2[m - 1]).all()
+
+
+@pytest.mark.gpu
+def test_large_and_small_values():
+    # scales over the whole range a checkpoint's fp16 or bf16 may take, inputs of 2^60 and 2^-60
+    k, n, group = 256, 64, 64
+    rng = np.random.default_rng(4)
+    q = rng.integers(0, 16, (k, n)).astype(np.uint8)
+    s = f64(torch.from_numpy(2.0 ** rng.integers(-60, 30, (4, n)) * rng.uniform(1, 2, (4, n))).bfloat16())
+    z = rng.integers(0, 17, (4, n)).astype(np.uint8)
+    W4 = lf.lora_int4_pack(torch.from_numpy(q).cuda(), torch.from_numpy(s).float().cuda(), torch.from_numpy(z).cuda(), group=group)
+    W = values(q, s, z, group)
+    W = W, rounded(W), s[np.arange(k) // group] * (32.0 + q + z[np.arange(k) // group])
+    for m in (1, 20, 70):
+        X = bf16_randn((m, k), 1.0, torch.Generator().manual_seed(m)) * torch.tensor([2.0 ** 60, 2.0 ** -60])[torch.arange(m) % 2, None].bfloat16()
+        near("Y", lf.lora_int4_frozen_fwd(X.cuda(), W4), *product(m, f64(X), W))
+
+
+# ---- use: streams, graphs, autograd ---------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,r,p", [(1, 16, 0.0), (1, 16, 0.1), (40, 64, 0.0), (300, 16, 0.1)])
+def test_captured_layer_replays_match_eager(m, r, p):
+    k, n, alpha = 520, 264, 2.0
+    X, W4, _, A, B, dY = case(m, k, n, r, 64, seed=5)
+    X, A, B, dY = X.cuda(), A.cuda(), B.cuda(), dY.cuda()
+
+    def run():
+        Y, S, keep = lf.lora_int4_linear_fwd(X, W4, A, B, alpha, p, 9, 0)
+        return (Y, S, lf.lora_int4_frozen_fwd(X, W4), lf.lora_int4_frozen_bwd(dY, W4),
+                *lf.lora_int4_linear_bwd(dY, X, W4, A, B, S, keep, alpha, p))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for rep in range(3):
+        X.copy_(bf16_randn((m, k), 1.0, torch.Generator().manual_seed(100 + rep)))
+        dY.copy_(bf16_randn((m, n), 1.0, torch.Generator().manual_seed(200 + rep)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for i, (a, b) in enumerate(zip(got, run())):
+            assert torch.equal(a, b), f"replay {rep}: output {i}"
+
+
+@pytest.mark.gpu
+def test_two_graphs_and_eager_calls_at_once():
+    # graphs of the same shapes replayed at once on two streams, each with scratch of its own
+    k, n, ranks = 520, 264, [16, 40]
+    g = torch.Generator().manual_seed(2)
+    W4 = case(3, k, n, 8, 128, seed=12)[1]
+    so = torch.tensor([0, 3, 7], dtype=torch.int64, device="cuda")
+    sa = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    sides = []
+    for i in range(2):
+        As = [bf16_randn((k, r), k ** -0.5, g).cuda() for r in ranks]
+        Bs = [bf16_randn((r, n), 0.02 ** 0.5, g).cuda() for r in ranks]
+        table = lf.adapter_table(As, Bs, [2.0, 0.5], [0.1, 0.0])
+        X = bf16_randn((7, k), 1.0, g).cuda()
+
+        def run(X=X, table=table, keep=(As, Bs)):
+            return lf.multi_lora_int4_linear_fwd(X, W4, table, 2, so, sa, 40, 3, 8)
+
+        run()
+        torch.cuda.synchronize()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            out = run()
+        sides.append((graph, stream, out, run))
+    want = [[t.clone() for t in run()] for *_, run in sides]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph, stream, _, _ in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager = sides[0][3]()
+        torch.cuda.synchronize()
+        for (_, _, out, _), w in zip(sides, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+        assert all(torch.equal(a, b) for a, b in zip(eager, want[0]))
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    m, k, n, r = 40, 2056, 520, 16
+    X, W4, _, A, B, _ = case(m, k, n, r, 128, seed=6)
+    X2 = bf16_randn((m, k), 1.0, torch.Generator().manual_seed(8)).cuda()
+    X, A, B = X.cuda(), A.cuda(), B.cuda()
+    want = [lf.lora_int4_linear_fwd(x, W4, A, B, 2.0, 0.0)[0] for x in (X, X2)]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        got.append((lf.lora_int4_linear_fwd(X, W4, A, B, 2.0, 0.0, stream=s1)[0],
+                    lf.lora_int4_linear_fwd(X2, W4, A, B, 2.0, 0.0, stream=s2)[0]))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    X, W4, _, A, B, dY = case(4, 136, 72, 8, 32, seed=1)
+    A, B = A.cuda(), B.cuda()
+    X0, dY0 = X[:0].cuda(), dY[:0].cuda()
+    assert lf.lora_int4_frozen_fwd(X0, W4).shape == (0, 72) and lf.lora_int4_frozen_bwd(dY0, W4).shape == (0, 136)
+    Y, S, keep = lf.lora_int4_linear_fwd(X0, W4, A, B, 2.0, 0.1)
+    dX, dA, dB = lf.lora_int4_linear_bwd(dY0, X0, W4, A, B, S, keep, 2.0, 0.1)
+    torch.cuda.synchronize()
+    assert Y.shape == (0, 72) and dX.shape == (0, 136) and not dA.any() and not dB.any()
+
+
+@pytest.mark.gpu
+def test_weight_past_32_bits():
+    # 2^32 values, codes past 2^31 bytes: the same 1024 columns over and over
+    k, n, m, wide = 4096, 1 << 20, 3, 1024
+    X, small, W, _, _, dY = case(m, k, wide, 8, 128, seed=91)
+    rep = n // wide
+    W4 = lf.Int4Weight(small.codes.repeat(rep, 1, 1, 1, 1), small.scales.repeat(rep, 1, 1), k, n, 128)
+    Y = lf.lora_int4_frozen_fwd(X.cuda(), W4).view(m, rep, wide)
+    assert torch.equal(Y, Y[:, :1].expand(m, rep, wide))
+    near("Y", Y[:, -1], *product(m, f64(X), W))
+    back = lf.lora_int4_dequantize(W4)
+    one = lf.lora_int4_dequantize(small)
+    assert torch.equal(back[:, -wide:], one) and torch.equal(back[-1].view(rep, wide), one[-1].expand(rep, wide))
+    again = lf.lora_int4_quantize(back, 128)
+    other = lf.lora_int4_quantize(one, 128)
+    assert torch.equal(again.codes[-wide // 16:], other.codes) and torch.equal(again.scales[-wide // 16:], other.scales)
+    assert torch.equal(again.codes[:wide // 16], other.codes)
+
+
+@pytest.mark.gpu
+def test_binding_rejects_on_the_gpu():
+    X, W4, _, A, B, dY = case(4, 136, 72, 8, 32, seed=1)
+    X, A, B = X.cuda(), A.cuda(), B.cuda()
+    with pytest.raises(ValueError, match="do not hold"):
+        lf.lora_int4_frozen_fwd(X, W4._replace(n=200))
+    with pytest.raises(ValueError, match="X must be"):
+        lf.lora_int4_frozen_fwd(X[:, :128].contiguous(), W4)
+    with pytest.raises(ValueError, match="contiguous"):
+        lf.lora_int4_frozen_fwd(X.t().contiguous().t(), W4)
+    with pytest.raises(ValueError, match="B must be"):
+        lf.lora_int4_linear_fwd(X, W4, A, B[:4].contiguous(), 2.0, 0.0)
+    with pytest.raises(ValueError, match="Y must be"):
+        lf.lora_int4_frozen_fwd(X, W4, Y=torch.empty(3, 72, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="zeros must be"):
+        lf.lora_int4_pack(torch.zeros(64, 64, dtype=torch.uint8, device="cuda"), torch.ones(2, 64, device="cuda"),
+                          torch.zeros(1, 64, dtype=torch.uint8, device="cuda"), group=32)
+    need = lf.lora_int4_linear_bwd_workspace_size(4, 136, 72, 32, 8)
+    _, S, keep = lf.lora_int4_linear_fwd(X, W4, A, B, 2.0, 0.0)
+    with pytest.raises(lf.LoraError, match="workspace"):
+        lf.lora_int4_linear_bwd(dY.cuda(), X, W4, A, B, S, keep, 2.0, 0.0,
+                                workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_gradient_against_differences():
+    # L = <Y, dY> is affine in one value of A, B or X: central differences of the 64-bit layer over the bf16 weight
+    m, k, n, r, alpha = 5, 136, 72, 4, 2.0
+    X, W4, W, A, B, dY = case(m, k, n, r, 32, seed=21)
+    _, S, keep = lf.lora_int4_linear_fwd(X.cuda(), W4, A.cuda(), B.cuda(), alpha, 0.0)
+    got = lf.lora_int4_linear_bwd(dY.cuda(), X.cuda(), W4, A.cuda(), B.cuda(), S, keep, alpha, 0.0)
+    args = {"dX": f64(X), "dA": f64(A), "dB": f64(B)}
+
+    def loss(d):
+        return ((d["dX"] @ W[1] + alpha * (d["dX"] @ d["dA"]) @ d["dB"]) * f64(dY)).sum()
+
+    _, slack = layer_reference(X, W[1], A, B, dY, alpha, 0.0, 0, 0)
+    for name, t in zip(("dX", "dA", "dB"), got):
+        at = np.random.default_rng(1).integers(0, args[name].size, 12)
+        for i in at:
+            h = np.zeros(args[name].size)
+            h[i] = 0.5
+            h = h.reshape(args[name].shape)
+            want = loss({**args, name: args[name] + h}) - loss({**args, name: args[name] - h})
+            have = f64(t).reshape(-1)[i]
+            assert abs(have - want) <= 2.0 ** -8 * abs(want) + 1.01 * slack[name].reshape(-1)[i] + 1e-9, (name, i)
+
+
+@pytest.mark.gpu
+def test_autograd_and_module():
+    m, k, n, r, group = 150, 264, 136, 16, 64
+    X, W4, W, A, B, dY = case(2 * m, k, n, r, group, seed=12)
+    x = X.view(2, m, k).cuda().requires_grad_()
+    a, b = A.cuda().requires_grad_(), B.cuda().requires_grad_()
+    y = lf.lora_linear(x, W4, a, b, 2.0, 0.1, 11, 8)
+    y.backward(dY.view(2, m, n).cuda())
+    want, slack = reference(X, W, A, B, dY, 2.0, 0.1, 11, 8, 2 * m)
+    for name, t in zip(("Y", "dX", "dA", "dB"), (y, x.grad, a.grad, b.grad)):
+        near(name, t.reshape(want[name].shape), want[name], slack[name])
+    layer = lf.LoraLinear(W4, r, 2.0, 0.0)
+    with torch.no_grad():
+        layer.B.copy_(B.cuda())
+    twin = lf.LoraLinear(lf.lora_int4_quantize(torch.zeros(k, n, dtype=torch.bfloat16, device="cuda"), group), r, 2.0)
+    twin.load_state_dict(layer.state_dict())
+    y = layer(X.cuda())
+    assert torch.equal(y, twin(X.cuda()))
+    y.float().square().sum().backward()
+    assert layer.A.grad is not None and layer.B.grad is not None and layer.weight_codes.dtype == torch.uint8
+
+
+@pytest.mark.gpu
+def test_mixed_autograd():
+    m, k, n, ranks = 50, 264, 136, [16, 8]
+    X, W4, W, _, _, dY = case(m, k, n, 8, 32, seed=14)
+    g = torch.Generator().manual_seed(2)
+    As = [bf16_randn((k, r), k ** -0.5, g).cuda().requires_grad_() for r in ranks]
+    Bs = [bf16_randn((r, n), 0.02 ** 0.5, g).cuda().requires_grad_() for r in ranks]
+    so = torch.tensor([0, 20, m], dtype=torch.int64, device="cuda")
+    sa = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    x = X.cuda().requires_grad_()
+    Y = lf.multi_lora_linear(x, W4, so, sa, As, Bs, [2.0, 1.0], [0.1, 0.0], 3, 16)
+    Y.backward(dY.cuda())
+    for lo, hi, a, alpha, p in ((0, 20, 1, 1.0, 0.0), (20, m, 0, 2.0, 0.1)):
+        want, slack = reference(X[lo:hi], W, As[a], Bs[a], dY[lo:hi], alpha, p, 3, 16 + lo * k, m)
+        near("Y", Y[lo:hi], want["Y"], slack["Y"])
+        near("dX", x.grad[lo:hi], want["dX"], slack["dX"])
+        near("dA", As[a].grad, want["dA"], slack["dA"])
+        near("dB", Bs[a].grad, want["dB"], slack["dB"])
