@@ -80,7 +80,9 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n, int64_t group) { return m 
 #define EXPAND() HIPCHK(launch_int4_dequantize(codes, scales, k, n, group, workspace, stream), "4-bit dequantise launch")
 
 extern "C" size_t lora_int4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group) {
-    return sizes_ok(m, k, n, group) ? expanded_bytes(m, k, n) : 0;
+    if (!sizes_ok(m, k, n, group) || m == 0) return 0;
+    const I4Plan pl = int4_plan(m, k, n, group, 0, 0);
+    return pl.kind ? pl.part_bytes : expanded_bytes(m, k, n);
 }
 
 extern "C" size_t lora_int4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group) {
@@ -95,6 +97,12 @@ extern "C" lora_status lora_int4_frozen_fwd(const void *X, const void *codes, co
     REQ_PTR(X, 16);
     REQ_PTR(Y, 16);
     REQ_WORKSPACE(lora_int4_frozen_fwd_workspace_size(m, k, n, group));
+    const I4Plan pl = int4_plan(m, k, n, group, 0, 0);
+    if (pl.kind) {
+        HIPCHK(launch_int4_gemm(pl, X, codes, scales, group, (int)m, (int)k, (int)n, AdapterSource{}, MxDropout{}, nullptr, Y,
+                                (float *)workspace, nullptr, stream), "4-bit product launch");
+        return LORA_OK;
+    }
     EXPAND();
     return lora_frozen_fwd(X, workspace, m, k, n, Y, stream);
 }
@@ -113,7 +121,9 @@ extern "C" lora_status lora_int4_frozen_bwd(const void *dY, const void *codes, c
 
 extern "C" size_t lora_int4_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r) {
     if (!sizes_ok(m, k, n, group) || m == 0 || r < 1 || r > 256) return 0;
-    return expanded_bytes(m, k, n) + lora_linear_fwd_workspace_size(m, k, n, r);
+    const I4Plan pl = int4_plan(m, k, n, group, r, 0);
+    const size_t layer = lora_linear_fwd_workspace_size(m, k, n, r);
+    return pl.kind ? align_up(pl.part_bytes) + std::max(pl.spart_bytes, layer) : expanded_bytes(m, k, n) + layer;
 }
 
 extern "C" size_t lora_int4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r) {
@@ -136,6 +146,15 @@ extern "C" lora_status lora_int4_linear_fwd(const void *X, const void *codes, co
     REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     REQ_WORKSPACE(lora_int4_linear_fwd_workspace_size(m, k, n, group, r));
+    const I4Plan pl = int4_plan(m, k, n, group, r, 0);
+    if (pl.kind) {
+        char *rest = ws_at(workspace, align_up(pl.part_bytes));
+        if (pl.SK == 0) CHECK(forward_s_only(X, A, m, k, r, p, seed, offset, S, keep_bits, rest, stream));
+        HIPCHK(launch_int4_gemm(pl, X, codes, scales, group, (int)m, (int)k, (int)n, single_source(A, B, nullptr, nullptr, r, alpha, p),
+                                MxDropout{seed, offset, keep_bits}, S, Y, (float *)workspace, (float *)rest, stream),
+               "4-bit product launch");
+        return LORA_OK;
+    }
     const size_t w = expanded_bytes(m, k, n);
     EXPAND();
     return lora_linear_fwd(X, workspace, A, B, m, k, n, r, alpha, p, seed, offset, Y, S, keep_bits, ws_at(workspace, w),
@@ -173,7 +192,9 @@ extern "C" lora_status lora_int4_linear_bwd(const void *dY, const void *X, const
 extern "C" size_t multi_lora_int4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max, int32_t num_adapters,
                                                      int32_t num_segments) {
     if (!sizes_ok(m, k, n, group) || m == 0 || r_max < 1 || r_max > 256 || num_adapters < 0 || num_segments < 0) return 0;
-    return expanded_bytes(m, k, n) + multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    const I4Plan pl = int4_plan(m, k, n, group, r_max, num_segments);
+    const size_t layer = multi_lora_fwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    return pl.kind ? align_up(pl.part_bytes) + std::max(pl.spart_bytes, layer) : expanded_bytes(m, k, n) + layer;
 }
 
 extern "C" size_t multi_lora_int4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max, int32_t num_adapters,
@@ -197,6 +218,15 @@ extern "C" lora_status multi_lora_int4_linear_fwd(const void *X, const void *cod
     REQ_PTR(S, 4);
     REQ_PTR(keep_bits, 4);
     REQ_WORKSPACE(multi_lora_int4_fwd_workspace_size(m, k, n, group, r_max, num_adapters, num_segments));
+    const I4Plan pl = int4_plan(m, k, n, group, r_max, num_segments);
+    if (pl.kind) {
+        const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+        char *rest = ws_at(workspace, align_up(pl.part_bytes));
+        if (pl.SK == 0) CHECK(multi_forward_s_only(X, src, m, k, seed, offset, S, keep_bits, rest, stream));
+        HIPCHK(launch_int4_gemm(pl, X, codes, scales, group, (int)m, (int)k, (int)n, src, MxDropout{seed, offset, keep_bits}, S, Y,
+                                (float *)workspace, (float *)rest, stream), "4-bit product launch");
+        return LORA_OK;
+    }
     const size_t w = expanded_bytes(m, k, n);
     EXPAND();
     return multi_lora_linear_fwd(X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, m, k, n, r_max, seed, offset, Y,

@@ -36,39 +36,25 @@
 
 #include "launch.hpp"
 #include "mxfp4.hpp"
+#include "s_job.hpp"
 
 namespace lora {
 
 namespace {
 
-struct MxGemmParams {
-    const uint16_t *X;
+struct MxGemmParams : SJobParams {
     const uint8_t *codes, *scales;
     uint16_t *Y;   // KS == 1
     float *part;   // KS > 1: [KS][M][N]
-    int M, N, K;
+    int N;
     int groups, blocks;  // N16, KB
-    int tiles_m, tiles_n;
+    int tiles_n;
     int KS, per;         // slices of k, stages of a slice
     const float *S;      // the epilogue's LoRA term: M x r fp32 (nullptr: none)
     const uint16_t *B;   // r x N
-    int r;
     float alpha;
-    // partial sums of S = X A by further work-groups
-    const uint16_t *A;
-    float *spart;     // [SK][M][rs], rs = r rounded up to 4
-    int rs, SK, jobs; // partial sums; work-groups that form them (a multiple of 8)
-    uint32_t *keep;   // their dropout mask, M x ceil(K / 32) words, written here (nullptr: none)
-    uint64_t seed, offset;
-    uint32_t drop;    // threshold of the mask's 16-bit numbers
-    // rows in segments with an adapter each (nullptr: one adapter); r is then the largest rank
-    const lora_adapter *adapters;
-    const int64_t *seg_off;
-    const int32_t *seg_adapter;
-    int num_adapters, nseg;
+    int jobs;  // work-groups that form S (a multiple of 8)
 };
-
-constexpr int kSK = 1024;  // k of one partial sum of S
 
 template <int WM_, int WN_, int WK_, int MB_, int NB_, int XR_, int NS_>
 struct MxTile {
@@ -87,122 +73,8 @@ struct MxTile {
     static constexpr int RT = SHARE > 2 ? 1 : 2;
     static constexpr bool RIDE = WM == 1;  // the adapter's S rides along, a second launch adds alpha S B
     static_assert(SU <= NW && LDS <= 160 * 1024, "tile does not fit");
+    static_assert(!RIDE || (NW == 8 && TM == 16 * MB && 8 * MB * RT * 1024 <= LDS), "no room for the partial sums of S");
 };
-
-// One work-group's share of keep.X A: 1024 of k (128 a wave), up to TM rows of one
-// adapter and 16 RT ranks.  X's rows and A's columns come straight from memory
-// (8 two-byte loads make a 16-rank operand: A's rows are r values long), every
-// load of a wave before its first use; the waves are added in LDS in wave order.
-// A lane's 8 elements of X are one counter of the dropout mask and one byte of
-// keep, which the first rank tile's work-groups write.
-template <class T>
-__device__ __forceinline__ void s_job(const MxGemmParams &P, int job, uint4 *smem) {
-    constexpr int MB = T::MB, RT = T::RT;
-    static_assert(T::NW == 8 && T::WM == 1 && MB * RT <= 8 && 8 * MB * RT * 1024 <= T::LDS, "no room for the partial sums");
-    const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int ks = job % P.SK;
-    int rest = job / P.SK, m0, mend = P.M, r = P.r;
-    const uint16_t *A = P.A;
-    uint32_t drop = P.drop;
-    if (P.adapters != nullptr) {  // a segment's rows in tiles; most segments have fewer than the batch
-        const int seg = rest % P.nseg;
-        rest /= P.nseg;
-        const int which = P.seg_adapter[seg];
-        if (which < 0 || which >= P.num_adapters) return;
-        const lora_adapter ad = P.adapters[which];
-        if (ad.r < 1 || ad.r > P.r) return;
-        // (clamped before anything is added: an offset may be any int64)
-        m0 = (int)min(max((int64_t)0, P.seg_off[seg]), (int64_t)P.M) + rest % P.tiles_m * T::TM;
-        mend = (int)min(max((int64_t)0, P.seg_off[seg + 1]), (int64_t)P.M);
-        if (m0 >= mend) return;
-        A = (const uint16_t *)ad.A;
-        r = ad.r;
-        drop = drop_threshold(ad.p);
-    } else {
-        m0 = rest % P.tiles_m * T::TM;
-    }
-    const int r0 = rest / P.tiles_m * 16 * RT;
-    if (r0 >= r) return;  // (the count is rounded up)
-    mend = min(mend, m0 + T::TM);
-    const int k0 = ks * kSK + wave * (kSK / 8);
-    // rows past the end read as zeros; the host keeps A under 2 GiB
-    const __amdgpu_buffer_rsrc_t rX = make_rsrc(P.X + (size_t)m0 * P.K, (uint64_t)(mend - m0) * P.K * 2u);
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, (uint64_t)P.K * r * 2u);
-    f32x4_t acc[MB][RT];
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int J = kSK / 8 / 32;
-    uint4 x[J][MB];
-    uint32_t h[J][RT][8];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int k = k0 + 32 * j + 8 * lg;
-#pragma unroll
-        for (int a = 0; a < MB; ++a)
-            x[j][a] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                          rX, k < P.K ? ((uint32_t)(16 * a + l16) * (uint32_t)P.K + (uint32_t)k) * 2u : kOOB, 0, 0));
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int rank = r0 + 16 * t + l16;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                h[j][t][e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
-                    rA, rank < r && k < P.K ? ((uint32_t)(k + e) * (uint32_t)r + (uint32_t)rank) * 2u : kOOB, 0, 0);
-        }
-    }
-    if (P.keep != nullptr) {
-        uint32_t bytes[J][MB];
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int a = 0; a < MB; ++a) bytes[j][a] = 0xFFu;
-        if (drop > 0) {  // (one branch: the generators' chains interleave)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int a = 0; a < MB; ++a)
-                    bytes[j][a] = keep_byte(P.offset + (uint64_t)(m0 + 16 * a + l16) * (uint64_t)P.K + (uint64_t)(k0 + 32 * j + 8 * lg),
-                                            P.seed, drop);
-        }
-        const uint32_t row_bytes = (uint32_t)((P.K + 31) / 32) * 4u;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int a = 0; a < MB; ++a) {
-                const int k = k0 + 32 * j + 8 * lg, row = m0 + 16 * a + l16;
-                const uint32_t byte = k < P.K ? bytes[j][a] : 0u;
-                x[j][a] = apply_keep(x[j][a], byte);
-                if (r0 == 0 && row < mend && (uint32_t)k / 8u < row_bytes)
-                    ((uint8_t *)P.keep)[(size_t)row * row_bytes + k / 8] = (uint8_t)byte;
-            }
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const uint32_t *q = h[j][t];
-            const uint4 w = make_uint4(pack2(q[0], q[1]), pack2(q[2], q[3]), pack2(q[4], q[5]), pack2(q[6], q[7]));
-#pragma unroll
-            for (int a = 0; a < MB; ++a) acc[a][t] = mfma16x16x32(w, x[j][a], acc[a][t]);
-        }
-    f32x4_t *red = (f32x4_t *)smem;
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) red[(wave * MB * RT + a * RT + t) * 64 + lane] = acc[a][t];
-    __syncthreads();
-    if (wave >= MB * RT) return;
-    // wave w adds tile w of every wave: lane (g, l) has ranks 4g .. 4g+3 of row l
-    f32x4_t sum = red[wave * 64 + lane];
-#pragma unroll
-    for (int c = 1; c < 8; ++c) sum += red[(c * MB * RT + wave) * 64 + lane];
-    const int row = m0 + 16 * (wave / RT) + l16, rank = r0 + 16 * (wave % RT) + 4 * lg;
-    if (row >= mend) return;
-    if (rank < P.rs) *(f32x4_t *)(P.spart + ((size_t)ks * P.M + row) * P.rs + rank) = sum;  // (zeros past r)
-}
 
 template <class T>
 __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) {
@@ -221,7 +93,7 @@ __global__ __launch_bounds__(64 * T::NW) void mxfp4_gemm_kernel(MxGemmParams P) 
     const int total = P.tiles_m * P.tiles_n * P.KS;
     int id = blockIdx.x;
     if constexpr (T::RIDE) {
-        if (id < P.jobs) return s_job<T>(P, id, mx_smem);
+        if (id < P.jobs) return s_job<T::NW, T::MB, T::RT>(P, id, mx_smem);
         id -= P.jobs;
     }
     id = xcd_order(id, total);
@@ -733,15 +605,20 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     P.seg_adapter = src.seg_adapter;
     P.num_adapters = src.num_adapters;
     P.nseg = src.num_segments;
-    int slot = prof_begin(kKinds[pl.kind - 1].name, stream);
+    const int slot = prof_begin(kKinds[pl.kind - 1].name, stream);
     const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
     if (e != hipSuccess || !pl.finish) return e;
     if (src.table != nullptr)
         return launch_mxfp4_join(true, part, pl.KS, m, n, S, r, pl.SK, spart, nullptr, src, Y, stream);
-    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)src.B, src.alpha, drop_scale(src.p), S,
-                           (uint16_t *)Y};
-    slot = prof_begin("mxfp4_finish", stream);
+    return launch_mxfp4_finish(part, pl.KS, m, n, S, pl.SK, spart, src, Y, stream);
+}
+
+hipError_t launch_mxfp4_finish(const float *part, int KS, int m, int n, float *S, int SK, const float *spart,
+                               const AdapterSource &src, void *Y, hipStream_t stream) {
+    const MxFinishParams F{part, KS, m, n, SK > 0 ? spart : S, SK, src.r, (src.r + 3) / 4 * 4, (const uint16_t *)src.B, src.alpha,
+                           drop_scale(src.p), S, (uint16_t *)Y};
+    const int slot = prof_begin("mxfp4_finish", stream);
     hipLaunchKernelGGL(mxfp4_finish_kernel, dim3((unsigned)((n + 127) / 128), (unsigned)((m + 15) / 16)), dim3(256), 0, stream,
                        F);
     prof_end(slot, stream);

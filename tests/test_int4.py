@@ -7,7 +7,7 @@ Tolerances, derived (half a step of bf16 is 2^-8 of a value, of fp32 2^-24):
 * packing is exact, unpacking to the nearest bf16 of s (q - z), which fp32 holds
   exactly (16 and 8 significant bits).
 * a product's entry is an fp32 sum rounded once to bf16: half a bf16 step, and
-  2^-24 of the terms' magnitudes for each addition.  Up to FEW rows the terms are
+  2^-24 of the terms' magnitudes for each addition.  Up to 64 rows the terms are
   x (16 + q) and x (16 + z), so their magnitudes are |x| s (32 + q + z), and there
   are k + 16 additions to count with the scales' products; the weight itself is
   not rounded.  With more rows, and in the backward, the weight is the bf16 one
@@ -28,7 +28,7 @@ from test_mxfp4 import f64, layer_reference, near
 HALF = 2.0 ** -24
 FAKE = 0x10000  # aligned, never dereferenced
 INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
-FEW = 0  # rows up to which the weight is not rounded
+FEW = 64  # rows up to which the weight is not rounded
 
 
 # ---- the format, from its definition ---------------------------------------------------------
