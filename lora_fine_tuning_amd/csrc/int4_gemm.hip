@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "int4.hpp"
 #include "launch.hpp"
@@ -33,15 +34,25 @@ struct I4Params : SJobParams {
     uint16_t *Y;          // direct
     float *part;          // [KS][M][N] (nullptr: direct)
     int N, N16, K128, G;
-    int each;             // blocks of 128 rows that share a scale (groups of 128 rows or more)
+    int each;             // blocks of 128 rows that share a scale (groups of 128 rows or more),
+    uint32_t each_inv;    // and floor(2^32 / each) + 1: block t's group is the product's high word
     int tiles_n, KS, per; // slices of k, blocks of 128 rows in one
     int jobs;
 };
 
-// Word d of 16 bytes of codes -> the MFMA operand of values 16 + q.
-__device__ __forceinline__ uint4 i4_frag(uint32_t w, uint32_t mask) {
-    constexpr uint32_t kBias = 0x41804180u;
-    return make_uint4(((w << 3) & mask) | kBias, ((w >> 1) & mask) | kBias, ((w >> 5) & mask) | kBias, ((w >> 9) & mask) | kBias);
+// Word d of 16 bytes of codes -> the MFMA operand of values 16 + q.  The constants are
+// a vector and a scalar register, which the one instruction for and-or takes.
+struct I4Bits {
+    uint32_t mask, bias;
+};
+__device__ __forceinline__ I4Bits i4_bits() {
+    I4Bits c;
+    asm("v_mov_b32 %0, 0x00780078" : "=v"(c.mask));
+    asm("s_mov_b32 %0, 0x41804180" : "=s"(c.bias));
+    return c;
+}
+__device__ __forceinline__ uint4 i4_frag(uint32_t w, const I4Bits &c) {
+    return make_uint4(((w << 3) & c.mask) | c.bias, ((w >> 1) & c.mask) | c.bias, ((w >> 5) & c.mask) | c.bias, ((w >> 9) & c.mask) | c.bias);
 }
 
 // A work-group takes 16 NB columns and a slice of k; its WK waves take every WK-th
@@ -82,7 +93,7 @@ __global__ __launch_bounds__(64 * T::WK) void int4_gemm_kernel(I4Params P) {
         wp[b] = P.codes + (size_t)c * P.K128 * 64 + lane;
         sp[b] = P.scales + (size_t)c * P.G * 4 + lg;
     }
-    const uint32_t mask = 0x00780078u;
+    const I4Bits bits = i4_bits();
     const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
 
     struct Block {
@@ -101,7 +112,7 @@ __global__ __launch_bounds__(64 * T::WK) void int4_gemm_kernel(I4Params P) {
                 B.x[j][a] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                 rX, live && k < P.K ? xo[a] + (uint32_t)(128 * at + 32 * j) * 2u : kOOB, 0, 0));
             }
-        const int gr = STEPS < 4 ? at * GR : P.each == 1 ? at : at / P.each;
+        const int gr = STEPS < 4 ? at * GR : P.each == 1 ? at : (int)__umulhi((uint32_t)at, P.each_inv);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -130,7 +141,7 @@ __global__ __launch_bounds__(64 * T::WK) void int4_gemm_kernel(I4Params P) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const uint4 &v = B.w[b];
-                    const uint4 w = i4_frag(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, mask);
+                    const uint4 w = i4_frag(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, bits);
 #pragma unroll
                     for (int a = 0; a < MB; ++a) acc[a][b] = mfma16x16x32(w, B.x[j][a], acc[a][b]);
                 }
@@ -179,54 +190,337 @@ __global__ __launch_bounds__(64 * T::WK) void int4_gemm_kernel(I4Params P) {
     }
 }
 
+// More rows: a work-group takes 16 MB rows and 16 WN NB columns, and X and the weight
+// come through an LDS ring of three stages by direct-to-LDS loads, two stages ahead, so
+// that the WN waves beside each other share X.  A stage is WK blocks of 128 rows, one
+// for each of the WK waves along k.  X takes 256 bytes a row and block; piece 4j + g
+// (16 bytes: what lane group g reads in step j) of row i sits at place (4j + g) ^ (i mod
+// 16), which puts the 16 lanes that a 16-byte read serves together on different banks.
+template <int MB_, int NB_, int WN_, int WK_, int STEPS_>
+struct I4Ring {
+    static constexpr int MB = MB_, NB = NB_, WN = WN_, WK = WK_, STEPS = STEPS_;
+    static constexpr int NW = WN * WK, G = WN * NB, TN = 16 * G, GR = 4 / STEPS;
+    static constexpr int XU = 4 * MB * WK, WU = G * WK, SU = (G * WK * GR + 15) / 16;  // 1 KiB loads of a stage
+    static constexpr int XPW = (XU + NW - 1) / NW, WPW = (WU + NW - 1) / NW, SPW = (SU + NW - 1) / NW, UPW = XPW + WPW + SPW;
+    static constexpr int XB = XU * 1024, WB = WU * 1024, STAGE = XB + WB + SU * 1024;
+    static constexpr int NS = 3 * STAGE + 1024 <= 160 * 1024 ? 3 : 2;  // stages of the ring
+    static constexpr int SPARE = NS * STAGE;  // 1 KiB that surplus loads fill with zeros
+    static constexpr int RT = MB * 2 <= NW ? 2 : 1;
+    static constexpr int RED = WK * WN * MB * NB * 1024, JOB = NW * MB * RT * 1024;
+    static constexpr int MOST = RED > JOB ? RED : JOB;
+    static constexpr int LDS = SPARE + 1024 > MOST ? SPARE + 1024 : MOST;
+    static_assert(NW % 4 == 0 && LDS <= 160 * 1024, "tile does not fit");
+};
+
 template <class T>
+__global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
+    constexpr int MB = T::MB, NB = T::NB, WN = T::WN, WK = T::WK, STEPS = T::STEPS, GR = T::GR, NW = T::NW, G = T::G;
+    extern __shared__ uint4 i4_smem[];
+    lds_char *smem = (lds_char *)i4_smem;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wk = wave % WK, wn = wave / WK;
+    int id = blockIdx.x;
+    if (id < P.jobs) return s_job<NW, MB, T::RT>(P, id, i4_smem);
+    id = xcd_order(id - P.jobs, P.tiles_n * P.KS);
+    int tn = id, ks = 0;
+    if (P.KS > 1) ks = id / P.tiles_n, tn = id - ks * P.tiles_n;
+    const int c0 = tn * G, t0 = ks * P.per, t1 = min(P.K128, t0 + P.per);
+    const int nit = (t1 - t0 + WK - 1) / WK;
+
+    // the host keeps every offset below 2^31
+    const uint32_t row_bytes = (uint32_t)P.K * 2u, code_bytes = (uint32_t)P.K128 * 1024u, scale_bytes = (uint32_t)P.G * 64u;
+    const uint32_t ng = (uint32_t)min(P.N16 - c0, G);
+    const sgpr4_t dX = make_desc(P.X, (uint32_t)P.M * row_bytes);
+    const sgpr4_t dW = make_desc((const char *)P.codes + (size_t)c0 * code_bytes, ng * code_bytes);
+    const sgpr4_t dS = make_desc((const char *)P.scales + (size_t)c0 * scale_bytes, ng * scale_bytes);
+
+    // This wave's loads of a stage.  Unit u of X: rows 4 (u mod 4 MB) .. +3 of block
+    // u / 4 MB of the stage; of codes: column group u mod G, block u / G; of scales: 16
+    // pieces q of 64 bytes, column group q mod G, block q / G / GR, group q / G mod GR of
+    // the block.  xo, wo, so: byte offsets at stage 0 (kOOB: zeros); a lane's k of X is xk
+    // in every unit of a wave (4 divides NW), counted from its block.
+    const int xk = 8 * (l16 ^ ((4 * (wave & 3) + lg) & 15)), kend = min(P.K, 128 * t1);
+    uint32_t xo[T::XPW], wo[T::WPW], so[T::SPW];
+    int st[T::SPW];
+#pragma unroll
+    for (int i = 0; i < T::XPW; ++i) {
+        const int u = wave + NW * i, row = u % (4 * MB) * 4 + lg;
+        xo[i] = u < T::XU && row < P.M ? (uint32_t)row * row_bytes + (uint32_t)(128 * (t0 + u / (4 * MB)) + xk) * 2u : kOOB;
+    }
+#pragma unroll
+    for (int i = 0; i < T::WPW; ++i) {
+        const int u = wave + NW * i, c = u % G;
+        wo[i] = u < T::WU && c < (int)ng ? (uint32_t)c * code_bytes + (uint32_t)(t0 + u / G) * 1024u + (uint32_t)lane * 16u : kOOB;
+    }
+#pragma unroll
+    for (int i = 0; i < T::SPW; ++i) {
+        const int q = (wave + NW * i) * 16 + (lane >> 2), c = q % G;
+        st[i] = t0 + q / G / GR;
+        so[i] = q < G * WK * GR && c < (int)ng ? (uint32_t)c * scale_bytes + (uint32_t)(q / G % GR) * 64u + (uint32_t)(lane & 3) * 16u : kOOB;
+    }
+    auto issue_one = [&](int it, int buf, int i) {
+        const uint32_t base = lds0 + (uint32_t)buf * T::STAGE + (uint32_t)wave * 1024u, spare = lds0 + T::SPARE;
+        const int dt = it * WK;
+        if (i < T::XPW) {
+            const int u = wave + NW * i;
+            dma16_at(dX, xk < kend - 128 * (t0 + dt + u / (4 * MB)) ? xo[i] : kOOB, (uint32_t)dt * 256u,
+                     T::XU % NW == 0 || u < T::XU ? base + (uint32_t)(NW * i) * 1024u : spare);
+        } else if (i < T::XPW + T::WPW) {
+            const int j = i - T::XPW, u = wave + NW * j;
+            dma16_at(dW, t0 + dt + u / G < t1 ? wo[j] : kOOB, (uint32_t)dt * 1024u,
+                     T::WU % NW == 0 || u < T::WU ? base + T::XB + (uint32_t)(NW * j) * 1024u : spare);
+        } else {
+            const int j = i - T::XPW - T::WPW, at = st[j] + dt;
+            const uint32_t gr = STEPS < 4 ? (uint32_t)at * GR : P.each == 1 ? (uint32_t)at : __umulhi((uint32_t)at, P.each_inv);
+            dma16_at(dS, at < t1 && so[j] != kOOB ? so[j] + gr * 64u : kOOB, 0u,
+                     T::SU % NW == 0 || wave + NW * j < T::SU ? base + T::XB + T::WB + (uint32_t)(NW * j) * 1024u : spare);
+        }
+    };
+    // A stage has landed (`later` ones may be in flight), and this wave's LDS reads
+    // are done; after the barrier both hold for every wave.
+    auto stage_ready = [&](auto later) {
+        wait_vmcnt_lds<T::UPW * decltype(later)::value>();
+        asm volatile("" ::: "memory");  // keep LDS reads and loads into LDS on their side of the barrier
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    f32x4_t total[MB][NB], acc[MB][NB], sum[MB];
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) total[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const I4Bits bits = i4_bits();
+    const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+
+    // x[j % 2] holds X's rows of step j, q the wave's codes of the stage
+    uint4 x[2][MB], q[NB];
+    auto read_x = [&](int buf, int j, int a) {
+        x[j & 1][a] = *(const uint4 *)(smem + buf * T::STAGE + (wk * MB + a) * 4096 + l16 * 256 + (((4 * j + lg) ^ l16) << 4));
+    };
+    auto read_w = [&](int buf) {
+        const lds_char *sw = smem + buf * T::STAGE + T::XB + (wk * G + wn * NB) * 1024 + lane * 16;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) q[b] = *(const uint4 *)(sw + b * 1024);
+    };
+    auto read_s = [&](int buf, int e, uint4 (&s4)[NB]) {
+        const lds_char *ss = smem + buf * T::STAGE + T::XB + T::WB + ((wk * GR + e) * G + wn * NB) * 64 + lg * 16;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) s4[b] = *(const uint4 *)(ss + b * 64);
+    };
+    auto dword = [](const uint4 &v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
+    // Step j's MFMAs over the codes qc; the next step's X rows are read meanwhile, and
+    // `side` does its work after each column group.
+    auto step = [&](int j, const uint32_t (&qc)[NB], int xbuf, auto side) {
+        const bool first = j % STEPS == 0;
+        const f32x4_t zero = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint4 w = i4_frag(qc[b], bits);
+#pragma unroll
+            for (int a = 0; a < MB; ++a) {
+                if (b == 0) {
+                    sum[a] = mfma16x16x32(ones, x[j & 1][a], first ? zero : sum[a]);
+                    if (j < 3) read_x(xbuf, j + 1, a);
+                }
+                acc[a][b] = mfma16x16x32(w, x[j & 1][a], first ? zero : acc[a][b]);
+            }
+            side(b);
+        }
+    };
+    // lane (g, l): columns 4g .. 4g+3 of row l
+    auto close = [&](const uint4 (&s4)[NB]) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t word[4] = {s4[b].x, s4[b].y, s4[b].z, s4[b].w};
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float s = __uint_as_float(word[v] & 0xFFFFFF00u), z = 16.f + (float)(word[v] & 0xFFu);
+#pragma unroll
+                for (int a = 0; a < MB; ++a) total[a][b][v] = fmaf(s, fmaf(-z, sum[a][v], acc[a][b][v]), total[a][b][v]);
+            }
+        }
+    };
+
+#pragma unroll
+    for (int s = 0; s < T::NS; ++s)
+#pragma unroll
+        for (int i = 0; i < T::UPW; ++i) issue_one(s, s, i);
+    stage_ready(std::integral_constant<int, T::NS - 1>{});
+    read_w(0);
+#pragma unroll
+    for (int a = 0; a < MB; ++a) read_x(0, 0, a);
+    int buf = 0;
+    for (int it = 0; it < nit; ++it) {
+        uint32_t qc[NB];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qc[b] = dword(q[b], j);
+            step(j, qc, buf, [](int) {});
+            if ((j + 1) % STEPS == 0) {
+                uint4 s4[NB];
+                read_s(buf, j / STEPS, s4);
+                close(s4);
+            }
+        }
+        // step 3's operands are in registers: this stage's buffer takes stage it + NS, and
+        // the next stage's first operands are read while step 3 multiplies
+        uint4 s4[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) qc[b] = q[b].w;
+        read_s(buf, GR - 1, s4);
+        const int next = buf == T::NS - 1 ? 0 : buf + 1, here = buf;
+        stage_ready(std::integral_constant<int, T::NS - 2>{});
+        read_w(next);
+#pragma unroll
+        for (int a = 0; a < MB; ++a) read_x(next, 0, a);
+        constexpr int EACH = (T::UPW + NB - 1) / NB;
+        step(3, qc, 0, [&](int b) {
+#pragma unroll
+            for (int e = 0; e < EACH; ++e)
+                if (b * EACH + e < T::UPW) issue_one(it + T::NS, here, b * EACH + e);
+        });
+        close(s4);
+        buf = next;
+    }
+    wait_vmcnt<0>();  // (the last loads fill zeros: nothing may land in the space used below)
+    __syncthreads();
+
+    // the waves along k, in wave order
+    f32x4_t *red = (f32x4_t *)i4_smem;
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) red[((wk * WN + wn) * MB * NB + a * NB + b) * 64 + lane] = total[a][b];
+    __syncthreads();
+    for (int q = wave; q < WN * MB * NB; q += NW) {
+        const int a = q / NB % MB, b = q % NB, n = q / (MB * NB);
+        f32x4_t v = red[q * 64 + lane];
+#pragma unroll
+        for (int c = 1; c < WK; ++c) v += red[(c * WN * MB * NB + q) * 64 + lane];
+        const int row = 16 * a + l16, col = (c0 + n * NB + b) * 16 + 4 * lg;
+        if (row >= P.M || col >= P.N) continue;
+        if (P.part != nullptr)
+            *(f32x4_t *)(P.part + ((size_t)ks * P.M + row) * P.N + col) = v;
+        else
+            *(uint2 *)(P.Y + (size_t)row * P.N + col) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+}
+
+template <class T, bool RING>
 hipError_t launch_t(const I4Params &P, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void *)int4_gemm_kernel<T>, T::LDS, done);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((int4_gemm_kernel<T>), dim3((unsigned)(P.tiles_n * P.KS + P.jobs)), dim3(64 * T::WK), T::LDS, stream, P);
+    const dim3 grid((unsigned)(P.tiles_n * P.KS + P.jobs));
+    if constexpr (RING) {
+        const hipError_t e = allow_lds((const void *)int4_ring_kernel<T>, T::LDS, done);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((int4_ring_kernel<T>), grid, dim3(64 * T::NW), T::LDS, stream, P);
+    } else {
+        const hipError_t e = allow_lds((const void *)int4_gemm_kernel<T>, T::LDS, done);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((int4_gemm_kernel<T>), grid, dim3(64 * T::WK), T::LDS, stream, P);
+    }
     return hipGetLastError();
 }
 
+// Tile shapes, and what a call with one costs.  `stage` and `row`: microseconds that a
+// stage of WK blocks takes a work-group when `share` of them fill every CU, and what
+// each row adds to it (the direct shapes read X once a wave); group 128.
 struct I4Kind {
     const char *name;  // in the timing pool
     hipError_t (*launch[3])(const I4Params &, hipStream_t);  // groups of 32, 64, 128 rows or more
-    int tm, tn, ranks;  // rows and columns of a tile, ranks of one job of S
+    int tm, tn, step, ranks;  // rows and columns of a tile, blocks of 128 rows of a stage, ranks of one job of S
+    float stage, row;
+    int share;
 };
 template <int MB, int NB, int WK>
-constexpr I4Kind kind_of(const char *name) {
-    return I4Kind{name, {launch_t<I4Tile<MB, NB, WK, 1>>, launch_t<I4Tile<MB, NB, WK, 2>>, launch_t<I4Tile<MB, NB, WK, 4>>}, 16 * MB, 16 * NB,
-                  16 * I4Tile<MB, NB, WK, 4>::RT};
+constexpr I4Kind direct(const char *name, float stage, float row, int share) {
+    using T = I4Tile<MB, NB, WK, 4>;
+    return I4Kind{name, {launch_t<I4Tile<MB, NB, WK, 1>, false>, launch_t<I4Tile<MB, NB, WK, 2>, false>, launch_t<T, false>}, 16 * MB,
+                  16 * NB, WK, 16 * T::RT, stage, row, share};
+}
+template <int MB, int NB, int WN, int WK>
+constexpr I4Kind ring(const char *name, float stage, int share) {
+    using T = I4Ring<MB, NB, WN, WK, 4>;
+    return I4Kind{name, {launch_t<I4Ring<MB, NB, WN, WK, 1>, true>, launch_t<I4Ring<MB, NB, WN, WK, 2>, true>, launch_t<T, true>}, 16 * MB,
+                  T::TN, WK, 16 * T::RT, stage, 0.f, share};
 }
 const I4Kind kKinds[] = {
-    kind_of<1, 1, 8>("int4_gemm 16x16"),
-    kind_of<2, 2, 8>("int4_gemm 32x32"),
-    kind_of<4, 2, 8>("int4_gemm 64x32"),
+    direct<1, 1, 8>("int4_gemm 16x16", 0.80f, 0.07f, 2),
+    direct<1, 2, 8>("int4_gemm 16x32", 1.30f, 0.06f, 2),
+    ring<1, 1, 2, 4>("int4_ring 16x32", 0.43f, 2),
+    ring<1, 2, 4, 2>("int4_ring 16x128", 0.60f, 1),
+    ring<2, 1, 2, 4>("int4_ring 32x32", 0.62f, 1),
+    ring<2, 2, 2, 4>("int4_ring 32x64", 0.97f, 1),
+    ring<3, 1, 2, 4>("int4_ring 48x32", 0.86f, 1),
+    ring<3, 2, 2, 4>("int4_ring 48x64", 1.31f, 1),
+    ring<4, 1, 4, 2>("int4_ring 64x64", 0.98f, 1),
+    ring<4, 2, 4, 2>("int4_ring 64x128", 1.45f, 1),
 };
 
 }  // namespace
 
-I4Plan int4_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
-    I4Plan p{};
-    // (offsets into X stay below 2^31, and counts within an int)
-    if (m <= 0 || m > kI4Rows || k > (1 << 20) || n > (1 << 24)) return p;
-    p.kind = m <= 16 ? 1 : m <= 32 ? 2 : 3;
-    const I4Kind &K = kKinds[p.kind - 1];
-    p.tiles_n = (int)((n + K.tn - 1) / K.tn);
-    p.KS = 1;
-    p.per = (int)((k + 127) / 128);
-    p.finish = r > 0;
-    p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
-    if (r > 0) {
-        const int64_t jobs = (k + kSK - 1) / kSK * ((r + K.ranks - 1) / K.ranks) * std::max(nseg, 1);
-        if (nseg == 0 || jobs <= 1024) {
-            p.SK = (int)((k + kSK - 1) / kSK);
-            p.jobs = (int)((jobs + 7) / 8 * 8);
-            p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
+// The cheapest of the tile shapes, with k split as far as pays, by a model of their
+// times: 4.2 us, rounds of work-groups (stages x stage time each, and at least their
+// share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); a finishing launch
+// 3.5 us and its partial sums at 8 TB/s.
+// Measured in a graph, groups of 128, model in brackets: 1 x 4096 x 14336 9.8 us (9.9),
+// 1 x 8192 x 28672 25.2 (26.9), 32 x 4096 x 14336 12.3 (11.6), 48 x 14336 x 4096 18.4
+// (17.7), 64 x 4096 x 14336 19.9 (19.1), 33 x 28672 x 8192 44.3 (44.9).
+static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
+    I4Plan best{};
+    // (offsets into X and a tile's codes stay below 2^31, and counts within an int)
+    if (m <= 0 || m > kI4Rows || k > (1 << 20) || n > (1 << 24)) return best;
+    const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t k128 = cdiv(k, 128);
+    const double bytes = (double)k * n * (0.5 + 4.0 / (double)std::min<int64_t>(group, 128));
+    double least = 1e30;
+    for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
+        const I4Kind &K = kKinds[kind - 1];
+        if (m > K.tm || (m <= 16 && K.tm > 16)) continue;
+        I4Plan p{};
+        p.kind = kind;
+        p.tiles_n = (int)cdiv(n, K.tn);
+        const int64_t stages = cdiv(k128, K.step);
+        if (r > 0) {
+            const int64_t jobs = cdiv(k, kSK) * cdiv(r, K.ranks) * std::max(nseg, 1);
+            if (nseg == 0 || jobs <= 1024) {
+                p.SK = (int)cdiv(k, kSK);
+                p.jobs = (int)cdiv(jobs, 8) * 8;
+                p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
+            }
+        }
+        for (int want = 1; want <= 16 && want <= stages; ++want) {
+            const int64_t per = cdiv(stages, want);
+            p.KS = (int)cdiv(stages, per);
+            if (p.KS != want) continue;
+            p.per = (int)(per * K.step);
+            p.finish = p.KS > 1 || r > 0;
+            p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
+            const int64_t groups = (int64_t)p.tiles_n * p.KS + p.jobs, slots = 256 * K.share;
+            if (groups > (1 << 24)) continue;
+            const double one = (double)per * (K.stage + K.row * (double)m), each = bytes / 5.5e6 / (double)groups;
+            const int64_t full = groups / slots, rest = groups % slots;
+            double t = 4.2 + (double)full * std::max(one, each * (double)slots);
+            // (a ring's stages take their time however few run; the direct shapes' share of X's bytes shrinks)
+            const double least_part = K.row > 0.f ? 0.45 : 0.95;
+            if (rest > 0) t += std::max(one * std::max(least_part, (double)rest / (double)slots), each * (double)rest);
+            t += 0.7 * (double)(full + (rest > 0) - 1);
+            if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 8e6;
+            if (t < least) {
+                least = t;
+                best = p;
+            }
         }
     }
-    (void)group;
-    return p;
+    return best;
+}
+
+I4Plan int4_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
+    return remembered<I4Plan>(m, k, n, ((int64_t)nseg << 32) ^ (group << 10) ^ r, [&] { return find_plan(m, k, n, group, r, nseg); });
 }
 
 hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, const void *scales, int64_t group, int m, int k, int n,
@@ -260,7 +554,8 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
     P.N16 = (int)s.n16;
     P.K128 = (int)s.k128;
     P.G = (int)s.groups;
-    P.each = group < 128 ? 1 : (int)(group / 128);
+    P.each = group < 128 ? 1 : (int)std::min<int64_t>(group / 128, s.k128);
+    P.each_inv = P.each > 1 ? (uint32_t)((1ull << 32) / (uint32_t)P.each + 1) : 0u;
     P.tiles_n = pl.tiles_n;
     P.KS = pl.KS;
     P.per = pl.per;
@@ -270,8 +565,7 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
     const hipError_t e = K.launch[group == 32 ? 0 : group == 64 ? 1 : 2](P, stream);
     prof_end(slot, stream);
     if (e != hipSuccess || !pl.finish) return e;
-    if (src.table != nullptr) return launch_mxfp4_join(true, part, pl.KS, m, n, S, src.r, pl.SK, spart, nullptr, src, Y, stream);
-    return launch_mxfp4_finish(part, pl.KS, m, n, S, pl.SK, spart, src, Y, stream);
+    return launch_int4_finish(part, pl.KS, m, n, S, pl.SK, spart, src, Y, stream);
 }
 
 }  // namespace lora

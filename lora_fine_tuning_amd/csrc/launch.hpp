@@ -318,12 +318,6 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
                              int n, const AdapterSource &src, const MxDropout &drop, float *S, void *Y, float *part,
                              float *spart, hipStream_t stream);
 
-// The k slices' partial sums ([KS][m][n]) and one adapter's term: Y, rounded.  SK > 0:
-// S is the sum of SK partial sums ([SK][m][r rounded up to 4]), and written; src.r == 0:
-// no adapter.
-hipError_t launch_mxfp4_finish(const float *part, int KS, int m, int n, float *S, int SK, const float *spart,
-                               const AdapterSource &src, void *Y, hipStream_t stream);
-
 // Y = X W' (+ alpha S B) for up to kI4Rows rows, W' in 4-bit integers (int4_gemm.hip).
 // SK > 0: the product's launch also forms S and drop.keep, in SK partial sums.
 constexpr int kI4Rows = 64;
@@ -340,6 +334,12 @@ I4Plan int4_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg
 hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, const void *scales, int64_t group, int m, int k, int n,
                             const AdapterSource &src, const MxDropout &drop, float *S, void *Y, float *part, float *spart,
                             hipStream_t stream);
+
+// The k slices' partial sums ([KS][m][n]) and the adapters' term: Y, rounded
+// (int4_finish.hip).  SK > 0: S is the sum of SK partial sums ([SK][m][src.r rounded up
+// to 4]), and written; src.r == 0: no adapter.
+hipError_t launch_int4_finish(const float *part, int KS, int m, int n, float *S, int SK, const float *spart, const AdapterSource &src,
+                              void *Y, hipStream_t stream);
 
 // dX = dY W'^T (+ scale keep.(dS A^T)) straight from the packed weight
 // (mxfp4_gemm_t.hip).

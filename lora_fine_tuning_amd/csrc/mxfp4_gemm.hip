@@ -605,20 +605,15 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
     P.seg_adapter = src.seg_adapter;
     P.num_adapters = src.num_adapters;
     P.nseg = src.num_segments;
-    const int slot = prof_begin(kKinds[pl.kind - 1].name, stream);
+    int slot = prof_begin(kKinds[pl.kind - 1].name, stream);
     const hipError_t e = kKinds[pl.kind - 1].launch(P, stream);
     prof_end(slot, stream);
     if (e != hipSuccess || !pl.finish) return e;
     if (src.table != nullptr)
         return launch_mxfp4_join(true, part, pl.KS, m, n, S, r, pl.SK, spart, nullptr, src, Y, stream);
-    return launch_mxfp4_finish(part, pl.KS, m, n, S, pl.SK, spart, src, Y, stream);
-}
-
-hipError_t launch_mxfp4_finish(const float *part, int KS, int m, int n, float *S, int SK, const float *spart,
-                               const AdapterSource &src, void *Y, hipStream_t stream) {
-    const MxFinishParams F{part, KS, m, n, SK > 0 ? spart : S, SK, src.r, (src.r + 3) / 4 * 4, (const uint16_t *)src.B, src.alpha,
-                           drop_scale(src.p), S, (uint16_t *)Y};
-    const int slot = prof_begin("mxfp4_finish", stream);
+    const MxFinishParams F{part, pl.KS, m, n, pl.SK > 0 ? spart : S, pl.SK, r, P.rs, (const uint16_t *)src.B, src.alpha, drop_scale(src.p), S,
+                           (uint16_t *)Y};
+    slot = prof_begin("mxfp4_finish", stream);
     hipLaunchKernelGGL(mxfp4_finish_kernel, dim3((unsigned)((n + 127) / 128), (unsigned)((m + 15) / 16)), dim3(256), 0, stream,
                        F);
     prof_end(slot, stream);
