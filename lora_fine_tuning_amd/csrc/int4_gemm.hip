@@ -465,8 +465,9 @@ const I4Kind kKinds[] = {
 
 // The cheapest of the tile shapes, with k split as far as pays, by a model of their
 // times: 4.2 us, rounds of work-groups (stages x stage time each, and at least their
-// share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); a finishing launch
-// 3.5 us and its partial sums at 8 TB/s.
+// share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); the work-groups that
+// form S 0.8 us, 5 where they keep some of the product's from starting; a finishing
+// launch 3.5 us, 0.25 a slice more, and its partial sums at 5 TB/s.
 // Measured in a graph, groups of 128, model in brackets: 1 x 4096 x 14336 9.8 us (9.9),
 // 1 x 8192 x 28672 25.2 (26.9), 32 x 4096 x 14336 12.3 (11.6), 48 x 14336 x 4096 18.4
 // (17.7), 64 x 4096 x 14336 19.9 (19.1), 33 x 28672 x 8192 44.3 (44.9).
@@ -500,7 +501,7 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             p.per = (int)(per * K.step);
             p.finish = p.KS > 1 || r > 0;
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
-            const int64_t groups = (int64_t)p.tiles_n * p.KS + p.jobs, slots = 256 * K.share;
+            const int64_t groups = (int64_t)p.tiles_n * p.KS, slots = 256 * K.share;
             if (groups > (1 << 24)) continue;
             const double one = (double)per * (K.stage + K.row * (double)m), each = bytes / 5.5e6 / (double)groups;
             const int64_t full = groups / slots, rest = groups % slots;
@@ -509,7 +510,8 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             const double least_part = K.row > 0.f ? 0.45 : 0.95;
             if (rest > 0) t += std::max(one * std::max(least_part, (double)rest / (double)slots), each * (double)rest);
             t += 0.7 * (double)(full + (rest > 0) - 1);
-            if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 8e6;
+            if (p.jobs > 0) t += rest + p.jobs > slots ? 5.0 : 0.8;
+            if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 5e6 + 0.25 * (p.KS - 1);
             if (t < least) {
                 least = t;
                 best = p;

@@ -28,9 +28,10 @@ struct SJobParams {
 };
 
 // One work-group's share of keep.X A: 1024 of k (split over its NW waves), up to
-// 16 MB rows of one adapter and 16 RT ranks.  X's rows and A's columns come straight from memory
-// (8 two-byte loads make a 16-rank operand: A's rows are r values long), every
-// load of a wave before its first use; the waves are added in LDS in wave order.
+// 16 MB rows of one adapter and 16 RT ranks.  X's rows come straight from memory, A's as
+// 16 ranks of 32 rows a load, turned through 1 KiB of LDS (with 8 two-byte loads for an
+// operand instead, a job of 16 ranks took 7 us where this takes S_JOB_US); every load of
+// a wave before its first use; the waves are added in LDS in wave order.
 // A lane's 8 elements of X are one counter of the dropout mask and one byte of
 // keep, which the first rank tile's work-groups write.  `smem`: NW MB RT KiB.
 template <int NW, int MB, int RT>
@@ -64,9 +65,8 @@ __device__ __forceinline__ void s_job(const SJobParams &P, int job, uint4 *smem)
     if (r0 >= r) return;  // (the count is rounded up)
     mend = min(mend, m0 + TM);
     const int k0 = ks * kSK + wave * (kSK / NW);
-    // rows past the end read as zeros; the host keeps A under 2 GiB
+    // rows past the end read as zeros
     const __amdgpu_buffer_rsrc_t rX = make_rsrc(P.X + (size_t)m0 * P.K, (uint64_t)(mend - m0) * P.K * 2u);
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, (uint64_t)P.K * r * 2u);
     f32x4_t acc[MB][RT];
 #pragma unroll
     for (int a = 0; a < MB; ++a)
@@ -74,21 +74,27 @@ __device__ __forceinline__ void s_job(const SJobParams &P, int job, uint4 *smem)
         for (int t = 0; t < RT; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     constexpr int J = kSK / NW / 32;
     uint4 x[J][MB];
-    uint32_t h[J][RT][8];
+    uint4 h[J][RT];  // row lane / 2 of 32, ranks 8 (lane mod 2) .. +7 of 16
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int k = k0 + 32 * j + 8 * lg;
+        const int k = k0 + 32 * j + 8 * lg, ka = k0 + 32 * j + (lane >> 1);
 #pragma unroll
         for (int a = 0; a < MB; ++a)
             x[j][a] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                           rX, k < P.K ? ((uint32_t)(16 * a + l16) * (uint32_t)P.K + (uint32_t)k) * 2u : kOOB, 0, 0));
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const int rank = r0 + 16 * t + l16;
+            const int rank = r0 + 16 * t + 8 * (lane & 1), left = r - rank;
+            const uint16_t *src = A + (size_t)ka * r + rank;
+            h[j][t] = make_uint4(0u, 0u, 0u, 0u);
+            if (ka < P.K && left >= 8) {
+                __builtin_memcpy(&h[j][t], src, 16);  // (A may be unaligned)
+            } else if (ka < P.K && left > 0) {
+                uint32_t q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                h[j][t][e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
-                    rA, rank < r && k < P.K ? ((uint32_t)(k + e) * (uint32_t)r + (uint32_t)rank) * 2u : kOOB, 0, 0);
+                for (int e = 0; e < 8; ++e) q[e] = e < left ? src[e] : 0u;
+                h[j][t] = make_uint4(pack2(q[0], q[1]), pack2(q[2], q[3]), pack2(q[4], q[5]), pack2(q[6], q[7]));
+            }
         }
     }
     if (P.keep != nullptr) {
@@ -117,15 +123,24 @@ __device__ __forceinline__ void s_job(const SJobParams &P, int job, uint4 *smem)
                     ((uint8_t *)P.keep)[(size_t)row * row_bytes + k / 8] = (uint8_t)byte;
             }
     }
+    // (a wave's LDS accesses are taken in order: one step's rows after the last's reads)
+    lds_char *turn = (lds_char *)smem + wave * MB * RT * 1024;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < J; ++j) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < RT; ++t) *(uint4 *)(turn + t * 1024 + lane * 16) = h[j][t];
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const uint32_t *q = h[j][t];
-            const uint4 w = make_uint4(pack2(q[0], q[1]), pack2(q[2], q[3]), pack2(q[4], q[5]), pack2(q[6], q[7]));
+            const lds_char *at = turn + t * 1024 + (8 * lg + (l16 >> 2)) * 32 + (l16 & 3) * 8;
+            const uint2 w0 = lds_read_tr4(at), w1 = lds_read_tr4(at + 128);
+            const uint4 w = make_uint4(w0.x, w0.y, w1.x, w1.y);
 #pragma unroll
             for (int a = 0; a < MB; ++a) acc[a][t] = mfma16x16x32(w, x[j][a], acc[a][t]);
         }
+    }
+    asm volatile("" ::: "memory");
     f32x4_t *red = (f32x4_t *)smem;
 #pragma unroll
     for (int a = 0; a < MB; ++a)
