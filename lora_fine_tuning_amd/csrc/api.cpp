@@ -347,7 +347,7 @@ extern "C" lora_status lora_linear_fwd_concat(const void *X, const void *W, cons
 }
 
 // B1 and B2: dA, dB, and dS (with its split for B3 where the plan has one) in the workspace.
-static lora_status backward_low_rank(const BwdPlan &pl, const void *dY, const void *X, const AdapterSource &src,
+static lora_status backward_low_rank(const BwdPlan &pl, const void *dY, const LayerInput &X, const AdapterSource &src,
                                      const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
                                      int32_t r, float p, void *workspace, hipStream_t stream) {
     float *dS = (float *)ws_at(workspace, pl.off_ds);
@@ -361,11 +361,11 @@ static lora_status backward_low_rank(const BwdPlan &pl, const void *dY, const vo
                             pl.b1.slots, stream, dss, pl.dss_ld),
            "dS/dB reduction launch");
     if (pl.b2w) {
-        HIPCHK(launch_b2w(X, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, pl.items2,
-                          dApart, nullptr, stream, dss, pl.dss_ld), "B2 launch");
+        HIPCHK(launch_b2w(X.x, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, pl.items2,
+                          dApart, nullptr, stream, dss, pl.dss_ld, X.scales), "B2 launch");
     } else {
         if (m > 0)
-            HIPCHK(launch_b2(X, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, chunks,
+            HIPCHK(launch_b2(X.x, p == 0.0f ? nullptr : keep_bits, dS, (int)m, (int)k, r, pl.rows2, src, chunks,
                              pl.C2, dApart, stream), "B2 launch");
         HIPCHK(launch_grad_reduce(1, dApart, (int)m, (int)k, (int)n, r, src, pl.rows2, chunks, stream),
                "dA reduction launch");
@@ -374,12 +374,24 @@ static lora_status backward_low_rank(const BwdPlan &pl, const void *dY, const vo
 }
 
 namespace lora {
-lora_status backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+lora_status backward_low_rank_only(const void *dY, const LayerInput &X, const AdapterSource &src, const float *S,
                                    const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r,
                                    void *workspace, const float **dS_out, hipStream_t stream) {
     const BwdPlan pl = plan_bwd(m, k, n, r, false, 0, 1);
     *dS_out = (const float *)ws_at(workspace, pl.off_ds);
     return backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, r, src.p, workspace, stream);
+}
+
+lora_status linear_backward(const void *dY, const LayerInput &X, const void *W, const AdapterSource &src, const float *S,
+                            const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace, hipStream_t stream) {
+    const BwdPlan pl = plan_bwd(m, k, n, src.r, false, 0, 1);
+    CHECK(backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, src.r, src.p, workspace, stream));
+    const float *dS = (const float *)ws_at(workspace, pl.off_ds);
+    const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
+    if (m > 0 && dX != nullptr)
+        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r, src.p == 0.0f ? nullptr : keep_bits,
+                           (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
+    return LORA_OK;
 }
 }  // namespace lora
 
@@ -410,14 +422,7 @@ extern "C" lora_status lora_linear_bwd(const void *dY, const void *X, const void
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     if (pl.bytes) REQ_PTR(workspace, 16);
 
-    const AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
-    CHECK(backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, r, p, workspace, stream));
-    const float *dS = (const float *)ws_at(workspace, pl.off_ds);
-    const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
-    if (m > 0 && dX != nullptr)
-        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, r, p == 0.0f ? nullptr : keep_bits,
-                           (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
-    return LORA_OK;
+    return linear_backward(dY, X, W, single_source(A, B, dA, dB, r, alpha, p), S, keep_bits, m, k, n, dX, workspace, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -505,7 +510,7 @@ extern "C" lora_status multi_lora_linear_fwd(const void *X, const void *W, const
 }
 
 // The router, B1 and B2: dA, dB, and dS (with its split for B3 where the plan has one) in the workspace.
-static lora_status multi_backward_low_rank(const BwdPlan &pl, const void *dY, const void *X, AdapterSource src,
+static lora_status multi_backward_low_rank(const BwdPlan &pl, const void *dY, const LayerInput &X, AdapterSource src,
                                            const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
                                            void *workspace, hipStream_t stream) {
     const int32_t r_max = src.r_cap;
@@ -533,11 +538,11 @@ static lora_status multi_backward_low_rank(const BwdPlan &pl, const void *dY, co
                             pl.b1.slots, stream, dss, pl.dss_ld),
            "dS/dB reduction launch");
     if (pl.b2w) {
-        HIPCHK(launch_b2w(X, keep_bits, dS, (int)m, (int)k, r_max, pl.rows2, src, pl.items2, dApart, aditems,
-                          stream, dss, pl.dss_ld), "B2 launch");
+        HIPCHK(launch_b2w(X.x, keep_bits, dS, (int)m, (int)k, r_max, pl.rows2, src, pl.items2, dApart, aditems,
+                          stream, dss, pl.dss_ld, X.scales), "B2 launch");
     } else {
         if (m > 0)
-            HIPCHK(launch_b2(X, keep_bits, dS, (int)m, (int)k, r_max, pl.rows2, src, chunks, pl.C2, dApart, stream),
+            HIPCHK(launch_b2(X.x, keep_bits, dS, (int)m, (int)k, r_max, pl.rows2, src, chunks, pl.C2, dApart, stream),
                    "B2 launch");
         HIPCHK(launch_grad_reduce(1, dApart, (int)m, (int)k, (int)n, r_max, src, pl.rows2, chunks, stream),
                "dA reduction launch");
@@ -552,12 +557,25 @@ lora_status multi_forward_s_only(const void *X, const AdapterSource &src, int64_
                            workspace, stream);
 }
 
-lora_status multi_backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+lora_status multi_backward_low_rank_only(const void *dY, const LayerInput &X, const AdapterSource &src, const float *S,
                                          const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *workspace,
                                          const float **dS_out, hipStream_t stream) {
     const BwdPlan pl = plan_bwd(m, k, n, src.r_cap, true, src.num_segments, src.num_adapters);
     *dS_out = (const float *)ws_at(workspace, pl.off_ds);
     return multi_backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, workspace, stream);
+}
+
+lora_status multi_linear_backward(const void *dY, const LayerInput &X, const void *W, const AdapterSource &src, const float *S,
+                                  const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace,
+                                  hipStream_t stream) {
+    const BwdPlan pl = plan_bwd(m, k, n, src.r_cap, true, src.num_segments, src.num_adapters);
+    CHECK(multi_backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, workspace, stream));
+    const float *dS = (const float *)ws_at(workspace, pl.off_ds);
+    const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
+    if (m > 0 && dX != nullptr)
+        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r_cap, keep_bits, (int)((k + 31) / 32),
+                           src, stream, dss, pl.dss_ld), "B3 launch");
+    return LORA_OK;
 }
 }  // namespace lora
 
@@ -583,14 +601,8 @@ extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, cons
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
     REQ_PTR(workspace, 16);
 
-    const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
-    CHECK(multi_backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, workspace, stream));
-    const float *dS = (const float *)ws_at(workspace, pl.off_ds);
-    const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
-    if (m > 0 && dX != nullptr)
-        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, r_max, keep_bits, (int)((k + 31) / 32),
-                           src, stream, dss, pl.dss_ld), "B3 launch");
-    return LORA_OK;
+    return multi_linear_backward(dY, X, W, multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max), S,
+                                 keep_bits, m, k, n, dX, workspace, stream);
 }
 
 extern "C" lora_status multi_lora_check_segments(const int64_t *seg_off_host, const int32_t *seg_adapter_host,

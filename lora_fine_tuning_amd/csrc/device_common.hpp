@@ -300,6 +300,19 @@ __device__ __forceinline__ void dma16(sgpr4_t desc, uint32_t voff, uint32_t lds_
         : "memory");
 }
 
+// The same with 4 bytes a lane, at LDS byte lds_base + 4*l.
+__device__ __forceinline__ void dma4(sgpr4_t desc, uint32_t voff, uint32_t lds_base) {
+    uint32_t saved_m0;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "buffer_load_dword %1, %2, 0 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved_m0)
+        : "v"(voff), "s"(desc), "s"(lds_base)
+        : "memory");
+}
+
 // Transposing LDS read of 4 bf16 (8 bytes): within each 16-lane group, lane
 // l receives element (l % 4) of the 8-byte rows addressed by lanes
 // 4*i + l/4, i = 0..3 -- i.e. given 4 rows x 16 columns addressed as 4-column

@@ -12,6 +12,9 @@ namespace lora {
 
 struct ChunkEntry;
 
+// Blocks of 32 of the padded k of an input saved in 8 bits.
+inline int64_t i8_blocks(int64_t k) { return (k + 127) / 128 * 4; }
+
 // Rows handled by one work item of each low-rank kernel.
 constexpr int kF1Rows = 64;    // mask + down-projection
 constexpr int kBwdRows = 256;  // dS/dB and dA kernels
@@ -115,6 +118,14 @@ inline AdapterSource multi_source(const lora_adapter *adapters, int32_t nad, con
     return s;
 }
 
+// The input that a backward reads: bf16, or 8-bit codes with their scales (only where
+// b2w_ok holds for the rank).
+struct LayerInput {
+    const void *x;
+    const void *scales;  // NULL: bf16
+    LayerInput(const void *x_, const void *scales_ = nullptr) : x(x_), scales(scales_) {}
+};
+
 // Which router table a kernel's work items come from.
 enum WorkTable { kTabF1 = 0, kTabBwd = 1, kTabB1 = 2 };
 
@@ -216,7 +227,8 @@ inline bool b2w_ok(int r_lds, int RS) { return r_lds <= 128 && RS % 4 == 0; }
 inline int presplit_ld(int r_lds) { return b2w_ok(r_lds, 4) && b2w_blocks(r_lds) >= 4 ? 32 * b2w_blocks(r_lds) : 0; }
 hipError_t launch_b2w(const void *X, const uint32_t *keep, const float *dS, int m, int k, int RS, int rows,
                       const AdapterSource &src, int items, float *part, const int32_t *ad_items,
-                      hipStream_t stream, const uint16_t *dss = nullptr, int dss_ld = 0);
+                      hipStream_t stream, const uint16_t *dss = nullptr, int dss_ld = 0,
+                      const void *xscales = nullptr);
 
 // rows: rows per partial of the single-adapter form; slots: partials
 // written (an upper bound in the mixed-adapter form, where the router's chunk
@@ -282,8 +294,7 @@ hipError_t launch_mxfp4_quantize(const void *W, int64_t k, int64_t n, void *code
 hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_t k, int64_t n, void *W,
                                    hipStream_t stream);
 
-// Inputs saved in 8 bits: blocks of 32 of the padded k (mxint8_kernels.hip).
-inline int64_t i8_blocks(int64_t k) { return (k + 127) / 128 * 4; }
+// Inputs saved in 8 bits (mxint8_kernels.hip).
 hipError_t launch_mxint8_quantize(const void *X, int64_t m, int64_t k, void *codes, void *scales, hipStream_t stream);
 hipError_t launch_mxint8_dequantize(const void *codes, const void *scales, int64_t m, int64_t k, void *X, hipStream_t stream);
 
@@ -362,13 +373,27 @@ hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, f
 // The layers' low-rank steps alone (api.cpp), in a workspace of the bf16 layer's
 // size.  B1 and B2 write dA, dB and dS (m x r fp32, in the workspace, where
 // *dS_out points afterwards).
-lora_status backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+lora_status backward_low_rank_only(const void *dY, const LayerInput &X, const AdapterSource &src, const float *S,
                                    const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r,
                                    void *workspace, const float **dS_out, hipStream_t stream);
 lora_status multi_forward_s_only(const void *X, const AdapterSource &src, int64_t m, int64_t k, uint64_t seed,
                                  uint64_t offset, float *S, uint32_t *keep_bits, void *workspace, hipStream_t stream);
-lora_status multi_backward_low_rank_only(const void *dY, const void *X, const AdapterSource &src, const float *S,
+lora_status multi_backward_low_rank_only(const void *dY, const LayerInput &X, const AdapterSource &src, const float *S,
                                          const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *workspace,
                                          const float **dS_out, hipStream_t stream);
+
+// The layers' backward calls after their checks: bf16 weights (api.cpp) and MXFP4 ones
+// (mxfp4_api.cpp).
+lora_status linear_backward(const void *dY, const LayerInput &X, const void *W, const AdapterSource &src, const float *S,
+                            const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace, hipStream_t stream);
+lora_status multi_linear_backward(const void *dY, const LayerInput &X, const void *W, const AdapterSource &src, const float *S,
+                                  const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace,
+                                  hipStream_t stream);
+lora_status mxfp4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, const AdapterSource &src,
+                                  const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace,
+                                  hipStream_t stream);
+lora_status multi_mxfp4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales,
+                                        const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
+                                        int64_t n, void *dX, void *workspace, hipStream_t stream);
 
 }  // namespace lora

@@ -15,6 +15,7 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "mxint8.hpp"
 
 namespace lora {
 
@@ -1429,8 +1430,14 @@ __global__ __launch_bounds__(256) void b2s_kernel(B2Params P) {
 // blocks) and is loaded straight into a 32 x 512-byte tile with X's chunk
 // swizzle, which the MFMAs read with transposing LDS reads: no split work
 // and no extra barrier per sub-block.
+// X may be saved in 8 bits (X8: mxint8_kernels.hip describes the format): a sub-block is
+// then 32 x 256 bytes of codes and 256 bytes of scales, an 8-bit transposing LDS read
+// hands a lane eight rows of its column, and the codes times their rows' scales become
+// the bf16 operand that the expanded input would be, bit for bit.  X8_FIGURES
 struct B2WParams {
-    const uint16_t *X;
+    const void *X;          // bf16, or codes
+    const uint8_t *xscales; // X8
+    int kb;                 // X8: blocks of 32 of a row
     const uint32_t *keep;
     const float *dS;
     const uint16_t *dss;  // MAXT >= 4: split s*dS rows, dss_ld bf16 apart
@@ -1441,20 +1448,23 @@ struct B2WParams {
     float *part;    // [item][nct][256][RPT]
 };
 
-template <int MAXT>
+template <int MAXT, bool X8 = false>
 struct B2W {
     static constexpr int RPT = 16 * MAXT;                  // ranks per partial row
     static constexpr bool PRESPLIT = MAXT >= 4;            // rank side from the split rows
-    static constexpr int X_BYTES = 32 * 512;
+    static constexpr int X_BYTES = X8 ? 32 * 256 : 32 * 512;
+    static constexpr int NX = X_BYTES / 4096;              // X loads per wave
     // fp32 dS rows: aux 1 KiB loads of mask, then dS (slots past NA load zeros
     // into the stage's spare kibibytes); split rows: 4 loads per wave of the
     // 16 KiB tile, plus the mask (wave 0) or a dummy load (waves 1..3)
     static constexpr int NA = PRESPLIT ? 1 : 1 + (32 * RPT * 4) / 1024;
-    static constexpr int NPW = PRESPLIT ? 5 : (NA + 3) / 4;  // aux loads per wave
+    // the codes' scales (X8) take the spare load after the last: wave 1's dummy, or slot NA
+    static constexpr int NPW = PRESPLIT ? 5 : (NA + (X8 ? 1 : 0) + 3) / 4;  // aux loads per wave
+    static constexpr int SC_OFF = PRESPLIT ? X_BYTES + 16384 + 1024 : X_BYTES + NA * 1024;
     static constexpr int SPL_OFF = X_BYTES;                   // split tile (PRESPLIT)
     static constexpr int MASK_OFF = PRESPLIT ? X_BYTES + 16384 : X_BYTES;
     static constexpr int DS_OFF = X_BYTES + 1024;             // fp32 dS rows (not PRESPLIT)
-    static constexpr int STAGE = PRESPLIT ? X_BYTES + 16384 + 2048 : X_BYTES + 4 * NPW * 1024;
+    static constexpr int STAGE = PRESPLIT ? X_BYTES + 16384 + (X8 ? 3072 : 2048) : X_BYTES + 4 * NPW * 1024;
     static constexpr int NST = MAXT == 2 ? 3 : 4;           // ring depth
     static constexpr int LDS = NST * STAGE;
 };
@@ -1467,9 +1477,26 @@ __device__ __forceinline__ int mask_word(int t, int c) {
     return (((2 * t + (c >> 2)) ^ (((t >> 3) & 3) << 2)) << 2) + (c & 3);
 }
 
-template <int MAXT>
+// Eight rows (row0 .. row0+7, a multiple of 8) of column 16 cb + (lane mod 16) of a 32 x
+// 256-byte tile whose 16-byte chunk c of row r sits at place c ^ (r mod 16) (a half-wave's
+// sixteen rows of a chunk then fall on different banks), times the rows' scales.
+__device__ __forceinline__ uint4 tile_rows8_i8(const lds_char *tile, int row0, int cb, int lane, const float scale[8]) {
+    typedef int v2i_t __attribute__((ext_vector_type(2)));
+    const int row = row0 + ((lane & 15) >> 1);
+    const lds_char *p = tile + row * 256 + ((cb ^ (row & 15)) << 4) + (lane & 1) * 8;
+    const v2i_t q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i_t *)p);
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = (uint32_t)q[e >> 1] >> (16 * (e & 1));
+        o[e] = pack_bf16x2((float)(int8_t)w * scale[2 * e], (float)(int8_t)(w >> 8) * scale[2 * e + 1]);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int MAXT, bool X8>
 __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
-    using C = B2W<MAXT>;
+    using C = B2W<MAXT, X8>;
     constexpr int RPT = C::RPT;
     extern __shared__ uint4 b2w_smem[];
     lds_char *smem = (lds_char *)b2w_smem;
@@ -1502,7 +1529,9 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
     const int nsb = (nrows + 31) / 32;
     const bool has_mask = P.keep != nullptr;
     auto clampb = [](uint64_t v) { return (uint32_t)(v < 0x7FFFFFF0ull ? v : 0x7FFFFFF0ull); };
-    const sgpr4_t dX = make_desc(P.X + (size_t)row_lo * P.k, clampb((uint64_t)nrows * P.k * 2));
+    const int xrow = X8 ? P.kb * 32 : 2 * P.k;  // bytes of a row of X
+    const sgpr4_t dX = make_desc((const char *)P.X + (size_t)row_lo * xrow, clampb((uint64_t)nrows * xrow));
+    const sgpr4_t dC = make_desc(X8 ? P.xscales + (size_t)row_lo * P.kb : nullptr, X8 ? clampb((uint64_t)nrows * P.kb) : 0u);
     const sgpr4_t dK = make_desc(has_mask ? P.keep + (size_t)row_lo * P.KW : P.keep,
                                  has_mask ? clampb((uint64_t)nrows * P.KW * 4) : 0u);
     const sgpr4_t dD = C::PRESPLIT
@@ -1511,22 +1540,33 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
 
     // this lane's X offsets inside sub-block 0 (4 loads of 2 rows x 512 bytes);
     // the split rows use the same rows and chunk swizzle
+    // (X8: 2 loads of 4 rows x 256 bytes)
     uint32_t offX[4], offD[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int rr = 2 * (4 * wave + j) + (lane >> 5);
         const int c = (lane & 31) ^ swz512(rr);
-        const int col = k0 + 8 * c;
-        offX[j] = col < P.k ? (uint32_t)(((size_t)rr * P.k + col) * 2) : kOOBL;
+        if constexpr (X8) {
+            const int rc = 4 * (2 * wave + j) + (lane >> 4), at = k0 + 16 * ((lane & 15) ^ (rc & 15));
+            offX[j] = j < 2 && at < xrow ? (uint32_t)rc * (uint32_t)xrow + (uint32_t)at : kOOBL;
+        } else {
+            const int col = k0 + 8 * c;
+            offX[j] = col < P.k ? (uint32_t)(((size_t)rr * P.k + col) * 2) : kOOBL;
+        }
         offD[j] = 8 * c < 2 * rpa ? (uint32_t)(((size_t)rr * P.dss_ld + 8 * c) * 2) : kOOBL;
     }
     auto issue = [&](int sb, int stage) {
         const uint32_t base = lds0 + stage * C::STAGE;
         const bool live = sb < nsb;
-        const uint32_t xo = (uint32_t)((size_t)sb * 32 * P.k * 2);
+        const uint32_t xo = (uint32_t)((size_t)sb * 32 * xrow);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            dma16(dX, (live && offX[j] != kOOBL) ? offX[j] + xo : kOOBL, base + (4 * wave + j) * 1024);
+        for (int j = 0; j < C::NX; ++j)
+            dma16(dX, (live && offX[j] != kOOBL) ? offX[j] + xo : kOOBL, base + (C::NX * wave + j) * 1024);
+        // X8: two words of scales a row, lane 2 t + h word h of tile row t
+        auto scale_off = [&]() {
+            const int row = sb * 32 + (lane >> 1), at = (k0 >> 5) + 4 * (lane & 1);
+            return live && at < P.kb && row < nrows ? (uint32_t)row * (uint32_t)P.kb + (uint32_t)at : kOOBL;
+        };
         // mask words: lane l fills the 16-byte slot l of the stage's mask tile
         // with words 4 h .. 4 h + 3 of tile row t, where 2 t + h = l ^ (((l >> 4) & 3) << 2)
         // (mask_word below reads them back)
@@ -1544,13 +1584,19 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
                 dma16(dD, (live && row < nrows && offD[j] != kOOBL) ? offD[j] + so : kOOBL,
                       base + C::SPL_OFF + (4 * wave + j) * 1024);
             }
-            // wave 0: the mask words; the others a dummy load into the kibibyte past them
-            dma16(dK, wave == 0 ? mask_off() : kOOBL, base + C::MASK_OFF + (wave == 0 ? 0 : 1024));
+            // wave 0: the mask words; wave 1 (X8): the scales; the others a dummy load into the
+            // last kibibyte
+            if (X8 && wave == 1) dma4(dC, scale_off(), base + C::SC_OFF);
+            else dma16(dK, wave == 0 ? mask_off() : kOOBL, base + C::MASK_OFF + (wave == 0 ? 0 : X8 ? 2048 : 1024));
         } else {
 #pragma unroll
             for (int q0 = 0; q0 < C::NPW; ++q0) {
                 const int q = wave * C::NPW + q0;
                 const uint32_t dst = base + C::X_BYTES + q * 1024;
+                if (X8 && q == C::NA) {
+                    dma4(dC, scale_off(), dst);
+                    continue;
+                }
                 uint32_t off = kOOBL;
                 if (q == 0) {
                     off = mask_off();
@@ -1567,7 +1613,7 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
     // The main loop is instantiated per number of 16-rank blocks the chunk's
     // adapter needs (1, 2, 4 or 8, at most MAXT), so the MFMA stream has no
     // per-block branches and the accumulators stay in fixed registers.
-    constexpr int NPS = 4 + C::NPW;  // loads per wave per stage
+    constexpr int NPS = C::NX + C::NPW;  // loads per wave per stage
     auto body = [&](auto nb_c) {
         constexpr int NB = decltype(nb_c)::value;
         f32x4_t acc[4][NB];
@@ -1602,10 +1648,22 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
                     split_frag(v, bhi[bt], blo[bt]);
                 }
             }
+            // X8: the scales of rows 8g .. 8g+7 in the wave's two blocks of 32 columns
+            float sc[2][8];
+            if constexpr (X8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w = *(const uint32_t *)(xt + C::SC_OFF + (8 * g + e) * 8 + (wave >> 1) * 4) >> (16 * (wave & 1));
+                    sc[0][e] = i8_scale(w & 255u);
+                    sc[1][e] = i8_scale((w >> 8) & 255u);
+                }
+            }
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
                 const int cb = 4 * wave + mb;
-                uint4 xf = tile_rows8(xt, 8 * g, cb, lane);
+                uint4 xf;
+                if constexpr (X8) xf = tile_rows8_i8(xt, 8 * g, cb, lane, sc[mb >> 1]);
+                else xf = tile_rows8(xt, 8 * g, cb, lane);
                 if (has_mask) {
                     const int bit = 16 * (cb & 1) + li;
                     uint32_t mm[4];
@@ -2406,9 +2464,11 @@ hipError_t launch_b2(const void *X, const uint32_t *keep, const float *dS, int m
 
 hipError_t launch_b2w(const void *X, const uint32_t *keep, const float *dS, int m, int k, int RS, int rows,
                       const AdapterSource &src, int items, float *part, const int32_t *ad_items, hipStream_t stream,
-                      const uint16_t *dss, int dss_ld) {
+                      const uint16_t *dss, int dss_ld, const void *xscales) {
     B2WParams P;
-    P.X = (const uint16_t *)X;
+    P.X = X;
+    P.xscales = (const uint8_t *)xscales;
+    P.kb = (int)i8_blocks(k);
     P.keep = keep;
     P.dS = dS;
     P.dss = dss;
@@ -2428,11 +2488,16 @@ hipError_t launch_b2w(const void *X, const uint32_t *keep, const float *dS, int 
     if (items > 0 && m > 0) {
         const dim3 grid((unsigned)items, (unsigned)P.nct);
         const int slot = prof_begin("b2_da", stream);
+        auto go = [&](auto mt_c) {
+            constexpr int MT = decltype(mt_c)::value;
+            if (xscales != nullptr) launch_with_lds(b2w_kernel<MT, true>, grid, (size_t)B2W<MT, true>::LDS, stream, P);
+            else launch_with_lds(b2w_kernel<MT, false>, grid, (size_t)B2W<MT>::LDS, stream, P);
+        };
         switch (mt) {
-        case 1: launch_with_lds(b2w_kernel<1>, grid, (size_t)B2W<1>::LDS, stream, P); break;
-        case 2: launch_with_lds(b2w_kernel<2>, grid, (size_t)B2W<2>::LDS, stream, P); break;
-        case 4: launch_with_lds(b2w_kernel<4>, grid, (size_t)B2W<4>::LDS, stream, P); break;
-        default: launch_with_lds(b2w_kernel<8>, grid, (size_t)B2W<8>::LDS, stream, P); break;
+        case 1: go(std::integral_constant<int, 1>{}); break;
+        case 2: go(std::integral_constant<int, 2>{}); break;
+        case 4: go(std::integral_constant<int, 4>{}); break;
+        default: go(std::integral_constant<int, 8>{}); break;
         }
         const hipError_t e = finish_launch(slot, stream);
         if (e != hipSuccess) return e;

@@ -163,6 +163,49 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
                            ws_at(workspace, w), workspace_bytes - w, stream);
 }
 
+namespace lora {
+lora_status mxfp4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, const AdapterSource &src,
+                                  const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace,
+                                  hipStream_t stream) {
+    const int32_t r = src.r;
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
+    if (pl.kind) {
+        const float *dS = nullptr;
+        CHECK(backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, r, ws_at(workspace, align_up(pl.part_bytes)), &dS, stream));
+        if (dX != nullptr) {
+            HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
+                   "MXFP4 transposed product launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, r, 0,
+                                     nullptr, src.p == 0.0f ? nullptr : keep_bits, src, dX, stream), "MXFP4 sum launch");
+        }
+        return LORA_OK;
+    }
+    if (m > 0 && dX != nullptr)
+        HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, ws_at(workspace, expanded_bytes(m, k, n)), stream);
+}
+
+lora_status multi_mxfp4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales,
+                                        const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
+                                        int64_t n, void *dX, void *workspace, hipStream_t stream) {
+    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, src.r_cap);
+    if (pl.kind) {
+        const float *dS = nullptr;
+        CHECK(multi_backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, ws_at(workspace, align_up(pl.part_bytes)), &dS, stream));
+        if (dX != nullptr) {
+            HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
+                   "MXFP4 transposed product launch");
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, src.r_cap, 0,
+                                     nullptr, keep_bits, src, dX, stream), "MXFP4 sum launch");
+        }
+        return LORA_OK;
+    }
+    if (m > 0 && dX != nullptr)
+        HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
+    return multi_linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, ws_at(workspace, expanded_bytes(m, k, n)), stream);
+}
+}  // namespace lora
+
 extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales,
                                              const void *A, const void *B, const float *S,
                                              const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, int32_t r,
@@ -186,25 +229,8 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
         REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     }
     REQ_WORKSPACE(lora_mxfp4_linear_bwd_workspace_size(m, k, n, r));
-    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
-    if (pl.kind) {
-        const float *dS = nullptr;
-        const AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
-        CHECK(backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, r, ws_at(workspace, align_up(pl.part_bytes)), &dS,
-                                     stream));
-        if (dX != nullptr) {
-            HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
-                   "MXFP4 transposed product launch");
-            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, r, 0,
-                                     nullptr, p == 0.0f ? nullptr : keep_bits, src, dX, stream), "MXFP4 sum launch");
-        }
-        return LORA_OK;
-    }
-    const size_t w = expanded_bytes(m, k, n);
-    if (m > 0 && dX != nullptr)
-        HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
-    return lora_linear_bwd(dY, X, m > 0 ? workspace : codes, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
-                           ws_at(workspace, w), workspace_bytes - w, stream);
+    return mxfp4_linear_backward(dY, X, codes, scales, single_source(A, B, dA, dB, r, alpha, p), S, keep_bits, m, k, n, dX, workspace,
+                                 stream);
 }
 
 extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
@@ -277,23 +303,7 @@ extern "C" lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X
         REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
     }
     REQ_WORKSPACE(multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments));
-    const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r_max);
-    if (pl.kind) {
-        const AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
-        const float *dS = nullptr;
-        CHECK(multi_backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, ws_at(workspace, align_up(pl.part_bytes)),
-                                           &dS, stream));
-        if (dX != nullptr) {
-            HIPCHK(launch_mxfp4_gemm_t(pl, dY, codes, scales, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
-                   "MXFP4 transposed product launch");
-            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, r_max, 0,
-                                     nullptr, keep_bits, src, dX, stream), "MXFP4 sum launch");
-        }
-        return LORA_OK;
-    }
-    const size_t w = expanded_bytes(m, k, n);
-    if (m > 0 && dX != nullptr)
-        HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
-    return multi_lora_linear_bwd(dY, X, m > 0 ? workspace : codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
-                                 keep_bits, m, k, n, r_max, dX, ws_at(workspace, w), workspace_bytes - w, stream);
+    return multi_mxfp4_linear_backward(dY, X, codes, scales,
+                                       multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max), S, keep_bits, m,
+                                       k, n, dX, workspace, stream);
 }

@@ -39,8 +39,11 @@ extern "C" lora_status lora_mxint8_dequantize(const void *codes, const void *sca
     return LORA_OK;
 }
 
-// The expanded input sits at the start of the workspace, the layer's own after it.
-static size_t input_bytes(int64_t m, int64_t k) { return align_up((size_t)m * (size_t)k * 2); }
+// The dA pass reads the codes themselves where it takes all ranks at once (b2w_ok: ranks
+// up to 128, multiples of 4); for other ranks the input is expanded to bf16 first, at the
+// start of the workspace, the layer's own after it.
+static bool direct(int32_t r) { return b2w_ok((r + 15) / 16 * 16, r); }
+static size_t input_bytes(int64_t m, int64_t k, int32_t r) { return direct(r) ? 0 : align_up((size_t)m * (size_t)k * 2); }
 
 static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
     return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && m * k < (1LL << 46) && k * n < (1LL << 46);
@@ -71,7 +74,7 @@ extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t gr
     const size_t layer = kind == LORA_WEIGHT_BF16    ? lora_linear_bwd_workspace_size(m, k, n, r)
                          : kind == LORA_WEIGHT_MXFP4 ? lora_mxfp4_linear_bwd_workspace_size(m, k, n, r)
                                                      : lora_int4_linear_bwd_workspace_size(m, k, n, group, r);
-    return input_bytes(m, k) + layer;
+    return input_bytes(m, k, r) + layer;
 }
 
 extern "C" size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r_max,
@@ -80,19 +83,24 @@ extern "C" size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t gro
     const size_t layer = kind == LORA_WEIGHT_BF16    ? multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
                          : kind == LORA_WEIGHT_MXFP4 ? multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
                                                      : multi_lora_int4_bwd_workspace_size(m, k, n, group, r_max, num_adapters, num_segments);
-    return input_bytes(m, k) + layer;
+    return input_bytes(m, k, r_max) + layer;
 }
 
-// The layer's backward over a weight of either kind.
-static lora_status layer_bwd(int32_t kind, const void *W, const void *W_scales, int64_t group, const void *dY, const void *X,
-                             const void *A, const void *B, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
-                             int32_t r, float alpha, float p, void *dX, void *dA, void *dB, void *workspace, size_t bytes,
-                             hipStream_t stream) {
-    if (kind == LORA_WEIGHT_BF16)
-        return lora_linear_bwd(dY, X, W, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB, workspace, bytes, stream);
+// The layer's backward over a weight of any form, after the checks.
+static lora_status layer_backward(bool multi, int32_t kind, const void *W, const void *W_scales, int64_t group, const void *dY,
+                                  const LayerInput &X, const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m,
+                                  int64_t k, int64_t n, void *dX, void *workspace, hipStream_t stream) {
     if (kind == LORA_WEIGHT_MXFP4)
-        return lora_mxfp4_linear_bwd(dY, X, W, W_scales, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB, workspace, bytes, stream);
-    return lora_int4_linear_bwd(dY, X, W, W_scales, group, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB, workspace, bytes, stream);
+        return multi ? multi_mxfp4_linear_backward(dY, X, W, W_scales, src, S, keep_bits, m, k, n, dX, workspace, stream)
+                     : mxfp4_linear_backward(dY, X, W, W_scales, src, S, keep_bits, m, k, n, dX, workspace, stream);
+    if (kind == LORA_WEIGHT_INT4) {
+        if (m > 0 && dX != nullptr)
+            HIPCHK(launch_int4_dequantize(W, W_scales, k, n, group, workspace, stream), "4-bit dequantise launch");
+        W = workspace;
+        workspace = ws_at(workspace, m > 0 ? align_up((size_t)k * (size_t)n * 2) : 0);
+    }
+    return multi ? multi_linear_backward(dY, X, W, src, S, keep_bits, m, k, n, dX, workspace, stream)
+                 : linear_backward(dY, X, W, src, S, keep_bits, m, k, n, dX, workspace, stream);
 }
 
 extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind, const void *W,
@@ -110,12 +118,16 @@ extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_code
     REQ_PTR(dA, 2);
     REQ_PTR(dB, 2);
     CHECK(check_rows(m, dY, S, keep_bits, p != 0.0f, dX));
-    const size_t need = lora_mxint8_linear_bwd_workspace_size(kind, group, m, k, n, r), w = input_bytes(m, k);
+    const size_t need = lora_mxint8_linear_bwd_workspace_size(kind, group, m, k, n, r), w = input_bytes(m, k, r);
     if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (need > 0) REQ_PTR(workspace, 16);
-    if (m > 0) HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
-    return layer_bwd(kind, W, W_scales, group, dY, workspace, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
-                     ws_at(workspace, w), workspace_bytes - w, stream);
+    LayerInput X(x_codes, x_scales);
+    if (w > 0) {
+        HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
+        X = LayerInput(workspace);
+    }
+    return layer_backward(false, kind, W, W_scales, group, dY, X, single_source(A, B, dA, dB, r, alpha, p), S, keep_bits, m, k, n, dX,
+                          ws_at(workspace, w), stream);
 }
 
 extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind, const void *W,
@@ -131,17 +143,16 @@ extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *
     CHECK(multi_lora_linear_fwd(nullptr, W, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max, 0, 0, nullptr,
                                 nullptr, nullptr, nullptr, 0, stream));
     CHECK(check_rows(m, dY, S, keep_bits, true, dX));
-    const size_t need = multi_lora_mxint8_bwd_workspace_size(kind, group, m, k, n, r_max, num_adapters, num_segments), w = input_bytes(m, k);
+    const size_t need = multi_lora_mxint8_bwd_workspace_size(kind, group, m, k, n, r_max, num_adapters, num_segments);
+    const size_t w = input_bytes(m, k, r_max);
     if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (need > 0) REQ_PTR(workspace, 16);
-    if (m > 0) HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
-    char *rest = ws_at(workspace, w);
-    if (kind == LORA_WEIGHT_BF16)
-        return multi_lora_linear_bwd(dY, workspace, W, adapters, num_adapters, seg_off, seg_adapter, num_segments, S, keep_bits, m, k, n,
-                                     r_max, dX, rest, workspace_bytes - w, stream);
-    if (kind == LORA_WEIGHT_MXFP4)
-        return multi_lora_mxfp4_linear_bwd(dY, workspace, W, W_scales, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
-                                           keep_bits, m, k, n, r_max, dX, rest, workspace_bytes - w, stream);
-    return multi_lora_int4_linear_bwd(dY, workspace, W, W_scales, group, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
-                                      keep_bits, m, k, n, r_max, dX, rest, workspace_bytes - w, stream);
+    LayerInput X(x_codes, x_scales);
+    if (w > 0) {
+        HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
+        X = LayerInput(workspace);
+    }
+    return layer_backward(true, kind, W, W_scales, group, dY, X,
+                          multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max), S, keep_bits, m, k, n, dX,
+                          ws_at(workspace, w), stream);
 }
