@@ -53,16 +53,16 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi, bool symmetr
     return bits | (uint32_t)rint(-(double)lo / (double)__uint_as_float(bits));
 }
 
-// The nearest of 0 .. 15 to w / s + z (ties of w / s to even): the rounded quotient
-// is off by one at most, and w - h s is exact in fp32 for the whole numbers h in
-// question (s has 16 significant bits, w eight), so the remainder decides.
-__device__ __forceinline__ uint32_t group_code(float w, float s, float inv, float z) {
-    float h = rintf(w * inv);
-    const float half = 0.5f * s, rest = fmaf(-h, s, w);
-    const bool odd = ((int)h & 1) != 0;
-    if (rest > half || (rest == half && odd)) h += 1.f;
-    if (rest < -half || (rest == -half && odd)) h -= 1.f;
-    return (uint32_t)__builtin_amdgcn_fmed3f(h + z, 0.f, 15.f);
+// w / s to the nearest integer (ties to even), plus z, kept in 0 .. 15; inv = 1 / s.  A
+// quotient that is no tie is at least 2^-21 of its size away from one (w has 8
+// significant bits, s 16, the tie 5), so an error of two fp32 steps does no harm, and a
+// step of refinement makes a tie exact.  Adding 1.5 * 2^23 rounds and leaves the integer
+// in the low bits; z_bits is z less that sum's other bits.
+__device__ __forceinline__ uint32_t group_code(float w, float s, float inv, int z_bits) {
+    float h = w * inv;
+    h = fmaf(fmaf(-h, s, w), inv, h);
+    const int q = __float_as_int(h + 12582912.f) + z_bits;
+    return (uint32_t)min(max(q, 0), 15);
 }
 
 // 8 codes of a column -> a stored word.
@@ -70,79 +70,85 @@ __device__ __forceinline__ uint32_t code_word(const uint32_t q[8]) {
     return q[0] | q[2] << 4 | q[4] << 8 | q[6] << 12 | q[1] << 16 | q[3] << 20 | q[5] << 24 | q[7] << 28;
 }
 
-// One thread: 128 rows of two columns in registers, so that a group's scale and its
-// codes take one read of W.  GIVEN: scales have been made (groups of more rows).
+// Value of `v` in the lane whose number differs in bit 0 or bit 1.
+template <int BIT>
+__device__ __forceinline__ uint32_t quad(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, BIT == 0 ? 0xB1 : 0x4E, 0xF, 0xF, true);
+}
+template <int BIT>
+__device__ __forceinline__ float quad(float v) {
+    return __uint_as_float(quad<BIT>(__float_as_uint(v)));
+}
+
+// A wave: 128 rows of 32 columns; lane 4 p + d has rows 32d .. 32d+31 of columns 2p and
+// 2p+1 in registers, so that a group's scale (the quad's lanes together) and its codes
+// take one read of W.  The quad turns its words so that each lane writes the 16 bytes of
+// one g.  GIVEN: scales have been made (groups of more than 128 rows).  HBM-bound, 2
+// bytes in and 0.5 out a value, with 12 instructions a value beside: QUANT_FIGURES
 template <bool GIVEN>
 __global__ __launch_bounds__(256) void int4_quantize_kernel(const uint16_t *W, I4Shape S, bool symmetric, uint8_t *codes,
                                                             uint32_t *scales) {
-    const int64_t nc = S.n16 * 8, items = S.k128 * nc;
+    const int lane = threadIdx.x & 63, d = lane & 3;
+    const int64_t n32 = (S.n16 + 1) / 2, waves = S.k128 * n32;
     const int each = GIVEN ? 4 : (int)S.group / 32;  // blocks of 32 rows that share a scale (of the 4 here)
-    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
-        const int64_t t = it / nc, col = (it - t * nc) * 2, row0 = t * 128;
-        const int rows = col < S.n ? (int)min((int64_t)128, S.k - row0) : 0;
+    for (int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); w < waves;
+         w += (int64_t)gridDim.x * 4) {
+        const int64_t t = w / n32, col = (w - t * n32) * 32 + (lane >> 2) * 2, row0 = t * 128 + 32 * d;
+        const int rows = col < S.n ? (int)min((int64_t)32, max((int64_t)0, S.k - row0)) : 0;  // (a multiple of 8)
         const uint16_t *src = W + row0 * S.n + col;
-        uint32_t r[128];
+        uint32_t r[32];
 #pragma unroll
-        for (int i = 0; i < 128; ++i) r[i] = i < rows ? *(const uint32_t *)(src + i * S.n) : 0u;
-        uint8_t *dst = codes + ((((col >> 4) * S.k128 + t) * 4) * 16 + (col & 15)) * 16;
-        uint32_t *sc = scales + ((col >> 4) * S.groups + (GIVEN ? row0 / S.group : t * (4 / each))) * 16 + (col & 15);
+        for (int i = 0; i < 32; ++i) r[i] = i < rows ? *(const uint32_t *)(src + i * S.n) : 0u;
+        const int64_t cg = col >> 4;
+        if (cg >= S.n16) continue;  // (whole quads; an odd last group of columns)
+        uint8_t *dst = codes + (((cg * S.k128 + t) * 4) * 16 + (col & 15)) * 16;
+        uint32_t *sc = scales + (cg * S.groups + (GIVEN ? t * 128 / S.group : t * (4 / each) + d / each)) * 16 + (col & 15);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             auto value = [&](int i) { return __uint_as_float(c ? r[i] & 0xFFFF0000u : r[i] << 16); };
-            float lo[4], hi[4];  // of 32 rows
-            bool bad[4];
-            if constexpr (!GIVEN) {
+            uint32_t word;
+            if constexpr (GIVEN) {
+                word = sc[c];
+            } else {
+                float lo = 0.f, hi = 0.f;
+                uint32_t top = 0u;  // magnitudes order as their bit patterns
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    lo[d] = hi[d] = 0.f;
-                    bad[d] = false;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float w = value(32 * d + i);
-                        lo[d] = fminf(lo[d], w);
-                        hi[d] = fmaxf(hi[d], w);
-                        bad[d] |= w != w;
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    lo = fminf(lo, value(i));
+                    hi = fmaxf(hi, value(i));
+                    top = max(top, __float_as_uint(value(i)) & 0x7FFFFFFFu);
                 }
-#pragma unroll
-                for (int d = 0; d < 4; d += 2)
-                    if (each >= 2) {
-                        lo[d] = lo[d + 1] = fminf(lo[d], lo[d + 1]);
-                        hi[d] = hi[d + 1] = fmaxf(hi[d], hi[d + 1]);
-                        bad[d] = bad[d + 1] = bad[d] || bad[d + 1];
-                    }
-                if (each >= 4) {
-                    lo[0] = lo[1] = lo[2] = lo[3] = fminf(lo[0], lo[2]);
-                    hi[0] = hi[1] = hi[2] = hi[3] = fmaxf(hi[0], hi[2]);
-                    bad[0] = bad[1] = bad[2] = bad[3] = bad[0] || bad[2];
-                }
+                if (each >= 2) lo = fminf(lo, quad<0>(lo)), hi = fmaxf(hi, quad<0>(hi)), top = max(top, quad<0>(top));
+                if (each >= 4) lo = fminf(lo, quad<1>(lo)), hi = fmaxf(hi, quad<1>(hi)), top = max(top, quad<1>(top));
+                word = top >= 0x7F800000u ? 0x7FC00000u : group_scale(lo, hi, symmetric);
+                // (groups past k, and padding columns, hold zeros)
+                if (d % each == 0) sc[c] = rows > 0 ? word : 0u;
             }
-            uint32_t out[4][4];
+            const float s = __uint_as_float(word & 0xFFFFFF00u), inv = 1.f / s;
+            const int z_bits = (int)(word & 0xFFu) - 0x4B400000;
+            const bool nan = s != s;
+            uint32_t out[4];
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                uint32_t word;
-                if constexpr (GIVEN) {
-                    word = sc[c];
-                } else {
-                    word = bad[d] ? 0x7FC00000u : group_scale(lo[d], hi[d], symmetric);
-                    // (groups past k, and padding columns, hold zeros)
-                    if (d % each == 0) sc[d / each * 16 + c] = 32 * d < rows ? word : 0u;
-                }
-                const float s = __uint_as_float(word & 0xFFFFFF00u), z = (float)(word & 0xFFu), inv = 1.f / s;
-                const bool nan = s != s;
+            for (int g = 0; g < 4; ++g) {
+                uint32_t q[8];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t q[8];
+                for (int e = 0; e < 8; ++e) q[e] = group_code(value(8 * g + e), s, inv, z_bits);
+                out[g] = nan || 8 * g >= rows ? 0u : code_word(q);
+            }
+            // the quad's 4 x 4 words turned: lane d gets word g = d of every lane, in lane order
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = 32 * d + 8 * g + e;
-                        q[e] = nan || i >= rows ? 0u : group_code(value(i), s, inv, z);
-                    }
-                    out[g][d] = code_word(q);
-                }
+            for (int g = 0; g < 4; g += 2) {
+                const uint32_t give = d & 1 ? out[g] : out[g + 1], got = quad<0>(give);
+                out[g] = d & 1 ? got : out[g];
+                out[g + 1] = d & 1 ? out[g + 1] : got;
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g) *(uint4 *)(dst + g * 256 + c * 16) = make_uint4(out[g][0], out[g][1], out[g][2], out[g][3]);
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t give = d & 2 ? out[g] : out[g + 2], got = quad<1>(give);
+                out[g] = d & 2 ? got : out[g];
+                out[g + 2] = d & 2 ? out[g + 2] : got;
+            }
+            *(uint4 *)(dst + d * 256 + c * 16) = make_uint4(out[0], out[1], out[2], out[3]);
         }
     }
 }
@@ -272,7 +278,7 @@ unsigned i4_grid(int64_t items) { return (unsigned)std::min<int64_t>((items + 25
 hipError_t launch_int4_quantize(const void *W, int64_t k, int64_t n, int64_t group, bool symmetric, void *codes, void *scales,
                                 hipStream_t stream) {
     const I4Shape s = i4_shape(k, n, group);
-    const dim3 grid(i4_grid(s.k128 * s.n16 * 8));
+    const dim3 grid(i4_grid(s.k128 * ((s.n16 + 1) / 2) * 64));
     const int slot = prof_begin("int4_quantize", stream);
     if (group <= 128) {
         hipLaunchKernelGGL((int4_quantize_kernel<false>), grid, dim3(256), 0, stream, (const uint16_t *)W, s, symmetric,

@@ -1479,16 +1479,19 @@ __device__ __forceinline__ int mask_word(int t, int c) {
 
 // Eight rows (row0 .. row0+7, a multiple of 8) of column 16 cb + (lane mod 16) of a 32 x
 // 256-byte tile whose 16-byte chunk c of row r sits at place c ^ (r mod 16) (a half-wave's
-// sixteen rows of a chunk then fall on different banks), times the rows' scales.
-__device__ __forceinline__ uint4 tile_rows8_i8(const lds_char *tile, int row0, int cb, int lane, const float scale[8]) {
+// sixteen rows of a chunk then fall on different banks).
+__device__ __forceinline__ uint2 tile_rows8_i8(const lds_char *tile, int row0, int cb, int lane) {
     typedef int v2i_t __attribute__((ext_vector_type(2)));
     const int row = row0 + ((lane & 15) >> 1);
     const lds_char *p = tile + row * 256 + ((cb ^ (row & 15)) << 4) + (lane & 1) * 8;
-    const v2i_t q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i_t *)p);
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i_t *)p));
+}
+// Eight codes times their rows' scales -> an MFMA operand, exact.
+__device__ __forceinline__ uint4 times_scales(const uint2 &q, const float scale[8]) {
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t w = (uint32_t)q[e >> 1] >> (16 * (e & 1));
+        const uint32_t w = (e < 2 ? q.x : q.y) >> (16 * (e & 1));
         o[e] = pack_bf16x2((float)(int8_t)w * scale[2 * e], (float)(int8_t)(w >> 8) * scale[2 * e + 1]);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
@@ -1614,8 +1617,11 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
     // adapter needs (1, 2, 4 or 8, at most MAXT), so the MFMA stream has no
     // per-block branches and the accumulators stay in fixed registers.
     constexpr int NPS = C::NX + C::NPW;  // loads per wave per stage
-    auto body = [&](auto nb_c) {
+    // X8: masked or not is compiled in too, and a stage's operands are all read before
+    // the first is used (one after the other, the waits took half of the kernel's time).
+    auto body_m = [&](auto nb_c, auto mask_c) {
         constexpr int NB = decltype(nb_c)::value;
+        const bool masked = X8 ? decltype(mask_c)::value : has_mask;
         f32x4_t acc[4][NB];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -1648,12 +1654,23 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
                     split_frag(v, bhi[bt], blo[bt]);
                 }
             }
-            // X8: the scales of rows 8g .. 8g+7 in the wave's two blocks of 32 columns
+            // X8: rows 8g .. 8g+7 of the wave's columns, their scales in its two blocks of 32
+            // columns, and their mask words
             float sc[2][8];
+            uint2 q8[4], mw[8];
             if constexpr (X8) {
+                uint32_t sw[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sw[e] = *(const uint32_t *)(xt + C::SC_OFF + (8 * g + e) * 8 + (wave >> 1) * 4);
+#pragma unroll
+                for (int mb = 0; mb < 4; ++mb) q8[mb] = tile_rows8_i8(xt, 8 * g, 4 * wave + mb, lane);
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mw[e] = *(const uint2 *)(mk + mask_word(8 * g + e, 2 * wave));
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t w = *(const uint32_t *)(xt + C::SC_OFF + (8 * g + e) * 8 + (wave >> 1) * 4) >> (16 * (wave & 1));
+                    const uint32_t w = sw[e] >> (16 * (wave & 1));
                     sc[0][e] = i8_scale(w & 255u);
                     sc[1][e] = i8_scale((w >> 8) & 255u);
                 }
@@ -1662,15 +1679,21 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
             for (int mb = 0; mb < 4; ++mb) {
                 const int cb = 4 * wave + mb;
                 uint4 xf;
-                if constexpr (X8) xf = tile_rows8_i8(xt, 8 * g, cb, lane, sc[mb >> 1]);
+                if constexpr (X8) xf = times_scales(q8[mb], sc[mb >> 1]);
                 else xf = tile_rows8(xt, 8 * g, cb, lane);
-                if (has_mask) {
+                if (masked) {
                     const int bit = 16 * (cb & 1) + li;
                     uint32_t mm[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t w0 = mk[mask_word(8 * g + 2 * q, cb >> 1)];
-                        const uint32_t w1 = mk[mask_word(8 * g + 2 * q + 1, cb >> 1)];
+                        uint32_t w0, w1;
+                        if constexpr (X8) {
+                            w0 = mb < 2 ? mw[2 * q].x : mw[2 * q].y;
+                            w1 = mb < 2 ? mw[2 * q + 1].x : mw[2 * q + 1].y;
+                        } else {
+                            w0 = mk[mask_word(8 * g + 2 * q, cb >> 1)];
+                            w1 = mk[mask_word(8 * g + 2 * q + 1, cb >> 1)];
+                        }
                         // each keep bit sign-extended to a whole word, the pair
                         // merged into one 16-bit mask per element (3 instructions)
                         const uint32_t e0 = (uint32_t)__builtin_amdgcn_sbfe((int)w0, bit, 1);
@@ -1700,6 +1723,12 @@ __global__ __launch_bounds__(256) void b2w_kernel(B2WParams P) {
             for (int bt = 0; bt < NB; ++bt)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) pp[((4 * wave + mb) * 16 + 4 * g + v) * (16 * NB) + 16 * bt + li] = acc[mb][bt][v];
+    };
+    auto body = [&](auto nb_c) {
+        if constexpr (X8) {
+            if (!has_mask) return body_m(nb_c, std::false_type{});
+        }
+        body_m(nb_c, std::true_type{});
     };
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
