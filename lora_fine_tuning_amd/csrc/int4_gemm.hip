@@ -1,4 +1,4 @@
-// Y = X W' + alpha S B for up to 64 rows, W' = s (q - z) in 4-bit integers
+// Y = X W' + alpha S B for few and middling numbers of rows, W' = s (q - z) in 4-bit integers
 // (int4_kernels.hip describes the storage).
 //
 // With few rows the weight's bytes bound the product.  It is read once, straight into
@@ -34,6 +34,9 @@ struct I4Params : SJobParams {
     uint16_t *Y;          // direct
     float *part;          // [KS][M][N] (nullptr: direct)
     int N, N16, K128, G;
+    const float *S;       // the epilogue's LoRA term: M x r fp32 (nullptr: none)
+    const uint16_t *B;    // r x N
+    float alpha;
     int each;             // blocks of 128 rows that share a scale (groups of 128 rows or more),
     uint32_t each_inv;    // and floor(2^32 / each) + 1: block t's group is the product's high word
     int tiles_n, KS, per; // slices of k, blocks of 128 rows in one
@@ -190,54 +193,65 @@ __global__ __launch_bounds__(64 * T::WK) void int4_gemm_kernel(I4Params P) {
     }
 }
 
-// More rows: a work-group takes 16 MB rows and 16 WN NB columns, and X and the weight
-// come through an LDS ring of three stages by direct-to-LDS loads, two stages ahead, so
-// that the WN waves beside each other share X.  A stage is WK blocks of 128 rows, one
-// for each of the WK waves along k.  X takes 256 bytes a row and block; piece 4j + g
+// More rows: a work-group takes 16 WM MB rows and 16 WN NB columns, and X and the weight
+// come through an LDS ring of two or three stages by direct-to-LDS loads, so that the WN
+// waves beside each other share X and the WM waves the weight.  A stage is WK blocks of
+// 128 rows of the weight, one for each of the WK waves along k.  X takes 256 bytes a row and block; piece 4j + g
 // (16 bytes: what lane group g reads in step j) of row i sits at place (4j + g) ^ (i mod
 // 16), which puts the 16 lanes that a 16-byte read serves together on different banks.
-template <int MB_, int NB_, int WN_, int WK_, int STEPS_>
+// The shapes for up to 64 rows (WM = 1) form S beside the product and leave alpha S B to
+// the finishing launch; the others are given S and add alpha S B themselves, where k is
+// not split.
+template <int MB_, int NB_, int WM_, int WN_, int WK_, int STEPS_>
 struct I4Ring {
-    static constexpr int MB = MB_, NB = NB_, WN = WN_, WK = WK_, STEPS = STEPS_;
-    static constexpr int NW = WN * WK, G = WN * NB, TN = 16 * G, GR = 4 / STEPS;
-    static constexpr int XU = 4 * MB * WK, WU = G * WK, SU = (G * WK * GR + 15) / 16;  // 1 KiB loads of a stage
+    static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, WK = WK_, STEPS = STEPS_;
+    static constexpr bool RIDE = WM == 1;
+    static constexpr int NW = WM * WN * WK, G = WN * NB, TM = 16 * WM * MB, TN = 16 * G, GR = 4 / STEPS;
+    static constexpr int XU = 4 * WM * MB * WK, WU = G * WK, SU = (G * WK * GR + 15) / 16;  // 1 KiB loads of a stage
     static constexpr int XPW = (XU + NW - 1) / NW, WPW = (WU + NW - 1) / NW, SPW = (SU + NW - 1) / NW, UPW = XPW + WPW + SPW;
     static constexpr int XB = XU * 1024, WB = WU * 1024, STAGE = XB + WB + SU * 1024;
     static constexpr int NS = 3 * STAGE + 1024 <= 160 * 1024 ? 3 : 2;  // stages of the ring
     static constexpr int SPARE = NS * STAGE;  // 1 KiB that surplus loads fill with zeros
     static constexpr int RT = MB * 2 <= NW ? 2 : 1;
-    static constexpr int RED = WK * WN * MB * NB * 1024, JOB = NW * MB * RT * 1024;
+    static constexpr int RED = WK > 1 ? WK * WN * MB * NB * 1024 : 0, JOB = RIDE ? NW * MB * RT * 1024 : 0;
     static constexpr int MOST = RED > JOB ? RED : JOB;
     static constexpr int LDS = SPARE + 1024 > MOST ? SPARE + 1024 : MOST;
-    static_assert(NW % 4 == 0 && LDS <= 160 * 1024, "tile does not fit");
+    static_assert(NW % 4 == 0 && LDS <= 160 * 1024 && (RIDE || WK == 1), "tile does not fit");
 };
 
 template <class T>
 __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
-    constexpr int MB = T::MB, NB = T::NB, WN = T::WN, WK = T::WK, STEPS = T::STEPS, GR = T::GR, NW = T::NW, G = T::G;
+    constexpr int MB = T::MB, NB = T::NB, WM = T::WM, WN = T::WN, WK = T::WK, STEPS = T::STEPS, GR = T::GR, NW = T::NW, G = T::G;
+    constexpr int XT = 4 * WM * MB;  // units of X of a block
     extern __shared__ uint4 i4_smem[];
     lds_char *smem = (lds_char *)i4_smem;
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
     const int lane = threadIdx.x & 63, l16 = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int wk = wave % WK, wn = wave / WK;
+    const int wk = wave % WK, wn = wave / WK % WN, wm = wave / (WK * WN);
     int id = blockIdx.x;
-    if (id < P.jobs) return s_job<NW, MB, T::RT>(P, id, i4_smem);
-    id = xcd_order(id - P.jobs, P.tiles_n * P.KS);
-    int tn = id, ks = 0;
-    if (P.KS > 1) ks = id / P.tiles_n, tn = id - ks * P.tiles_n;
+    if constexpr (T::RIDE) {
+        if (id < P.jobs) return s_job<NW, MB, T::RT>(P, id, i4_smem);
+        id -= P.jobs;
+    }
+    // (row tiles innermost: a weight tile is fetched into one L2 once)
+    id = xcd_order(id, P.tiles_m * P.tiles_n * P.KS);
+    int tm = 0, tn = id, ks = 0;
+    if (P.tiles_m > 1) tn = id / P.tiles_m, tm = id - tn * P.tiles_m;
+    if (P.KS > 1) ks = tn / P.tiles_n, tn -= ks * P.tiles_n;
+    const int m0 = tm * T::TM, rows = min(P.M - m0, T::TM);
     const int c0 = tn * G, t0 = ks * P.per, t1 = min(P.K128, t0 + P.per);
     const int nit = (t1 - t0 + WK - 1) / WK;
 
     // the host keeps every offset below 2^31
     const uint32_t row_bytes = (uint32_t)P.K * 2u, code_bytes = (uint32_t)P.K128 * 1024u, scale_bytes = (uint32_t)P.G * 64u;
     const uint32_t ng = (uint32_t)min(P.N16 - c0, G);
-    const sgpr4_t dX = make_desc(P.X, (uint32_t)P.M * row_bytes);
+    const sgpr4_t dX = make_desc(P.X + (size_t)m0 * P.K, (uint32_t)rows * row_bytes);
     const sgpr4_t dW = make_desc((const char *)P.codes + (size_t)c0 * code_bytes, ng * code_bytes);
     const sgpr4_t dS = make_desc((const char *)P.scales + (size_t)c0 * scale_bytes, ng * scale_bytes);
 
-    // This wave's loads of a stage.  Unit u of X: rows 4 (u mod 4 MB) .. +3 of block
-    // u / 4 MB of the stage; of codes: column group u mod G, block u / G; of scales: 16
+    // This wave's loads of a stage.  Unit u of X: rows 4 (u mod XT) .. +3 of block
+    // u / XT of the stage; of codes: column group u mod G, block u / G; of scales: 16
     // pieces q of 64 bytes, column group q mod G, block q / G / GR, group q / G mod GR of
     // the block.  xo, wo, so: byte offsets at stage 0 (kOOB: zeros); a lane's k of X is xk
     // in every unit of a wave (4 divides NW), counted from its block.
@@ -246,8 +260,8 @@ __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
     int st[T::SPW];
 #pragma unroll
     for (int i = 0; i < T::XPW; ++i) {
-        const int u = wave + NW * i, row = u % (4 * MB) * 4 + lg;
-        xo[i] = u < T::XU && row < P.M ? (uint32_t)row * row_bytes + (uint32_t)(128 * (t0 + u / (4 * MB)) + xk) * 2u : kOOB;
+        const int u = wave + NW * i, row = u % XT * 4 + lg;
+        xo[i] = u < T::XU && row < rows ? (uint32_t)row * row_bytes + (uint32_t)(128 * (t0 + u / XT) + xk) * 2u : kOOB;
     }
 #pragma unroll
     for (int i = 0; i < T::WPW; ++i) {
@@ -265,7 +279,7 @@ __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
         const int dt = it * WK;
         if (i < T::XPW) {
             const int u = wave + NW * i;
-            dma16_at(dX, xk < kend - 128 * (t0 + dt + u / (4 * MB)) ? xo[i] : kOOB, (uint32_t)dt * 256u,
+            dma16_at(dX, xk < kend - 128 * (t0 + dt + u / XT) ? xo[i] : kOOB, (uint32_t)dt * 256u,
                      T::XU % NW == 0 || u < T::XU ? base + (uint32_t)(NW * i) * 1024u : spare);
         } else if (i < T::XPW + T::WPW) {
             const int j = i - T::XPW, u = wave + NW * j;
@@ -298,7 +312,7 @@ __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
     // x[j % 2] holds X's rows of step j, q the wave's codes of the stage
     uint4 x[2][MB], q[NB];
     auto read_x = [&](int buf, int j, int a) {
-        x[j & 1][a] = *(const uint4 *)(smem + buf * T::STAGE + (wk * MB + a) * 4096 + l16 * 256 + (((4 * j + lg) ^ l16) << 4));
+        x[j & 1][a] = *(const uint4 *)(smem + buf * T::STAGE + (wk * WM * MB + wm * MB + a) * 4096 + l16 * 256 + (((4 * j + lg) ^ l16) << 4));
     };
     auto read_w = [&](int buf) {
         const lds_char *sw = smem + buf * T::STAGE + T::XB + (wk * G + wn * NB) * 1024 + lane * 16;
@@ -387,33 +401,76 @@ __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
         buf = next;
     }
     wait_vmcnt<0>();  // (the last loads fill zeros: nothing may land in the space used below)
-    __syncthreads();
-
-    // the waves along k, in wave order
-    f32x4_t *red = (f32x4_t *)i4_smem;
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) red[((wk * WN + wn) * MB * NB + a * NB + b) * 64 + lane] = total[a][b];
-    __syncthreads();
-    for (int q = wave; q < WN * MB * NB; q += NW) {
-        const int a = q / NB % MB, b = q % NB, n = q / (MB * NB);
-        f32x4_t v = red[q * 64 + lane];
-#pragma unroll
-        for (int c = 1; c < WK; ++c) v += red[(c * WN * MB * NB + q) * 64 + lane];
-        const int row = 16 * a + l16, col = (c0 + n * NB + b) * 16 + 4 * lg;
-        if (row >= P.M || col >= P.N) continue;
+    const auto store = [&](int row, int col, f32x4_t v) {  // lane (g, l): columns 4g .. 4g+3 of row l
+        if (row >= rows || col >= P.N) return;
         if (P.part != nullptr)
-            *(f32x4_t *)(P.part + ((size_t)ks * P.M + row) * P.N + col) = v;
+            *(f32x4_t *)(P.part + ((size_t)ks * P.M + m0 + row) * P.N + col) = v;
         else
-            *(uint2 *)(P.Y + (size_t)row * P.N + col) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            *(uint2 *)(P.Y + (size_t)(m0 + row) * P.N + col) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    };
+    if constexpr (WK > 1) {
+        // the waves along k, in wave order
+        __syncthreads();
+        f32x4_t *red = (f32x4_t *)i4_smem;
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) red[((wk * WN + wn) * MB * NB + a * NB + b) * 64 + lane] = total[a][b];
+        __syncthreads();
+        for (int q = wave; q < WN * MB * NB; q += NW) {
+            const int a = q / NB % MB, b = q % NB, n = q / (MB * NB);
+            f32x4_t v = red[q * 64 + lane];
+#pragma unroll
+            for (int c = 1; c < WK; ++c) v += red[(c * WN * MB * NB + q) * 64 + lane];
+            store(16 * a + l16, (c0 + n * NB + b) * 16 + 4 * lg, v);
+        }
+    } else {
+        // alpha S B: ranks 32 a step, alpha S split into bf16 hi + lo
+        if (!T::RIDE && P.S != nullptr) {
+            const __amdgpu_buffer_rsrc_t rS = make_rsrc(P.S + (size_t)m0 * P.r, (uint64_t)rows * P.r * 4u);
+            const __amdgpu_buffer_rsrc_t rB = make_rsrc(P.B, (uint64_t)P.r * P.N * 2u);
+#pragma unroll 1
+            for (int r0 = 0; r0 < P.r; r0 += 32) {
+                const int rb = r0 + 8 * lg;
+                uint4 hi[MB], lo[MB];
+#pragma unroll
+                for (int a = 0; a < MB; ++a) {
+                    const uint32_t row = (uint32_t)((wm * MB + a) * 16 + l16);  // past the last row: past the resource
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = P.alpha * __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                             rS, rb + e < P.r ? (row * (uint32_t)P.r + (uint32_t)(rb + e)) * 4u : kOOB, 0, 0));
+                    split_frag(v, hi[a], lo[a]);
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int col = (c0 + wn * NB + b) * 16 + l16;
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        h[e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
+                            rB, rb + e < P.r && col < P.N ? ((uint32_t)(rb + e) * (uint32_t)P.N + (uint32_t)col) * 2u : kOOB, 0, 0);
+                    const uint4 w = make_uint4(pack2(h[0], h[1]), pack2(h[2], h[3]), pack2(h[4], h[5]), pack2(h[6], h[7]));
+#pragma unroll
+                    for (int a = 0; a < MB; ++a) {
+                        total[a][b] = mfma16x16x32(w, hi[a], total[a][b]);
+                        total[a][b] = mfma16x16x32(w, lo[a], total[a][b]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) store((wm * MB + a) * 16 + l16, (c0 + wn * NB + b) * 16 + 4 * lg, total[a][b]);
     }
 }
 
 template <class T, bool RING>
 hipError_t launch_t(const I4Params &P, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const dim3 grid((unsigned)(P.tiles_n * P.KS + P.jobs));
+    const dim3 grid((unsigned)(P.tiles_m * P.tiles_n * P.KS + P.jobs));
     if constexpr (RING) {
         const hipError_t e = allow_lds((const void *)int4_ring_kernel<T>, T::LDS, done);
         if (e != hipSuccess) return e;
@@ -442,51 +499,63 @@ constexpr I4Kind direct(const char *name, float stage, float row, int share) {
     return I4Kind{name, {launch_t<I4Tile<MB, NB, WK, 1>, false>, launch_t<I4Tile<MB, NB, WK, 2>, false>, launch_t<T, false>}, 16 * MB,
                   16 * NB, WK, 16 * T::RT, stage, row, share};
 }
-template <int MB, int NB, int WN, int WK>
+template <int MB, int NB, int WM, int WN, int WK>
 constexpr I4Kind ring(const char *name, float stage, int share) {
-    using T = I4Ring<MB, NB, WN, WK, 4>;
-    return I4Kind{name, {launch_t<I4Ring<MB, NB, WN, WK, 1>, true>, launch_t<I4Ring<MB, NB, WN, WK, 2>, true>, launch_t<T, true>}, 16 * MB,
-                  T::TN, WK, 16 * T::RT, stage, 0.f, share};
+    using T = I4Ring<MB, NB, WM, WN, WK, 4>;
+    return I4Kind{name, {launch_t<I4Ring<MB, NB, WM, WN, WK, 1>, true>, launch_t<I4Ring<MB, NB, WM, WN, WK, 2>, true>, launch_t<T, true>},
+                  T::TM, T::TN, WK, T::RIDE ? 16 * T::RT : 0, stage, 0.f, share};
 }
 const I4Kind kKinds[] = {
     direct<1, 1, 8>("int4_gemm 16x16", 0.80f, 0.07f, 2),
     direct<1, 2, 8>("int4_gemm 16x32", 1.30f, 0.06f, 2),
-    ring<1, 1, 2, 4>("int4_ring 16x32", 0.43f, 2),
-    ring<1, 2, 4, 2>("int4_ring 16x128", 0.60f, 1),
-    ring<2, 1, 2, 4>("int4_ring 32x32", 0.62f, 1),
-    ring<2, 2, 2, 4>("int4_ring 32x64", 0.97f, 1),
-    ring<3, 1, 2, 4>("int4_ring 48x32", 0.86f, 1),
-    ring<3, 2, 2, 4>("int4_ring 48x64", 1.31f, 1),
-    ring<4, 1, 4, 2>("int4_ring 64x64", 0.98f, 1),
-    ring<4, 2, 4, 2>("int4_ring 64x128", 1.45f, 1),
+    ring<1, 1, 1, 2, 4>("int4_ring 16x32", 0.43f, 2),
+    ring<1, 2, 1, 4, 2>("int4_ring 16x128", 0.60f, 1),
+    ring<2, 1, 1, 2, 4>("int4_ring 32x32", 0.62f, 1),
+    ring<2, 2, 1, 2, 4>("int4_ring 32x64", 0.97f, 1),
+    ring<3, 1, 1, 2, 4>("int4_ring 48x32", 0.86f, 1),
+    ring<3, 2, 1, 2, 4>("int4_ring 48x64", 1.31f, 1),
+    ring<4, 1, 1, 4, 2>("int4_ring 64x64", 0.98f, 1),
+    ring<4, 2, 1, 4, 2>("int4_ring 64x128", 1.45f, 1),
+    ring<4, 1, 2, 4, 1>("int4_ring 128x64", 0.92f, 1),
+    ring<4, 2, 2, 4, 1>("int4_ring 128x128", 1.30f, 1),
 };
 
 }  // namespace
 
-// The cheapest of the tile shapes, with k split as far as pays, by a model of their
-// times: 4.2 us, rounds of work-groups (stages x stage time each, and at least their
-// share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); the work-groups that
-// form S 0.8 us, 5 where they keep some of the product's from starting; a finishing
-// launch 3.5 us, 0.25 a slice more, and its partial sums at 5 TB/s.
+// The cheapest of the tile shapes, with k split as far as pays, and for more than 64 rows
+// of expanding the weight for the bf16 product (kind 0), by a model of their times:
+//   shape:  4.2 us, rounds of work-groups (stages x stage time each, and at least their
+//           share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); the
+//           work-groups that form S 0.8 us, 5 where they keep some of the product's from
+//           starting; a finishing launch 3.5 us, 0.25 a slice more, and its partial sums
+//           at 5 TB/s
+//   expand: expanded_us (S is formed apart either way)
 // Measured in a graph, groups of 128, model in brackets: 1 x 4096 x 14336 9.8 us (9.9),
 // 1 x 8192 x 28672 25.2 (26.9), 32 x 4096 x 14336 12.3 (11.6), 48 x 14336 x 4096 18.4
-// (17.7), 64 x 4096 x 14336 19.9 (19.1), 33 x 28672 x 8192 44.3 (44.9).
+// (17.7), 64 x 4096 x 14336 19.9 (19.1), 33 x 28672 x 8192 44.3 (44.9), 100 x 4096 x 4096
+// 18.1 (18.0; expanded 83), 256 x 4096 x 14336 46 (46; expanded 108), 1000 x 14336 x 4096
+// 144 (150; expanded 277), 2000 x 4096 x 4096 expanded 86 (84; packed 90).
+// More rows than these shapes serve are left to the expansion because a work-group that
+// unpacks for itself spends as long on that and on scaling as on its MFMAs: 128 x 256
+// tiles 86 us at 2000 x 4096 x 4096 and 344 at 8192 x 4096 x 4096 (expanded 201).
 static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
     I4Plan best{};
     // (offsets into X and a tile's codes stay below 2^31, and counts within an int)
-    if (m <= 0 || m > kI4Rows || k > (1 << 20) || n > (1 << 24)) return best;
+    if (m <= 0 || m > (1 << 19) || k > (1 << 20) || n > (1 << 24)) return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t k128 = cdiv(k, 128);
     const double bytes = (double)k * n * (0.5 + 4.0 / (double)std::min<int64_t>(group, 128));
-    double least = 1e30;
+    double least = m <= kI4Rows ? 1e30 : expanded_us(m, n, k, (double)k * n);
     for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
         const I4Kind &K = kKinds[kind - 1];
-        if (m > K.tm || (m <= 16 && K.tm > 16)) continue;
+        const bool wide = K.ranks == 0;
+        if (wide != (m > kI4Rows) || (!wide && m > K.tm) || (m <= 16 && K.tm > 16)) continue;
         I4Plan p{};
         p.kind = kind;
+        p.tiles_m = (int)cdiv(m, K.tm);
         p.tiles_n = (int)cdiv(n, K.tn);
         const int64_t stages = cdiv(k128, K.step);
-        if (r > 0) {
+        if (r > 0 && !wide) {
             const int64_t jobs = cdiv(k, kSK) * cdiv(r, K.ranks) * std::max(nseg, 1);
             if (nseg == 0 || jobs <= 1024) {
                 p.SK = (int)cdiv(k, kSK);
@@ -499,9 +568,9 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             p.KS = (int)cdiv(stages, per);
             if (p.KS != want) continue;
             p.per = (int)(per * K.step);
-            p.finish = p.KS > 1 || r > 0;
+            p.finish = p.KS > 1 || (r > 0 && (!wide || nseg > 0));
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
-            const int64_t groups = (int64_t)p.tiles_n * p.KS, slots = 256 * K.share;
+            const int64_t groups = (int64_t)p.tiles_m * p.tiles_n * p.KS, slots = 256 * K.share;
             if (groups > (1 << 24)) continue;
             const double one = (double)per * (K.stage + K.row * (double)m), each = bytes / 5.5e6 / (double)groups;
             const int64_t full = groups / slots, rest = groups % slots;
@@ -533,7 +602,7 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
     P.X = (const uint16_t *)X;
     P.M = m;
     P.K = k;
-    P.tiles_m = 1;
+    P.tiles_m = pl.tiles_m;
     P.A = (const uint16_t *)src.A;
     P.r = src.r;
     P.spart = spart;
@@ -562,6 +631,11 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
     P.KS = pl.KS;
     P.per = pl.per;
     P.jobs = pl.jobs;
+    if (!pl.finish && src.r > 0) {  // (the plan has S formed before)
+        P.S = S;
+        P.B = (const uint16_t *)src.B;
+        P.alpha = src.alpha;
+    }
     const I4Kind &K = kKinds[pl.kind - 1];
     const int slot = prof_begin(K.name, stream);
     const hipError_t e = K.launch[group == 32 ? 0 : group == 64 ? 1 : 2](P, stream);

@@ -309,7 +309,7 @@ hipError_t launch_int4_dequantize(const void *codes, const void *scales, int64_t
 
 // Y = X W' (+ alpha S B) straight from the packed weight (mxfp4_gemm.hip).
 struct MxGemmPlan {
-    int kind;  // tile shape; 0: not for this shape
+    int kind;  // tile shape; 0: expand the weight, or the shape is too large
     int tiles_m, tiles_n, KS, per;
     bool finish;           // a second launch adds partial sums and the LoRA term
     size_t part_bytes;     // fp32 partial sums of the k slices
@@ -329,12 +329,13 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
                              int n, const AdapterSource &src, const MxDropout &drop, float *S, void *Y, float *part,
                              float *spart, hipStream_t stream);
 
-// Y = X W' (+ alpha S B) for up to kI4Rows rows, W' in 4-bit integers (int4_gemm.hip).
+// Y = X W' (+ alpha S B) straight from a weight of 4-bit integers (int4_gemm.hip): always
+// for up to kI4Rows rows, for more where that is faster than expanding it.
 // SK > 0: the product's launch also forms S and drop.keep, in SK partial sums.
 constexpr int kI4Rows = 64;
 struct I4Plan {
     int kind;  // tile shape; 0: not for this shape
-    int tiles_n, KS, per;
+    int tiles_m, tiles_n, KS, per;
     bool finish;        // a second launch adds partial sums and the LoRA term
     size_t part_bytes;
     int SK, jobs;       // partial sums of S, and the work-groups that form them

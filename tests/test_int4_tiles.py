@@ -19,13 +19,15 @@ from test_int4 import case, f64, near, product, reference
 
 # m, k, n, the tile, and whether the contraction is split
 SHAPES = [
-    (1, 136, 72, "int4_gemm 16x16", False), (3, 8200, 72, "int4_gemm 16x16", True), (1, 520, 8200, "int4_gemm 16x32", False),
+    (1, 136, 72, "int4_gemm 16x16", False), (3, 16392, 72, "int4_gemm 16x16", True), (1, 520, 8200, "int4_gemm 16x32", False),
     (3, 3000, 8200, "int4_gemm 16x32", False), (11, 136, 72, "int4_ring 16x32", False), (15, 8200, 72, "int4_ring 16x32", True),
-    (1, 136, 16392, "int4_ring 16x128", False), (20, 136, 72, "int4_ring 32x32", False), (27, 4104, 72, "int4_ring 32x32", True),
-    (20, 136, 8200, "int4_ring 32x64", False), (29, 4104, 1032, "int4_ring 32x64", True), (33, 136, 72, "int4_ring 48x32", False),
-    (47, 4104, 72, "int4_ring 48x32", True), (33, 520, 8200, "int4_ring 48x64", False), (45, 4104, 1032, "int4_ring 48x64", True),
-    (50, 136, 72, "int4_ring 64x64", False), (63, 1032, 72, "int4_ring 64x64", True), (20, 136, 16392, "int4_ring 64x128", False),
-    (55, 2056, 2056, "int4_ring 64x128", True),
+    (1, 136, 16392, "int4_ring 16x128", False), (20, 136, 72, "int4_ring 32x32", False), (27, 8200, 72, "int4_ring 32x32", True),
+    (20, 136, 8200, "int4_ring 32x64", False), (29, 14344, 2056, "int4_ring 32x64", True), (33, 136, 72, "int4_ring 48x32", False),
+    (47, 4104, 72, "int4_ring 48x32", True), (33, 520, 8200, "int4_ring 48x64", False), (45, 14344, 2056, "int4_ring 48x64", True),
+    (50, 136, 72, "int4_ring 64x64", False), (55, 2056, 2056, "int4_ring 64x64", True), (20, 136, 16392, "int4_ring 64x128", False),
+    (55, 4104, 6152, "int4_ring 64x128", True),
+    (65, 136, 72, "int4_ring 128x64", False), (141, 4104, 136, "int4_ring 128x64", True), (385, 520, 4104, "int4_ring 128x128", False),
+    (141, 4104, 2056, "int4_ring 128x128", True),
 ]
 
 
@@ -79,7 +81,7 @@ def test_layer(at, r, p):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m", [1, 2, 9, 16, 17, 31, 48, 64])
+@pytest.mark.parametrize("m", [1, 2, 9, 16, 17, 31, 48, 64, 100, 300])
 @pytest.mark.parametrize("nseg", [1, 5, 70, 400])
 def test_segments(m, nseg):
     # more segments than rows (most are empty), more than the product's launch forms S for, an adapter with rank 256
