@@ -1433,7 +1433,9 @@ __global__ __launch_bounds__(256) void b2s_kernel(B2Params P) {
 // X may be saved in 8 bits (X8: mxint8_kernels.hip describes the format): a sub-block is
 // then 32 x 256 bytes of codes and 256 bytes of scales, an 8-bit transposing LDS read
 // hands a lane eight rows of its column, and the codes times their rows' scales become
-// the bf16 operand that the expanded input would be, bit for bit.  X8_FIGURES
+// the bf16 operand that the expanded input would be, bit for bit.  8192 x 4096, rank 16:
+// 20 us, where expanding the input first took 23 for this pass and 18 for the expansion;
+// 8192 x 8192, 8 adapters of rank 128 at most: 52 us (52 and 34).
 struct B2WParams {
     const void *X;          // bf16, or codes
     const uint8_t *xscales; // X8

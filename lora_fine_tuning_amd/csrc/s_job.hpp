@@ -29,9 +29,9 @@ struct SJobParams {
 
 // One work-group's share of keep.X A: 1024 of k (split over its NW waves), up to
 // 16 MB rows of one adapter and 16 RT ranks.  X's rows come straight from memory, A's as
-// 16 ranks of 32 rows a load, turned through 1 KiB of LDS (with 8 two-byte loads for an
-// operand instead, a job of 16 ranks took 7 us where this takes S_JOB_US); every load of
-// a wave before its first use; the waves are added in LDS in wave order.
+// 16 ranks of 32 rows a load, turned through 1 KiB of LDS (the layer of 1 row, 4096 x 4096
+// in 4 bits, rank 16: 9.2 us in a graph, 10.1 with 8 two-byte loads for an operand); every
+// load of a wave before its first use; the waves are added in LDS in wave order.
 // A lane's 8 elements of X are one counter of the dropout mask and one byte of
 // keep, which the first rank tile's work-groups write.  `smem`: NW MB RT KiB.
 template <int NW, int MB, int RT>
