@@ -227,7 +227,8 @@ class LoraLinear(torch.nn.Module):
         self.offset = 0  # next unused dropout counter (a multiple of 8)
 
     def forward(self, X: torch.Tensor, X8=None) -> torch.Tensor:
-        if X8 is None and self.save_bits == 8 and torch.is_grad_enabled():
+        wanted = X.requires_grad or self.A.requires_grad or self.B.requires_grad
+        if X8 is None and self.save_bits == 8 and wanted and torch.is_grad_enabled():
             X8 = mxint8.lora_mxint8_quantize(X.detach().reshape(-1, X.shape[-1]).contiguous())
         p = self.p if self.training else 0.0
         offset = self.offset
