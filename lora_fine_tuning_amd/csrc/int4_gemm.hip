@@ -526,7 +526,7 @@ const I4Kind kKinds[] = {
 // of expanding the weight for the bf16 product (kind 0), by a model of their times:
 //   shape:  4.2 us, rounds of work-groups (stages x stage time each, and at least their
 //           share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); the
-//           work-groups that form S 0.8 us, 5 where they keep some of the product's from
+//           work-groups that form S 0.8 us, 7 where they keep some of the product's from
 //           starting; a finishing launch 3.5 us, 0.25 a slice more, and its partial sums
 //           at 5 TB/s
 //   expand: expanded_us (S is formed apart either way)
@@ -579,7 +579,7 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             const double least_part = K.row > 0.f ? 0.45 : 0.95;
             if (rest > 0) t += std::max(one * std::max(least_part, (double)rest / (double)slots), each * (double)rest);
             t += 0.7 * (double)(full + (rest > 0) - 1);
-            if (p.jobs > 0) t += rest + p.jobs > slots ? 5.0 : 0.8;
+            if (p.jobs > 0) t += rest + p.jobs > slots ? 7.0 : 0.8;
             if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 5e6 + 0.25 * (p.KS - 1);
             if (t < least) {
                 least = t;

@@ -73,8 +73,9 @@ def _matrix(t, name: str):
 
 def _out(t, shape, dtype, name: str, dev):
     if t is None:
-        if len(shape) == 2:  # (with strides the call takes 1.0 us, without 1.4)
-            return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=dev)
+        if len(shape) < 4:  # (with strides the call takes 1.0 us, without 1.4)
+            strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+            return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
         return torch.empty(shape, dtype=dtype, device=dev)
     _need_on(t, shape, dtype, name, dev)
     return t
