@@ -384,12 +384,12 @@ lora_status backward_low_rank_only(const void *dY, const LayerInput &X, const Ad
 
 lora_status linear_backward(const void *dY, const LayerInput &X, const void *W, const AdapterSource &src, const float *S,
                             const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace, hipStream_t stream) {
-    const BwdPlan pl = plan_bwd(m, k, n, src.r, false, 0, 1);
-    CHECK(backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, src.r, src.p, workspace, stream));
+    const BwdPlan pl = plan_bwd(m, k, n, src.r_cap, false, 0, 1);
+    CHECK(backward_low_rank(pl, dY, X, src, S, keep_bits, m, k, n, src.r_cap, src.p, workspace, stream));
     const float *dS = (const float *)ws_at(workspace, pl.off_ds);
     const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
     if (m > 0 && dX != nullptr)
-        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r, src.p == 0.0f ? nullptr : keep_bits,
+        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r_cap, src.p == 0.0f ? nullptr : keep_bits,
                            (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
     return LORA_OK;
 }

@@ -1423,7 +1423,7 @@ hipError_t launch_gemm(bool nn, int epi, const void *Arow, const void *Bcol, voi
     P.keep = keep;
     P.KW = KW;
     P.ext = (const uint16_t *)(epi == 1 ? src.B : src.A);
-    P.ext_r = src.r;
+    P.ext_r = epi == 1 ? src.r : src.a_r;
     P.ext_scale = epi == 1 ? src.alpha : drop_scale(src.p);
     P.adapters = src.table;
     P.num_adapters = src.num_adapters;

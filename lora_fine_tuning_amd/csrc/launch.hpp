@@ -73,6 +73,7 @@ struct AdapterSource {
     void *dA;
     void *dB;
     int32_t r;
+    int32_t a_r;  // values of a row of A: r, or more with zeros past r (read by the dX product alone)
     float alpha;
     float p;
     // multi adapter (table != nullptr)
@@ -97,7 +98,7 @@ inline AdapterSource single_source(const void *A, const void *B, void *dA, void 
     s.B = B;
     s.dA = dA;
     s.dB = dB;
-    s.r = r;
+    s.r = s.a_r = r;
     s.alpha = alpha;
     s.p = p;
     s.table = nullptr;
@@ -119,7 +120,7 @@ inline AdapterSource multi_source(const lora_adapter *adapters, int32_t nad, con
 }
 
 // The input that a backward reads: bf16, or 8-bit codes with their scales (only where
-// b2w_ok holds for the rank).
+// b2w_ok holds for the rank and the rows of S).
 struct LayerInput {
     const void *x;
     const void *scales;  // NULL: bf16
@@ -297,6 +298,10 @@ hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_
 // Inputs saved in 8 bits (mxint8_kernels.hip).
 hipError_t launch_mxint8_quantize(const void *X, int64_t m, int64_t k, void *codes, void *scales, hipStream_t stream);
 hipError_t launch_mxint8_dequantize(const void *codes, const void *scales, int64_t m, int64_t k, void *X, hipStream_t stream);
+// S (m x r fp32) and A (k x r bf16, k = 0: not) with rows of `row` (a multiple of 4) values, zeros
+// past r; the outputs 16-byte aligned.
+hipError_t launch_widen_rows(const float *S, int64_t m, const void *A, int64_t k, int r, int row, float *S_out, void *A_out,
+                             hipStream_t stream);
 
 // Weights as 4-bit integers in groups of rows (int4_kernels.hip).  scale_type of
 // given scales: 0 fp32, 1 bf16, 2 fp16; zeros may be NULL (all 8).

@@ -167,7 +167,7 @@ namespace lora {
 lora_status mxfp4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, const AdapterSource &src,
                                   const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n, void *dX, void *workspace,
                                   hipStream_t stream) {
-    const int32_t r = src.r;
+    const int32_t r = src.r_cap;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
     if (pl.kind) {
         const float *dS = nullptr;

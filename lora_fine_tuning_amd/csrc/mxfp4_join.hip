@@ -298,7 +298,7 @@ hipError_t launch_mxfp4_join(bool up, const float *part, int KS, int m, int n, f
     P.SK = SK;
     P.spart = spart;
     P.R = (const uint16_t *)(up ? src.B : src.A);
-    P.r = src.r;
+    P.r = up ? src.r : src.a_r;
     P.scale = up ? src.alpha : drop_scale(src.p);
     P.adapters = src.table;
     P.seg_off = src.seg_off;

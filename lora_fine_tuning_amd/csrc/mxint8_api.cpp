@@ -39,11 +39,46 @@ extern "C" lora_status lora_mxint8_dequantize(const void *codes, const void *sca
     return LORA_OK;
 }
 
-// The dA pass reads the codes themselves where it takes all ranks at once (b2w_ok: ranks
-// up to 128, multiples of 4); for other ranks the input is expanded to bf16 first, at the
-// start of the workspace, the layer's own after it.
-static bool direct(int32_t r) { return b2w_ok((r + 15) / 16 * 16, r); }
-static size_t input_bytes(int64_t m, int64_t k, int32_t r) { return direct(r) ? 0 : align_up((size_t)m * (size_t)k * 2); }
+// The dA pass reads the codes themselves where it takes all ranks at once, up to 128; for
+// higher ranks the input is expanded to bf16 first.  The fast kernels of all passes read S,
+// dS and A in pieces of 8 ranks, so a rank that is no multiple of 8 gets copies of S and of
+// one adapter's A with rows as long as that takes (333 x 1032 x 776, rank 5: 69 us with the
+// input expanded and the general kernels, 60 so; 436 x 1328 x 2336, rank 113: 409 and 173).
+// All sit at the start of the workspace, the layer's own after them.
+static int32_t row_of(int32_t r) { return (r + 7) / 8 * 8; }
+struct InputPlan {
+    bool expand, widen;
+    size_t s_at, a_at, bytes;
+};
+static InputPlan input_plan(int64_t m, int64_t k, int32_t r, bool multi) {
+    InputPlan p{r > 128, row_of(r) != r, 0, 0, 0};
+    if (m == 0) return InputPlan{};
+    if (p.expand) p.bytes = align_up((size_t)m * (size_t)k * 2);
+    p.s_at = p.bytes;
+    if (p.widen) p.bytes += align_up((size_t)m * (size_t)row_of(r) * 4);
+    p.a_at = p.bytes;
+    if (p.widen && !multi) p.bytes += align_up((size_t)k * (size_t)row_of(r) * 2);
+    return p;
+}
+
+// The input, S and one adapter's A as the backward is to read them.
+static lora_status prepare(const InputPlan &pl, const void *x_codes, const void *x_scales, int64_t m, int64_t k, int32_t r, LayerInput &X,
+                           const float *&S, AdapterSource &src, void *workspace, hipStream_t stream) {
+    const bool multi = src.table != nullptr;
+    src.r_cap = row_of(r);
+    if (pl.expand) {
+        HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
+        X = LayerInput(workspace);
+    }
+    if (pl.widen) {
+        float *wide = (float *)ws_at(workspace, pl.s_at);
+        void *a = ws_at(workspace, pl.a_at);
+        HIPCHK(launch_widen_rows(S, m, src.A, multi ? 0 : k, r, row_of(r), wide, a, stream), "S and A copy launch");
+        S = wide;
+        if (!multi) src.A = a, src.a_r = row_of(r);
+    }
+    return LORA_OK;
+}
 
 static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
     return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && m * k < (1LL << 46) && k * n < (1LL << 46);
@@ -71,19 +106,19 @@ static lora_status check_rows(int64_t m, const void *dY, const float *S, const u
 
 extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r) {
     if (!sizes_ok(m, k, n) || r < 1 || r > 256) return 0;
-    const size_t layer = kind == LORA_WEIGHT_BF16    ? lora_linear_bwd_workspace_size(m, k, n, r)
-                         : kind == LORA_WEIGHT_MXFP4 ? lora_mxfp4_linear_bwd_workspace_size(m, k, n, r)
-                                                     : lora_int4_linear_bwd_workspace_size(m, k, n, group, r);
-    return input_bytes(m, k, r) + layer;
+    const size_t layer = kind == LORA_WEIGHT_BF16    ? lora_linear_bwd_workspace_size(m, k, n, row_of(r))
+                         : kind == LORA_WEIGHT_MXFP4 ? lora_mxfp4_linear_bwd_workspace_size(m, k, n, row_of(r))
+                                                     : lora_int4_linear_bwd_workspace_size(m, k, n, group, row_of(r));
+    return input_plan(m, k, r, false).bytes + layer;
 }
 
 extern "C" size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                        int32_t num_adapters, int32_t num_segments) {
     if (!sizes_ok(m, k, n) || r_max < 1 || r_max > 256 || num_adapters < 1 || num_segments < 0) return 0;
-    const size_t layer = kind == LORA_WEIGHT_BF16    ? multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
-                         : kind == LORA_WEIGHT_MXFP4 ? multi_lora_mxfp4_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments)
-                                                     : multi_lora_int4_bwd_workspace_size(m, k, n, group, r_max, num_adapters, num_segments);
-    return input_bytes(m, k, r_max) + layer;
+    const size_t layer = kind == LORA_WEIGHT_BF16    ? multi_lora_bwd_workspace_size(m, k, n, row_of(r_max), num_adapters, num_segments)
+                         : kind == LORA_WEIGHT_MXFP4 ? multi_lora_mxfp4_bwd_workspace_size(m, k, n, row_of(r_max), num_adapters, num_segments)
+                                                     : multi_lora_int4_bwd_workspace_size(m, k, n, group, row_of(r_max), num_adapters, num_segments);
+    return input_plan(m, k, r_max, true).bytes + layer;
 }
 
 // The layer's backward over a weight of any form, after the checks.
@@ -118,16 +153,14 @@ extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_code
     REQ_PTR(dA, 2);
     REQ_PTR(dB, 2);
     CHECK(check_rows(m, dY, S, keep_bits, p != 0.0f, dX));
-    const size_t need = lora_mxint8_linear_bwd_workspace_size(kind, group, m, k, n, r), w = input_bytes(m, k, r);
+    const size_t need = lora_mxint8_linear_bwd_workspace_size(kind, group, m, k, n, r);
     if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (need > 0) REQ_PTR(workspace, 16);
     LayerInput X(x_codes, x_scales);
-    if (w > 0) {
-        HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
-        X = LayerInput(workspace);
-    }
-    return layer_backward(false, kind, W, W_scales, group, dY, X, single_source(A, B, dA, dB, r, alpha, p), S, keep_bits, m, k, n, dX,
-                          ws_at(workspace, w), stream);
+    AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
+    const InputPlan pl = input_plan(m, k, r, false);
+    CHECK(prepare(pl, x_codes, x_scales, m, k, r, X, S, src, workspace, stream));
+    return layer_backward(false, kind, W, W_scales, group, dY, X, src, S, keep_bits, m, k, n, dX, ws_at(workspace, pl.bytes), stream);
 }
 
 extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind, const void *W,
@@ -144,15 +177,11 @@ extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *
                                 nullptr, nullptr, nullptr, 0, stream));
     CHECK(check_rows(m, dY, S, keep_bits, true, dX));
     const size_t need = multi_lora_mxint8_bwd_workspace_size(kind, group, m, k, n, r_max, num_adapters, num_segments);
-    const size_t w = input_bytes(m, k, r_max);
     if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (need > 0) REQ_PTR(workspace, 16);
     LayerInput X(x_codes, x_scales);
-    if (w > 0) {
-        HIPCHK(launch_mxint8_dequantize(x_codes, x_scales, m, k, workspace, stream), "MXINT8 dequantise launch");
-        X = LayerInput(workspace);
-    }
-    return layer_backward(true, kind, W, W_scales, group, dY, X,
-                          multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max), S, keep_bits, m, k, n, dX,
-                          ws_at(workspace, w), stream);
+    AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
+    const InputPlan pl = input_plan(m, k, r_max, true);
+    CHECK(prepare(pl, x_codes, x_scales, m, k, r_max, X, S, src, workspace, stream));
+    return layer_backward(true, kind, W, W_scales, group, dY, X, src, S, keep_bits, m, k, n, dX, ws_at(workspace, pl.bytes), stream);
 }

@@ -132,6 +132,25 @@ __global__ __launch_bounds__(256) void mxint8_dequantize_kernel(const uint8_t *c
     }
 }
 
+__global__ __launch_bounds__(256) void widen_rows_kernel(const float *S, int64_t m, const uint16_t *A, int64_t k, int r, int row,
+                                                         float *S_out, uint16_t *A_out) {
+    const int each = row / 4;
+    const int64_t total = (m + k) * each;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t y = i / each;
+        const int c = (int)(i - y * each) * 4;
+        if (y < m) {
+            const float *src = S + y * r + c;
+            ((float4 *)S_out)[i] =
+                make_float4(c < r ? src[0] : 0.f, c + 1 < r ? src[1] : 0.f, c + 2 < r ? src[2] : 0.f, c + 3 < r ? src[3] : 0.f);
+        } else {
+            const uint16_t *src = A + (y - m) * r + c;
+            const uint32_t v0 = c < r ? src[0] : 0u, v1 = c + 1 < r ? src[1] : 0u, v2 = c + 2 < r ? src[2] : 0u, v3 = c + 3 < r ? src[3] : 0u;
+            ((uint2 *)A_out)[i - m * each] = make_uint2(v0 | v1 << 16, v2 | v3 << 16);
+        }
+    }
+}
+
 I8Shape i8_shape(int64_t m, int64_t k) { return I8Shape{m, k, i8_blocks(k), (i8_blocks(k) * 32 + kWaveValues - 1) / kWaveValues}; }
 
 unsigned i8_grid(const I8Shape &s) { return (unsigned)std::min<int64_t>((s.m * s.chunks + 3) / 4, 1 << 20); }
@@ -152,6 +171,15 @@ hipError_t launch_mxint8_dequantize(const void *codes, const void *scales, int64
     const int slot = prof_begin("mxint8_dequantize", stream);
     hipLaunchKernelGGL(mxint8_dequantize_kernel, dim3(i8_grid(s)), dim3(256), 0, stream, (const uint8_t *)codes,
                        (const uint8_t *)scales, s, (uint16_t *)X);
+    prof_end(slot, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_widen_rows(const float *S, int64_t m, const void *A, int64_t k, int r, int row, float *S_out, void *A_out,
+                             hipStream_t stream) {
+    const unsigned grid = (unsigned)std::min<int64_t>(((m + k) * (row / 4) + 255) / 256, 1 << 20);
+    const int slot = prof_begin("widen_rows", stream);
+    hipLaunchKernelGGL(widen_rows_kernel, dim3(grid), dim3(256), 0, stream, S, m, (const uint16_t *)A, k, r, row, S_out, (uint16_t *)A_out);
     prof_end(slot, stream);
     return hipGetLastError();
 }

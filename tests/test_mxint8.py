@@ -4,9 +4,10 @@ The format's reference is written here from its definition, in 64 bits with nump
 
 Tolerances, derived: saving and reading back are exact (every value that codes and
 scales stand for is a bf16), so the backward from a saved input is the bf16 layer's
-over that input: where the same kernels run, bit for bit (dX and dB always do: they
-do not read the input), and otherwise within test_mxfp4.layer_reference's slack of
-the 64-bit formulas.
+over that input: where the same kernels run (ranks that are multiples of 8), bit for
+bit, and otherwise within test_mxfp4.layer_reference's slack of the 64-bit
+formulas.  dX and dB do not read the input: their formulas are those over X itself,
+which S is of.
 """
 import gc
 import os
@@ -279,7 +280,7 @@ BWD = [
     # m, k, n, r, p
     (1, 8, 8, 1, 0.0), (1, 136, 72, 8, 0.1), (5, 264, 136, 5, 0.3), (17, 1032, 264, 16, 0.0), (31, 128, 40, 13, 0.1), (33, 392, 136, 32, 0.2),
     (64, 2056, 72, 64, 0.1), (100, 520, 264, 48, 0.0), (257, 648, 136, 128, 0.1), (300, 264, 520, 100, 0.05), (333, 1032, 776, 5, 0.2),
-    (520, 400, 264, 130, 0.1), (40, 136, 72, 256, 0.0), (1030, 4104, 136, 16, 0.1), (2100, 2048, 72, 12, 0.0), (700, 8192, 40, 64, 0.1),
+    (436, 1328, 264, 113, 0.05), (90, 136, 72, 26, 0.0), (129, 264, 136, 127, 0.2), (520, 400, 264, 130, 0.1), (40, 136, 72, 256, 0.0), (1030, 4104, 136, 16, 0.1), (2100, 2048, 72, 12, 0.0), (700, 8192, 40, 64, 0.1),
 ]
 
 
@@ -300,8 +301,11 @@ def test_backward(at, form):
     rX, rA, rB = layer_bwd(W)(dY, Xr, W, A, B, S, keep, 2.0, p)
     torch.cuda.synchronize()
     assert (dXb[m:] == 5).all()
-    assert torch.equal(dX, rX) and torch.equal(dB, rB)
-    assert torch.equal(dA, rA)
+    if r % 8 == 0:
+        assert torch.equal(dX, rX) and torch.equal(dA, rA) and torch.equal(dB, rB)
+    want, slack = layer_reference(X.cpu(), f64(in_bf16(W)), A, B, dY.cpu(), 2.0, p, 7, 16)
+    near("dX", dX, want["dX"], slack["dX"])
+    near("dB", dB, want["dB"], slack["dB"])
     want, slack = layer_reference(Xr.cpu(), f64(in_bf16(W)), A, B, dY.cpu(), 2.0, p, 7, 16)
     near("dA", dA, want["dA"], slack["dA"])
     none, dA2, dB2 = lf.lora_mxint8_linear_bwd(dY, X8, W, A, B, S, keep, 2.0, p, want_dX=False)
@@ -311,7 +315,7 @@ def test_backward(at, form):
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", ["bf16", "mxfp4", "int4"])
 @pytest.mark.parametrize("m,k,n,nseg,r_max", [(1, 136, 72, 1, 8), (40, 1032, 264, 7, 16), (100, 264, 136, 60, 40), (600, 520, 136, 5, 128),
-                                              (300, 264, 72, 4, 13), (200, 392, 136, 9, 200), (2000, 2056, 72, 6, 64)])
+                                              (300, 264, 72, 4, 13), (150, 264, 136, 3, 93), (200, 392, 136, 9, 200), (2000, 2056, 72, 6, 64)])
 def test_mixed_backward(m, k, n, nseg, r_max, form):
     g = torch.Generator().manual_seed(m + nseg)
     W = weights(k, n, g)[["bf16", "mxfp4", "int4"].index(form)]
@@ -338,18 +342,23 @@ def test_mixed_backward(m, k, n, nseg, r_max, form):
         dX = call(dY, x, W, table, na, so, sa, S, keep, rm)
         torch.cuda.synchronize()
         outs.append((dX, *dAs, *dBs))
-    for i, (a, b) in enumerate(zip(*outs)):
-        assert torch.equal(a, b), i
+    if rm % 8 == 0:
+        for i, (a, b) in enumerate(zip(*outs)):
+            assert torch.equal(a, b), i
     assert not outs[0][na].any()  # the last adapter has no rows
     sums = {}
     for s, a in enumerate(seg_ad):
         lo, hi = seg_off[s], seg_off[s + 1]
         if hi > lo:
-            want, slack = layer_reference(Xr[lo:hi].cpu(), f64(in_bf16(W)), As[a], Bs[a], dY[lo:hi].cpu(), 0.5, ps[a], 3, 8 + lo * k)
-            w, e = sums.get(a, (0.0, 0.0))
-            sums[a] = w + want["dA"], e + slack["dA"] + (nseg + 1) * 2.0 ** -24 * np.abs(want["dA"])
-    for a, (w, e) in sums.items():
-        near(f"dA[{a}]", outs[0][1 + a], w, e)
+            want, slack = layer_reference(X[lo:hi].cpu(), f64(in_bf16(W)), As[a], Bs[a], dY[lo:hi].cpu(), 0.5, ps[a], 3, 8 + lo * k)
+            near(f"dX[{s}]", outs[0][0][lo:hi], want["dX"], slack["dX"])
+            saved, sslack = layer_reference(Xr[lo:hi].cpu(), f64(in_bf16(W)), As[a], Bs[a], dY[lo:hi].cpu(), 0.5, ps[a], 3, 8 + lo * k)
+            for at, w, e in ((1 + a, saved["dA"], sslack["dA"]), (1 + na + a, want["dB"], slack["dB"])):
+                # (the other segments' sums are added: their roundings and one more for each segment)
+                w0, e0 = sums.get(at, (0.0, 0.0))
+                sums[at] = w0 + w, e0 + e + (nseg + 1) * 2.0 ** -24 * np.abs(w)
+    for at, (w, e) in sums.items():
+        near(f"gradient {at}", outs[0][at], w, e)
 
 
 @pytest.mark.gpu
