@@ -37,6 +37,7 @@ struct I4Params : SJobParams {
     const float *S;       // the epilogue's LoRA term: M x r fp32 (nullptr: none)
     const uint16_t *B;    // r x N
     float alpha;
+    int s_wide;           // S may be read 16 bytes at a time
     int each;             // blocks of 128 rows that share a scale (groups of 128 rows or more),
     uint32_t each_inv;    // and floor(2^32 / each) + 1: block t's group is the product's high word
     int tiles_n, KS, per; // slices of k, blocks of 128 rows in one
@@ -436,11 +437,22 @@ __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
 #pragma unroll
                 for (int a = 0; a < MB; ++a) {
                     const uint32_t row = (uint32_t)((wm * MB + a) * 16 + l16);  // past the last row: past the resource
+                    const uint32_t at = (row * (uint32_t)P.r + (uint32_t)rb) * 4u;
                     float v[8];
+                    if (P.s_wide) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = P.alpha * __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                             rS, rb + e < P.r ? (row * (uint32_t)P.r + (uint32_t)(rb + e)) * 4u : kOOB, 0, 0));
+                        for (int e = 0; e < 8; e += 4) {
+                            const f32x4_t s = __builtin_bit_cast(
+                                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rS, rb + e < P.r ? at + 4u * e : kOOB, 0, 0));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[e + i] = P.alpha * s[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = P.alpha * __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                 rS, rb + e < P.r ? at + 4u * e : kOOB, 0, 0));
+                    }
                     split_frag(v, hi[a], lo[a]);
                 }
 #pragma unroll
@@ -484,47 +496,59 @@ hipError_t launch_t(const I4Params &P, hipStream_t stream) {
 }
 
 // Tile shapes, and what a call with one costs.  `stage` and `row`: microseconds that a
-// stage of WK blocks takes a work-group when `share` of them fill every CU, and what
-// each row adds to it (the direct shapes read X once a wave); group 128.
+// stage of WK blocks takes a work-group when `share` of them fill every CU, for groups
+// of 32, 64 and 128 rows or more (a group is closed in fp32: a multiply-add for the zero
+// and one for the scale), and what each row adds to it (the direct shapes read X once a
+// wave).
+using I4Launch = hipError_t (*)(const I4Params &, hipStream_t);
 struct I4Kind {
     const char *name;  // in the timing pool
-    hipError_t (*launch[3])(const I4Params &, hipStream_t);  // groups of 32, 64, 128 rows or more
+    I4Launch launch[3];  // groups of 32, 64, 128 rows or more (nullptr: not for these)
     int tm, tn, step, ranks;  // rows and columns of a tile, blocks of 128 rows of a stage, ranks of one job of S
-    float stage, row;
+    float stage[3], row;
     int share;
 };
-template <int MB, int NB, int WK>
-constexpr I4Kind direct(const char *name, float stage, float row, int share) {
-    using T = I4Tile<MB, NB, WK, 4>;
-    return I4Kind{name, {launch_t<I4Tile<MB, NB, WK, 1>, false>, launch_t<I4Tile<MB, NB, WK, 2>, false>, launch_t<T, false>}, 16 * MB,
-                  16 * NB, WK, 16 * T::RT, stage, row, share};
+template <class T, bool RING, bool USED>
+constexpr I4Launch launch_of() {
+    if constexpr (USED) return launch_t<T, RING>;
+    return nullptr;
 }
-template <int MB, int NB, int WM, int WN, int WK>
-constexpr I4Kind ring(const char *name, float stage, int share) {
+// LEAST: the smallest groups that a shape is for (of smaller ones others are faster).
+template <int MB, int NB, int WK, int LEAST>
+constexpr I4Kind direct(const char *name, float s32, float s64, float s128, float row, int share) {
+    using T = I4Tile<MB, NB, WK, 4>;
+    return I4Kind{name, {launch_of<I4Tile<MB, NB, WK, 1>, false, LEAST <= 32>(), launch_of<I4Tile<MB, NB, WK, 2>, false, LEAST <= 64>(),
+                         launch_t<T, false>}, 16 * MB, 16 * NB, WK, 16 * T::RT, {s32, s64, s128}, row, share};
+}
+template <int MB, int NB, int WM, int WN, int WK, int LEAST = 32>
+constexpr I4Kind ring(const char *name, float s32, float s64, float s128, int share) {
     using T = I4Ring<MB, NB, WM, WN, WK, 4>;
-    return I4Kind{name, {launch_t<I4Ring<MB, NB, WM, WN, WK, 1>, true>, launch_t<I4Ring<MB, NB, WM, WN, WK, 2>, true>, launch_t<T, true>},
-                  T::TM, T::TN, WK, T::RIDE ? 16 * T::RT : 0, stage, 0.f, share};
+    return I4Kind{name, {launch_of<I4Ring<MB, NB, WM, WN, WK, 1>, true, LEAST <= 32>(),
+                         launch_of<I4Ring<MB, NB, WM, WN, WK, 2>, true, LEAST <= 64>(), launch_t<T, true>},
+                  T::TM, T::TN, WK, T::RIDE ? 16 * T::RT : 0, {s32, s64, s128}, 0.f, share};
 }
 const I4Kind kKinds[] = {
-    direct<1, 1, 8>("int4_gemm 16x16", 0.80f, 0.07f, 2),
-    direct<1, 2, 8>("int4_gemm 16x32", 1.30f, 0.06f, 2),
-    ring<1, 1, 1, 2, 4>("int4_ring 16x32", 0.43f, 2),
-    ring<1, 2, 1, 4, 2>("int4_ring 16x128", 0.60f, 1),
-    ring<2, 1, 1, 2, 4>("int4_ring 32x32", 0.62f, 1),
-    ring<2, 2, 1, 2, 4>("int4_ring 32x64", 0.97f, 1),
-    ring<3, 1, 1, 2, 4>("int4_ring 48x32", 0.86f, 1),
-    ring<3, 2, 1, 2, 4>("int4_ring 48x64", 1.31f, 1),
-    ring<4, 1, 1, 4, 2>("int4_ring 64x64", 0.98f, 1),
-    ring<4, 2, 1, 4, 2>("int4_ring 64x128", 1.45f, 1),
-    ring<4, 1, 2, 4, 1>("int4_ring 128x64", 0.92f, 1),
-    ring<4, 2, 2, 4, 1>("int4_ring 128x128", 1.30f, 1),
+    direct<1, 1, 8, 32>("int4_gemm 16x16", 1.75f, 1.20f, 0.80f, 0.07f, 2),
+    direct<1, 2, 8, 64>("int4_gemm 16x32", 3.10f, 1.90f, 1.30f, 0.06f, 2),
+    ring<1, 1, 1, 2, 4>("int4_ring 16x32", 1.04f, 0.78f, 0.67f, 2),
+    ring<1, 2, 1, 4, 2>("int4_ring 16x128", 1.17f, 0.77f, 0.60f, 1),
+    ring<2, 1, 1, 2, 4>("int4_ring 32x32", 0.98f, 0.70f, 0.65f, 1),
+    ring<2, 2, 1, 2, 4>("int4_ring 32x64", 1.59f, 1.22f, 0.97f, 1),
+    ring<3, 1, 1, 2, 4>("int4_ring 48x32", 1.20f, 1.15f, 1.05f, 1),
+    ring<3, 2, 1, 2, 4>("int4_ring 48x64", 2.03f, 1.58f, 1.31f, 1),
+    ring<4, 1, 1, 4, 2>("int4_ring 64x64", 1.30f, 1.05f, 0.95f, 1),
+    ring<4, 2, 1, 4, 2>("int4_ring 64x128", 2.90f, 1.60f, 1.42f, 1),
+    ring<4, 1, 2, 4, 1>("int4_ring 128x64", 1.33f, 1.05f, 0.95f, 1),
+    ring<4, 2, 2, 4, 1>("int4_ring 128x128", 2.08f, 1.52f, 1.30f, 1),
+    ring<8, 2, 2, 4, 1, 128>("int4_ring 256x128", 3.67f, 4.68f, 2.45f, 1),
 };
 
 }  // namespace
 
 // The cheapest of the tile shapes, with k split as far as pays, and for more than 64 rows
 // of expanding the weight for the bf16 product (kind 0), by a model of their times:
-//   shape:  4.2 us, rounds of work-groups (stages x stage time each, and at least their
+//   shape:  4.2 us, rounds of work-groups (stages x stage time each, with two more for
+//           each 32 ranks that a tile of 128 rows or more adds itself, and at least their
 //           share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); the
 //           work-groups that form S 0.8 us, 7 where they keep some of the product's from
 //           starting; a finishing launch 3.5 us, 0.25 a slice more, and its partial sums
@@ -534,10 +558,12 @@ const I4Kind kKinds[] = {
 // 1 x 8192 x 28672 25.2 (26.9), 32 x 4096 x 14336 12.3 (11.6), 48 x 14336 x 4096 18.4
 // (17.7), 64 x 4096 x 14336 19.9 (19.1), 33 x 28672 x 8192 44.3 (44.9), 100 x 4096 x 4096
 // 18.1 (18.0; expanded 83), 256 x 4096 x 14336 46 (46; expanded 108), 1000 x 14336 x 4096
-// 144 (150; expanded 277), 2000 x 4096 x 4096 expanded 86 (84; packed 90).
-// More rows than these shapes serve are left to the expansion because a work-group that
-// unpacks for itself spends as long on that and on scaling as on its MFMAs: 128 x 256
-// tiles 86 us at 2000 x 4096 x 4096 and 344 at 8192 x 4096 x 4096 (expanded 201).
+// 144 (150; expanded 269), 2000 x 4096 x 4096 83 (83; expanded 86), 2000 x 14336 x 4096
+// expanded 274 (296).  More rows than fill one round of these shapes are left to the
+// expansion: a work-group that unpacks for itself spends as long on that and on scaling as
+// on its MFMAs (8192 x 4096 x 4096 344 us from 128 x 256 tiles, expanded 201), and neither
+// closing a group behind the next one's MFMAs from two sets of accumulators nor a wave's
+// priority moved that: the compiler spills.
 static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
     I4Plan best{};
     // (offsets into X and a tile's codes stay below 2^31, and counts within an int)
@@ -549,7 +575,9 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
     for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
         const I4Kind &K = kKinds[kind - 1];
         const bool wide = K.ranks == 0;
-        if (wide != (m > kI4Rows) || (!wide && m > K.tm) || (m <= 16 && K.tm > 16)) continue;
+        const int form = group == 32 ? 0 : group == 64 ? 1 : 2;
+        const double stage = K.stage[form];
+        if (K.launch[form] == nullptr || wide != (m > kI4Rows) || (!wide && m > K.tm) || (m <= 16 && K.tm > 16)) continue;
         I4Plan p{};
         p.kind = kind;
         p.tiles_m = (int)cdiv(m, K.tm);
@@ -572,11 +600,13 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
             const int64_t groups = (int64_t)p.tiles_m * p.tiles_n * p.KS, slots = 256 * K.share;
             if (groups > (1 << 24)) continue;
-            const double one = (double)per * (K.stage + K.row * (double)m), each = bytes / 5.5e6 / (double)groups;
+            const double lora = wide && !p.finish ? 2.0 * (double)cdiv(r, 32) : 0.0;  // stages that the epilogue takes
+            const double one = (double)per * (stage + K.row * (double)m) + lora * stage, each = bytes / 5.5e6 / (double)groups;
             const int64_t full = groups / slots, rest = groups % slots;
             double t = 4.2 + (double)full * std::max(one, each * (double)slots);
-            // (a ring's stages take their time however few run; the direct shapes' share of X's bytes shrinks)
-            const double least_part = K.row > 0.f ? 0.45 : 0.95;
+            // (a ring's stages take their time however few run, two work-groups of a CU share some of
+            // it; the direct shapes' share of X's bytes shrinks)
+            const double least_part = K.row > 0.f ? 0.45 : K.share > 1 ? 0.67 : 0.95;
             if (rest > 0) t += std::max(one * std::max(least_part, (double)rest / (double)slots), each * (double)rest);
             t += 0.7 * (double)(full + (rest > 0) - 1);
             if (p.jobs > 0) t += rest + p.jobs > slots ? 7.0 : 0.8;
@@ -635,6 +665,7 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
         P.S = S;
         P.B = (const uint16_t *)src.B;
         P.alpha = src.alpha;
+        P.s_wide = src.r % 4 == 0 && ((uintptr_t)S & 15) == 0;
     }
     const I4Kind &K = kKinds[pl.kind - 1];
     const int slot = prof_begin(K.name, stream);

@@ -63,12 +63,12 @@ static void plans(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nse
     const I4Plan p = int4_plan(m, k, n, group, r, nseg);
     HOLDS(p.kind > 0 || m > kI4Rows || k > (1 << 20) || n > (1 << 24));
     if (!p.kind) return;
-    const int tms[] = {16, 16, 16, 16, 32, 32, 48, 48, 64, 64, 128, 128}, tns[] = {16, 32, 32, 128, 32, 64, 32, 64, 64, 128, 64, 128},
-              steps[] = {8, 8, 4, 2, 4, 4, 4, 4, 2, 2, 1, 1};
-    HOLDS(p.kind <= 12);
+    const int tms[] = {16, 16, 16, 16, 32, 32, 48, 48, 64, 64, 128, 128, 256},
+              tns[] = {16, 32, 32, 128, 32, 64, 32, 64, 64, 128, 64, 128, 128}, steps[] = {8, 8, 4, 2, 4, 4, 4, 4, 2, 2, 1, 1, 1};
+    HOLDS(p.kind <= 13);
     const int64_t tm = tms[p.kind - 1], tn = tns[p.kind - 1], k128 = (k + 127) / 128;
     HOLDS(p.tiles_m * tm >= m && (p.tiles_m - 1) * tm < m);
-    HOLDS(p.tiles_m == 1 || tm == 128);
+    HOLDS(p.tiles_m == 1 || tm >= 128);
     HOLDS(p.tiles_n * tn >= n && (p.tiles_n - 1) * tn < n);
     HOLDS(p.per % steps[p.kind - 1] == 0);
     HOLDS(p.KS >= 1 && (int64_t)p.KS * p.per >= k128 && (int64_t)(p.KS - 1) * p.per < k128);

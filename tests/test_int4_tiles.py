@@ -19,16 +19,18 @@ from test_int4 import case, f64, near, product, reference
 
 # m, k, n, the tile, and whether the contraction is split
 SHAPES = [
-    (1, 136, 72, "int4_gemm 16x16", False), (3, 16392, 72, "int4_gemm 16x16", True), (1, 520, 8200, "int4_gemm 16x32", False),
-    (3, 3000, 8200, "int4_gemm 16x32", False), (11, 136, 72, "int4_ring 16x32", False), (15, 8200, 72, "int4_ring 16x32", True),
+    (1, 520, 72, "int4_gemm 16x16", False), (3, 16392, 72, "int4_gemm 16x16", True), (1, 520, 8200, "int4_gemm 16x32", False),
+    (3, 3000, 8200, "int4_gemm 16x32", False), (11, 136, 72, "int4_ring 16x32", False), (15, 8200, 1032, "int4_ring 16x32", True),
     (1, 136, 16392, "int4_ring 16x128", False), (20, 136, 72, "int4_ring 32x32", False), (27, 8200, 72, "int4_ring 32x32", True),
-    (20, 136, 8200, "int4_ring 32x64", False), (29, 14344, 2056, "int4_ring 32x64", True), (33, 136, 72, "int4_ring 48x32", False),
-    (47, 4104, 72, "int4_ring 48x32", True), (33, 520, 8200, "int4_ring 48x64", False), (45, 14344, 2056, "int4_ring 48x64", True),
-    (50, 136, 72, "int4_ring 64x64", False), (55, 2056, 2056, "int4_ring 64x64", True), (20, 136, 16392, "int4_ring 64x128", False),
-    (55, 4104, 6152, "int4_ring 64x128", True),
-    (65, 136, 72, "int4_ring 128x64", False), (141, 4104, 136, "int4_ring 128x64", True), (385, 520, 4104, "int4_ring 128x128", False),
-    (141, 4104, 2056, "int4_ring 128x128", True),
+    (20, 264, 8200, "int4_ring 32x64", False), (29, 16392, 2056, "int4_ring 32x64", True), (33, 264, 72, "int4_ring 48x32", False),
+    (47, 3000, 72, "int4_ring 48x32", True), (33, 264, 8200, "int4_ring 48x64", False), (45, 14344, 2056, "int4_ring 48x64", True),
+    (50, 136, 72, "int4_ring 64x64", False), (55, 2056, 72, "int4_ring 64x64", True), (20, 136, 16392, "int4_ring 64x128", False),
+    (55, 4104, 6152, "int4_ring 64x128", True), (65, 136, 72, "int4_ring 128x64", False), (141, 4104, 136, "int4_ring 128x64", True),
+    (385, 520, 4104, "int4_ring 128x128", False), (141, 4104, 2056, "int4_ring 128x128", True),
+    (1300, 520, 4104, "int4_ring 256x128", False), (550, 8, 9888, "int4_ring 256x128", False),
 ]
+# the smallest groups that a case takes its tile for
+LEAST = {(1, 520, 8200): 64, (3, 3000, 8200): 64, (55, 4104, 6152): 64, (1300, 520, 4104): 128, (550, 8, 9888): 128}
 
 
 def ran(call):
@@ -53,8 +55,7 @@ def test_every_shape_has_a_case():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("group", [32, 64, 128, 384])
-@pytest.mark.parametrize("m,k,n,tile,split", SHAPES)
+@pytest.mark.parametrize("m,k,n,tile,split,group", [(*s, g) for s in SHAPES for g in (32, 64, 128, 384) if g >= LEAST.get(s[:3], 32)])
 def test_frozen(m, k, n, tile, split, group):
     log(f"frozen {m} x {k} x {n} group {group}: {tile}")
     X, W4, W, _, _, _ = case(m, k, n, 8, group, seed=m + k)
@@ -70,7 +71,7 @@ def test_frozen(m, k, n, tile, split, group):
 @pytest.mark.parametrize("at", range(len(SHAPES)))
 def test_layer(at, r, p):
     m, k, n, _, _ = SHAPES[at]
-    group = (32, 64, 128)[at % 3]
+    group = max((32, 64, 128)[at % 3], LEAST.get((m, k, n), 32))
     X, W4, W, A, B, dY = case(m, k, n, r, group, seed=500 + at)
     Y, S, keep = lf.lora_int4_linear_fwd(X.cuda(), W4, A.cuda(), B.cuda(), 0.5, p, 5, 8)
     want, slack = reference(X, W, A, B, dY, 0.5, p, 5, 8, m)
