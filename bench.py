@@ -63,6 +63,12 @@ def parse():
     ap.add_argument("--mxfp4", action="store_true",
                     help="instead of the headline step: the layer over a frozen weight in MXFP4 against the "
                          "same layer over the bf16 weight, from one token to a training batch")
+    ap.add_argument("--int4", action="store_true",
+                    help="instead of the headline step: the layer over a frozen weight of 4-bit integers in "
+                         "groups of 128 rows against the same layer over the bf16 weight")
+    ap.add_argument("--mxint8", action="store_true",
+                    help="instead of the headline step: saving a layer's input in 8 bits, and the backward from "
+                         "it against the backward from the bf16 input")
     ap.add_argument("--adamw", action="store_true",
                     help="instead of the headline step: the AdamW step over a model's adapter tensors, with "
                          "moments in 32 and in 8 bits")
@@ -291,6 +297,110 @@ def mxfp4_report(args):
                           "weight_bytes": {"mxfp4": held[0], "bf16": held[1]},
                           "bf16_weight": {"ms": both16, "ms_forward": fwd16, "speedup": both16 / both4,
                                           "speedup_forward": fwd16 / fwd4}}), flush=True)
+
+
+def int4_report(args):
+    """The frozen weight in 4-bit integers, groups of 128 rows: packing 28672 x 8192,
+    then the layer (r 16, no dropout for the forward alone, p 0.1 for forward and
+    backward) over the packed and over the bf16 weight, k = 4096 -> n = 14336, from 1
+    to 8192 tokens.  Medians of event-timed trials after a cache flush, as for MXFP4."""
+    import torch
+
+    import lora_fine_tuning_amd as lf
+
+    lf.load()
+    timer = Timer(torch, torch.cuda.current_stream())
+    g = torch.Generator(device="cuda").manual_seed(13)
+
+    def timed(fn):
+        return timer.median(fn, args.steps, args.warmup)
+
+    def rand(*shape, scale):
+        return (torch.randn(*shape, device="cuda", generator=g) * scale).bfloat16()
+
+    k, n, group = 28672, 8192, 128
+    W = rand(k, n, scale=k ** -0.5)
+    W4 = lf.lora_int4_quantize(W, group)
+    nbytes = 2 * k * n + W4.codes.numel() + 4 * W4.scales.numel()
+    for name, fn in (("quantise", lambda: lf.lora_int4_quantize(W, group, codes=W4.codes, scales=W4.scales)),
+                     ("dequantise", lambda: lf.lora_int4_dequantize(W4, out=W))):
+        ms = timed(fn)
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        print(json.dumps({"metric": f"4-bit integer weight {name}, GB/s of compulsory traffic", "value": gbs, "unit": "GB/s",
+                          "ms": ms, "steps": args.steps, "warmup": args.warmup, "higher_is_better": True,
+                          "dtype": "bf16, int4", "data": "synthetic", "config": {"workload": f"W {k} x {n}, group {group}"},
+                          "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                                       "frac": gbs / PEAK_HBM_GBS, "traffic": None}}), flush=True)
+    del W, W4
+    k, n, r = 4096, 14336, 16
+    W = rand(k, n, scale=k ** -0.5)
+    W4 = lf.lora_int4_quantize(W, group)
+    A, B = rand(k, r, scale=k ** -0.5), rand(r, n, scale=0.02 ** 0.5)
+    held = (W4.codes.numel() + 4 * W4.scales.numel(), 2 * k * n)
+    for m in (1, 16, 48, 256, 1024, 8192):
+        X, dY = rand(m, k, scale=1.0), rand(m, n, scale=1.0)
+
+        def step(w, fwd, bwd):
+            Y, S, keep = fwd(X, w, A, B, 2.0, 0.1, 1, 0)
+            bwd(dY, X, w, A, B, S, keep, 2.0, 0.1)
+
+        fwd4 = timed(lambda: lf.lora_int4_linear_fwd(X, W4, A, B, 2.0, 0.0))
+        fwd16 = timed(lambda: lf.lora_linear_fwd(X, W, A, B, 2.0, 0.0))
+        both4 = timed(lambda: step(W4, lf.lora_int4_linear_fwd, lf.lora_int4_linear_bwd))
+        both16 = timed(lambda: step(W, lf.lora_linear_fwd, lf.lora_linear_bwd))
+        print(json.dumps({"metric": "LoRA linear over a weight of 4-bit integers, tokens/s forward",
+                          "value": m / (fwd4 * 1e-3), "unit": "tokens/s", "ms_forward": fwd4, "ms": both4,
+                          "steps": args.steps, "warmup": args.warmup, "higher_is_better": True, "dtype": "bf16",
+                          "data": "synthetic", "config": {"workload": f"m {m}, k {k}, n {n}, r {r}, group {group}"},
+                          "weight_bytes": {"int4": held[0], "bf16": held[1]},
+                          "bf16_weight": {"ms": both16, "ms_forward": fwd16, "speedup": both16 / both4,
+                                          "speedup_forward": fwd16 / fwd4}}), flush=True)
+
+
+def mxint8_report(args):
+    """A layer's input saved in 8 bits: saving 8192 rows of 4096 and of 14336 values,
+    and the backward (p 0.1) from it against the one from bf16, k = 4096 -> n = 4096.
+    Medians of event-timed trials after a cache flush."""
+    import torch
+
+    import lora_fine_tuning_amd as lf
+
+    lf.load()
+    timer = Timer(torch, torch.cuda.current_stream())
+    g = torch.Generator(device="cuda").manual_seed(17)
+
+    def timed(fn):
+        return timer.median(fn, args.steps, args.warmup)
+
+    def rand(*shape, scale):
+        return (torch.randn(*shape, device="cuda", generator=g) * scale).bfloat16()
+
+    m, n = 8192, 4096
+    for k in (4096, 14336):
+        X = rand(m, k, scale=1.0)
+        X8 = lf.lora_mxint8_quantize(X)
+        nbytes = 2 * m * k + X8.codes.numel() + X8.scales.numel()
+        ms = timed(lambda: lf.lora_mxint8_quantize(X, codes=X8.codes, scales=X8.scales))
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        print(json.dumps({"metric": "input saved in 8 bits, GB/s of compulsory traffic", "value": gbs, "unit": "GB/s", "ms": ms,
+                          "steps": args.steps, "warmup": args.warmup, "higher_is_better": True, "dtype": "bf16, int8",
+                          "data": "synthetic", "config": {"workload": f"X {m} x {k}"},
+                          "input_bytes": {"mxint8": X8.codes.numel() + X8.scales.numel(), "bf16": 2 * m * k},
+                          "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                                       "frac": gbs / PEAK_HBM_GBS, "traffic": None}}), flush=True)
+    k = 4096
+    W = rand(k, n, scale=k ** -0.5)
+    for r in (16, 64, 128):
+        X, dY = rand(m, k, scale=1.0), rand(m, n, scale=1.0)
+        A, B = rand(k, r, scale=k ** -0.5), rand(r, n, scale=0.02 ** 0.5)
+        _, S, keep = lf.lora_linear_fwd(X, W, A, B, 2.0, 0.1, 1, 0)
+        X8 = lf.lora_mxint8_quantize(X)
+        ms8 = timed(lambda: lf.lora_mxint8_linear_bwd(dY, X8, W, A, B, S, keep, 2.0, 0.1))
+        ms16 = timed(lambda: lf.lora_linear_bwd(dY, X, W, A, B, S, keep, 2.0, 0.1))
+        print(json.dumps({"metric": "LoRA backward from an input saved in 8 bits, tokens/s", "value": m / (ms8 * 1e-3),
+                          "unit": "tokens/s", "ms": ms8, "steps": args.steps, "warmup": args.warmup, "higher_is_better": True,
+                          "dtype": "bf16", "data": "synthetic", "config": {"workload": f"m {m}, k {k}, n {n}, r {r}"},
+                          "bf16_input": {"ms": ms16, "speedup": ms16 / ms8}}), flush=True)
 
 
 def adamw_report(args):
@@ -749,6 +859,12 @@ def main():
         return
     if args.mxfp4:
         mxfp4_report(args)
+        return
+    if args.int4:
+        int4_report(args)
+        return
+    if args.mxint8:
+        mxint8_report(args)
         return
     if args.adamw:
         adamw_report(args)
