@@ -477,8 +477,9 @@ def test_mixed_matches_definition(m, k, n, nseg, r_max, group):
 @pytest.mark.gpu
 @pytest.mark.parametrize("seg_off,seg_ad", [([0, -(1 << 33) + 5, 1 << 40, 20], [0, 1, 0]), ([0, 30, 10, 20], [1, 0, 1]),
                                             ([-7, 4, 4, 1 << 33], [0, 9, -3]), ([5, 6, 7, 8], [1, 1, 0])])
-def test_bad_segment_tables_stay_in_bounds(seg_off, seg_ad):
-    m, k, n = 20, 264, 136
+@pytest.mark.parametrize("m", [20, 100])
+def test_bad_segment_tables_stay_in_bounds(m, seg_off, seg_ad):
+    k, n = 264, 136
     g = torch.Generator().manual_seed(8)
     X, W4, _, _, _, dY = case(m, k, n, 8, 32, seed=8)
     As = [bf16_randn((k, r), 1.0, g).cuda() for r in (8, 40)]

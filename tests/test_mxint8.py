@@ -422,8 +422,9 @@ def test_unaligned_adapter_gives_the_same(m, r):
 
 
 @pytest.mark.gpu
-def test_no_rows():
-    k, n, r = 136, 72, 8
+@pytest.mark.parametrize("r", [8, 5, 130])
+def test_no_rows(r):
+    k, n = 136, 72
     g = torch.Generator().manual_seed(1)
     A, B = bf16_randn((k, r), 1.0, g).cuda(), bf16_randn((r, n), 1.0, g).cuda()
     for W in weights(k, n, g):
