@@ -397,11 +397,12 @@ lora_status lora_int4_dequantize(const void *codes, const void *scales, int64_t 
  *
  * A forward multiplies W' as it is where it reads the packed weight, group by
  * group in fp32: always for up to 64 rows, and for more where that is faster
- * than expanding W'.  Otherwise, and in every backward, W' is expanded into
- * the workspace and each of its values rounded to bf16.  Equal sizes take equal
- * ways.  From the packed weight a row's products are sums of x (16 + q) less
- * (16 + z) times the sum of x: a row of X with an infinity gives NaN, as does
- * one whose sum of 271 |x| over a group is past fp32's range. */
+ * than expanding W' into the workspace.  An expanded W', and W' in every
+ * backward, has each of its values rounded to bf16.  Equal sizes take equal
+ * ways.  In a forward from the packed weight a row's products are sums of
+ * x (16 + q) less (16 + z) times the sum of x: a row of X with an infinity
+ * gives NaN, as does one whose sum of 271 |x| over a group is past fp32's
+ * range. */
 size_t lora_int4_frozen_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group);
 lora_status lora_int4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t group, int64_t m,
                                  int64_t k, int64_t n, void *Y, void *workspace, size_t workspace_bytes,

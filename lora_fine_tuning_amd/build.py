@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.cpp", "mxfp4_api.cpp", "adamw_api.cpp", "packer.cpp", "lowrank_kernels.hip", "gemm_kernels.hip",
            "dora_kernels.hip", "mxfp4_kernels.hip", "mxfp4_gemm.hip", "mxfp4_gemm_t.hip", "mxfp4_join.hip",
            "adamw_kernels.hip", "mxint8_api.cpp", "mxint8_kernels.hip", "int4_api.cpp", "int4_kernels.hip",
-           "int4_gemm.hip", "int4_finish.hip"]
+           "int4_gemm.hip", "int4_gemm_t.hip", "int4_finish.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-I", INCLUDE, "-I", CSRC,
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

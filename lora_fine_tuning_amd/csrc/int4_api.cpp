@@ -86,7 +86,9 @@ extern "C" size_t lora_int4_frozen_fwd_workspace_size(int64_t m, int64_t k, int6
 }
 
 extern "C" size_t lora_int4_frozen_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group) {
-    return sizes_ok(m, k, n, group) ? expanded_bytes(m, k, n) : 0;
+    if (!sizes_ok(m, k, n, group) || m == 0) return 0;
+    const I4TPlan pl = int4_t_plan(m, k, n, group, 0);
+    return pl.kind ? pl.part_bytes : expanded_bytes(m, k, n);
 }
 
 extern "C" lora_status lora_int4_frozen_fwd(const void *X, const void *codes, const void *scales, int64_t group, int64_t m, int64_t k,
@@ -115,6 +117,15 @@ extern "C" lora_status lora_int4_frozen_bwd(const void *dY, const void *codes, c
     REQ_PTR(dY, 16);
     REQ_PTR(dX, 16);
     REQ_WORKSPACE(lora_int4_frozen_bwd_workspace_size(m, k, n, group));
+    const I4TPlan pl = int4_t_plan(m, k, n, group, 0);
+    if (pl.kind) {
+        HIPCHK(launch_int4_gemm_t(pl, dY, codes, scales, group, (int)m, (int)k, (int)n, dX, (float *)workspace, stream),
+               "4-bit transposed product launch");
+        if (pl.finish)
+            HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, nullptr, 0, 0, nullptr, nullptr,
+                                     AdapterSource{}, dX, stream), "4-bit sum launch");
+        return LORA_OK;
+    }
     EXPAND();
     return lora_frozen_bwd(dY, workspace, m, k, n, dX, stream);
 }
@@ -126,9 +137,16 @@ extern "C" size_t lora_int4_linear_fwd_workspace_size(int64_t m, int64_t k, int6
     return pl.kind ? align_up(pl.part_bytes) + std::max(pl.spart_bytes, layer) : expanded_bytes(m, k, n) + layer;
 }
 
+// What the layers' backward needs before the bf16 layer's own workspace.
+static size_t weight_bytes(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r) {
+    if (m == 0) return 0;
+    const I4TPlan pl = int4_t_plan(m, k, n, group, r);
+    return pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n);
+}
+
 extern "C" size_t lora_int4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r) {
     if (!sizes_ok(m, k, n, group) || r < 1 || r > 256) return 0;
-    return expanded_bytes(m, k, n) + lora_linear_bwd_workspace_size(m, k, n, r);
+    return weight_bytes(m, k, n, group, r) + lora_linear_bwd_workspace_size(m, k, n, r);
 }
 
 extern "C" lora_status lora_int4_linear_fwd(const void *X, const void *codes, const void *scales, int64_t group, const void *A,
@@ -161,6 +179,46 @@ extern "C" lora_status lora_int4_linear_fwd(const void *X, const void *codes, co
                            workspace_bytes - w, stream);
 }
 
+namespace lora {
+lora_status int4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, int64_t group,
+                                 const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                                 void *dX, void *workspace, hipStream_t stream) {
+    const I4TPlan pl = int4_t_plan(m, k, n, group, src.r_cap);
+    char *rest = ws_at(workspace, weight_bytes(m, k, n, group, src.r_cap));
+    if (pl.kind) {
+        const float *dS = nullptr;
+        CHECK(backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, src.r_cap, rest, &dS, stream));
+        if (dX == nullptr) return LORA_OK;
+        HIPCHK(launch_int4_gemm_t(pl, dY, codes, scales, group, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
+               "4-bit transposed product launch");
+        HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, src.r_cap, 0, nullptr,
+                                 src.p == 0.0f ? nullptr : keep_bits, src, dX, stream), "4-bit sum launch");
+        return LORA_OK;
+    }
+    if (m > 0 && dX != nullptr) EXPAND();
+    return linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, rest, stream);
+}
+
+lora_status multi_int4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, int64_t group,
+                                       const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
+                                       int64_t n, void *dX, void *workspace, hipStream_t stream) {
+    const I4TPlan pl = int4_t_plan(m, k, n, group, src.r_cap);
+    char *rest = ws_at(workspace, weight_bytes(m, k, n, group, src.r_cap));
+    if (pl.kind) {
+        const float *dS = nullptr;
+        CHECK(multi_backward_low_rank_only(dY, X, src, S, keep_bits, m, k, n, rest, &dS, stream));
+        if (dX == nullptr) return LORA_OK;
+        HIPCHK(launch_int4_gemm_t(pl, dY, codes, scales, group, (int)m, (int)k, (int)n, nullptr, (float *)workspace, stream),
+               "4-bit transposed product launch");
+        HIPCHK(launch_mxfp4_join(false, (const float *)workspace, pl.KS, (int)m, (int)k, (float *)dS, src.r_cap, 0, nullptr, keep_bits,
+                                 src, dX, stream), "4-bit sum launch");
+        return LORA_OK;
+    }
+    if (m > 0 && dX != nullptr) EXPAND();
+    return multi_linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, rest, stream);
+}
+}  // namespace lora
+
 extern "C" lora_status lora_int4_linear_bwd(const void *dY, const void *X, const void *codes, const void *scales, int64_t group,
                                             const void *A, const void *B, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
                                             int64_t n, int32_t r, float alpha, float p, void *dX, void *dA, void *dB, void *workspace,
@@ -183,10 +241,8 @@ extern "C" lora_status lora_int4_linear_bwd(const void *dY, const void *X, const
         REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     }
     REQ_WORKSPACE(lora_int4_linear_bwd_workspace_size(m, k, n, group, r));
-    const size_t w = expanded_bytes(m, k, n);
-    if (m > 0 && dX != nullptr) EXPAND();
-    return lora_linear_bwd(dY, X, m > 0 ? workspace : codes, A, B, S, keep_bits, m, k, n, r, alpha, p, dX, dA, dB,
-                           ws_at(workspace, w), workspace_bytes - w, stream);
+    return int4_linear_backward(dY, X, codes, scales, group, single_source(A, B, dA, dB, r, alpha, p), S, keep_bits, m, k, n, dX,
+                                workspace, stream);
 }
 
 extern "C" size_t multi_lora_int4_fwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max, int32_t num_adapters,
@@ -200,7 +256,7 @@ extern "C" size_t multi_lora_int4_fwd_workspace_size(int64_t m, int64_t k, int64
 extern "C" size_t multi_lora_int4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max, int32_t num_adapters,
                                                      int32_t num_segments) {
     if (!sizes_ok(m, k, n, group) || r_max < 1 || r_max > 256 || num_adapters < 0 || num_segments < 0) return 0;
-    return expanded_bytes(m, k, n) + multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
+    return weight_bytes(m, k, n, group, r_max) + multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
 }
 
 extern "C" lora_status multi_lora_int4_linear_fwd(const void *X, const void *codes, const void *scales, int64_t group,
@@ -251,8 +307,7 @@ extern "C" lora_status multi_lora_int4_linear_bwd(const void *dY, const void *X,
         REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
     }
     REQ_WORKSPACE(multi_lora_int4_bwd_workspace_size(m, k, n, group, r_max, num_adapters, num_segments));
-    const size_t w = expanded_bytes(m, k, n);
-    if (m > 0 && dX != nullptr) EXPAND();
-    return multi_lora_linear_bwd(dY, X, m > 0 ? workspace : codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, S,
-                                 keep_bits, m, k, n, r_max, dX, ws_at(workspace, w), workspace_bytes - w, stream);
+    return multi_int4_linear_backward(dY, X, codes, scales, group,
+                                      multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max), S, keep_bits, m,
+                                      k, n, dX, workspace, stream);
 }

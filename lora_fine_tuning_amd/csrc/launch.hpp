@@ -370,6 +370,17 @@ MxGemmTPlan mx_gemm_t_plan(int64_t m, int64_t k, int64_t n, int r);
 hipError_t launch_mxfp4_gemm_t(const MxGemmTPlan &pl, const void *dY, const void *codes, const void *scales, int m, int k,
                                int n, void *dX, float *part, hipStream_t stream);
 
+// The same from a weight of 4-bit integers (int4_gemm_t.hip).
+struct I4TPlan {
+    int kind;  // tile shape; 0: expand the weight
+    int tiles_m, tiles_k, KS, per;
+    bool finish;
+    size_t part_bytes;
+};
+I4TPlan int4_t_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r);
+hipError_t launch_int4_gemm_t(const I4TPlan &pl, const void *dY, const void *codes, const void *scales, int64_t group, int m, int k, int n,
+                              void *dX, float *part, hipStream_t stream);
+
 // The partial sums of either product ([KS][m][n]) and the adapters' term
 // (mxfp4_join.hip): up for Y, with segments only; otherwise for dX.  SK > 0: S is
 // the sum of SK partial sums ([SK][m][RS rounded up to 4]), and written.
@@ -401,5 +412,12 @@ lora_status mxfp4_linear_backward(const void *dY, const LayerInput &X, const voi
 lora_status multi_mxfp4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales,
                                         const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
                                         int64_t n, void *dX, void *workspace, hipStream_t stream);
+// (int4_api.cpp)
+lora_status int4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, int64_t group,
+                                 const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k, int64_t n,
+                                 void *dX, void *workspace, hipStream_t stream);
+lora_status multi_int4_linear_backward(const void *dY, const LayerInput &X, const void *codes, const void *scales, int64_t group,
+                                       const AdapterSource &src, const float *S, const uint32_t *keep_bits, int64_t m, int64_t k,
+                                       int64_t n, void *dX, void *workspace, hipStream_t stream);
 
 }  // namespace lora

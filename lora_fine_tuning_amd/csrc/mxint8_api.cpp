@@ -128,12 +128,9 @@ static lora_status layer_backward(bool multi, int32_t kind, const void *W, const
     if (kind == LORA_WEIGHT_MXFP4)
         return multi ? multi_mxfp4_linear_backward(dY, X, W, W_scales, src, S, keep_bits, m, k, n, dX, workspace, stream)
                      : mxfp4_linear_backward(dY, X, W, W_scales, src, S, keep_bits, m, k, n, dX, workspace, stream);
-    if (kind == LORA_WEIGHT_INT4) {
-        if (m > 0 && dX != nullptr)
-            HIPCHK(launch_int4_dequantize(W, W_scales, k, n, group, workspace, stream), "4-bit dequantise launch");
-        W = workspace;
-        workspace = ws_at(workspace, m > 0 ? align_up((size_t)k * (size_t)n * 2) : 0);
-    }
+    if (kind == LORA_WEIGHT_INT4)
+        return multi ? multi_int4_linear_backward(dY, X, W, W_scales, group, src, S, keep_bits, m, k, n, dX, workspace, stream)
+                     : int4_linear_backward(dY, X, W, W_scales, group, src, S, keep_bits, m, k, n, dX, workspace, stream);
     return multi ? multi_linear_backward(dY, X, W, src, S, keep_bits, m, k, n, dX, workspace, stream)
                  : linear_backward(dY, X, W, src, S, keep_bits, m, k, n, dX, workspace, stream);
 }

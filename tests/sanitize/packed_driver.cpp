@@ -79,6 +79,21 @@ static void plans(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nse
     HOLDS(p.spart_bytes == (size_t)p.SK * m * ((r + 3) / 4 * 4) * 4);
 }
 
+static void plans_t(int64_t m, int64_t k, int64_t n, int64_t group, int r) {
+    const I4TPlan p = int4_t_plan(m, k, n, group, r);
+    if (!p.kind) return;
+    const int tms[] = {16, 32, 48, 64, 128}, nwds[] = {256, 256, 256, 256, 128};
+    HOLDS(p.kind <= 5);
+    const int64_t tm = tms[p.kind - 1], nwd = nwds[p.kind - 1];
+    HOLDS(p.tiles_m * tm >= m && (p.tiles_m - 1) * tm < m);
+    HOLDS((int64_t)p.tiles_k * 128 >= k && (int64_t)(p.tiles_k - 1) * 128 < k);
+    HOLDS(p.KS >= 1 && (int64_t)p.KS * p.per * nwd >= n && (int64_t)(p.KS - 1) * p.per * nwd < n);
+    HOLDS(p.finish == (p.KS > 1 || r > 0));
+    HOLDS(p.part_bytes == (p.finish ? (size_t)p.KS * m * k * 4 : 0));
+    HOLDS((int64_t)p.tiles_m * p.tiles_k * p.KS < (1LL << 31) / 512);
+    HOLDS((n + 15) / 16 * ((k + 127) / 128) * 1024 < (1LL << 31));
+}
+
 int main() {
     void *F = (void *)(uintptr_t)0x10000;  // aligned, never dereferenced
     void *odd = (void *)(uintptr_t)0x10008;
@@ -112,6 +127,7 @@ int main() {
         const int64_t group = i % 7 == 0 ? 32 : i % 7 == 1 ? 64 : 128 * (i % 7 == 2 ? draw(10) : 1);
         const int r = i % 3 ? (int)draw(8) : 0;
         plans(m, k, n, group, r, r > 0 && i % 2 ? (int)draw(10) : 0);
+        plans_t(m, k, n, group, r);
     }
 
     // packing
@@ -143,7 +159,7 @@ int main() {
     EXPECT(lora_int4_frozen_fwd(nullptr, F, F, 32, 0, 64, 64, nullptr, nullptr, 0, nullptr), OK);
     EXPECT(lora_int4_frozen_fwd(F, F, F, 32, 4000, 4096, 4096, F, F, 0, nullptr), WS);
     EXPECT(lora_int4_frozen_bwd(F, F, F, 32, 4, 64, 64, nullptr, F, big, nullptr), INV);
-    EXPECT(lora_int4_frozen_bwd(F, F, F, 32, 4, 64, 64, F, F, 0, nullptr), WS);
+    EXPECT(lora_int4_frozen_bwd(F, F, F, 32, 4000, 4096, 4096, F, F, 0, nullptr), WS);
     EXPECT(lora_int4_frozen_bwd(nullptr, F, F, 32, 0, 64, 64, nullptr, nullptr, 0, nullptr), OK);
     for (int32_t r : {INT32_MIN, 0, 257, INT32_MAX}) {
         EXPECT(lora_int4_linear_fwd(F, F, F, 64, F, F, 64, 64, 64, r, 1.f, 0.1f, 0, 0, F, Ff, Fu, F, big, nullptr), INV);

@@ -33,16 +33,25 @@ SHAPES = [
 LEAST = {(1, 520, 8200): 64, (3, 3000, 8200): 64, (55, 4104, 6152): 64, (1300, 520, 4104): 128, (550, 8, 9888): 128}
 
 
-def ran(call):
-    """The library's launches during `call`, by name."""
+# the backward's: m, k, n, the tile, and whether the contraction (over n) is split
+SHAPES_T = [
+    (13, 136, 72, "int4_gemm_t 16x128", False), (13, 264, 4104, "int4_gemm_t 16x128", True), (600, 1032, 520, "int4_gemm_t 32x128", False),
+    (20, 8200, 2056, "int4_gemm_t 32x128", True), (130, 8200, 2056, "int4_gemm_t 48x128", False), (40, 8200, 2056, "int4_gemm_t 48x128", True),
+    (1500, 1032, 520, "int4_gemm_t 64x128", False), (60, 8200, 2056, "int4_gemm_t 64x128", True),
+    (300, 8200, 2056, "int4_gemm_t 128x128", False), (2000, 264, 4104, "int4_gemm_t 128x128", True),
+]
+
+
+def ran(call, finish="int4_finish"):
+    """The library's launches during `call`, by name, and whether a launch `finish` was among them."""
     lf.lora_profiling_enable(True, 64)
     lf.lora_profiling_reset()
     try:
         out = call()
         torch.cuda.synchronize()
-        names = {s[3] for s in SHAPES}
+        names = {s[3] for s in SHAPES + SHAPES_T}
         seen = {n for n in names if lf.lora_profiling_query(n)[0] > 0}
-        split = lf.lora_profiling_query("int4_finish")[0] > 0
+        split = lf.lora_profiling_query(finish)[0] > 0
     finally:
         lf.lora_profiling_enable(False)
     return out, seen, split
@@ -52,6 +61,8 @@ def test_every_shape_has_a_case():
     text = open(_lib.__file__.replace("_lib.py", "csrc/int4_gemm.hip")).read()
     names = set(re.findall(r'"(int4_(?:gemm|ring) \d+x\d+)"', text))
     assert names == {s[3] for s in SHAPES}
+    text = open(_lib.__file__.replace("_lib.py", "csrc/int4_gemm_t.hip")).read()
+    assert set(re.findall(r'"(int4_gemm_t \d+x\d+)"', text)) == {s[3] for s in SHAPES_T}
 
 
 @pytest.mark.gpu
@@ -64,6 +75,33 @@ def test_frozen(m, k, n, tile, split, group):
     assert tile in seen and finish == split
     assert (Yb[m:] == 5).all()
     near("Y", Yb[:m], *product(m, f64(X), W))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [32, 64, 128, 384])
+@pytest.mark.parametrize("m,k,n,tile,split", SHAPES_T)
+def test_frozen_backward(m, k, n, tile, split, group):
+    log(f"frozen backward {m} x {k} x {n} group {group}: {tile}")
+    _, W4, W, _, _, dY = case(m, k, n, 8, group, seed=m + n)
+    dXb = torch.full((m + 2, k), 5.0, dtype=torch.bfloat16, device="cuda")
+    _, seen, finish = ran(lambda: lf.lora_int4_frozen_bwd(dY.cuda(), W4, dX=dXb[:m]), "mxfp4_join_down")
+    assert tile in seen and finish == split
+    assert (dXb[m:] == 5).all()
+    dy = f64(dY)
+    near("dX", dXb[:m], dy @ W[1].T, n * 2.0 ** -24 * (np.abs(dy) @ np.abs(W[1]).T))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r,p", [(7, 0.0), (200, 0.1)])
+@pytest.mark.parametrize("at", range(len(SHAPES_T)))
+def test_layer_backward(at, r, p):
+    m, k, n, _, _ = SHAPES_T[at]
+    X, W4, W, A, B, dY = case(m, k, n, r, (32, 64, 128)[at % 3], seed=700 + at)
+    Y, S, keep = lf.lora_int4_linear_fwd(X.cuda(), W4, A.cuda(), B.cuda(), 0.5, p, 5, 8)
+    dX, dA, dB = lf.lora_int4_linear_bwd(dY.cuda(), X.cuda(), W4, A.cuda(), B.cuda(), S, keep, 0.5, p)
+    want, slack = reference(X, W, A, B, dY, 0.5, p, 5, 8, m)
+    for name, t in (("dX", dX), ("dA", dA), ("dB", dB)):
+        near(name, t, want[name], slack[name])
 
 
 @pytest.mark.gpu

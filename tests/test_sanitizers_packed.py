@@ -9,7 +9,7 @@ import pytest
 
 from test_sanitizers import BUILD, CLANGXX, CSRC, HERE, HIPCC, ROOT, SAN_HOST, run
 
-CHECKED = ["api.cpp", "mxfp4_api.cpp", "int4_api.cpp", "mxint8_api.cpp", "mxfp4_gemm.hip", "int4_gemm.hip"]
+CHECKED = ["api.cpp", "mxfp4_api.cpp", "int4_api.cpp", "mxint8_api.cpp", "mxfp4_gemm.hip", "int4_gemm.hip", "int4_gemm_t.hip"]
 PLAIN = ["lowrank_kernels.hip", "gemm_kernels.hip", "dora_kernels.hip", "mxfp4_kernels.hip", "mxfp4_gemm_t.hip",
          "mxfp4_join.hip", "int4_kernels.hip", "int4_finish.hip", "mxint8_kernels.hip"]
 
