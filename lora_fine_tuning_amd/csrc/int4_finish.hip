@@ -1,5 +1,6 @@
-// The second launch of the products over a weight of 4-bit integers (up to 64 rows): the
-// partial sums of the contraction's slices and the adapters' term, rounded once.
+// The second launch of the products over a weight of 4-bit integers: the partial sums of
+// the contraction's slices and the adapters' term, rounded once.  (Mixed batches of more
+// than 64 rows end in mxfp4_join.hip.)
 //
 //   Y = sum_s part_s + alpha S B             (S: M x RS, B: r x N)
 //

@@ -621,7 +621,8 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
 }
 
 I4Plan int4_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
-    return remembered<I4Plan>(m, k, n, ((int64_t)nseg << 32) ^ (group << 10) ^ r, [&] { return find_plan(m, k, n, group, r, nseg); });
+    // (groups beyond the largest k are one and the same; r is at most 256)
+    return remembered<I4Plan>(m, k, n, (int64_t)nseg << 32 | std::min<int64_t>(group, 1 << 20) << 10 | r, [&] { return find_plan(m, k, n, group, r, nseg); });
 }
 
 hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, const void *scales, int64_t group, int m, int k, int n,

@@ -1,5 +1,6 @@
-// The second launch of the products over an MXFP4 weight: the partial sums of
-// the contraction's slices in slice order, and the adapters' term, rounded once.
+// The second launch of the products over an MXFP4 weight, and over one of 4-bit integers
+// of dX and of mixed batches of more than 64 rows: the partial sums of the contraction's
+// slices in slice order, and the adapters' term, rounded once.
 //
 //   up:    Y  = sum_s part_s + alpha S B             (S: M x RS, B: r x N)
 //   down:  dX = sum_s part_s + s keep.(dS A^T)       (A: N x r, s = 1 / (1 - p))

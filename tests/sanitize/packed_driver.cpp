@@ -130,6 +130,10 @@ int main() {
         plans_t(m, k, n, group, r);
     }
 
+    // (a plan is remembered by all that it depends on: no group stands for segments)
+    for (int64_t group : {(int64_t)128, ((int64_t)1 << 22) + 128})
+        for (int nseg : {0, 1, 0}) plans(1000, 4096, 4096, group, 16, nseg);
+
     // packing
     for (int64_t g : {(int64_t)0, (int64_t)-32, (int64_t)16, (int64_t)96, (int64_t)200, INT64_MIN, INT64_MAX}) {
         EXPECT(lora_int4_quantize(F, 64, 64, g, 0, F, F, nullptr), INV);
