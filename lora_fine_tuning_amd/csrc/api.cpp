@@ -389,8 +389,8 @@ lora_status linear_backward(const void *dY, const LayerInput &X, const void *W, 
     const float *dS = (const float *)ws_at(workspace, pl.off_ds);
     const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
     if (m > 0 && dX != nullptr)
-        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r_cap, src.p == 0.0f ? nullptr : keep_bits,
-                           (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
+        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r_cap, src.p == 0.0f ? nullptr : X.keep ? X.keep : keep_bits,
+                           X.keep ? X.keep_row : (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
     return LORA_OK;
 }
 }  // namespace lora
@@ -573,8 +573,8 @@ lora_status multi_linear_backward(const void *dY, const LayerInput &X, const voi
     const float *dS = (const float *)ws_at(workspace, pl.off_ds);
     const uint16_t *dss = pl.dss_ld > 0 ? (const uint16_t *)ws_at(workspace, pl.off_dss) : nullptr;
     if (m > 0 && dX != nullptr)
-        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r_cap, keep_bits, (int)((k + 31) / 32),
-                           src, stream, dss, pl.dss_ld), "B3 launch");
+        HIPCHK(launch_gemm(false, 2, dY, W, dX, (int)m, (int)k, (int)n, dS, src.r_cap, X.keep ? X.keep : keep_bits,
+                           X.keep ? X.keep_row : (int)((k + 31) / 32), src, stream, dss, pl.dss_ld), "B3 launch");
     return LORA_OK;
 }
 }  // namespace lora

@@ -124,6 +124,9 @@ inline AdapterSource multi_source(const lora_adapter *adapters, int32_t nad, con
 struct LayerInput {
     const void *x;
     const void *scales;  // NULL: bf16
+    // the mask as the dX product over a bf16 weight reads it, rows of keep_row words (NULL: as it is given)
+    const uint32_t *keep = nullptr;
+    int keep_row = 0;
     LayerInput(const void *x_, const void *scales_ = nullptr) : x(x_), scales(scales_) {}
 };
 
@@ -298,10 +301,20 @@ hipError_t launch_mxfp4_dequantize(const void *codes, const void *scales, int64_
 // Inputs saved in 8 bits (mxint8_kernels.hip).
 hipError_t launch_mxint8_quantize(const void *X, int64_t m, int64_t k, void *codes, void *scales, hipStream_t stream);
 hipError_t launch_mxint8_dequantize(const void *codes, const void *scales, int64_t m, int64_t k, void *X, hipStream_t stream);
-// S (m x r fp32) and A (k x r bf16, k = 0: not) with rows of `row` (a multiple of 4) values, zeros
-// past r; the outputs 16-byte aligned.
-hipError_t launch_widen_rows(const float *S, int64_t m, const void *A, int64_t k, int r, int row, float *S_out, void *A_out,
-                             hipStream_t stream);
+// Copies with longer rows, zeros past the old ones, 16-byte aligned: S (m x r fp32) and A (k x r
+// bf16) with rows of `row` values, a multiple of 4; the mask (m rows of kw words) with rows of
+// keep_row, a multiple of 4.  A NULL output is not made.
+struct WidenRows {
+    int64_t m, k;
+    int r, row, kw, keep_row;
+    const float *S;
+    float *S_out;
+    const void *A;
+    void *A_out;
+    const uint32_t *keep;
+    uint32_t *keep_out;
+};
+hipError_t launch_widen_rows(const WidenRows &w, hipStream_t stream);
 
 // Weights as 4-bit integers in groups of rows (int4_kernels.hip).  scale_type of
 // given scales: 0 fp32, 1 bf16, 2 fp16; zeros may be NULL (all 8).

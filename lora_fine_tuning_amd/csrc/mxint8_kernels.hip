@@ -132,21 +132,27 @@ __global__ __launch_bounds__(256) void mxint8_dequantize_kernel(const uint8_t *c
     }
 }
 
-__global__ __launch_bounds__(256) void widen_rows_kernel(const float *S, int64_t m, const uint16_t *A, int64_t k, int r, int row,
-                                                         float *S_out, uint16_t *A_out) {
-    const int each = row / 4;
-    const int64_t total = (m + k) * each;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t y = i / each;
-        const int c = (int)(i - y * each) * 4;
-        if (y < m) {
-            const float *src = S + y * r + c;
-            ((float4 *)S_out)[i] =
-                make_float4(c < r ? src[0] : 0.f, c + 1 < r ? src[1] : 0.f, c + 2 < r ? src[2] : 0.f, c + 3 < r ? src[3] : 0.f);
+__global__ __launch_bounds__(256) void widen_rows_kernel(WidenRows P, int64_t s_items, int64_t a_items, int64_t items) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        if (i < s_items) {
+            const int64_t y = i / (P.row / 4);
+            const int c = (int)(i - y * (P.row / 4)) * 4;
+            const float *src = P.S + y * P.r + c;
+            ((float4 *)P.S_out)[i] = make_float4(c < P.r ? src[0] : 0.f, c + 1 < P.r ? src[1] : 0.f, c + 2 < P.r ? src[2] : 0.f,
+                                                 c + 3 < P.r ? src[3] : 0.f);
+        } else if (i < s_items + a_items) {
+            const int64_t at = i - s_items, y = at / (P.row / 4);
+            const int c = (int)(at - y * (P.row / 4)) * 4;
+            const uint16_t *src = (const uint16_t *)P.A + y * P.r + c;
+            const uint32_t v0 = c < P.r ? src[0] : 0u, v1 = c + 1 < P.r ? src[1] : 0u, v2 = c + 2 < P.r ? src[2] : 0u,
+                           v3 = c + 3 < P.r ? src[3] : 0u;
+            ((uint2 *)P.A_out)[at] = make_uint2(v0 | v1 << 16, v2 | v3 << 16);
         } else {
-            const uint16_t *src = A + (y - m) * r + c;
-            const uint32_t v0 = c < r ? src[0] : 0u, v1 = c + 1 < r ? src[1] : 0u, v2 = c + 2 < r ? src[2] : 0u, v3 = c + 3 < r ? src[3] : 0u;
-            ((uint2 *)A_out)[i - m * each] = make_uint2(v0 | v1 << 16, v2 | v3 << 16);
+            const int64_t at = i - s_items - a_items, y = at / (P.keep_row / 4);
+            const int c = (int)(at - y * (P.keep_row / 4)) * 4;
+            const uint32_t *src = P.keep + y * P.kw + c;
+            ((uint4 *)P.keep_out)[at] =
+                make_uint4(c < P.kw ? src[0] : 0u, c + 1 < P.kw ? src[1] : 0u, c + 2 < P.kw ? src[2] : 0u, c + 3 < P.kw ? src[3] : 0u);
         }
     }
 }
@@ -175,11 +181,11 @@ hipError_t launch_mxint8_dequantize(const void *codes, const void *scales, int64
     return hipGetLastError();
 }
 
-hipError_t launch_widen_rows(const float *S, int64_t m, const void *A, int64_t k, int r, int row, float *S_out, void *A_out,
-                             hipStream_t stream) {
-    const unsigned grid = (unsigned)std::min<int64_t>(((m + k) * (row / 4) + 255) / 256, 1 << 20);
+hipError_t launch_widen_rows(const WidenRows &w, hipStream_t stream) {
+    const int64_t s = w.S_out ? w.m * (w.row / 4) : 0, a = w.A_out ? w.k * (w.row / 4) : 0;
+    const int64_t items = s + a + (w.keep_out ? w.m * (w.keep_row / 4) : 0);
     const int slot = prof_begin("widen_rows", stream);
-    hipLaunchKernelGGL(widen_rows_kernel, dim3(grid), dim3(256), 0, stream, S, m, (const uint16_t *)A, k, r, row, S_out, (uint16_t *)A_out);
+    hipLaunchKernelGGL(widen_rows_kernel, dim3((unsigned)std::min<int64_t>((items + 255) / 256, 1 << 20)), dim3(256), 0, stream, w, s, a, items);
     prof_end(slot, stream);
     return hipGetLastError();
 }

@@ -4,8 +4,8 @@ The format's reference is written here from its definition, in 64 bits with nump
 
 Tolerances, derived: saving and reading back are exact (every value that codes and
 scales stand for is a bf16), so the backward from a saved input is the bf16 layer's
-over that input: where the same kernels run (ranks that are multiples of 8), bit for
-bit, and otherwise within test_mxfp4.layer_reference's slack of the 64-bit
+over that input: where the same kernels run (ranks that are multiples of 8; dX without a
+mask, or of a multiple of 128 columns), bit for bit, and otherwise within test_mxfp4.layer_reference's slack of the 64-bit
 formulas.  dX and dB do not read the input: their formulas are those over X itself,
 which S is of.
 """
@@ -302,7 +302,8 @@ def test_backward(at, form):
     torch.cuda.synchronize()
     assert (dXb[m:] == 5).all()
     if r % 8 == 0:
-        assert torch.equal(dX, rX) and torch.equal(dA, rA) and torch.equal(dB, rB)
+        assert torch.equal(dA, rA) and torch.equal(dB, rB)
+        assert (p > 0 and k % 128) or torch.equal(dX, rX)
     want, slack = layer_reference(X.cpu(), f64(in_bf16(W)), A, B, dY.cpu(), 2.0, p, 7, 16)
     near("dX", dX, want["dX"], slack["dX"])
     near("dB", dB, want["dB"], slack["dB"])
@@ -344,7 +345,7 @@ def test_mixed_backward(m, k, n, nseg, r_max, form):
         outs.append((dX, *dAs, *dBs))
     if rm % 8 == 0:
         for i, (a, b) in enumerate(zip(*outs)):
-            assert torch.equal(a, b), i
+            assert (i == 0 and k % 128) or torch.equal(a, b), i
     assert not outs[0][na].any()  # the last adapter has no rows
     sums = {}
     for s, a in enumerate(seg_ad):
