@@ -1466,7 +1466,7 @@ struct B2W {
     static constexpr int SPL_OFF = X_BYTES;                   // split tile (PRESPLIT)
     static constexpr int MASK_OFF = PRESPLIT ? X_BYTES + 16384 : X_BYTES;
     static constexpr int DS_OFF = X_BYTES + 1024;             // fp32 dS rows (not PRESPLIT)
-    static constexpr int STAGE = PRESPLIT ? X_BYTES + 16384 + (X8 ? 3072 : 2048) : X_BYTES + 4 * NPW * 1024;
+    static constexpr int STAGE = PRESPLIT ? X_BYTES + 16384 + (X8 ? 3 : 2) * 1024 : X_BYTES + 4 * NPW * 1024;
     static constexpr int NST = MAXT == 2 ? 3 : 4;           // ring depth
     static constexpr int LDS = NST * STAGE;
 };

@@ -441,14 +441,16 @@ def test_no_rows(r):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("m,r,p", [(5, 16, 0.1), (333, 5, 0.1), (700, 64, 0.0)])
-def test_captured_step_replays_match_eager(m, r, p):
+@pytest.mark.parametrize("form", [0, 2])
+def test_captured_step_replays_match_eager(form, m, r, p):
     k, n = 520, 264
     g = torch.Generator().manual_seed(5)
-    W = weights(k, n, g)[2]
+    W = weights(k, n, g)[form]
+    forward = lf.lora_int4_linear_fwd if form else lf.lora_linear_fwd
     X, A, B, dY = (bf16_randn(s, 1.0, g).cuda() for s in ((m, k), (k, r), (r, n), (m, n)))
 
     def run():
-        Y, S, keep = lf.lora_int4_linear_fwd(X, W, A, B, 2.0, p, 9, 0)
+        Y, S, keep = forward(X, W, A, B, 2.0, p, 9, 0)
         X8 = lf.lora_mxint8_quantize(X)
         return (Y, *X8[:2], lf.lora_mxint8_dequantize(X8), *lf.lora_mxint8_linear_bwd(dY, X8, W, A, B, S, keep, 2.0, p))
 
