@@ -479,6 +479,16 @@ __global__ __launch_bounds__(64 * T::NW) void int4_ring_kernel(I4Params P) {
     }
 }
 
+// S of a mixed batch of more than 64 rows, whose joining launch adds its partial sums: jobs
+// of 64 rows and 32 ranks in a launch of their own (beside the product's tiles, which fill
+// the CUs, they took longer).  100 x 4096 x 4096 of 4 segments 33 us with the bf16 layer's
+// router and pass, 27 so, 1000 x 14336 x 4096 189 and 170; one adapter's pass is as fast.
+constexpr int kSRows = 64, kSRanks = 32;
+__global__ __launch_bounds__(512) void int4_s_kernel(SJobParams P) {
+    extern __shared__ uint4 i4s_smem[];
+    s_job<8, kSRows / 16, kSRanks / 16>(P, blockIdx.x, i4s_smem);
+}
+
 template <class T, bool RING>
 hipError_t launch_t(const I4Params &P, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
@@ -552,8 +562,10 @@ const I4Kind kKinds[] = {
 //           share of the weight's bytes at 5.5 TB/s; 0.7 us between rounds); the
 //           work-groups that form S 0.8 us, 7 where they keep some of the product's from
 //           starting; a finishing launch 3.5 us, 0.25 a slice more, and its partial sums
-//           at 5 TB/s
-//   expand: expanded_us (S is formed apart either way)
+//           at 5 TB/s (int4_finish at least 14 us a million outputs)
+//   expand: expanded_us
+//   S apart: a mixed batch's in partial sums 5 us, else by the bf16 layer's pass, 9 us, 14 for
+//           a mixed batch, and X's bytes at 4 TB/s
 // Measured in a graph, groups of 128, model in brackets: 1 x 4096 x 14336 9.8 us (9.9),
 // 1 x 8192 x 28672 25.2 (26.9), 32 x 4096 x 14336 12.3 (11.6), 48 x 14336 x 4096 18.4
 // (17.7), 64 x 4096 x 14336 19.9 (19.1), 33 x 28672 x 8192 44.3 (44.9), 100 x 4096 x 4096
@@ -571,7 +583,8 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t k128 = cdiv(k, 128);
     const double bytes = (double)k * n * (0.5 + 4.0 / (double)std::min<int64_t>(group, 128));
-    double least = m <= kI4Rows ? 1e30 : expanded_us(m, n, k, (double)k * n);
+    const double f1 = r > 0 ? (nseg > 0 ? 14.0 : 9.0) + (double)m * k * 2 / 4e6 : 0.0;
+    double least = m <= kI4Rows ? 1e30 : expanded_us(m, n, k, (double)k * n) + f1;
     for (int kind = 1; kind <= (int)(sizeof(kKinds) / sizeof(kKinds[0])); ++kind) {
         const I4Kind &K = kKinds[kind - 1];
         const bool wide = K.ranks == 0;
@@ -583,6 +596,7 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
         p.tiles_m = (int)cdiv(m, K.tm);
         p.tiles_n = (int)cdiv(n, K.tn);
         const int64_t stages = cdiv(k128, K.step);
+        const int64_t s_jobs = cdiv(k, kSK) * cdiv(m, kSRows) * cdiv(r, kSRanks) * std::max(nseg, 1);
         if (r > 0 && !wide) {
             const int64_t jobs = cdiv(k, kSK) * cdiv(r, K.ranks) * std::max(nseg, 1);
             if (nseg == 0 || jobs <= 1024) {
@@ -598,6 +612,11 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             p.per = (int)(per * K.step);
             p.finish = p.KS > 1 || (r > 0 && (!wide || nseg > 0));
             p.part_bytes = p.finish ? (size_t)p.KS * m * n * sizeof(float) : 0;
+            if (wide) {
+                p.s_jobs = nseg > 0 && r > 0 && s_jobs <= 1024 ? (int)s_jobs : 0;
+                p.SK = p.s_jobs > 0 ? (int)cdiv(k, kSK) : 0;
+                p.spart_bytes = (size_t)p.SK * m * ((r + 3) / 4 * 4) * sizeof(float);
+            }
             const int64_t groups = (int64_t)p.tiles_m * p.tiles_n * p.KS, slots = 256 * K.share;
             if (groups > (1 << 24)) continue;
             const double lora = wide && !p.finish ? 2.0 * (double)cdiv(r, 32) : 0.0;  // stages that the epilogue takes
@@ -610,7 +629,12 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
             if (rest > 0) t += std::max(one * std::max(least_part, (double)rest / (double)slots), each * (double)rest);
             t += 0.7 * (double)(full + (rest > 0) - 1);
             if (p.jobs > 0) t += rest + p.jobs > slots ? 7.0 : 0.8;
-            if (p.finish) t += 3.5 + (double)p.part_bytes * 2 / 5e6 + 0.25 * (p.KS - 1);
+            if (p.s_jobs > 0) t += 5.0 + 4.0 * (p.s_jobs / 512);
+            else if (p.jobs == 0) t += f1;
+            if (p.finish) {
+                const double sums = 3.5 + (double)p.part_bytes * 2 / 5e6 + 0.25 * (p.KS - 1);
+                t += wide && nseg == 0 ? std::max(sums, 14e-6 * (double)m * (double)n) : sums;
+            }
             if (t < least) {
                 least = t;
                 best = p;
@@ -668,6 +692,15 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
         P.alpha = src.alpha;
         P.s_wide = src.r % 4 == 0 && ((uintptr_t)S & 15) == 0;
     }
+    if (pl.s_jobs > 0) {
+        SJobParams Q = P;
+        Q.tiles_m = (m + kSRows - 1) / kSRows;
+        const int slot = prof_begin("int4_s", stream);
+        hipLaunchKernelGGL(int4_s_kernel, dim3((unsigned)pl.s_jobs), dim3(512), 8 * (kSRows / 16) * (kSRanks / 16) * 1024, stream, Q);
+        prof_end(slot, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const I4Kind &K = kKinds[pl.kind - 1];
     const int slot = prof_begin(K.name, stream);
     const hipError_t e = K.launch[group == 32 ? 0 : group == 64 ? 1 : 2](P, stream);
@@ -675,7 +708,7 @@ hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, 
     if (e != hipSuccess || !pl.finish) return e;
     // (int4_finish's work-groups of 32 columns pay where few rows leave CUs idle: 1000 x 4096 x 4096 of 4
     // segments 120 us with it, 76 with the join's of 128)
-    if (m > kI4Rows && src.table != nullptr) return launch_mxfp4_join(true, part, pl.KS, m, n, S, src.r, 0, nullptr, nullptr, src, Y, stream);
+    if (m > kI4Rows && src.table != nullptr) return launch_mxfp4_join(true, part, pl.KS, m, n, S, src.r, pl.SK, spart, nullptr, src, Y, stream);
     return launch_int4_finish(part, pl.KS, m, n, S, pl.SK, spart, src, Y, stream);
 }
 

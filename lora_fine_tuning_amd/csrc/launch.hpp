@@ -327,7 +327,7 @@ hipError_t launch_int4_dequantize(const void *codes, const void *scales, int64_t
 
 // Y = X W' (+ alpha S B) straight from the packed weight (mxfp4_gemm.hip).
 struct MxGemmPlan {
-    int kind;  // tile shape; 0: expand the weight, or the shape is too large
+    int kind;  // tile shape; 0: not for this shape
     int tiles_m, tiles_n, KS, per;
     bool finish;           // a second launch adds partial sums and the LoRA term
     size_t part_bytes;     // fp32 partial sums of the k slices
@@ -349,14 +349,15 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
 
 // Y = X W' (+ alpha S B) straight from a weight of 4-bit integers (int4_gemm.hip): always
 // for up to kI4Rows rows, for more where that is faster than expanding it.
-// SK > 0: the product's launch also forms S and drop.keep, in SK partial sums.
+// SK > 0: S and drop.keep are formed too, in SK partial sums.
 constexpr int kI4Rows = 64;
 struct I4Plan {
-    int kind;  // tile shape; 0: not for this shape
+    int kind;  // tile shape; 0: expand the weight
     int tiles_m, tiles_n, KS, per;
     bool finish;        // a second launch adds partial sums and the LoRA term
     size_t part_bytes;
-    int SK, jobs;       // partial sums of S, and the work-groups that form them
+    int SK, jobs;       // partial sums of S, and the work-groups beside the product that form them,
+    int s_jobs;         // or those of a launch before it
     size_t spart_bytes;
 };
 // r == 0: no adapter; nseg > 0: rows in segments, r the largest rank.

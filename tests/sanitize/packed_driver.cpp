@@ -75,7 +75,8 @@ static void plans(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nse
     HOLDS(p.finish == (p.KS > 1 || (r > 0 && (tm < 128 || nseg > 0))));
     HOLDS(p.part_bytes == (p.finish ? (size_t)p.KS * m * n * 4 : 0));
     HOLDS((int64_t)p.tiles_m * p.tiles_n * p.KS + p.jobs < (1LL << 31) / 512);
-    HOLDS(p.jobs % 8 == 0 && (p.jobs > 0) == (p.SK > 0) && (p.SK == 0 || (tm < 128 && (int64_t)p.SK * 1024 >= k)));
+    HOLDS(p.jobs % 8 == 0 && (p.jobs > 0 || p.s_jobs > 0) == (p.SK > 0) && (p.SK == 0 || (p.finish && (int64_t)p.SK * 1024 >= k)));
+    HOLDS(p.s_jobs == 0 || (tm >= 128 && p.jobs == 0));
     HOLDS(p.spart_bytes == (size_t)p.SK * m * ((r + 3) / 4 * 4) * 4);
 }
 
