@@ -258,7 +258,7 @@ extern "C" size_t lora_linear_fwd_workspace_size(int64_t m, int64_t k, int64_t n
 }
 
 extern "C" size_t lora_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
-    if (m < 0 || k <= 0 || n <= 0 || r < 1) return 0;
+    if (m < 0 || k <= 0 || n <= 0 || r < 1 || !bwd_k_ok(k)) return 0;
     return plan_bwd(m, k, n, r, false, 0, 1).bytes;
 }
 
@@ -404,6 +404,7 @@ extern "C" lora_status lora_linear_bwd(const void *dY, const void *X, const void
     CHECK(check_rank(r));
     CHECK(check_p(p));
     CHECK(check_b_size(r, k, n));
+    CHECK(check_bwd_k(k));
     REQ_PTR(W, 16);
     REQ_PTR(A, 2);
     REQ_PTR(B, 2);
@@ -449,7 +450,7 @@ extern "C" size_t multi_lora_fwd_workspace_size(int64_t m, int64_t k, int64_t n,
 
 extern "C" size_t multi_lora_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                 int32_t num_adapters, int32_t num_segments) {
-    if (m < 0 || k <= 0 || n <= 0 || r_max < 1 || num_segments < 0 || num_adapters < 1) return 0;
+    if (m < 0 || k <= 0 || n <= 0 || r_max < 1 || num_segments < 0 || num_adapters < 1 || !bwd_k_ok(k)) return 0;
     return plan_bwd(m, k, n, r_max, true, num_segments, num_adapters).bytes;
 }
 
@@ -588,6 +589,7 @@ extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, cons
     CHECK(check_shape(m, k, n));
     CHECK(check_multi(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max));
     CHECK(check_b_size(r_max, k, n));
+    CHECK(check_bwd_k(k));
     REQ_PTR(W, 16);
     if (m > 0) {
         REQ_PTR(dY, 16);
@@ -740,6 +742,7 @@ extern "C" lora_status lora_linear_bwd_noalloc(const void *dY, const void *X, co
                                                void *dX, void *dA, void *dB, hipStream_t stream) {
     CHECK(check_shape(m, k, n));
     CHECK(check_rank(r));
+    CHECK(check_bwd_k(k));
     const size_t need = plan_bwd(m, k, n, r, false, 0, 1).bytes;
     if (need > kScratchBytes)
         return host_fail(LORA_ERR_UNSUPPORTED,

@@ -46,6 +46,14 @@ inline lora_status check_b_size(int32_t r, int64_t k, int64_t n) {
     return LORA_OK;
 }
 
+// The backward's dA kernels take runs of 32 rows of X or more, whose bytes they address
+// with 32 bits.
+inline bool bwd_k_ok(int64_t k) { return k * 64 < (1LL << 31); }
+inline lora_status check_bwd_k(int64_t k) {
+    if (!bwd_k_ok(k)) return host_fail(LORA_ERR_UNSUPPORTED, "32 rows of X of k = %lld exceed 2 GiB", (long long)k);
+    return LORA_OK;
+}
+
 inline lora_status check_p(float p) {
     REQUIRE(p >= 0.0f && p < 1.0f, "dropout p = %g must be in [0, 1)", (double)p);
     return LORA_OK;

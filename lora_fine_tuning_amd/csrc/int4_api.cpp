@@ -145,7 +145,7 @@ static size_t weight_bytes(int64_t m, int64_t k, int64_t n, int64_t group, int32
 }
 
 extern "C" size_t lora_int4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r) {
-    if (!sizes_ok(m, k, n, group) || r < 1 || r > 256) return 0;
+    if (!sizes_ok(m, k, n, group) || r < 1 || r > 256 || !bwd_k_ok(k)) return 0;
     return weight_bytes(m, k, n, group, r) + lora_linear_bwd_workspace_size(m, k, n, r);
 }
 
@@ -228,6 +228,7 @@ extern "C" lora_status lora_int4_linear_bwd(const void *dY, const void *X, const
     CHECK(check_rank(r));
     CHECK(check_p(p));
     CHECK(check_b_size(r, k, n));
+    CHECK(check_bwd_k(k));
     REQ_PTR(A, 2);
     REQ_PTR(B, 2);
     REQ_PTR(dA, 2);
@@ -255,7 +256,7 @@ extern "C" size_t multi_lora_int4_fwd_workspace_size(int64_t m, int64_t k, int64
 
 extern "C" size_t multi_lora_int4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int64_t group, int32_t r_max, int32_t num_adapters,
                                                      int32_t num_segments) {
-    if (!sizes_ok(m, k, n, group) || r_max < 1 || r_max > 256 || num_adapters < 0 || num_segments < 0) return 0;
+    if (!sizes_ok(m, k, n, group) || r_max < 1 || r_max > 256 || num_adapters < 0 || num_segments < 0 || !bwd_k_ok(k)) return 0;
     return weight_bytes(m, k, n, group, r_max) + multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
 }
 
@@ -299,6 +300,7 @@ extern "C" lora_status multi_lora_int4_linear_bwd(const void *dY, const void *X,
     // (the forward on no rows makes the same checks of the adapter and segment tables, and enqueues nothing)
     CHECK(multi_lora_linear_fwd(X, codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max, 0, 0, nullptr,
                                 nullptr, nullptr, workspace, workspace_bytes, stream));
+    CHECK(check_bwd_k(k));
     if (m > 0) {
         REQ_PTR(dY, 16);
         REQ_PTR(X, 16);

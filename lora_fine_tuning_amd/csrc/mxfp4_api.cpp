@@ -123,7 +123,7 @@ extern "C" size_t lora_mxfp4_linear_fwd_workspace_size(int64_t m, int64_t k, int
 }
 
 extern "C" size_t lora_mxfp4_linear_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r) {
-    if (!sizes_ok(m, k, n) || !ranks_ok(r, 0, 0)) return 0;
+    if (!sizes_ok(m, k, n) || !ranks_ok(r, 0, 0) || !bwd_k_ok(k)) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r);
     return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) + lora_linear_bwd_workspace_size(m, k, n, r);
 }
@@ -216,6 +216,7 @@ extern "C" lora_status lora_mxfp4_linear_bwd(const void *dY, const void *X, cons
     CHECK(check_rank(r));
     CHECK(check_p(p));
     CHECK(check_b_size(r, k, n));
+    CHECK(check_bwd_k(k));
     REQ_PTR(A, 2);
     REQ_PTR(B, 2);
     REQ_PTR(dA, 2);
@@ -243,7 +244,7 @@ extern "C" size_t multi_lora_mxfp4_fwd_workspace_size(int64_t m, int64_t k, int6
 
 extern "C" size_t multi_lora_mxfp4_bwd_workspace_size(int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                       int32_t num_adapters, int32_t num_segments) {
-    if (!sizes_ok(m, k, n) || !ranks_ok(r_max, num_adapters, num_segments)) return 0;
+    if (!sizes_ok(m, k, n) || !ranks_ok(r_max, num_adapters, num_segments) || !bwd_k_ok(k)) return 0;
     const MxGemmTPlan pl = mx_gemm_t_plan(m, k, n, r_max);
     return (pl.kind ? align_up(pl.part_bytes) : expanded_bytes(m, k, n)) +
            multi_lora_bwd_workspace_size(m, k, n, r_max, num_adapters, num_segments);
@@ -295,6 +296,7 @@ extern "C" lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X
     // (the forward on no rows makes the same checks of the adapter and segment tables, and enqueues nothing)
     CHECK(multi_lora_linear_fwd(X, codes, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max,
                                 0, 0, nullptr, nullptr, nullptr, workspace, workspace_bytes, stream));
+    CHECK(check_bwd_k(k));
     if (m > 0) {
         REQ_PTR(dY, 16);
         REQ_PTR(X, 16);

@@ -135,7 +135,7 @@ static lora_status check_rows(int64_t m, const void *dY, const float *S, const u
 }
 
 extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r) {
-    if (!sizes_ok(m, k, n) || !group_ok(kind, group) || r < 1 || r > 256) return 0;
+    if (!sizes_ok(m, k, n) || !group_ok(kind, group) || r < 1 || r > 256 || !bwd_k_ok(k)) return 0;
     const size_t layer = kind == LORA_WEIGHT_BF16    ? lora_linear_bwd_workspace_size(m, k, n, row_of(r))
                          : kind == LORA_WEIGHT_MXFP4 ? lora_mxfp4_linear_bwd_workspace_size(m, k, n, row_of(r))
                                                      : lora_int4_linear_bwd_workspace_size(m, k, n, group, row_of(r));
@@ -144,7 +144,7 @@ extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t gr
 
 extern "C" size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                        int32_t num_adapters, int32_t num_segments) {
-    if (!sizes_ok(m, k, n) || !group_ok(kind, group) || r_max < 1 || r_max > 256 || num_adapters < 1 || num_segments < 0) return 0;
+    if (!sizes_ok(m, k, n) || !group_ok(kind, group) || r_max < 1 || r_max > 256 || num_adapters < 1 || num_segments < 0 || !bwd_k_ok(k)) return 0;
     const size_t layer = kind == LORA_WEIGHT_BF16    ? multi_lora_bwd_workspace_size(m, k, n, row_of(r_max), num_adapters, num_segments)
                          : kind == LORA_WEIGHT_MXFP4 ? multi_lora_mxfp4_bwd_workspace_size(m, k, n, row_of(r_max), num_adapters, num_segments)
                                                      : multi_lora_int4_bwd_workspace_size(m, k, n, group, row_of(r_max), num_adapters, num_segments);
@@ -175,6 +175,7 @@ extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_code
     CHECK(check_rank(r));
     CHECK(check_p(p));
     CHECK(check_b_size(r, k, n));
+    CHECK(check_bwd_k(k));
     REQ_PTR(A, 2);
     REQ_PTR(B, 2);
     REQ_PTR(dA, 2);
@@ -202,6 +203,7 @@ extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *
     // (the forward on no rows makes the checks of the adapter and segment tables, and enqueues nothing)
     CHECK(multi_lora_linear_fwd(nullptr, W, adapters, num_adapters, seg_off, seg_adapter, num_segments, 0, k, n, r_max, 0, 0, nullptr,
                                 nullptr, nullptr, nullptr, 0, stream));
+    CHECK(check_bwd_k(k));
     CHECK(check_rows(m, dY, S, keep_bits, true, dX));
     const size_t need = multi_lora_mxint8_bwd_workspace_size(kind, group, m, k, n, r_max, num_adapters, num_segments);
     if (workspace_bytes < need) return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);

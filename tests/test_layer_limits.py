@@ -1,0 +1,72 @@
+"""Sizes at and past what the layer's calls address with 32 bits: refused on the host, with nothing enqueued.
+
+No kernel is launched: the pointers are fake, and every call here is refused."""
+import os
+
+import pytest
+import torch
+
+import lora_fine_tuning_amd as lf
+from lora_fine_tuning_amd import _lib
+
+FAKE = 0x10000  # aligned, never dereferenced
+UNSUPPORTED, WORKSPACE = -2, -3
+BF16, MXFP4, INT4 = 0, 1, 2
+F, BIG = FAKE, 1 << 62
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if torch.cuda.is_available():
+        pytest.skip("host-only checks; a GPU is visible")
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("library not built")
+    return _lib.load()
+
+
+def backwards(lib, m, k, n, r, wsb=BIG):
+    """Every backward call of the layer at a size, by name."""
+    tail = (F, F, F, F, wsb, None)  # dX, dA, dB, the workspace
+    multi = (F, F, wsb, None)
+    yield "bf16", lib.lora_linear_bwd(F, F, F, F, F, F, F, m, k, n, r, 1.0, 0.1, *tail)
+    yield "bf16 noalloc", lib.lora_linear_bwd_noalloc(F, F, F, F, F, F, F, m, k, n, r, 1.0, 0.1, F, F, F, None)
+    yield "bf16 mixed", lib.multi_lora_linear_bwd(F, F, F, F, 2, F, F, 1, F, F, m, k, n, r, *multi)
+    yield "mxfp4", lib.lora_mxfp4_linear_bwd(F, F, F, F, F, F, F, F, m, k, n, r, 1.0, 0.1, *tail)
+    yield "mxfp4 mixed", lib.multi_lora_mxfp4_linear_bwd(F, F, F, F, F, 2, F, F, 1, F, F, m, k, n, r, *multi)
+    yield "int4", lib.lora_int4_linear_bwd(F, F, F, F, 64, F, F, F, F, m, k, n, r, 1.0, 0.1, *tail)
+    yield "int4 mixed", lib.multi_lora_int4_linear_bwd(F, F, F, F, 64, F, 2, F, F, 1, F, F, m, k, n, r, *multi)
+    yield from saved_backwards(lib, m, k, n, r, wsb)
+
+
+def saved_backwards(lib, m, k, n, r, wsb=BIG):
+    for kind in (BF16, MXFP4, INT4):
+        yield f"saved {kind}", lib.lora_mxint8_linear_bwd(F, F, F, kind, F, F, 64, F, F, F, F, m, k, n, r, 1.0, 0.1, F, F, F, F, wsb, None)
+        yield f"saved {kind} mixed", lib.multi_lora_mxint8_linear_bwd(F, F, F, kind, F, F, 64, F, 2, F, F, 1, F, F, m, k, n, r, F, F, wsb, None)
+
+
+def queries(m, k, n, r):
+    yield _lib.lora_linear_bwd_workspace_size(m, k, n, r)
+    yield _lib.multi_lora_bwd_workspace_size(m, k, n, r, 2, 1)
+    yield lf.lora_mxfp4_linear_bwd_workspace_size(m, k, n, r)
+    yield lf.multi_lora_mxfp4_bwd_workspace_size(m, k, n, r, 2, 1)
+    yield lf.lora_int4_linear_bwd_workspace_size(m, k, n, 64, r)
+    yield lf.multi_lora_int4_bwd_workspace_size(m, k, n, 64, r, 2, 1)
+    for kind in (BF16, MXFP4, INT4):
+        yield lf.lora_mxint8_linear_bwd_workspace_size(kind, 64, m, k, n, r)
+        yield lf.multi_lora_mxint8_bwd_workspace_size(kind, 64, m, k, n, r, 2, 1)
+
+
+@pytest.mark.parametrize("m", [0, 1, 100])
+@pytest.mark.parametrize("k", [1 << 25, (1 << 25) + 8, 1 << 26])
+def test_backward_of_too_long_rows(lib, m, k):
+    # (the plan divided by a row count of zero here, which ended the process)
+    assert all(q == 0 for q in queries(m, k, 8, 8))
+    for name, status in backwards(lib, m, k, 8, 8):
+        assert status == UNSUPPORTED, name
+
+
+def test_backward_of_the_longest_rows(lib):
+    k = (1 << 25) - 8
+    assert all(q > 0 for q in queries(4, k, 8, 8))
+    for name, status in backwards(lib, 4, k, 8, 8, wsb=0):
+        assert status == (UNSUPPORTED if name == "bf16 noalloc" else WORKSPACE), name
