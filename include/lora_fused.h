@@ -468,7 +468,8 @@ lora_status lora_mxint8_dequantize(const void *codes, const void *scales, int64_
  * dX and dB as before.  The weight is W (kind LORA_WEIGHT_BF16; W_scales and
  * group are not read), the codes and scales of an MXFP4 weight (group is not
  * read) or those of 4-bit integers.  Other arguments, outputs, checks and
- * errors as there. */
+ * errors as there; with one adapter and a dX, A's 2 GiB are counted with r
+ * rounded up to 8. */
 typedef enum { LORA_WEIGHT_BF16 = 0, LORA_WEIGHT_MXFP4 = 1, LORA_WEIGHT_INT4 = 2 } lora_weight_kind;
 size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r);
 lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_codes, const void *x_scales, int32_t kind,

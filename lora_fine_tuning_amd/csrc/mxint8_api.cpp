@@ -175,6 +175,7 @@ extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_code
     CHECK(check_rank(r));
     CHECK(check_p(p));
     CHECK(check_b_size(r, k, n));
+    if (dX != nullptr) CHECK(check_b_size(row_of(r), k, 0));  // (the dX product reads A's copy, whose rows are longer)
     CHECK(check_bwd_k(k));
     REQ_PTR(A, 2);
     REQ_PTR(B, 2);

@@ -70,3 +70,16 @@ def test_backward_of_the_longest_rows(lib):
     assert all(q > 0 for q in queries(4, k, 8, 8))
     for name, status in backwards(lib, 4, k, 8, 8, wsb=0):
         assert status == (UNSUPPORTED if name == "bf16 noalloc" else WORKSPACE), name
+
+
+@pytest.mark.parametrize("kind", [BF16, MXFP4, INT4])
+def test_saved_input_counts_the_widened_adapter(lib, kind):
+    # the dX product reads A with its ranks rounded up to 8: 57 x 2^24 bf16 is under 2 GiB, 64 x 2^24 is not
+    def status(k, r, dX, wsb=0):
+        return lib.lora_mxint8_linear_bwd(F, F, F, kind, F, F, 64, F, F, F, F, 4, k, 8, r, 1.0, 0.1, dX, F, F, F, wsb, None)
+
+    for k, r in ((1 << 24, 57), (1 << 24, 63), (1 << 23, 121), (1 << 22, 249)):
+        assert r * k * 2 < 1 << 31
+        assert status(k, r, F, BIG) == UNSUPPORTED
+        assert status(k, r, None) == WORKSPACE  # (without dX nothing reads A)
+        assert status(k - 8, r, F) == WORKSPACE
