@@ -93,7 +93,7 @@ static lora_status prepare(const InputPlan &pl, const void *x_codes, const void 
     if (pl.widen) {
         w.S_out = (float *)ws_at(workspace, pl.s_at);
         S = w.S_out;
-        if (!multi) {
+        if (!multi && want_dX) {  // (nothing else reads A)
             w.A_out = ws_at(workspace, pl.a_at);
             src.A = w.A_out;
             src.a_r = w.row;
