@@ -380,9 +380,9 @@ lora_status multi_lora_mxfp4_linear_bwd(const void *dY, const void *X, const voi
  *
  * lora_int4_pack makes both from a checkpoint's: Q (k x n bytes, the code in
  * the low four bits), group_scales (ceil(k / group) x n of scale_type 0: fp32,
- * rounded to 16 significant bits, 1: bf16, 2: fp16; an infinity reads as NaN)
- * and zeros (ceil(k / group) x n bytes; NULL: every zero is 8); Q and
- * group_scales 4-byte aligned. */
+ * rounded to 16 significant bits, 1: bf16, 2: fp16; an infinity, given or
+ * rounded to, reads as NaN) and zeros (ceil(k / group) x n bytes; NULL: every
+ * zero is 8); Q and group_scales 4-byte aligned. */
 size_t lora_int4_codes_size(int64_t k, int64_t n);
 size_t lora_int4_scales_size(int64_t k, int64_t n, int64_t group);
 lora_status lora_int4_quantize(const void *W, int64_t k, int64_t n, int64_t group, int32_t symmetric, void *codes,

@@ -27,11 +27,12 @@ namespace lora {
 
 namespace {
 
-// fp32 -> 16 significant bits, nearest even; infinities and NaN become NaN.
+// fp32 -> 16 significant bits, nearest even; infinities, values that round to one
+// (0x7F7FFF80 and more) and NaN become NaN.
 __device__ __forceinline__ uint32_t short_scale(float s) {
-    const uint32_t u = __float_as_uint(s);
-    if ((u & 0x7F800000u) == 0x7F800000u) return 0x7FC00000u;
-    return (u + 0x7Fu + ((u >> 8) & 1u)) & 0xFFFFFF00u;
+    constexpr uint32_t kExponent = 0x7F800000u;
+    const uint32_t u = __float_as_uint(s), v = (u + 0x7Fu + ((u >> 8) & 1u)) & 0xFFFFFF00u;
+    return (u & kExponent) == kExponent || (v & kExponent) == kExponent ? 0x7FC00000u : v;
 }
 
 // The same from a double (one rounding), for scales of at least 2^-120.
