@@ -398,8 +398,9 @@ lora_status lora_int4_dequantize(const void *codes, const void *scales, int64_t 
  * arguments, outputs, checks and errors.
  *
  * A forward multiplies W' as it is where it reads the packed weight, group by
- * group in fp32: always for up to 64 rows, and for more where that is faster
- * than expanding W' into the workspace.  An expanded W', and W' in every
+ * group in fp32: always for up to 64 rows with k <= 2^20 and n <= 2^24, and for
+ * more rows where that is faster than expanding W' into the workspace.  A
+ * larger weight is expanded at any row count.  An expanded W', and W' in every
  * backward, has each of its values rounded to bf16.  Equal sizes take equal
  * ways.  In a forward from the packed weight a row's products are sums of
  * x (16 + q) less (16 + z) times the sum of x: a row of X with an infinity

@@ -579,7 +579,7 @@ const I4Kind kKinds[] = {
 static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
     I4Plan best{};
     // (offsets into X and a tile's codes stay below 2^31, and counts within an int)
-    if (m <= 0 || m > (1 << 19) || k > (1 << 20) || n > (1 << 24)) return best;
+    if (m <= 0 || m > (1 << 19) || k > kI4MaxK || n > kI4MaxN) return best;
     const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t k128 = cdiv(k, 128);
     const double bytes = (double)k * n * (0.5 + 4.0 / (double)std::min<int64_t>(group, 128));
@@ -646,7 +646,7 @@ static I4Plan find_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, i
 
 I4Plan int4_plan(int64_t m, int64_t k, int64_t n, int64_t group, int r, int nseg) {
     // (groups beyond the largest k are one and the same; r is at most 256)
-    return remembered<I4Plan>(m, k, n, (int64_t)nseg << 32 | std::min<int64_t>(group, 1 << 20) << 10 | r, [&] { return find_plan(m, k, n, group, r, nseg); });
+    return remembered<I4Plan>(m, k, n, (int64_t)nseg << 32 | std::min<int64_t>(group, kI4MaxK) << 10 | r, [&] { return find_plan(m, k, n, group, r, nseg); });
 }
 
 hipError_t launch_int4_gemm(const I4Plan &pl, const void *X, const void *codes, const void *scales, int64_t group, int m, int k, int n,

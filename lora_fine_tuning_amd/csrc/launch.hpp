@@ -348,9 +348,11 @@ hipError_t launch_mxfp4_gemm(const MxGemmPlan &pl, const void *X, const void *co
                              float *spart, hipStream_t stream);
 
 // Y = X W' (+ alpha S B) straight from a weight of 4-bit integers (int4_gemm.hip): always
-// for up to kI4Rows rows, for more where that is faster than expanding it.
+// for up to kI4Rows rows, for more where that is faster than expanding it, both with k and n
+// up to the limits here (past them the weight is expanded).
 // SK > 0: S and drop.keep are formed too, in SK partial sums.
 constexpr int kI4Rows = 64;
+constexpr int64_t kI4MaxK = 1 << 20, kI4MaxN = 1 << 24;
 struct I4Plan {
     int kind;  // tile shape; 0: expand the weight
     int tiles_m, tiles_n, KS, per;

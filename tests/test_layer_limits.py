@@ -83,3 +83,12 @@ def test_saved_input_counts_the_widened_adapter(lib, kind):
         assert status(k, r, F, BIG) == UNSUPPORTED
         assert status(k, r, None) == WORKSPACE  # (without dX nothing reads A)
         assert status(k - 8, r, F) == WORKSPACE
+
+
+@pytest.mark.parametrize("m", [1, 64])
+def test_four_bit_forward_expands_past_its_limits_alone(m):
+    # up to 64 rows the packed weight is read for k <= 2^20 and n <= 2^24; past them there is room for W' in bf16
+    for k, n, expands in ((1 << 20, 16, False), ((1 << 20) + 8, 16, True), (16, 1 << 24, False), (16, (1 << 24) + 8, True)):
+        for need in (lf.lora_int4_frozen_fwd_workspace_size(m, k, n, 64), lf.lora_int4_linear_fwd_workspace_size(m, k, n, 64, 8)):
+            part = 16 * m * n * 4 + 4 * (k // 1024 + 1) * m * 8  # the most that slices and S's partial sums take
+            assert need >= 2 * k * n if expands else need <= part + (1 << 20), (k, n)
