@@ -1435,7 +1435,9 @@ __global__ __launch_bounds__(256) void b2s_kernel(B2Params P) {
 // hands a lane eight rows of its column, and the codes times their rows' scales become
 // the bf16 operand that the expanded input would be, bit for bit.  8192 x 4096, rank 16:
 // 20 us, where expanding the input first took 23 for this pass and 18 for the expansion;
-// 8192 x 8192, 8 adapters of rank 128 at most: 52 us (52 and 34).
+// 8192 x 8192, 8 adapters of rank 128 at most: 52 us (52 and 34).  From rank 64 on the pass
+// itself is as fast from bf16 (8192 x 4096, rank 64 25.6 us, 24.8 from bf16): half the bytes,
+// but a conversion and a product more for each value; what is saved there is the expansion.
 struct B2WParams {
     const void *X;          // bf16, or codes
     const uint8_t *xscales; // X8

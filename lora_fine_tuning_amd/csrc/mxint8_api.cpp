@@ -41,8 +41,8 @@ extern "C" lora_status lora_mxint8_dequantize(const void *codes, const void *sca
 
 // The dA pass reads the codes themselves where it takes all ranks at once, up to 128; for
 // higher ranks the input is expanded to bf16 first.  The fast kernels of all passes read S,
-// dS and A in pieces of 8 ranks, so a rank that is no multiple of 8 gets copies of S and of
-// one adapter's A with rows as long as that takes (333 x 1032 x 776, rank 5: 69 us with the
+// dS and A in pieces of 8 ranks, so a rank that is no multiple of 8 gets copies of S and, for
+// dX, of one adapter's A with rows as long as that takes (333 x 1032 x 776, rank 5: 69 us with the
 // input expanded and the general kernels, 60 so; 436 x 1328 x 2336, rank 113: 409 and 173).
 // The dX product over a bf16 weight reads the mask 128 columns at a time, so where its
 // rows are no multiple of that the mask is copied too (the product of 333 x 1032 x 776, rank 8:

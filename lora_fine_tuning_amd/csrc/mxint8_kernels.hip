@@ -58,7 +58,9 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
 
 // A wave takes 2048 values of a row, a lane 8 at a time (four lanes a block), all
 // loads before the first use.  Bound by HBM: 2 bytes in, 1.03 out a value; 8192 x 14336
-// 78 us (4.6 TB/s), read back 56 us (6.4 TB/s, the codes partly out of the last cache).
+// 54 us after 512 MiB of reads (6.6 TB/s), 78 right after a kernel that wrote 235 MB, whose
+// lines go back to memory beside it (4.6 TB/s); read back 56 us (6.4 TB/s, the codes partly
+// out of the last cache).
 __global__ __launch_bounds__(256) void mxint8_quantize_kernel(const uint16_t *X, I8Shape S, uint8_t *codes, uint8_t *scales) {
     const int lane = threadIdx.x & 63;
     const int64_t waves = S.m * S.chunks;
