@@ -112,10 +112,12 @@ static bool sizes_ok(int64_t m, int64_t k, int64_t n) {
     return m >= 0 && k > 0 && n > 0 && m < (1LL << 31) && k < (1LL << 31) && n < (1LL << 31) && m * k < (1LL << 46) && k * n < (1LL << 46);
 }
 
+static bool kind_ok(int32_t kind) { return kind == LORA_WEIGHT_BF16 || kind == LORA_WEIGHT_MXFP4 || kind == LORA_WEIGHT_INT4; }
+
 static bool group_ok(int32_t kind, int64_t group) { return kind != LORA_WEIGHT_INT4 || lora_int4_scales_size(128, 8, group) > 0; }
 
 static lora_status check_weight(int32_t kind, const void *W, const void *W_scales, int64_t group) {
-    REQUIRE(kind == LORA_WEIGHT_BF16 || kind == LORA_WEIGHT_MXFP4 || kind == LORA_WEIGHT_INT4, "weight kind %d is unknown", kind);
+    REQUIRE(kind_ok(kind), "weight kind %d is unknown", kind);
     REQ_PTR(W, 16);
     if (kind != LORA_WEIGHT_BF16) REQ_PTR(W_scales, 16);
     REQUIRE(group_ok(kind, group), "group = %lld must be 32, 64 or a multiple of 128",
@@ -135,7 +137,7 @@ static lora_status check_rows(int64_t m, const void *dY, const float *S, const u
 }
 
 extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r) {
-    if (!sizes_ok(m, k, n) || !group_ok(kind, group) || r < 1 || r > 256 || !bwd_k_ok(k)) return 0;
+    if (!sizes_ok(m, k, n) || !kind_ok(kind) || !group_ok(kind, group) || r < 1 || r > 256 || !bwd_k_ok(k)) return 0;
     const size_t layer = kind == LORA_WEIGHT_BF16    ? lora_linear_bwd_workspace_size(m, k, n, row_of(r))
                          : kind == LORA_WEIGHT_MXFP4 ? lora_mxfp4_linear_bwd_workspace_size(m, k, n, row_of(r))
                                                      : lora_int4_linear_bwd_workspace_size(m, k, n, group, row_of(r));
@@ -144,7 +146,7 @@ extern "C" size_t lora_mxint8_linear_bwd_workspace_size(int32_t kind, int64_t gr
 
 extern "C" size_t multi_lora_mxint8_bwd_workspace_size(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r_max,
                                                        int32_t num_adapters, int32_t num_segments) {
-    if (!sizes_ok(m, k, n) || !group_ok(kind, group) || r_max < 1 || r_max > 256 || num_adapters < 1 || num_segments < 0 || !bwd_k_ok(k)) return 0;
+    if (!sizes_ok(m, k, n) || !kind_ok(kind) || !group_ok(kind, group) || r_max < 1 || r_max > 256 || num_adapters < 1 || num_segments < 0 || !bwd_k_ok(k)) return 0;
     const size_t layer = kind == LORA_WEIGHT_BF16    ? multi_lora_bwd_workspace_size(m, k, n, row_of(r_max), num_adapters, num_segments)
                          : kind == LORA_WEIGHT_MXFP4 ? multi_lora_mxfp4_bwd_workspace_size(m, k, n, row_of(r_max), num_adapters, num_segments)
                                                      : multi_lora_int4_bwd_workspace_size(m, k, n, group, row_of(r_max), num_adapters, num_segments);

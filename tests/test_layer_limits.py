@@ -92,3 +92,10 @@ def test_four_bit_forward_expands_past_its_limits_alone(m):
         for need in (lf.lora_int4_frozen_fwd_workspace_size(m, k, n, 64), lf.lora_int4_linear_fwd_workspace_size(m, k, n, 64, 8)):
             part = 16 * m * n * 4 + 4 * (k // 1024 + 1) * m * 8  # the most that slices and S's partial sums take
             assert need >= 2 * k * n if expands else need <= part + (1 << 20), (k, n)
+
+
+@pytest.mark.parametrize("kind", [-1, 3, 7])
+def test_saved_input_query_of_an_unknown_weight(kind):
+    for r in (5, 8, 200):
+        assert lf.lora_mxint8_linear_bwd_workspace_size(kind, 64, 100, 264, 136, r) == 0
+        assert lf.multi_lora_mxint8_bwd_workspace_size(kind, 64, 100, 264, 136, r, 2, 1) == 0
