@@ -308,6 +308,7 @@ extern "C" lora_status lora_linear_fwd(const void *X, const void *W, const void 
     REQ_PTR(S, 4);
     REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
     REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
+    CHECK(check_fwd_tiles(m, k, n));
     const FwdPlan pl = plan_fwd(m, k, r, false, 0);
     if (workspace_bytes < pl.bytes)
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
@@ -338,6 +339,7 @@ extern "C" lora_status lora_linear_fwd_concat(const void *X, const void *W, cons
     if (!aligned(A, 16) || !aligned(B, 16))
         return host_fail(LORA_ERR_UNSUPPORTED, "the concatenated forward needs A and B 16-byte aligned");
     if (m == 0) return LORA_OK;
+    CHECK(check_fwd_tiles(m, k, n));
     REQ_PTR(X, 16);
     REQ_PTR(Y, 16);
     REQ_PTR(S, 4);
@@ -418,6 +420,7 @@ extern "C" lora_status lora_linear_bwd(const void *dY, const void *X, const void
         REQUIRE(keep_bits != nullptr || p == 0.0f, "keep_bits may be NULL only when p == 0");
         REQUIRE(aligned(keep_bits, 4), "keep_bits must be 4-byte aligned");
     }
+    if (dX != nullptr) CHECK(check_dx_tiles(m, k, n));
     const BwdPlan pl = plan_bwd(m, k, n, r, false, 0, 1);
     if (workspace_bytes < pl.bytes)
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
@@ -499,6 +502,7 @@ extern "C" lora_status multi_lora_linear_fwd(const void *X, const void *W, const
     REQ_PTR(Y, 16);
     REQ_PTR(S, 4);
     REQ_PTR(keep_bits, 4);
+    CHECK(check_fwd_tiles(m, k, n));
     const FwdPlan pl = plan_fwd(m, k, r_max, true, num_segments);
     if (workspace_bytes < pl.bytes)
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
@@ -598,6 +602,7 @@ extern "C" lora_status multi_lora_linear_bwd(const void *dY, const void *X, cons
         REQ_PTR(keep_bits, 4);
         REQUIRE(dX == nullptr || aligned(dX, 16), "dX must be 16-byte aligned (or NULL: no input gradient)");
     }
+    if (dX != nullptr) CHECK(check_dx_tiles(m, k, n));
     const BwdPlan pl = plan_bwd(m, k, n, r_max, true, num_segments, num_adapters);
     if (workspace_bytes < pl.bytes)
         return host_fail(LORA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes);
@@ -679,6 +684,7 @@ extern "C" lora_status lora_frozen_fwd(const void *X, const void *W, int64_t m, 
     REQ_PTR(X, 16);
     REQ_PTR(W, 16);
     REQ_PTR(Y, 16);
+    CHECK(check_fwd_tiles(m, k, n));
     AdapterSource src{};
     HIPCHK(launch_gemm(true, 0, X, W, Y, (int)m, (int)n, (int)k, nullptr, 0, nullptr, 0, src, stream),
            "frozen fwd launch");
@@ -691,6 +697,7 @@ extern "C" lora_status lora_frozen_bwd(const void *dY, const void *W, int64_t m,
     REQ_PTR(dY, 16);
     REQ_PTR(W, 16);
     REQ_PTR(dX, 16);
+    CHECK(check_dx_tiles(m, k, n));
     AdapterSource src{};
     HIPCHK(launch_gemm(false, 0, dY, W, dX, (int)m, (int)k, (int)n, nullptr, 0, nullptr, 0, src, stream),
            "frozen bwd launch");

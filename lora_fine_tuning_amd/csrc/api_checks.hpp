@@ -54,6 +54,22 @@ inline lora_status check_bwd_k(int64_t k) {
     return LORA_OK;
 }
 
+// The bf16 GEMM's tiles address their rows with 32-bit byte offsets: 256 of the row side
+// and of the output, and of W 64 (forward) or 256 (dX).
+inline bool tile_ok(int64_t rows, int64_t tile, int64_t len) { return (rows < tile ? rows : tile) * len * 2 < (1LL << 31); }
+inline lora_status check_fwd_tiles(int64_t m, int64_t k, int64_t n) {
+    if (m > 0 && !(tile_ok(m, 256, k) && tile_ok(m, 256, n) && tile_ok(k, 64, n)))
+        return host_fail(LORA_ERR_UNSUPPORTED, "256 rows of X or Y or 64 of W exceed 2 GiB (m = %lld, k = %lld, n = %lld)",
+                         (long long)m, (long long)k, (long long)n);
+    return LORA_OK;
+}
+inline lora_status check_dx_tiles(int64_t m, int64_t k, int64_t n) {
+    if (m > 0 && !(tile_ok(m, 256, n) && tile_ok(m, 256, k) && tile_ok(k, 256, n)))
+        return host_fail(LORA_ERR_UNSUPPORTED, "256 rows of dY, dX or W exceed 2 GiB (m = %lld, k = %lld, n = %lld)",
+                         (long long)m, (long long)k, (long long)n);
+    return LORA_OK;
+}
+
 inline lora_status check_p(float p) {
     REQUIRE(p >= 0.0f && p < 1.0f, "dropout p = %g must be in [0, 1)", (double)p);
     return LORA_OK;

@@ -105,6 +105,7 @@ extern "C" lora_status lora_int4_frozen_fwd(const void *X, const void *codes, co
                                 (float *)workspace, nullptr, stream), "4-bit product launch");
         return LORA_OK;
     }
+    CHECK(check_fwd_tiles(m, k, n));
     EXPAND();
     return lora_frozen_fwd(X, workspace, m, k, n, Y, stream);
 }
@@ -126,6 +127,7 @@ extern "C" lora_status lora_int4_frozen_bwd(const void *dY, const void *codes, c
                                      AdapterSource{}, dX, stream), "4-bit sum launch");
         return LORA_OK;
     }
+    CHECK(check_dx_tiles(m, k, n));
     EXPAND();
     return lora_frozen_bwd(dY, workspace, m, k, n, dX, stream);
 }
@@ -174,6 +176,7 @@ extern "C" lora_status lora_int4_linear_fwd(const void *X, const void *codes, co
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
+    CHECK(check_fwd_tiles(m, k, n));
     EXPAND();
     return lora_linear_fwd(X, workspace, A, B, m, k, n, r, alpha, p, seed, offset, Y, S, keep_bits, ws_at(workspace, w),
                            workspace_bytes - w, stream);
@@ -195,6 +198,7 @@ lora_status int4_linear_backward(const void *dY, const LayerInput &X, const void
                                  src.p == 0.0f ? nullptr : keep_bits, src, dX, stream), "4-bit sum launch");
         return LORA_OK;
     }
+    if (dX != nullptr) CHECK(check_dx_tiles(m, k, n));
     if (m > 0 && dX != nullptr) EXPAND();
     return linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, rest, stream);
 }
@@ -214,6 +218,7 @@ lora_status multi_int4_linear_backward(const void *dY, const LayerInput &X, cons
                                  src, dX, stream), "4-bit sum launch");
         return LORA_OK;
     }
+    if (dX != nullptr) CHECK(check_dx_tiles(m, k, n));
     if (m > 0 && dX != nullptr) EXPAND();
     return multi_linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, rest, stream);
 }
@@ -285,6 +290,7 @@ extern "C" lora_status multi_lora_int4_linear_fwd(const void *X, const void *cod
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
+    CHECK(check_fwd_tiles(m, k, n));
     EXPAND();
     return multi_lora_linear_fwd(X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, m, k, n, r_max, seed, offset, Y,
                                  S, keep_bits, ws_at(workspace, w), workspace_bytes - w, stream);

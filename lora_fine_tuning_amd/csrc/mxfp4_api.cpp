@@ -89,6 +89,7 @@ extern "C" lora_status lora_mxfp4_frozen_fwd(const void *X, const void *codes, c
                                  (float *)workspace, nullptr, stream), "MXFP4 product launch");
         return LORA_OK;
     }
+    CHECK(check_fwd_tiles(m, k, n));
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_frozen_fwd(X, workspace, m, k, n, Y, stream);
 }
@@ -111,6 +112,7 @@ extern "C" lora_status lora_mxfp4_frozen_bwd(const void *dY, const void *codes, 
                                      nullptr, nullptr, AdapterSource{}, dX, stream), "MXFP4 sum launch");
         return LORA_OK;
     }
+    CHECK(check_dx_tiles(m, k, n));
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_frozen_bwd(dY, workspace, m, k, n, dX, stream);
 }
@@ -158,6 +160,7 @@ extern "C" lora_status lora_mxfp4_linear_fwd(const void *X, const void *codes, c
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
+    CHECK(check_fwd_tiles(m, k, n));
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return lora_linear_fwd(X, workspace, A, B, m, k, n, r, alpha, p, seed, offset, Y, S, keep_bits,
                            ws_at(workspace, w), workspace_bytes - w, stream);
@@ -180,6 +183,7 @@ lora_status mxfp4_linear_backward(const void *dY, const LayerInput &X, const voi
         }
         return LORA_OK;
     }
+    if (dX != nullptr) CHECK(check_dx_tiles(m, k, n));
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, ws_at(workspace, expanded_bytes(m, k, n)), stream);
@@ -200,6 +204,7 @@ lora_status multi_mxfp4_linear_backward(const void *dY, const LayerInput &X, con
         }
         return LORA_OK;
     }
+    if (dX != nullptr) CHECK(check_dx_tiles(m, k, n));
     if (m > 0 && dX != nullptr)
         HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return multi_linear_backward(dY, X, workspace, src, S, keep_bits, m, k, n, dX, ws_at(workspace, expanded_bytes(m, k, n)), stream);
@@ -278,6 +283,7 @@ extern "C" lora_status multi_lora_mxfp4_linear_fwd(const void *X, const void *co
         return LORA_OK;
     }
     const size_t w = expanded_bytes(m, k, n);
+    CHECK(check_fwd_tiles(m, k, n));
     HIPCHK(launch_mxfp4_dequantize(codes, scales, k, n, workspace, stream), "MXFP4 dequantise launch");
     return multi_lora_linear_fwd(X, workspace, adapters, num_adapters, seg_off, seg_adapter, num_segments, m, k, n,
                                  r_max, seed, offset, Y, S, keep_bits, ws_at(workspace, w), workspace_bytes - w,

@@ -50,16 +50,16 @@ extern "C" lora_status lora_mxint8_dequantize(const void *codes, const void *sca
 // the start of the workspace, the layer's own after them.
 static int32_t row_of(int32_t r) { return (r + 7) / 8 * 8; }
 struct InputPlan {
-    bool expand, widen, mask;
+    bool expand, widen, mask, packed;  // packed: dX straight from a packed weight
     size_t s_at, a_at, keep_at, bytes;
 };
 static InputPlan input_plan(int32_t kind, int64_t group, int64_t m, int64_t k, int64_t n, int32_t r, bool multi) {
-    InputPlan p{r > 128, row_of(r) != r, false, 0, 0, 0, 0};
+    InputPlan p{r > 128, row_of(r) != r, false, false, 0, 0, 0, 0};
     if (m == 0) return InputPlan{};
     const int64_t kw = (k + 31) / 32;
-    const bool packed = kind == LORA_WEIGHT_MXFP4 ? mx_gemm_t_plan(m, k, n, row_of(r)).kind != 0
-                                                  : kind == LORA_WEIGHT_INT4 && int4_t_plan(m, k, n, group, row_of(r)).kind != 0;
-    p.mask = kw % 4 != 0 && !packed;
+    p.packed = kind == LORA_WEIGHT_MXFP4 ? mx_gemm_t_plan(m, k, n, row_of(r)).kind != 0
+                                         : kind == LORA_WEIGHT_INT4 && int4_t_plan(m, k, n, group, row_of(r)).kind != 0;
+    p.mask = kw % 4 != 0 && !p.packed;
     if (p.expand) p.bytes = align_up((size_t)m * (size_t)k * 2);
     p.s_at = p.bytes;
     if (p.widen) p.bytes += align_up((size_t)m * (size_t)row_of(r) * 4);
@@ -190,6 +190,7 @@ extern "C" lora_status lora_mxint8_linear_bwd(const void *dY, const void *x_code
     LayerInput X(x_codes, x_scales);
     AdapterSource src = single_source(A, B, dA, dB, r, alpha, p);
     const InputPlan pl = input_plan(kind, group, m, k, n, r, false);
+    if (dX != nullptr && !pl.packed) CHECK(check_dx_tiles(m, k, n));
     CHECK(prepare(pl, x_codes, x_scales, m, k, r, X, S, src, keep_bits, dX != nullptr, workspace, stream));
     return layer_backward(false, kind, W, W_scales, group, dY, X, src, S, keep_bits, m, k, n, dX, ws_at(workspace, pl.bytes), stream);
 }
@@ -214,6 +215,7 @@ extern "C" lora_status multi_lora_mxint8_linear_bwd(const void *dY, const void *
     LayerInput X(x_codes, x_scales);
     AdapterSource src = multi_source(adapters, num_adapters, seg_off, seg_adapter, num_segments, r_max);
     const InputPlan pl = input_plan(kind, group, m, k, n, r_max, true);
+    if (dX != nullptr && !pl.packed) CHECK(check_dx_tiles(m, k, n));
     CHECK(prepare(pl, x_codes, x_scales, m, k, r_max, X, S, src, keep_bits, dX != nullptr, workspace, stream));
     return layer_backward(true, kind, W, W_scales, group, dY, X, src, S, keep_bits, m, k, n, dX, ws_at(workspace, pl.bytes), stream);
 }

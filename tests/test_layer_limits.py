@@ -99,3 +99,47 @@ def test_saved_input_query_of_an_unknown_weight(kind):
     for r in (5, 8, 200):
         assert lf.lora_mxint8_linear_bwd_workspace_size(kind, 64, 100, 264, 136, r) == 0
         assert lf.multi_lora_mxint8_bwd_workspace_size(kind, 64, 100, 264, 136, r, 2, 1) == 0
+
+
+def forwards(lib, m, k, n, r=8, wsb=BIG):
+    tail = (F, F, F, F, wsb, None)  # Y, S, the mask, the workspace
+    yield "bf16 frozen", lib.lora_frozen_fwd(F, F, m, k, n, F, None)
+    yield "bf16", lib.lora_linear_fwd(F, F, F, F, m, k, n, r, 1.0, 0.1, 0, 0, *tail)
+    yield "bf16 concat", lib.lora_linear_fwd_concat(F, F, F, F, m, k, n, r, 1.0, F, F, None)
+    yield "bf16 mixed", lib.multi_lora_linear_fwd(F, F, F, 2, F, F, 1, m, k, n, r, 0, 0, *tail)
+    yield "mxfp4 frozen", lib.lora_mxfp4_frozen_fwd(F, F, F, m, k, n, F, F, wsb, None)
+    yield "mxfp4", lib.lora_mxfp4_linear_fwd(F, F, F, F, F, m, k, n, r, 1.0, 0.1, 0, 0, *tail)
+    yield "mxfp4 mixed", lib.multi_lora_mxfp4_linear_fwd(F, F, F, F, 2, F, F, 1, m, k, n, r, 0, 0, *tail)
+    yield "int4 frozen", lib.lora_int4_frozen_fwd(F, F, F, 64, m, k, n, F, F, wsb, None)
+    yield "int4", lib.lora_int4_linear_fwd(F, F, F, 64, F, F, m, k, n, r, 1.0, 0.1, 0, 0, *tail)
+    yield "int4 mixed", lib.multi_lora_int4_linear_fwd(F, F, F, 64, F, 2, F, F, 1, m, k, n, r, 0, 0, *tail)
+
+
+def frozen_backwards(lib, m, k, n, wsb=BIG):
+    yield "bf16 frozen", lib.lora_frozen_bwd(F, F, m, k, n, F, None)
+    yield "mxfp4 frozen", lib.lora_mxfp4_frozen_bwd(F, F, F, m, k, n, F, F, wsb, None)
+    yield "int4 frozen", lib.lora_int4_frozen_bwd(F, F, F, 64, m, k, n, F, F, wsb, None)
+
+
+@pytest.mark.parametrize("m,k,n", [(256, 1 << 22, 8), (1000, 1 << 22, 64), (100, 11 << 20, 8), (1, 64, (1 << 24) + 8), (256, 8, (1 << 24) + 8)])
+def test_forward_of_tiles_past_two_gigabytes(lib, m, k, n):
+    # (rows of a tile past 2^31 bytes were read as zeros, or as others past 2^32, and their outputs dropped)
+    for name, status in forwards(lib, m, k, n):
+        assert status == UNSUPPORTED, name
+
+
+@pytest.mark.parametrize("m,k,n", [(256, 8, 1 << 22), (300, 1 << 22, 8), (100, 11 << 20, 8), (8, 8, 1 << 27), (1, 256, 1 << 22)])
+def test_backward_of_tiles_past_two_gigabytes(lib, m, k, n):
+    for name, status in (*backwards(lib, m, k, n, 7), *frozen_backwards(lib, m, k, n)):
+        assert status == UNSUPPORTED, name
+
+
+def test_tiles_of_just_two_gigabytes(lib):
+    for m, k, n in ((255, 1 << 22, 8), (256, (1 << 22) - 8, 8), (1, 64, (1 << 24) - 8), (1, 1 << 24, 8)):
+        for name, status in forwards(lib, m, k, n, wsb=0):
+            assert status != UNSUPPORTED, name
+    for m, k, n in ((255, 8, 1 << 22), (256, 8, (1 << 22) - 8), (1, 248, 1 << 22), (7, 8, (1 << 27) - 8)):
+        for name, status in (*backwards(lib, m, k, n, 7, wsb=0), *frozen_backwards(lib, m, k, n, wsb=0)):
+            assert status != UNSUPPORTED or "noalloc" in name, name
+    # no dX: no product over W
+    assert lib.lora_linear_bwd(F, F, F, F, F, F, F, 256, 8, 1 << 22, 7, 1.0, 0.1, None, F, F, F, 0, None) == WORKSPACE
