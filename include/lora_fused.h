@@ -59,7 +59,7 @@
  * layer calls (forward and backward) return LORA_ERR_UNSUPPORTED when B
  * (r or r_max by n bf16) or A (k by r or r_max bf16) exceeds 2 GiB, and the
  * backward calls also when k >= 2^25 (their workspace queries are then 0).
- * Products over a bf16 or an expanded W take tiles of 2 GiB at most: 256 rows
+ * Products over a bf16 or an expanded W take tiles of less than 2 GiB: 256 rows
  * (all, if there are fewer) of X, Y, dY and dX, of W 64 in a forward and 256
  * for dX; larger ones are LORA_ERR_UNSUPPORTED too.
  * When m == 0 the m-sized buffers (X, Y, S, keep_bits, dY, dX) may be NULL.
